@@ -20,18 +20,27 @@
  * The R ranks are logical: rank r's [C, H] bf16 buffer is rows [r*C, (r+1)*C)
  * of one device allocation.
  *
- * A step.  Forward: moonep_route_stats, moonep_plan, moonep_weight_slots and
+ * A step.  Forward: moonep_router (ids and gates from the router's logits, and
+ * the balance loss), moonep_route_stats, moonep_plan, moonep_weight_slots and
  * moonep_prefetch_weights (the replicas' weights), moonep_dispatch, the expert
  * computation over the buffer (moonep_expert_gemm per projection, with the
  * caller's activation between projections), moonep_combine.  Backward:
  * moonep_combine_bwd, the expert's backward (the caller's), moonep_dispatch_bwd,
- * and moonep_replica_grad_reduce for the replicas' weight-gradients.
+ * moonep_router_bwd (d_gates and the loss to the logits), and
+ * moonep_replica_grad_reduce for the replicas' weight-gradients.
+ *
+ * An 8-bit forward, for serving: moonep_rmsnorm_quant (the residual stream to
+ * 8-bit token rows, with the bf16 rows for the router), moonep_router,
+ * moonep_plan, moonep_prefetch_weights over 8-bit weight rows
+ * (moonep_quant_weights wrote them once), moonep_dispatch_quant,
+ * moonep_expert_glu_quant (gate, up and the activation), moonep_expert_gemm_quant
+ * (down), moonep_combine.
  *
  * Conventions shared by every call:
  *  - All array arguments are DEVICE pointers owned by the caller; the library
  *    allocates nothing.  Between calls it keeps only the CU's LDS size (read
  *    once per process) and, per device, whether one kernel's dynamic-LDS limit
- *    has been raised for large E and R.
+ *    has been raised for large E and R (one kernel for bf16, and the 8-bit ones).
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).  Every
  *    call only enqueues work; none waits for the device, except
  *    moonep_read_error.  Output sizes depend on the shape alone, so no call
@@ -311,6 +320,184 @@ int moonep_expert_gemm(const moonep_shape *shape, const int32_t *plan, const int
                        int32_t B, int32_t in_dim, int32_t out_dim, const uint16_t *x,
                        const uint16_t *w_home, const uint16_t *pool, int64_t w_stride,
                        int64_t w_offset, uint16_t *y, void *stream);
+
+/*
+ * The router: scores of the experts, the K experts and gates of every token,
+ * and a balance loss that keeps maxvio low in training.
+ *
+ * logits: [R*S, E], fp32 or bf16 by opts->logits_type; computed in fp32.  With
+ * l the logits of one token,
+ *   softmax (MOONEP_SCORE_SOFTMAX): s_e = exp(l_e - max l), Z = sum_e s_e;
+ *   sigmoid (MOONEP_SCORE_SIGMOID): s_e = 1 / (1 + exp(-l_e)),
+ *                                   Z = sum_e s_e + 1e-20;
+ *   p_e = s_e / Z, the token's share of every expert.
+ * topk_idx: int32 [R*S*K], the K largest logits of each token, descending, ties
+ * to the lower expert id (-0 equals +0), so what moonep_route_stats takes.
+ * gates: fp32 [R*S*K], in the same order: scale * s_k / W with
+ * W = sum of the K chosen scores (+ 1e-20 with sigmoid) if opts->normalize, else
+ * scale * p_k (softmax) or scale * s_k (sigmoid).
+ * An expert masked by a logit of -inf has score 0; it is chosen only after all
+ * others, with gate 0, and a token whose logits are all -inf has gates and
+ * shares 0.  A NaN logit ranks below -inf, and the ids stay distinct and valid;
+ * NaN (and, with softmax, +inf) goes through the formulas, where a maximum
+ * leaves a NaN out, into the token's shares and gates.
+ *
+ * Balance loss (all of counts, prob_sum, loss and workspace given; for serving
+ * pass NULL for each and it is left out).  The tokens are cut into
+ * opts->groups equal runs of n = R*S / groups (1: all tokens; R: the tokens of
+ * each rank; R*S / length: each sequence).  For group g,
+ *   counts[g, e] = T_ge, int32 [groups, E]: entries routed to e;
+ *   prob_sum[g, e] = P_ge = sum of p_e over its tokens, fp32 [groups, E];
+ *   loss[0] = mean over g of E / (K n^2) * sum_e T_ge P_ge, fp32: 1 when
+ *             counts or shares are uniform.  0 when there are no tokens.
+ * Sums over tokens are fp32 within a workgroup's few and fp64 beyond, in an
+ * order that the shape fixes: the same inputs give the same bits.
+ *
+ * workspace: moonep_router_workspace_bytes, 16-byte aligned, no initial
+ * contents needed; one call at a time uses it.  Limits (MOONEP_ERR_ARG): an
+ * unknown score or logits type, groups < 1, R*S % groups != 0,
+ * groups > 2^20 or groups * E > 2^24, a scale that is not finite.
+ */
+enum { MOONEP_SCORE_SOFTMAX = 0, MOONEP_SCORE_SIGMOID = 1 };
+enum { MOONEP_F32 = 0, MOONEP_BF16 = 1 };
+
+typedef struct moonep_router_opts {
+    int32_t score;       /* MOONEP_SCORE_* */
+    int32_t normalize;   /* nonzero: gates of a token sum to scale */
+    int32_t groups;      /* runs of tokens the loss is taken over */
+    int32_t logits_type; /* MOONEP_F32 or MOONEP_BF16, of logits and d_logits */
+    float scale;         /* factor of the gates */
+} moonep_router_opts;
+
+/* Bytes of scratch for the balance loss; 0 for an invalid shape or options. */
+size_t moonep_router_workspace_bytes(const moonep_shape *shape, const moonep_router_opts *opts);
+
+int moonep_router(const moonep_shape *shape, const moonep_router_opts *opts, const void *logits,
+                  int32_t *topk_idx, float *gates, int32_t *counts, float *prob_sum, float *loss,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Router backward: the gradient of the gates (moonep_combine_bwd's d_gates) and
+ * of the balance loss with respect to the logits.  topk_idx, counts: as
+ * moonep_router wrote them (the ids of one token are distinct; one outside
+ * [0, E) contributes nothing).  d_gates: fp32 [R*S*K] or NULL for 0; d_loss:
+ * fp32 [1], the gradient of loss[0] (the loss's weight), or NULL with counts
+ * NULL for no loss.  With a_e = d_loss E / (K n^2 groups) T_ge and dg the
+ * token's d_gates at their experts (0 elsewhere),
+ *   ds_e = (a_e - sum_j a_j p_j) / Z
+ *          + scale (dg_e - sum_j dg_j s_j / W) / W  for chosen e, normalised;
+ *          + scale (dg_e - sum_j dg_j p_j) / Z      softmax, every e;
+ *          + scale dg_e                             sigmoid;
+ *   d_logits_e = ds_e s_e (softmax) or ds_e s_e (1 - s_e) (sigmoid),
+ * rounded once to the logits' type.  The counts are constants: choosing has no
+ * gradient.  Masked experts and all-masked tokens get 0.  d_logits must not
+ * overlap logits.
+ */
+int moonep_router_bwd(const moonep_shape *shape, const moonep_router_opts *opts,
+                      const void *logits, const int32_t *topk_idx, const int32_t *counts,
+                      const float *d_gates, const float *d_loss, void *d_logits, void *stream);
+
+/*
+ * 8-bit rows.  A value is an OCP e4m3 code (1 byte) times the scale of its
+ * block, 128 consecutive columns of one row (fewer at the end of the row).  A
+ * scale is a power of two in the E8M0 form: byte b stands for 2^(b - 127).
+ * These are the block scales that gfx950's matrix instructions multiply by
+ * themselves, so they cost the products no vector work.
+ * codes: [rows, cols] bytes; scales: [rows, moonep_scale_bytes(cols)] bytes,
+ * where the bytes past ceil(cols / 128) are 127 (1.0).
+ * Every call that writes scales takes the least power of two for which the
+ * block's largest magnitude is at most 448 times it, not below 2^-126; a block
+ * of zeros has the scale 1.  The codes are the values over their scale, rounded
+ * to the nearest e4m3 value, ties to even.  A block that holds an infinity or a
+ * NaN gets the scale 255 and the codes 0x7F, both NaN.
+ * Codes are 16-byte aligned, scales 4-byte aligned, and cols % 16 == 0
+ * (MOONEP_ERR_ARG).
+ */
+size_t moonep_scale_bytes(int32_t cols); /* 4 * ceil(cols / 512); 0 if cols < 1 */
+
+/*
+ * The residual's addition, RMS norm and its 8-bit output: what a layer does to
+ * its token rows before the router and the dispatch.  x, res: bf16 [R*S, H];
+ * weight: bf16 [H]; H % 16 == 0, H <= 65536 (MOONEP_ERR_ARG).
+ *   r = bf16(x + res) (x itself if res is NULL), written to res_out;
+ *   y = r * (1 / sqrt(mean over the row of r^2 + eps)) * weight, in fp32;
+ *   y8, ys = the 8-bit row of y: codes [R*S, H], scales
+ *            [R*S, moonep_scale_bytes(H)];
+ *   y_out  = bf16(y), [R*S, H], for the router and a shared expert; NULL to
+ *            leave it out.
+ * res and res_out are both given or both NULL.  res_out may be res or x (the
+ * row is read before it is written); otherwise outputs must not overlap inputs
+ * or each other.  eps is finite and >= 0 (MOONEP_ERR_ARG).
+ */
+int moonep_rmsnorm_quant(const moonep_shape *shape, const uint16_t *x, const uint16_t *res,
+                         const uint16_t *weight, float eps, uint16_t *res_out, uint16_t *y_out,
+                         uint8_t *y8, uint8_t *ys, void *stream);
+
+/*
+ * moonep_dispatch for 8-bit rows: buf8[slot_of[n]] = x8[n div K] and
+ * bufs[slot_of[n]] = xs[n div K], bit copies of H codes and
+ * moonep_scale_bytes(H) scale bytes; x8 [R*S, H], buf8 [R*S*K, H].  Rows whose
+ * slot_of is outside [0, R*S*K) are skipped.  H % 16 == 0.  The buffers must
+ * not overlap the rows, or each other.
+ */
+int moonep_dispatch_quant(const moonep_shape *shape, const uint8_t *x8, const uint8_t *xs,
+                          const int32_t *slot_of, uint8_t *buf8, uint8_t *bufs, void *stream);
+
+/*
+ * Expert weights in 8 bits, once when they are loaded: for every expert e of
+ * E, the bf16 matrix [out_dim, in_dim] at element w_offset of row e of w
+ * [E, w_stride] becomes codes [out_dim, in_dim] at byte code_offset and scales
+ * [ceil(out_dim / 128), moonep_scale_bytes(in_dim)] at byte scale_offset of row
+ * e of w8 [E, w8_stride], one scale for each 128 x 128 block (smaller at the
+ * edges).  A row of w8 holds every matrix of an expert, so that
+ * moonep_prefetch_weights moves it as it is.  Bytes outside the two windows are
+ * not touched.
+ * Limits (MOONEP_ERR_ARG): in_dim % 16 == 0, out_dim > 0, both at most 2^30, w_stride and w_offset
+ * multiples of 8, w8_stride and code_offset multiples of 16, scale_offset of 4;
+ * windows inside their rows, and apart from each other.  w and w8 16-byte
+ * aligned and not overlapping.
+ */
+int moonep_quant_weights(const moonep_shape *shape, int32_t in_dim, int32_t out_dim,
+                         const uint16_t *w, int64_t w_stride, int64_t w_offset, uint8_t *w8,
+                         int64_t w8_stride, int64_t code_offset, int64_t scale_offset,
+                         void *stream);
+
+/*
+ * moonep_expert_gemm in 8 bits: one projection of the expert-grouped buffer.
+ * x8 [R*S*K, in_dim] codes and xs [R*S*K, moonep_scale_bytes(in_dim)] scales
+ * (e.g. what moonep_dispatch_quant wrote); the weights of row r's segment are
+ * the codes and scales at code_offset and scale_offset of its 8-bit weight row
+ * (w_home [E, w_stride] or pool [R*B, w_stride] bytes, chosen as in
+ * moonep_expert_gemm):
+ *   y[r, n] = bf16( sum_k x[r, k] * W[n, k] )  (fp32 accumulation on the matrix
+ *             cores, one rounding to nearest even), y: bf16 [R*S*K, out_dim].
+ * Limits (MOONEP_ERR_ARG): in_dim % 16 == 0, in_dim <= 2^22, out_dim % 16 == 0,
+ * w_stride and code_offset multiples of 16, scale_offset of 4, windows inside
+ * the weight row.  x8, y, w_home, pool 16-byte aligned; y must not overlap an
+ * input.
+ */
+int moonep_expert_gemm_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
+                             int32_t B, int32_t in_dim, int32_t out_dim, const uint8_t *x8,
+                             const uint8_t *xs, const uint8_t *w_home, const uint8_t *pool,
+                             int64_t w_stride, int64_t code_offset, int64_t scale_offset,
+                             uint16_t *y, void *stream);
+
+/*
+ * Gate and up projections with the activation and its 8-bit output in one
+ * call: with g and u the two products of row r (fp32, not rounded in between),
+ *   h[r, n] = g[r, n] / (1 + exp(-g[r, n])) * u[r, n]
+ * and h8 [R*S*K, mid_dim], hs [R*S*K, moonep_scale_bytes(mid_dim)] its 8-bit
+ * rows, ready for the down projection.  gate_* and up_* are the windows of the
+ * two [mid_dim, in_dim] matrices; the limits are those of
+ * moonep_expert_gemm_quant with out_dim = mid_dim.  h8 and hs must not overlap
+ * an input or each other.
+ */
+int moonep_expert_glu_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
+                            int32_t B, int32_t in_dim, int32_t mid_dim, const uint8_t *x8,
+                            const uint8_t *xs, const uint8_t *w_home, const uint8_t *pool,
+                            int64_t w_stride, int64_t gate_code_offset, int64_t gate_scale_offset,
+                            int64_t up_code_offset, int64_t up_scale_offset, uint8_t *h8,
+                            uint8_t *hs, void *stream);
 
 /*
  * Reads the sticky device error word of a workspace into *host_code, then

@@ -32,7 +32,10 @@ EXPORTS = ("moonep_check_shape", "moonep_workspace_bytes", "moonep_plan_layout_o
            "moonep_combine", "moonep_combine_bwd", "moonep_dispatch_bwd",
            "moonep_replica_grad_reduce", "moonep_weight_slots", "moonep_prefetch_weights",
            "moonep_expert_gemm", "moonep_read_error", "moonep_plan_largest_first",
-           "moonep_plan_noalloc")
+           "moonep_plan_noalloc", "moonep_router_workspace_bytes", "moonep_router",
+           "moonep_router_bwd", "moonep_scale_bytes", "moonep_rmsnorm_quant",
+           "moonep_dispatch_quant", "moonep_quant_weights", "moonep_expert_gemm_quant",
+           "moonep_expert_glu_quant")
 
 
 class MoonepError(RuntimeError):
@@ -61,6 +64,21 @@ class Shape(ctypes.Structure):
         return f"Shape(R={self.R}, E={self.E}, S={self.S}, K={self.K}, H={self.H})"
 
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+F32, BF16 = 0, 1
+
+
+class RouterOpts(ctypes.Structure):
+    """moonep_router_opts: score (SCORE_*), normalize, groups, logits_type (F32
+    or BF16) and scale."""
+    _fields_ = [("score", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("logits_type", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+    def __init__(self, score=SCORE_SOFTMAX, normalize=False, groups=1, logits_type=F32, scale=1.0):
+        super().__init__(int(score), int(normalize), int(groups), int(logits_type), float(scale))
+
+
 class PlanLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "words", "cap", "header", "rep_expert", "rep_host", "rep_count", "rep_spill_off",
@@ -80,6 +98,7 @@ def lib():
                                "`python -m load_balancing_amd.build` (there is no fallback)")
         L = ctypes.CDLL(LIB_PATH)
         P, VP, SZ, I64 = ctypes.POINTER(Shape), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
+        I32, RO = ctypes.c_int32, ctypes.POINTER(RouterOpts)
         sig = {
             "moonep_check_shape": (ctypes.c_int, [P]),
             "moonep_workspace_bytes": (SZ, [P]),
@@ -99,6 +118,19 @@ def lib():
                                                   ctypes.c_int32, VP, VP, VP, I64, I64, VP, VP]),
             "moonep_read_error": (ctypes.c_int, [VP, SZ, ctypes.POINTER(ctypes.c_int32), VP]),
             "moonep_plan_noalloc": (ctypes.c_int, [P, VP, VP, VP, VP, VP, VP, VP]),
+            "moonep_router_workspace_bytes": (SZ, [P, RO]),
+            "moonep_router": (ctypes.c_int, [P, RO, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+            "moonep_router_bwd": (ctypes.c_int, [P, RO, VP, VP, VP, VP, VP, VP, VP]),
+            "moonep_scale_bytes": (SZ, [I32]),
+            "moonep_rmsnorm_quant": (ctypes.c_int, [P, VP, VP, VP, ctypes.c_float, VP, VP, VP, VP,
+                                                    VP]),
+            "moonep_dispatch_quant": (ctypes.c_int, [P, VP, VP, VP, VP, VP, VP]),
+            "moonep_quant_weights": (ctypes.c_int, [P, I32, I32, VP, I64, I64, VP, I64, I64, I64,
+                                                    VP]),
+            "moonep_expert_gemm_quant": (ctypes.c_int, [P, VP, VP, I32, I32, I32, VP, VP, VP, VP,
+                                                        I64, I64, I64, VP, VP]),
+            "moonep_expert_glu_quant": (ctypes.c_int, [P, VP, VP, I32, I32, I32, VP, VP, VP, VP,
+                                                       I64, I64, I64, I64, I64, VP, VP, VP]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -305,6 +337,123 @@ def moonep_expert_gemm(shape, plan, wslot, B, in_dim, out_dim, x, w_home, pool, 
         _dev_bytes(w_home, "w_home", shape.E * w_stride * 2),
         _dev_bytes(pool, "pool", shape.R * B * w_stride * 2), int(w_stride), int(w_offset),
         _dev(y, "y", shape.NK * out_dim, _BF16_OK), _stream(stream)), "moonep_expert_gemm")
+
+
+def moonep_router_workspace_bytes(shape, opts: RouterOpts) -> int:
+    return lib().moonep_router_workspace_bytes(ctypes.byref(shape), ctypes.byref(opts))
+
+
+def _logit_kinds(opts):
+    return _BF16_OK if opts.logits_type == BF16 else ("float32",)
+
+
+def moonep_router(shape, opts, logits, topk_idx, gates, counts=None, prob_sum=None, loss=None,
+                  workspace=None, stream=None):
+    """topk_idx and gates [R*S*K] of logits [R*S, E]; with counts and prob_sum
+    [groups, E], loss [1] and a workspace also the balance loss."""
+    some = any(t is not None for t in (counts, prob_sum, loss, workspace))
+    tab = opts.groups * shape.E if some else 0
+    _check(lib().moonep_router(
+        ctypes.byref(shape), ctypes.byref(opts),
+        _dev(logits, "logits", shape.N * shape.E, _logit_kinds(opts)),
+        _dev(topk_idx, "topk_idx", shape.NK, ("int32",)),
+        _dev(gates, "gates", shape.NK, ("float32",)), _dev(counts, "counts", tab, ("int32",)),
+        _dev(prob_sum, "prob_sum", tab, ("float32",)),
+        _dev(loss, "loss", 1 if some else 0, ("float32",)),
+        _dev(workspace, "workspace", workspace.numel() if workspace is not None else int(some),
+             ("uint8",)),
+        _nbytes(workspace) if workspace is not None else 0, _stream(stream)), "moonep_router")
+
+
+def moonep_router_bwd(shape, opts, logits, topk_idx, counts, d_gates, d_loss, d_logits,
+                      stream=None):
+    """d_logits [R*S, E] from d_gates [R*S*K] (None: 0) and d_loss [1] with the
+    forward's counts (both None: no loss)."""
+    n = shape.N * shape.E
+    _check(lib().moonep_router_bwd(
+        ctypes.byref(shape), ctypes.byref(opts), _dev(logits, "logits", n, _logit_kinds(opts)),
+        _dev(topk_idx, "topk_idx", shape.NK, ("int32",)),
+        _dev(counts, "counts", 0 if counts is None else opts.groups * shape.E, ("int32",)),
+        _dev(d_gates, "d_gates", 0 if d_gates is None else shape.NK, ("float32",)),
+        _dev(d_loss, "d_loss", 0 if d_loss is None else 1, ("float32",)),
+        _dev(d_logits, "d_logits", n, _logit_kinds(opts)), _stream(stream)), "moonep_router_bwd")
+
+
+_CODES = ("float8_e4m3fn", "uint8")
+_SCALES = ("float8_e8m0fnu", "uint8")
+
+
+def moonep_scale_bytes(cols: int) -> int:
+    """Bytes of the scales of one 8-bit row of `cols` columns."""
+    return lib().moonep_scale_bytes(int(cols))
+
+
+def moonep_rmsnorm_quant(shape, x, res, weight, eps, res_out, y_out, y8, ys, stream=None):
+    """res_out = x + res (both None: x alone), y8 and ys its RMS norm times weight
+    [H] as 8-bit rows, y_out (or None) the same in bf16."""
+    n = shape.N * shape.H
+    _check(lib().moonep_rmsnorm_quant(
+        ctypes.byref(shape), _dev(x, "x", n, _BF16_OK),
+        _dev(res, "res", 0 if res is None else n, _BF16_OK),
+        _dev(weight, "weight", shape.H, _BF16_OK), float(eps),
+        _dev(res_out, "res_out", 0 if res_out is None else n, _BF16_OK),
+        _dev(y_out, "y_out", 0 if y_out is None else n, _BF16_OK), _dev(y8, "y8", n, _CODES),
+        _dev(ys, "ys", shape.N * moonep_scale_bytes(shape.H), _SCALES), _stream(stream)),
+        "moonep_rmsnorm_quant")
+
+
+def moonep_dispatch_quant(shape, x8, xs, slot_of, buf8, bufs, stream=None):
+    """buf8 [R*S*K, H] and bufs get every token's codes and scales at its slots."""
+    sb = moonep_scale_bytes(shape.H)
+    _check(lib().moonep_dispatch_quant(
+        ctypes.byref(shape), _dev(x8, "x8", shape.N * shape.H, _CODES),
+        _dev(xs, "xs", shape.N * sb, _SCALES), _dev(slot_of, "slot_of", shape.NK, ("int32",)),
+        _dev(buf8, "buf8", shape.NK * shape.H, _CODES), _dev(bufs, "bufs", shape.NK * sb, _SCALES),
+        _stream(stream)), "moonep_dispatch_quant")
+
+
+def moonep_quant_weights(shape, in_dim, out_dim, w, w_stride, w_offset, w8, w8_stride, code_offset,
+                         scale_offset, stream=None):
+    """The [out_dim, in_dim] bf16 matrices at element w_offset of w [E, w_stride]
+    to codes and scales inside the weight rows of w8 [E, w8_stride] bytes."""
+    _check(lib().moonep_quant_weights(
+        ctypes.byref(shape), int(in_dim), int(out_dim),
+        _dev_bytes(w, "w", shape.E * w_stride * 2), int(w_stride), int(w_offset),
+        _dev_bytes(w8, "w8", shape.E * w8_stride), int(w8_stride), int(code_offset),
+        int(scale_offset), _stream(stream)), "moonep_quant_weights")
+
+
+def moonep_expert_gemm_quant(shape, plan, wslot, B, in_dim, out_dim, x8, xs, w_home, pool, w_stride,
+                             code_offset, scale_offset, y, stream=None):
+    """y [R*S*K, out_dim] bf16 = each 8-bit buffer row times its segment's 8-bit
+    weights; w_home [E, w_stride] and pool [R*B, w_stride] bytes."""
+    _check(lib().moonep_expert_gemm_quant(
+        ctypes.byref(shape), _dev(plan, "plan", moonep_plan_bytes(shape) // 4, ("int32",)),
+        _dev(wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(out_dim),
+        _dev(x8, "x8", shape.NK * in_dim, _CODES),
+        _dev(xs, "xs", shape.NK * moonep_scale_bytes(in_dim), _SCALES),
+        _dev_bytes(w_home, "w_home", shape.E * w_stride),
+        _dev_bytes(pool, "pool", shape.R * B * w_stride), int(w_stride), int(code_offset),
+        int(scale_offset), _dev(y, "y", shape.NK * out_dim, _BF16_OK), _stream(stream)),
+        "moonep_expert_gemm_quant")
+
+
+def moonep_expert_glu_quant(shape, plan, wslot, B, in_dim, mid_dim, x8, xs, w_home, pool, w_stride,
+                            gate_code_offset, gate_scale_offset, up_code_offset, up_scale_offset,
+                            h8, hs, stream=None):
+    """h8 [R*S*K, mid_dim] and hs: silu of the gate projection times the up
+    projection of each 8-bit buffer row, as 8-bit rows."""
+    _check(lib().moonep_expert_glu_quant(
+        ctypes.byref(shape), _dev(plan, "plan", moonep_plan_bytes(shape) // 4, ("int32",)),
+        _dev(wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(mid_dim),
+        _dev(x8, "x8", shape.NK * in_dim, _CODES),
+        _dev(xs, "xs", shape.NK * moonep_scale_bytes(in_dim), _SCALES),
+        _dev_bytes(w_home, "w_home", shape.E * w_stride),
+        _dev_bytes(pool, "pool", shape.R * B * w_stride), int(w_stride), int(gate_code_offset),
+        int(gate_scale_offset), int(up_code_offset), int(up_scale_offset),
+        _dev(h8, "h8", shape.NK * mid_dim, _CODES),
+        _dev(hs, "hs", shape.NK * moonep_scale_bytes(mid_dim), _SCALES), _stream(stream)),
+        "moonep_expert_glu_quant")
 
 
 def moonep_read_error(workspace, stream=None) -> int:

@@ -2,12 +2,13 @@
 // the host, then the launches.  Every call is asynchronous on the caller's
 // stream except moonep_read_error.  The operations each call performs are
 // described, with the pages that define them, in include/moonep.h.
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
 #include <mutex>
 
-#include "moonep_internal.hpp"
+#include "quant.hpp"
 
 namespace moonep {
 int launch_route_stats(const moonep_shape &s, const int32_t *topk, int32_t *counts, float *maxvio,
@@ -36,6 +37,26 @@ int launch_expert_gemm(const moonep_shape &s, const int32_t *plan, const int32_t
                        int32_t in_dim, int32_t out_dim, const uint16_t *x, const uint16_t *w_home,
                        const uint16_t *pool, int64_t w_stride, int64_t w_offset, uint16_t *y,
                        hipStream_t st);
+size_t router_workspace(const moonep_shape &s, int32_t groups);
+int launch_router(const moonep_shape &s, const moonep_router_opts &o, const void *logits,
+                  int32_t *topk_idx, float *gates, int32_t *counts, float *prob_sum, float *loss,
+                  void *ws, hipStream_t st);
+int launch_router_bwd(const moonep_shape &s, const moonep_router_opts &o, const void *logits,
+                      const int32_t *topk_idx, const int32_t *counts, const float *d_gates,
+                      const float *d_loss, void *d_logits, hipStream_t st);
+int launch_rmsnorm_quant(const moonep_shape &s, const uint16_t *x, const uint16_t *res,
+                         const uint16_t *weight, float eps, uint16_t *res_out, uint16_t *y_out,
+                         uint8_t *y8, uint8_t *ys, hipStream_t st);
+int launch_dispatch_quant(const moonep_shape &s, const uint8_t *x8, const uint8_t *xs,
+                          const int32_t *slot_of, uint8_t *buf8, uint8_t *bufs, hipStream_t st);
+int launch_quant_weights(const moonep_shape &s, int32_t in_dim, int32_t out_dim, const uint16_t *w,
+                         int64_t w_stride, int64_t w_offset, uint8_t *w8, int64_t w8_stride,
+                         int64_t code_offset, int64_t scale_offset, hipStream_t st);
+int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_t *wslot, int32_t B,
+                        int32_t in_dim, int32_t out_dim, const uint8_t *x8, const uint8_t *xs,
+                        const uint8_t *w_home, const uint8_t *pool, int64_t w_stride,
+                        const int64_t *code, const int64_t *scale, void *out, uint8_t *out_scales,
+                        hipStream_t st);
 }  // namespace moonep
 
 using namespace moonep;
@@ -404,6 +425,251 @@ int moonep_expert_gemm(const moonep_shape *shape, const int32_t *plan, const int
         return MOONEP_ERR_ALIAS;
     return launch_expert_gemm(*shape, plan, wslot, B, in_dim, out_dim, x, w_home, pool, w_stride,
                               w_offset, y, (hipStream_t)stream);
+}
+
+namespace {
+
+// The rules of moonep_router_opts.
+int router_status(const moonep_shape *s, const moonep_router_opts *o)
+{
+    if (!o)
+        return MOONEP_ERR_NULL_PTR;
+    if ((o->score != MOONEP_SCORE_SOFTMAX && o->score != MOONEP_SCORE_SIGMOID) ||
+        (o->logits_type != MOONEP_F32 && o->logits_type != MOONEP_BF16) || !isfinite(o->scale) ||
+        o->groups < 1 || o->groups > (1 << 20) || n_tokens(s) % o->groups != 0 ||
+        (int64_t)o->groups * s->E > (1 << 24))
+        return MOONEP_ERR_ARG;
+    return MOONEP_OK;
+}
+
+// A matrix of out_dim x in_dim codes and its scales inside a weight row of
+// `stride` bytes.
+struct Window {
+    int64_t code, scale, code_bytes, scale_bytes;
+
+    Window(int64_t c, int64_t sc, int32_t in_dim, int32_t out_dim)
+        : code(c), scale(sc), code_bytes((int64_t)out_dim * in_dim),
+          scale_bytes((int64_t)((out_dim - 1) / kQuantBlock + 1) * scale_row_bytes(in_dim))
+    {
+    }
+    bool inside(int64_t stride) const
+    {
+        return code >= 0 && code % 16 == 0 && scale >= 0 && scale % 4 == 0 &&
+               code_bytes <= stride && code <= stride - code_bytes && scale_bytes <= stride &&
+               scale <= stride - scale_bytes &&
+               (code + code_bytes <= scale || scale + scale_bytes <= code);
+    }
+};
+
+int expert_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot, int32_t B,
+                 int32_t in_dim, int32_t out_dim, const uint8_t *x8, const uint8_t *xs,
+                 const uint8_t *w_home, const uint8_t *pool, int64_t w_stride, int nmat,
+                 const int64_t *code, const int64_t *scale, void *out, int64_t out_row,
+                 uint8_t *out_scales, void *stream)
+{
+    const int rc = shape_status(shape);
+    if (rc != MOONEP_OK)
+        return rc;
+    // the kernel addresses a row of a tile by a 32-bit byte offset
+    constexpr int32_t kMaxDim = 1 << 22;
+    if (B < 0 || (int64_t)shape->R * B >= ((int64_t)1 << 31) || in_dim <= 0 || in_dim % 16 != 0 ||
+        in_dim > kMaxDim || out_dim <= 0 || out_dim % 16 != 0 || out_dim > (1 << 30) ||
+        w_stride <= 0 || w_stride % 16 != 0)
+        return MOONEP_ERR_ARG;
+    for (int m = 0; m < nmat; ++m)
+        if (!Window(code[m], scale[m], in_dim, out_dim).inside(w_stride))
+            return MOONEP_ERR_ARG;
+    const int64_t rows = n_entries(shape), pool_rows = (int64_t)shape->R * B;
+    if (!plan || !wslot || !w_home || !present(x8, rows) || !present(xs, rows) ||
+        !present(out, rows) || (nmat == 2 && !present(out_scales, rows)) || !present(pool, pool_rows))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(plan, 4) || !aligned(wslot, 4) || !aligned(x8, 16) || !aligned(xs, 4) ||
+        !aligned(out, 16) || !aligned(out_scales, 4) || !aligned(w_home, 16) || !aligned(pool, 16))
+        return MOONEP_ERR_MISALIGNED;
+    const void *in[] = {x8, xs, w_home, pool};
+    const size_t in_bytes[] = {(size_t)rows * in_dim, (size_t)rows * scale_row_bytes(in_dim),
+                               (size_t)shape->E * (size_t)w_stride,
+                               (size_t)pool_rows * (size_t)w_stride};
+    const size_t ob = (size_t)rows * (size_t)out_row;
+    const size_t sb = out_scales ? (size_t)rows * scale_row_bytes(out_dim) : 0;
+    for (int i = 0; i < 4; ++i)
+        if (overlap(out, ob, in[i], in_bytes[i]) || overlap(out_scales, sb, in[i], in_bytes[i]))
+            return MOONEP_ERR_ALIAS;
+    if (overlap(out, ob, out_scales, sb))
+        return MOONEP_ERR_ALIAS;
+    if (rows == 0)
+        return MOONEP_OK;
+    return launch_expert_quant(*shape, plan, wslot, B, in_dim, out_dim, x8, xs, w_home, pool,
+                               w_stride, code, scale, out, out_scales, (hipStream_t)stream);
+}
+
+}  // namespace
+
+size_t moonep_router_workspace_bytes(const moonep_shape *shape, const moonep_router_opts *opts)
+{
+    if (shape_status(shape) != MOONEP_OK || router_status(shape, opts) != MOONEP_OK)
+        return 0;
+    return router_workspace(*shape, opts->groups);
+}
+
+int moonep_router(const moonep_shape *shape, const moonep_router_opts *opts, const void *logits,
+                  int32_t *topk_idx, float *gates, int32_t *counts, float *prob_sum, float *loss,
+                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc = shape_status(shape);
+    if (rc != MOONEP_OK || (rc = router_status(shape, opts)) != MOONEP_OK)
+        return rc;
+    const int64_t nk = n_entries(shape);
+    const bool some = counts || prob_sum || loss || workspace;
+    if (!present(logits, nk) || !present(topk_idx, nk) || !present(gates, nk) ||
+        (some && !(counts && prob_sum && loss && workspace)))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(logits, opts->logits_type == MOONEP_BF16 ? 2 : 4) || !aligned(topk_idx, 4) ||
+        !aligned(gates, 4) || !aligned(counts, 4) || !aligned(prob_sum, 4) || !aligned(loss, 4) ||
+        !aligned(workspace, 16))
+        return MOONEP_ERR_MISALIGNED;
+    if (some && workspace_bytes < router_workspace(*shape, opts->groups))
+        return MOONEP_ERR_WORKSPACE;
+    const size_t lb = (size_t)n_tokens(shape) * shape->E * (opts->logits_type == MOONEP_BF16 ? 2 : 4);
+    if (overlap(topk_idx, nk * 4, logits, lb) || overlap(gates, nk * 4, logits, lb) ||
+        overlap(topk_idx, nk * 4, gates, nk * 4))
+        return MOONEP_ERR_ALIAS;
+    return launch_router(*shape, *opts, logits, topk_idx, gates, counts, prob_sum, loss, workspace,
+                         (hipStream_t)stream);
+}
+
+int moonep_router_bwd(const moonep_shape *shape, const moonep_router_opts *opts,
+                      const void *logits, const int32_t *topk_idx, const int32_t *counts,
+                      const float *d_gates, const float *d_loss, void *d_logits, void *stream)
+{
+    int rc = shape_status(shape);
+    if (rc != MOONEP_OK || (rc = router_status(shape, opts)) != MOONEP_OK)
+        return rc;
+    const int64_t nk = n_entries(shape);
+    if (!present(logits, nk) || !present(topk_idx, nk) || !present(d_logits, nk) ||
+        (counts != nullptr) != (d_loss != nullptr))
+        return MOONEP_ERR_NULL_PTR;
+    const size_t la = opts->logits_type == MOONEP_BF16 ? 2 : 4;
+    if (!aligned(logits, la) || !aligned(d_logits, la) || !aligned(topk_idx, 4) ||
+        !aligned(counts, 4) || !aligned(d_gates, 4) || !aligned(d_loss, 4))
+        return MOONEP_ERR_MISALIGNED;
+    const size_t lb = (size_t)n_tokens(shape) * shape->E * la;
+    if (overlap(d_logits, lb, logits, lb) || overlap(d_logits, lb, topk_idx, nk * 4) ||
+        overlap(d_logits, lb, d_gates, d_gates ? nk * 4 : 0))
+        return MOONEP_ERR_ALIAS;
+    return launch_router_bwd(*shape, *opts, logits, topk_idx, counts, d_gates, d_loss, d_logits,
+                             (hipStream_t)stream);
+}
+
+size_t moonep_scale_bytes(int32_t cols) { return cols < 1 ? 0 : (size_t)scale_row_bytes(cols); }
+
+int moonep_rmsnorm_quant(const moonep_shape *shape, const uint16_t *x, const uint16_t *res,
+                         const uint16_t *weight, float eps, uint16_t *res_out, uint16_t *y_out,
+                         uint8_t *y8, uint8_t *ys, void *stream)
+{
+    const int rc = shape_status(shape);
+    if (rc != MOONEP_OK)
+        return rc;
+    if (shape->H % 16 != 0 || shape->H > 65536 || !isfinite(eps) || eps < 0.0f)
+        return MOONEP_ERR_ARG;
+    const int64_t n = n_tokens(shape);
+    if (!present(x, n) || !weight || !present(y8, n) || !present(ys, n) ||
+        (res != nullptr) != (res_out != nullptr))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(x, 16) || !aligned(res, 16) || !aligned(weight, 16) || !aligned(res_out, 16) ||
+        !aligned(y_out, 16) || !aligned(y8, 16) || !aligned(ys, 4))
+        return MOONEP_ERR_MISALIGNED;
+    const size_t row = (size_t)n * shape->H * 2, wb = (size_t)shape->H * 2;
+    const void *in[] = {x, res, weight};
+    const size_t in_bytes[] = {row, res ? row : 0, wb};
+    const void *out[] = {res_out, y_out, y8, ys};
+    const size_t out_bytes[] = {res_out ? row : 0, y_out ? row : 0, row / 2,
+                                (size_t)n * scale_row_bytes(shape->H)};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 3; ++i)
+            if (!(o == 0 && i < 2 && out[o] == in[i]) &&
+                overlap(out[o], out_bytes[o], in[i], in_bytes[i]))
+                return MOONEP_ERR_ALIAS;
+        for (int p = 0; p < o; ++p)
+            if (overlap(out[o], out_bytes[o], out[p], out_bytes[p]))
+                return MOONEP_ERR_ALIAS;
+    }
+    return launch_rmsnorm_quant(*shape, x, res, weight, eps, res_out, y_out, y8, ys,
+                                (hipStream_t)stream);
+}
+
+int moonep_dispatch_quant(const moonep_shape *shape, const uint8_t *x8, const uint8_t *xs,
+                          const int32_t *slot_of, uint8_t *buf8, uint8_t *bufs, void *stream)
+{
+    const int rc = shape_status(shape);
+    if (rc != MOONEP_OK)
+        return rc;
+    if (shape->H % 16 != 0)
+        return MOONEP_ERR_ARG;
+    const int64_t nk = n_entries(shape), nt = n_tokens(shape);
+    if (!present(x8, nt) || !present(xs, nt) || !present(slot_of, nk) || !present(buf8, nk) ||
+        !present(bufs, nk))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(x8, 16) || !aligned(buf8, 16) || !aligned(xs, 4) || !aligned(bufs, 4) ||
+        !aligned(slot_of, 4))
+        return MOONEP_ERR_MISALIGNED;
+    const size_t row = (size_t)shape->H, sr = (size_t)scale_row_bytes(shape->H);
+    const void *in[] = {x8, xs, slot_of};
+    const size_t in_bytes[] = {nt * row, nt * sr, (size_t)nk * 4};
+    for (int i = 0; i < 3; ++i)
+        if (overlap(buf8, nk * row, in[i], in_bytes[i]) || overlap(bufs, nk * sr, in[i], in_bytes[i]))
+            return MOONEP_ERR_ALIAS;
+    if (overlap(buf8, nk * row, bufs, nk * sr))
+        return MOONEP_ERR_ALIAS;
+    return launch_dispatch_quant(*shape, x8, xs, slot_of, buf8, bufs, (hipStream_t)stream);
+}
+
+int moonep_quant_weights(const moonep_shape *shape, int32_t in_dim, int32_t out_dim,
+                         const uint16_t *w, int64_t w_stride, int64_t w_offset, uint8_t *w8,
+                         int64_t w8_stride, int64_t code_offset, int64_t scale_offset, void *stream)
+{
+    const int rc = shape_status(shape);
+    if (rc != MOONEP_OK)
+        return rc;
+    constexpr int32_t kMaxDim = 1 << 30;
+    if (in_dim <= 0 || in_dim % 16 != 0 || in_dim > kMaxDim || out_dim <= 0 || out_dim > kMaxDim ||
+        w_stride <= 0 || w_stride % 8 != 0 || w_offset < 0 || w_offset % 8 != 0 || w8_stride <= 0 ||
+        w8_stride % 16 != 0)
+        return MOONEP_ERR_ARG;
+    const Window win(code_offset, scale_offset, in_dim, out_dim);
+    if (win.code_bytes > w_stride || w_offset > w_stride - win.code_bytes || !win.inside(w8_stride))
+        return MOONEP_ERR_ARG;
+    if (!w || !w8)
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(w, 16) || !aligned(w8, 16))
+        return MOONEP_ERR_MISALIGNED;
+    if (overlap(w, (size_t)shape->E * (size_t)w_stride * 2, w8, (size_t)shape->E * (size_t)w8_stride))
+        return MOONEP_ERR_ALIAS;
+    return launch_quant_weights(*shape, in_dim, out_dim, w, w_stride, w_offset, w8, w8_stride,
+                                code_offset, scale_offset, (hipStream_t)stream);
+}
+
+int moonep_expert_gemm_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
+                             int32_t B, int32_t in_dim, int32_t out_dim, const uint8_t *x8,
+                             const uint8_t *xs, const uint8_t *w_home, const uint8_t *pool,
+                             int64_t w_stride, int64_t code_offset, int64_t scale_offset,
+                             uint16_t *y, void *stream)
+{
+    return expert_quant(shape, plan, wslot, B, in_dim, out_dim, x8, xs, w_home, pool, w_stride, 1,
+                        &code_offset, &scale_offset, y, (int64_t)out_dim * 2, nullptr, stream);
+}
+
+int moonep_expert_glu_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
+                            int32_t B, int32_t in_dim, int32_t mid_dim, const uint8_t *x8,
+                            const uint8_t *xs, const uint8_t *w_home, const uint8_t *pool,
+                            int64_t w_stride, int64_t gate_code_offset, int64_t gate_scale_offset,
+                            int64_t up_code_offset, int64_t up_scale_offset, uint8_t *h8,
+                            uint8_t *hs, void *stream)
+{
+    const int64_t code[2] = {gate_code_offset, up_code_offset};
+    const int64_t scale[2] = {gate_scale_offset, up_scale_offset};
+    return expert_quant(shape, plan, wslot, B, in_dim, mid_dim, x8, xs, w_home, pool, w_stride, 2,
+                        code, scale, h8, mid_dim, hs, stream);
 }
 
 int moonep_read_error(void *workspace, size_t workspace_bytes, int32_t *host_code, void *stream)

@@ -40,7 +40,7 @@
 // k = (l / 32) * 8 .. + 7; operand B lane l holds column l % 32, same k; the
 // 32 x 32 fp32 result holds, in lane l and register r, row
 // (r / 4) * 8 + (l / 32) * 4 + r % 4 and column l % 32.
-#include "moonep_internal.hpp"
+#include "segments.hpp"
 
 namespace moonep {
 
@@ -82,38 +82,8 @@ struct GemmCfg {
     __device__ static constexpr int swz(int r) { return (r / (16 / kCpr)) % kCpr; }
 };
 
-// Exclusive scan of one int per thread over a block of NW waves.
-template <int NW>
-__device__ __forceinline__ int block_scan_excl(int v, int *tmp, int *total)
-{
-    const int lane = lane_id(), wid = (int)threadIdx.x >> 6;
-    int incl = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(incl, d, 64);
-        if (lane >= d)
-            incl += o;
-    }
-    if (lane == 63)
-        tmp[wid] = incl;
-    __syncthreads();
-    int base = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        const int t = tmp[w];
-        base += w < wid ? t : 0;
-        sum += t;
-    }
-    __syncthreads();
-    *total = sum;
-    return base + incl - v;
-}
-
 struct GemmArgs {
-    const int32_t *plan;
-    PlanLayout pl;
-    const int32_t *wslot;
-    int32_t R, E, L, C, nslots;
+    SegTables seg;
     int32_t in_dim, out_dim;
     const uint16_t *x, *w_home, *pool;
     int64_t w_stride, w_offset;
@@ -131,92 +101,27 @@ __global__ __launch_bounds__((GemmCfg<BM, BN, WM, WN, BK, S>::kThreads)) void ex
     __shared__ int scan_tmp[G::kWavesG];
 
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid >> 6;
-    const int32_t cap = a.pl.cap;
-    const int32_t nr_raw = a.plan[a.pl.header + MOONEP_PLAN_H_N_REP];
-    const int32_t n_rep = nr_raw < 0 ? 0 : (nr_raw < cap ? nr_raw : cap);
-    const int32_t nseg = a.E + n_rep;
-
-    // ---- segment tile counts, scanned into seg_start ----------------------
-    // segment s < E: home expert s; s >= E: replica s - E.  A bad table entry
-    // makes an empty segment, so every access below stays in bounds.
-    auto seg_len = [&](int32_t s) -> int32_t {
-        if (s < a.E) {
-            const int32_t off = a.plan[a.pl.home_row_off + s], n = a.plan[a.pl.keep + s];
-            return (off >= 0 && n >= 0 && off <= a.C - n) ? n : 0;
-        }
-        const int32_t j = s - a.E;
-        const int32_t h = a.plan[a.pl.rep_host + j], e = a.plan[a.pl.rep_expert + j];
-        const int32_t off = a.plan[a.pl.rep_row_off + j], n = a.plan[a.pl.rep_count + j];
-        return (h >= 0 && h < a.R && e >= 0 && e < a.E && off >= 0 && n >= 0 && off <= a.C - n)
-                   ? n : 0;
-    };
-    const int32_t per = (nseg + G::kThreads - 1) / G::kThreads;
-    const int32_t s0 = tid * per;
-    int32_t mine = 0;
-    for (int32_t s = s0; s < s0 + per && s < nseg; ++s) {
-        const int32_t len = seg_len(s);
-        mine += len > 0 ? (len + BM - 1) / BM : 0;
-    }
-    int32_t total_tiles = 0;
-    int32_t run = block_scan_excl<G::kWavesG>(mine, scan_tmp, &total_tiles);
-    for (int32_t s = s0; s < s0 + per && s < nseg; ++s) {
-        seg_start[s] = run;
-        const int32_t len = seg_len(s);
-        run += len > 0 ? (len + BM - 1) / BM : 0;
-    }
-    if (tid == 0)
-        seg_start[nseg] = total_tiles;
-    __syncthreads();
+    const int32_t nseg = a.seg.E + a.seg.n_rep();
+    const int32_t total_tiles = scan_tiles<BM, G::kWavesG>(a.seg, nseg, seg_start, scan_tmp);
 
     // ---- items of this workgroup's XCD -------------------------------------
     const int32_t nbn = (a.out_dim + BN - 1) / BN;  // the last block may be part-empty
     const int64_t items = (int64_t)total_tiles * nbn;
-    // workgroup b runs on XCD b % 8; the XCD-x workgroups take the slots
-    // after those of XCDs 0..x-1 in each round (XCD x holds ceil((P - x)/8))
-    const int xcd = (int)(blockIdx.x % 8), q = (int)(blockIdx.x / 8);
     const int P = (int)gridDim.x;
-    int slot = q;
-    for (int x = 0; x < xcd; ++x)
-        slot += (P - x + 7) / 8;
+    const int slot = xcd_slot((int)blockIdx.x, P);
     const int32_t nk = a.in_dim / G::kBK;
     const int wm = wave / G::kWN, wn = wave % G::kWN;
-    int log_nseg = 0;
-    while ((1 << log_nseg) < nseg + 1)
-        ++log_nseg;
 
     for (int64_t it = slot; it < items; it += P) {
-        // item -> (row tile t, column block nb): group gi holds row tiles
-        // [gi*kGroupM, gi*kGroupM + gm), gm < kGroupM only for the last group
-        const int64_t gi = it / ((int64_t)kGroupM * nbn);
-        const int32_t within = (int32_t)(it - gi * ((int64_t)kGroupM * nbn));
-        const int32_t gleft = total_tiles - (int32_t)gi * kGroupM;
-        const int32_t gm = gleft < kGroupM ? gleft : kGroupM;
-        const int32_t t = (int32_t)gi * kGroupM + within % gm;
-        const int32_t nb = within / gm;
-        // segment holding tile t: last s with seg_start[s] <= t (fixed-depth search)
-        int32_t s = 0;
-        for (int b = log_nseg - 1; b >= 0; --b) {
-            const int32_t c = s + (1 << b);
-            if (c < nseg && seg_start[c] <= t)
-                s = c;
-        }
+        int32_t t, nb;
+        item_of<kGroupM>(it, total_tiles, nbn, &t, &nb);
+        const int32_t s = find_segment(seg_start, nseg, t);
         const int32_t mt = t - seg_start[s];
-        int64_t row0;
-        int32_t len;
-        const uint16_t *wbase;
-        if (s < a.E) {
-            row0 = (int64_t)(s / a.L) * a.C + a.plan[a.pl.home_row_off + s];
-            len = seg_len(s);
-            wbase = a.w_home + (int64_t)s * a.w_stride;
-        } else {
-            const int32_t j = s - a.E;
-            row0 = (int64_t)a.plan[a.pl.rep_host + j] * a.C + a.plan[a.pl.rep_row_off + j];
-            len = seg_len(s);
-            const int32_t ws = a.wslot[j];
-            wbase = (ws >= 0 && ws < a.nslots)
-                        ? a.pool + (int64_t)ws * a.w_stride
-                        : a.w_home + (int64_t)a.plan[a.pl.rep_expert + j] * a.w_stride;
-        }
+        int64_t wrow;
+        bool pooled;
+        const int64_t row0 = a.seg.first_row(s, &wrow, &pooled);
+        const int32_t len = a.seg.rows(s);
+        const uint16_t *wbase = (pooled ? a.pool : a.w_home) + wrow * a.w_stride;
         wbase += a.w_offset;
         const int64_t m0 = row0 + (int64_t)mt * BM;
         const int32_t mrows = len - mt * BM < BM ? len - mt * BM : BM;
@@ -383,7 +288,7 @@ template <int BM, int BN, int WM, int WN, int BK, int S>
 int run_gemm(const GemmArgs &ga, hipStream_t st)
 {
     using G = GemmCfg<BM, BN, WM, WN, BK, S>;
-    const size_t lds = (size_t)S * G::kStageBytes + (size_t)(ga.E + ga.pl.cap + 1) * 4;
+    const size_t lds = (size_t)S * G::kStageBytes + (size_t)(ga.seg.E + ga.seg.pl.cap + 1) * 4;
     int dev = 0, cus = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
@@ -423,14 +328,7 @@ int launch_expert_gemm(const moonep_shape &s, const int32_t *plan, const int32_t
     if ((int64_t)s.R * s.S * s.K == 0)
         return MOONEP_OK;
     GemmArgs ga;
-    ga.plan = plan;
-    ga.pl = plan_layout(s.E, s.R);
-    ga.wslot = wslot;
-    ga.R = s.R;
-    ga.E = s.E;
-    ga.L = s.E / s.R;
-    ga.C = s.S * s.K;
-    ga.nslots = s.R * B;
+    ga.seg = seg_tables(s, plan, wslot, B);
     ga.in_dim = in_dim;
     ga.out_dim = out_dim;
     ga.x = x;

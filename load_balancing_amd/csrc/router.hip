@@ -1,0 +1,632 @@
+// router.hip -- scores, the K experts and gates of every token, the balance
+// loss, and the gradient of gates and loss with respect to the logits.
+//
+// A token's E logits are held by the 16 lanes of one DPP row (four tokens per
+// wave), kV per lane: chunk i of 64 experts gives lane c the experts
+// 64 i + 4 c .. + 3, so that rows of E % 4 == 0 are read as whole vectors.  Sums
+// and maxima over a token are four DPP steps for four tokens at once.
+//
+// Choosing: K rounds of the row's maximum and the least expert id that has it,
+// on integer keys ordered as the logits are.
+//
+// The shares of a workgroup's tokens are summed in registers (each lane keeps
+// its experts), then over its rows and waves, into one partial row of E sums
+// per workgroup; a second kernel joins the partials in fp64 in a fixed order.
+// Counts are integer atomics in LDS.
+#include "quant.hpp"
+
+namespace moonep {
+
+namespace {
+
+constexpr int kRowLanes = 16, kRowsPerWave = 64 / kRowLanes;
+constexpr int kRowsPerBlock = kWaves * kRowsPerWave;
+constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;
+
+// Workgroups of the loss's first pass: enough to fill the chip, few enough that
+// their partial rows stay small beside the logits.
+constexpr int64_t kLossBlocks = 2048;
+constexpr int kJoinThreads = 1024, kJoinExperts = 16, kJoinRows = kJoinThreads / kJoinExperts;
+
+struct RouterLayout {
+    int64_t per_group;   // workgroups of one group
+    int64_t tokens;      // tokens of each of them
+    size_t prob_off, count_off, loss_off, ticket_off, bytes;
+};
+
+RouterLayout router_layout(const moonep_shape &s, int32_t groups)
+{
+    RouterLayout l{};
+    const int64_t n = (int64_t)s.R * s.S / groups;
+    int64_t per = kLossBlocks / groups;
+    const int64_t most = (n + 2 * kRowsPerBlock - 1) / (2 * kRowsPerBlock);
+    per = per < most ? per : most;
+    per = per < 1 ? 1 : per;
+    l.tokens = (n + per - 1) / per;
+    l.per_group = l.tokens ? (n + l.tokens - 1) / l.tokens : 1;
+    const size_t rows = (size_t)l.per_group * groups * s.E * 4;
+    const size_t nchunk = (size_t)(s.E + kJoinExperts - 1) / kJoinExperts;
+    l.prob_off = 256;
+    l.count_off = l.prob_off + rows;
+    l.loss_off = (l.count_off + rows + 15) & ~(size_t)15;
+    l.ticket_off = 0;
+    l.bytes = l.loss_off + nchunk * groups * 8;
+    return l;
+}
+
+// exp(x) for x <= 0 or any x that the caller lets overflow to infinity: 2^(x
+// log2 e), the product's rounding error carried as a correction so that large
+// |x| keeps its digits.  The hardware's exponential is good to one unit.
+__device__ __forceinline__ float exp_of(float x)
+{
+    constexpr float kHi = 1.44269502e+00f, kLo = 1.92596303e-08f, kLn2 = 0.693147181f;
+    const float t = x * kHi;
+    const float err = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
+    const float p = __builtin_amdgcn_exp2f(t);
+    const float q = __builtin_fmaf(p, err * kLn2, p);
+    // past the exponent's range p is 0 or infinite, and its correction inf - inf
+    return __builtin_fabsf(t) < 127.0f ? q : p;
+}
+
+__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + exp_of(-l)); }
+
+__device__ __forceinline__ int32_t key_of(float l)
+{
+    const int32_t b = __float_as_int(l + 0.0f);  // -0 -> +0
+    return l != l ? kNanKey : b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+
+__device__ __forceinline__ float value_of(int32_t key)
+{
+    return key == kNanKey ? __uint_as_float(0x7FC00000u)
+                          : __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF));
+}
+
+// Expert of element i in the row's lane c.
+__device__ __forceinline__ int32_t expert_of(int i, int c) { return (i >> 2) * 64 + c * 4 + (i & 3); }
+
+// One token's logits in fp32; experts past E are -inf (score 0).
+template <int kV, bool kBf16>
+__device__ __forceinline__ void load_row(const void *logits, int64_t tok, int32_t E, int c, bool vec,
+                                         bool on, float (&l)[kV])
+{
+    constexpr float kNone = -__builtin_huge_valf();
+#pragma unroll
+    for (int i = 0; i < kV; i += 4) {
+        const int32_t e = expert_of(i, c);
+        const int64_t at = tok * E + e;
+        if (vec) {
+            const bool in = on && e < E;
+            if (kBf16) {
+                u32x2 w = {0xFF80FF80u, 0xFF80FF80u};
+                if (in)
+                    w = *(const u32x2 *)((const uint16_t *)logits + at);
+                l[i] = bf16_lo(w[0]);
+                l[i + 1] = bf16_hi(w[0]);
+                l[i + 2] = bf16_lo(w[1]);
+                l[i + 3] = bf16_hi(w[1]);
+            } else {
+                f32x4 w = {kNone, kNone, kNone, kNone};
+                if (in)
+                    w = *(const f32x4 *)((const float *)logits + at);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    l[i + j] = w[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v = kNone;
+                if (on && e + j < E)
+                    v = kBf16 ? bf16_lo(((const uint16_t *)logits)[at + j])
+                              : ((const float *)logits)[at + j];
+                l[i + j] = v;
+            }
+        }
+    }
+}
+
+// Scores of the row in place of the logits, and 1 / Z (0 for a row with no
+// expert: every score is 0 there).  top: the largest logit (softmax only).
+template <int kV>
+__device__ __forceinline__ float scores(float (&l)[kV], int32_t score, float top)
+{
+    float z = 0.0f;
+    if (score == MOONEP_SCORE_SOFTMAX) {
+        // all masked: subtract 0, every exponential is 0
+        const float base = top == -__builtin_huge_valf() ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            l[i] = exp_of(l[i] - base);
+            z += l[i];
+        }
+        z = row16_sum(z);
+        return z == 0.0f ? 0.0f : 1.0f / z;
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        l[i] = sigmoid_of(l[i]);
+        z += l[i];
+    }
+    return 1.0f / (row16_sum(z) + 1e-20f);
+}
+
+template <int kV>
+__device__ __forceinline__ float row_top(const float (&l)[kV])
+{
+    // fmaxf drops a NaN; it comes back through its own exponential
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < kV; ++i)
+        m = fmaxf(m, l[i]);
+    m = fmaxf(m, __uint_as_float(dpp<kDppRowRor8>(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(dpp<kDppRowRor4>(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(dpp<kDppRowRor2>(__float_as_uint(m))));
+    return fmaxf(m, __uint_as_float(dpp<kDppRowRor1>(__float_as_uint(m))));
+}
+
+__device__ __forceinline__ int32_t row16_imax(int32_t v)
+{
+    v = max(v, (int32_t)dpp<kDppRowRor8>((uint32_t)v));
+    v = max(v, (int32_t)dpp<kDppRowRor4>((uint32_t)v));
+    v = max(v, (int32_t)dpp<kDppRowRor2>((uint32_t)v));
+    return max(v, (int32_t)dpp<kDppRowRor1>((uint32_t)v));
+}
+
+struct RouterArgs {
+    const void *logits;
+    int32_t *topk_idx;
+    float *gates;
+    float *prob_part;      // [blocks, E]
+    int32_t *count_part;   // [blocks, E]
+    uint32_t *ticket;
+    int64_t N, n, per_group, tokens;
+    int32_t E, K, score, normalize, vec;
+    float scale;
+};
+
+}  // namespace
+
+// Workgroup b takes `tokens` consecutive tokens of group b / per_group.
+template <int kV, bool kBf16, bool kLoss>
+__global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
+{
+    extern __shared__ __align__(16) uint32_t lds[];
+    int32_t *hist = (int32_t *)lds;        // [E]
+    float *sums = (float *)(lds + a.E);    // [kWaves][E]
+    const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
+    const int c = lane % kRowLanes, r = lane / kRowLanes;
+    const int64_t g = (int64_t)blockIdx.x / a.per_group;
+    const int64_t first = g * a.n + ((int64_t)blockIdx.x - g * a.per_group) * a.tokens;
+    const int64_t end = first + a.tokens < (g + 1) * a.n ? first + a.tokens : (g + 1) * a.n;
+    float acc[kV];
+    if (kLoss) {
+        for (int32_t e = (int32_t)threadIdx.x; e < a.E; e += kBlock)
+            hist[e] = 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            *a.ticket = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            acc[i] = 0.0f;
+    }
+    for (int64_t t0 = first + wave * kRowsPerWave; t0 < end; t0 += kRowsPerBlock) {
+        const int64_t tok = t0 + r;
+        const bool on = tok < end;
+        float l[kV];
+        load_row<kV, kBf16>(a.logits, on ? tok : first, a.E, c, a.vec != 0, on, l);
+        int32_t key[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            key[i] = expert_of(i, c) < a.E ? key_of(l[i]) : kNoKey;
+        const float top = row_top(l);
+        const float rz = scores(l, a.score, top);
+        if (kLoss) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                acc[i] += on ? l[i] * rz : 0.0f;
+        }
+        // K rounds; lane k % 16 keeps round k's expert and score, and a chunk of
+        // 16 rounds is written at once
+        const float base = top == -__builtin_huge_valf() ? 0.0f : top;
+        float wsum = 0.0f, mine = 0.0f;
+        for (int32_t k0 = 0; k0 < a.K; k0 += kRowLanes) {
+            const int32_t kn = a.K - k0 < kRowLanes ? a.K - k0 : kRowLanes;
+            int32_t my_key = kNoKey, my_e = 0;
+            for (int32_t k = 0; k < kn; ++k) {
+                int32_t m = key[0];
+#pragma unroll
+                for (int i = 1; i < kV; ++i)
+                    m = max(m, key[i]);
+                m = row16_imax(m);
+                uint32_t e = 0xFFFFu;
+#pragma unroll
+                for (int i = kV - 1; i >= 0; --i)
+                    e = key[i] == m ? (uint32_t)((i >> 2) * 64 + (i & 3)) : e;
+                e = row16_min(e + (uint32_t)c * 4);
+                const int32_t rel = (int32_t)e - c * 4;
+#pragma unroll
+                for (int i = 0; i < kV; ++i)
+                    key[i] = rel == (i >> 2) * 64 + (i & 3) ? kNoKey : key[i];
+                my_key = c == k ? m : my_key;
+                my_e = c == k ? (int32_t)e : my_e;
+            }
+            const float v = value_of(my_key);
+            mine = c < kn ? (a.score == MOONEP_SCORE_SOFTMAX ? exp_of(v - base) : sigmoid_of(v)) : 0.0f;
+            wsum += mine;
+            if (on && c < kn) {
+                a.topk_idx[tok * a.K + k0 + c] = my_e;
+                if (a.K > kRowLanes)
+                    a.gates[tok * a.K + k0 + c] = mine;
+                if (kLoss)
+                    atomicAdd(hist + my_e, 1);
+            }
+        }
+        float f = a.scale;
+        if (a.normalize) {
+            const float w = row16_sum(wsum) + (a.score == MOONEP_SCORE_SIGMOID ? 1e-20f : 0.0f);
+            f = w == 0.0f ? 0.0f : a.scale / w;
+        } else if (a.score == MOONEP_SCORE_SOFTMAX) {
+            f = a.scale * rz;
+        }
+        if (a.K <= kRowLanes) {
+            if (on && c < a.K)
+                a.gates[tok * a.K + c] = mine * f;
+        } else if (on) {
+            // each lane scales what it wrote itself
+            for (int32_t k = c; k < a.K; k += kRowLanes)
+                a.gates[tok * a.K + k] *= f;
+        }
+    }
+    if (kLoss) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            acc[i] += __shfl_xor(acc[i], 16, 64);
+            acc[i] += __shfl_xor(acc[i], 32, 64);
+            if (r == 0 && expert_of(i, c) < a.E)
+                sums[wave * a.E + expert_of(i, c)] = acc[i];
+        }
+        __syncthreads();
+        for (int32_t e = (int32_t)threadIdx.x; e < a.E; e += kBlock) {
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q)
+                s += sums[q * a.E + e];
+            a.prob_part[(int64_t)blockIdx.x * a.E + e] = s;
+            a.count_part[(int64_t)blockIdx.x * a.E + e] = hist[e];
+        }
+    }
+}
+
+// Joins the partial rows of one group and 16 experts: 64 rows at a time, 16
+// lanes each, then over the 64 in LDS.  The workgroup that finishes last sums
+// the (group, chunk) losses in their order.
+__global__ __launch_bounds__(kJoinThreads) void router_join_kernel(
+    const float *__restrict__ prob_part, const int32_t *__restrict__ count_part, int64_t per_group,
+    int32_t E, int32_t nchunk, int32_t groups, double factor, int32_t *__restrict__ counts,
+    float *__restrict__ prob_sum, double *losses, uint32_t *ticket, float *__restrict__ loss)
+{
+    __shared__ double prob[kJoinThreads];
+    __shared__ int32_t cnt[kJoinThreads];
+    __shared__ bool is_last;
+    const int t = (int)threadIdx.x;
+    const int64_t total = (int64_t)groups * nchunk;
+    const int64_t g = (int64_t)blockIdx.x / nchunk;
+    const int32_t chunk = (int32_t)((int64_t)blockIdx.x - g * nchunk);
+    const int32_t e = chunk * kJoinExperts + t % kJoinExperts;
+    double p = 0.0;
+    int32_t n = 0;
+    if (e < E)
+        for (int64_t b = t / kJoinExperts; b < per_group; b += kJoinRows) {
+            const int64_t at = (g * per_group + b) * E + e;
+            p += (double)prob_part[at];
+            n += count_part[at];
+        }
+    prob[t] = p;
+    cnt[t] = n;
+    for (int w = kJoinThreads / 2; w >= kJoinExperts; w >>= 1) {
+        __syncthreads();
+        if (t < w) {
+            prob[t] += prob[t + w];
+            cnt[t] += cnt[t + w];
+        }
+    }
+    if (t < kJoinExperts && e < E) {
+        counts[g * E + e] = cnt[t];
+        prob_sum[g * E + e] = (float)prob[t];
+    }
+    if (t == 0) {
+        double s = 0.0;
+        for (int j = 0; j < kJoinExperts && chunk * kJoinExperts + j < E; ++j)
+            s += (double)cnt[j] * prob[j];
+        losses[blockIdx.x] = s;
+        __threadfence();
+        is_last = atomicAdd(ticket, 1u) == (uint32_t)(total - 1);
+        __threadfence();
+    }
+    __syncthreads();
+    if (!is_last)
+        return;
+    double s = 0.0;
+    for (int64_t i = t; i < total; i += kJoinThreads)
+        s += __hip_atomic_load(losses + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    prob[t] = s;
+    for (int w = kJoinThreads / 2; w >= 1; w >>= 1) {
+        __syncthreads();
+        if (t < w)
+            prob[t] += prob[t + w];
+    }
+    if (t == 0)
+        loss[0] = (float)(prob[0] * factor);
+}
+
+namespace {
+
+struct RouterBwdArgs {
+    const void *logits;
+    const int32_t *topk_idx, *counts;
+    const float *d_gates, *d_loss;
+    void *d_logits;
+    int64_t N, n;
+    int32_t E, K, score, normalize, vec;
+    float scale, factor;
+};
+
+}  // namespace
+
+// Four tokens per wave.  What passes between a token's K entries (a lane each)
+// and its E experts goes through LDS, E floats for each row of lanes: the
+// scores, read at the chosen experts, and the gates' gradients, added up there.
+template <int kV, bool kBf16>
+__global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
+{
+    extern __shared__ __align__(16) uint32_t lds[];
+    const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
+    const int c = lane % kRowLanes, r = lane / kRowLanes;
+    float *own = (float *)lds + (wave * kRowsPerWave + r) * (kV * kRowLanes);
+    const float dl = a.d_loss ? a.d_loss[0] * a.factor : 0.0f;
+    const float tiny = a.score == MOONEP_SCORE_SIGMOID ? 1e-20f : 0.0f;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kRowsPerWave; t0 < a.N;
+         t0 += (int64_t)gridDim.x * kRowsPerBlock) {
+        const int64_t tok = t0 + r;
+        const bool on = tok < a.N;
+        float l[kV], s[kV], part[kV];
+        load_row<kV, kBf16>(a.logits, on ? tok : 0, a.E, c, a.vec != 0, on, l);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            s[i] = l[i];
+            part[i] = 0.0f;
+        }
+        const float rz = scores(s, a.score, row_top(l));
+        float all = 0.0f;  // what every expert's ds loses to the gates
+        if (a.d_gates) {
+#pragma unroll
+            for (int i = 0; i < kV; i += 4)
+                *(f32x4 *)(own + expert_of(i, c)) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+            wave_sync();
+            float w = 0.0f, gs = 0.0f;
+            for (int32_t k = c; k < a.K; k += kRowLanes) {
+                const uint32_t e = on ? (uint32_t)a.topk_idx[tok * a.K + k] : 0xFFFFFFFFu;
+                if (e < (uint32_t)a.E) {
+                    w += own[e];
+                    gs = __builtin_fmaf(a.d_gates[tok * a.K + k], own[e], gs);
+                }
+            }
+            w = row16_sum(w) + tiny;
+            gs = row16_sum(gs);
+            float mul = a.scale, sub = 0.0f;
+            if (a.normalize) {
+                const float rw = w == 0.0f ? 0.0f : 1.0f / w;
+                mul = a.scale * rw;
+                sub = gs * rw;
+            } else if (a.score == MOONEP_SCORE_SOFTMAX) {
+                mul = a.scale * rz;
+                all = mul * gs * rz;
+            }
+            wave_sync();
+#pragma unroll
+            for (int i = 0; i < kV; i += 4)
+                *(f32x4 *)(own + expert_of(i, c)) = f32x4{0, 0, 0, 0};
+            wave_sync();
+            for (int32_t k = c; k < a.K; k += kRowLanes) {
+                const uint32_t e = on ? (uint32_t)a.topk_idx[tok * a.K + k] : 0xFFFFFFFFu;
+                if (e < (uint32_t)a.E)
+                    atomicAdd(own + e, mul * (a.d_gates[tok * a.K + k] - sub));
+            }
+            wave_sync();
+#pragma unroll
+            for (int i = 0; i < kV; i += 4) {
+                const f32x4 v = *(const f32x4 *)(own + expert_of(i, c));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    part[i + j] = v[j];
+            }
+            wave_sync();
+        }
+        if (a.counts) {
+            // the loss: its gradient at p_e is dl * T_e
+            const int32_t *cnt = a.counts + (on ? tok / a.n : 0) * a.E;
+            float la[kV], dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int32_t e = expert_of(i, c);
+                la[i] = e < a.E ? dl * (float)cnt[e] : 0.0f;
+                dot = __builtin_fmaf(la[i], s[i], dot);
+            }
+            dot = row16_sum(dot) * rz;
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                part[i] += (la[i] - dot) * rz;
+        }
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float slope = s[i];
+            if (a.score == MOONEP_SCORE_SIGMOID) {
+                // s (1 - s) without the difference, which loses the digits of s near 1
+                const float d = exp_of(-__builtin_fabsf(l[i])), q = 1.0f / (1.0f + d);
+                slope = d * q * q;
+            }
+            s[i] = (part[i] - all) * slope;
+        }
+        if (!on)
+            continue;
+#pragma unroll
+        for (int i = 0; i < kV; i += 4) {
+            const int32_t e = expert_of(i, c);
+            const int64_t at = tok * a.E + e;
+            if (a.vec && e < a.E) {
+                if (kBf16)
+                    *(u32x2 *)((uint16_t *)a.d_logits + at) =
+                        u32x2{pack_bf16(s[i], s[i + 1]), pack_bf16(s[i + 2], s[i + 3])};
+                else
+                    *(f32x4 *)((float *)a.d_logits + at) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (e + j < a.E) {
+                        if (kBf16)
+                            ((uint16_t *)a.d_logits)[at + j] = (uint16_t)(pack_bf16(s[i + j], 0.0f) & 0xFFFFu);
+                        else
+                            ((float *)a.d_logits)[at + j] = s[i + j];
+                    }
+            }
+        }
+    }
+}
+
+namespace {
+
+int last() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP; }
+
+// Rows can be read as vectors of four: every row starts on one.
+bool row_vectors(const void *a, const void *b, int32_t E, bool bf16)
+{
+    const uintptr_t m = bf16 ? 7 : 15;
+    return E % 4 == 0 && (((uintptr_t)a | (uintptr_t)b) & m) == 0;
+}
+
+// f<kV>() for the fewest experts per lane that hold E.
+template <template <int> class F, class... Args>
+int by_experts(int32_t E, Args... args)
+{
+    if (E <= 64)
+        return F<4>::run(args...);
+    if (E <= 128)
+        return F<8>::run(args...);
+    if (E <= 256)
+        return F<16>::run(args...);
+    if (E <= 512)
+        return F<32>::run(args...);
+    return F<64>::run(args...);
+}
+
+template <int kV>
+struct RunRouter {
+    static int run(const RouterArgs &a, bool bf16, bool with_loss, int64_t blocks, hipStream_t st)
+    {
+        const size_t lds = with_loss ? (size_t)(1 + kWaves) * a.E * 4 : 0;
+        const dim3 grid((uint32_t)blocks), block(kBlock);
+        if (bf16 && with_loss)
+            hipLaunchKernelGGL((router_kernel<kV, true, true>), grid, block, lds, st, a);
+        else if (bf16)
+            hipLaunchKernelGGL((router_kernel<kV, true, false>), grid, block, lds, st, a);
+        else if (with_loss)
+            hipLaunchKernelGGL((router_kernel<kV, false, true>), grid, block, lds, st, a);
+        else
+            hipLaunchKernelGGL((router_kernel<kV, false, false>), grid, block, lds, st, a);
+        return last();
+    }
+};
+
+template <int kV>
+struct RunRouterBwd {
+    static int run(const RouterBwdArgs &a, bool bf16, int64_t blocks, hipStream_t st)
+    {
+        const size_t lds = a.d_gates ? (size_t)kRowsPerBlock * kV * kRowLanes * 4 : 0;
+        const dim3 grid((uint32_t)blocks), block(kBlock);
+        if (bf16)
+            hipLaunchKernelGGL((router_bwd_kernel<kV, true>), grid, block, lds, st, a);
+        else
+            hipLaunchKernelGGL((router_bwd_kernel<kV, false>), grid, block, lds, st, a);
+        return last();
+    }
+};
+
+}  // namespace
+
+size_t router_workspace(const moonep_shape &s, int32_t groups) { return router_layout(s, groups).bytes; }
+
+int launch_router(const moonep_shape &s, const moonep_router_opts &o, const void *logits,
+                  int32_t *topk_idx, float *gates, int32_t *counts, float *prob_sum, float *loss,
+                  void *ws, hipStream_t st)
+{
+    const RouterLayout lay = router_layout(s, o.groups);
+    const bool with_loss = loss != nullptr, bf16 = o.logits_type == MOONEP_BF16;
+    char *base = (char *)ws;
+    RouterArgs a;
+    a.logits = logits;
+    a.topk_idx = topk_idx;
+    a.gates = gates;
+    a.prob_part = with_loss ? (float *)(base + lay.prob_off) : nullptr;
+    a.count_part = with_loss ? (int32_t *)(base + lay.count_off) : nullptr;
+    a.ticket = with_loss ? (uint32_t *)(base + lay.ticket_off) : nullptr;
+    a.N = (int64_t)s.R * s.S;
+    a.E = s.E;
+    a.K = s.K;
+    a.score = o.score;
+    a.normalize = o.normalize;
+    a.vec = row_vectors(logits, nullptr, s.E, bf16);
+    a.scale = o.scale;
+    if (!with_loss) {
+        // one workgroup per 16 tokens, more where that would be over 2^20 workgroups
+        if (a.N == 0)
+            return MOONEP_OK;
+        a.n = a.N;
+        a.tokens = kRowsPerBlock * (1 + a.N / ((int64_t)kRowsPerBlock << 20));
+        a.per_group = (a.N + a.tokens - 1) / a.tokens;
+        return by_experts<RunRouter>(s.E, a, bf16, false, a.per_group, st);
+    }
+    a.n = a.N / o.groups;
+    a.tokens = lay.tokens;
+    a.per_group = lay.per_group;
+    const int rc = by_experts<RunRouter>(s.E, a, bf16, true, lay.per_group * o.groups, st);
+    if (rc != MOONEP_OK)
+        return rc;
+    const int32_t nchunk = (s.E + kJoinExperts - 1) / kJoinExperts;
+    const double n = (double)a.n;
+    const double factor = a.n ? (double)s.E / ((double)s.K * n * n * o.groups) : 0.0;
+    hipLaunchKernelGGL(router_join_kernel, dim3((uint32_t)((int64_t)nchunk * o.groups)),
+                       dim3(kJoinThreads), 0, st, a.prob_part, a.count_part, a.per_group, s.E, nchunk,
+                       o.groups, factor, counts, prob_sum, (double *)(base + lay.loss_off), a.ticket,
+                       loss);
+    return last();
+}
+
+int launch_router_bwd(const moonep_shape &s, const moonep_router_opts &o, const void *logits,
+                      const int32_t *topk_idx, const int32_t *counts, const float *d_gates,
+                      const float *d_loss, void *d_logits, hipStream_t st)
+{
+    RouterBwdArgs a;
+    a.logits = logits;
+    a.topk_idx = topk_idx;
+    a.counts = counts;
+    a.d_gates = d_gates;
+    a.d_loss = d_loss;
+    a.d_logits = d_logits;
+    a.N = (int64_t)s.R * s.S;
+    if (a.N == 0)
+        return MOONEP_OK;
+    a.n = a.N / o.groups;
+    a.E = s.E;
+    a.K = s.K;
+    a.score = o.score;
+    a.normalize = o.normalize;
+    const bool bf16 = o.logits_type == MOONEP_BF16;
+    a.vec = row_vectors(logits, d_logits, s.E, bf16);
+    a.scale = o.scale;
+    a.factor = (float)((double)s.E / ((double)s.K * (double)a.n * (double)a.n * o.groups));
+    const int64_t need = (a.N + kRowsPerBlock - 1) / kRowsPerBlock;
+    return by_experts<RunRouterBwd>(s.E, a, bf16, need < 8192 ? need : 8192, st);
+}
+
+}  // namespace moonep

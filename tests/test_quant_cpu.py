@@ -1,0 +1,160 @@
+"""What the router and the 8-bit calls refuse, found on the host before anything
+is enqueued, and the sizes they report (CPU only: no call here reaches the GPU)."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import load_balancing_amd as mx
+from quant_ref import quantise, scale_of, values
+
+vp, B, i64 = ctypes.c_void_p, ctypes.byref, ctypes.c_int64
+FAKE = 0x10000000  # never dereferenced: every call below fails validation first
+OK, SHAPE, NULL, MISALIGNED, WORKSPACE, ALIAS, ARG = 0, -1, -2, -3, -4, -6, -7
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(mx.LIB_PATH):
+        from load_balancing_amd import build
+        build.build()
+    return mx.lib()
+
+
+def at(n):
+    """A fake array of its own, far from the others."""
+    return vp(FAKE * (n + 1))
+
+
+def test_scale_bytes(L):
+    assert [mx.moonep_scale_bytes(c) for c in (-5, 0, 1, 16, 128, 512, 513, 1408, 2048, 7168)] == \
+        [0, 0, 4, 4, 4, 4, 8, 12, 16, 56]
+
+
+def test_router_options(L):
+    s = mx.Shape(4, 16, 6, 2, 64)
+    ok = mx.RouterOpts(groups=8)
+    assert mx.moonep_router_workspace_bytes(s, ok) > 0
+    nan, inf = float("nan"), float("inf")
+    for bad in (mx.RouterOpts(score=2), mx.RouterOpts(score=-1), mx.RouterOpts(logits_type=2), mx.RouterOpts(groups=0),
+                mx.RouterOpts(groups=5), mx.RouterOpts(groups=-1), mx.RouterOpts(scale=nan), mx.RouterOpts(scale=inf)):
+        assert mx.moonep_router_workspace_bytes(s, bad) == 0
+        assert L.moonep_router(B(s), B(bad), at(0), at(1), at(2), None, None, None, None, 0, None) == ARG
+        assert L.moonep_router_bwd(B(s), B(bad), at(0), at(1), None, at(2), None, at(3), None) == ARG
+    big = mx.Shape(1, 1024, 1 << 20, 1, 64)
+    assert mx.moonep_router_workspace_bytes(big, mx.RouterOpts(groups=1 << 14)) > 0
+    assert mx.moonep_router_workspace_bytes(big, mx.RouterOpts(groups=1 << 15)) == 0  # groups * E > 2^24
+    assert mx.moonep_router_workspace_bytes(mx.Shape(3, 16, 6, 2, 64), ok) == 0
+    assert L.moonep_router_workspace_bytes(B(s), None) == 0
+
+
+def test_router_refusals(L):
+    s, o = mx.Shape(4, 16, 128, 2, 64), mx.RouterOpts()
+    need = mx.moonep_router_workspace_bytes(s, o)
+    call = lambda lg=at(0), ids=at(1), g=at(2), c=at(3), p=at(4), ls=at(5), ws=at(6), n=need, opts=o, sh=s: \
+        L.moonep_router(B(sh), B(opts), lg, ids, g, c, p, ls, ws, n, None)  # noqa: E731
+    assert call(sh=mx.Shape(3, 16, 128, 2, 64)) == SHAPE
+    assert L.moonep_router(B(s), None, at(0), at(1), at(2), None, None, None, None, 0, None) == NULL
+    assert call(lg=None) == NULL and call(ids=None) == NULL and call(g=None) == NULL
+    # the loss's outputs and workspace: all or none
+    assert call(c=None) == NULL and call(p=None) == NULL and call(ls=None) == NULL and call(ws=None) == NULL
+    assert call(lg=vp(FAKE + 2)) == MISALIGNED
+    assert call(ws=vp(FAKE * 7 + 8)) == MISALIGNED and call(g=vp(FAKE * 3 + 1)) == MISALIGNED
+    assert call(n=need - 1) == WORKSPACE
+    assert call(ids=vp(FAKE + 4 * 100)) == ALIAS and call(g=vp(FAKE * 2 + 4)) == ALIAS
+    back = lambda lg=at(0), ids=at(1), c=at(2), dg=at(3), dl=at(4), out=at(5): \
+        L.moonep_router_bwd(B(s), B(o), lg, ids, c, dg, dl, out, None)  # noqa: E731
+    assert back(lg=None) == NULL and back(ids=None) == NULL and back(out=None) == NULL
+    assert back(c=None) == NULL and back(dl=None) == NULL
+    assert back(out=vp(FAKE * 6 + 2)) == MISALIGNED
+    assert back(out=at(0)) == ALIAS and back(out=at(3)) == ALIAS and back(out=at(1)) == ALIAS
+
+
+def test_norm_refusals(L):
+    s = mx.Shape(1, 1, 8, 1, 64)
+    call = lambda x=at(0), r=at(1), w=at(2), eps=1e-6, ro=at(3), y=at(4), y8=at(5), ys=at(6), sh=s: \
+        L.moonep_rmsnorm_quant(B(sh), x, r, w, ctypes.c_float(eps), ro, y, y8, ys, None)  # noqa: E731
+    assert call(sh=mx.Shape(1, 1, 8, 1, 60)) == SHAPE
+    assert call(sh=mx.Shape(1, 1, 8, 1, 72)) == ARG            # H % 16
+    assert call(sh=mx.Shape(1, 1, 8, 1, 65552)) == ARG         # H over 65536
+    assert call(eps=-1e-6) == ARG and call(eps=float("nan")) == ARG and call(eps=float("inf")) == ARG
+    assert call(x=None) == NULL and call(w=None) == NULL and call(y8=None) == NULL and call(ys=None) == NULL
+    assert call(r=None) == NULL and call(ro=None) == NULL      # both or neither
+    assert call(x=vp(FAKE + 8)) == MISALIGNED and call(ys=vp(FAKE * 7 + 2)) == MISALIGNED
+    assert call(y=at(0)) == ALIAS and call(y8=at(1)) == ALIAS and call(ys=vp(FAKE * 6 + 64)) == ALIAS
+    assert call(ro=vp(FAKE + 128)) == ALIAS                    # over x, but not x itself
+    assert call(ro=at(2)) == ALIAS
+
+
+def test_dispatch_refusals(L):
+    s = mx.Shape(4, 16, 8, 2, 64)
+    call = lambda x8=at(0), xs=at(1), so=at(2), b8=at(3), bs=at(4), sh=s: \
+        L.moonep_dispatch_quant(B(sh), x8, xs, so, b8, bs, None)  # noqa: E731
+    assert call(sh=mx.Shape(3, 16, 8, 2, 64)) == SHAPE
+    assert call(sh=mx.Shape(4, 16, 8, 2, 72)) == ARG
+    for k in ("x8", "xs", "so", "b8", "bs"):
+        assert call(**{k: None}) == NULL
+    assert call(b8=vp(FAKE * 4 + 8)) == MISALIGNED and call(bs=vp(FAKE * 5 + 2)) == MISALIGNED
+    assert call(b8=vp(FAKE + 16)) == ALIAS and call(bs=at(2)) == ALIAS and call(bs=vp(FAKE * 4 + 64)) == ALIAS
+
+
+def test_weight_refusals(L):
+    s = mx.Shape(1, 4, 0, 1, 16)
+    call = lambda inp=256, out=128, w=at(0), ws=256 * 128, wo=0, w8=at(1), st=256 * 128 + 16, co=0, so=256 * 128: \
+        L.moonep_quant_weights(B(s), inp, out, w, i64(ws), i64(wo), w8, i64(st), i64(co), i64(so), None)  # noqa: E731
+    assert call(inp=0) == ARG and call(inp=24) == ARG and call(out=0) == ARG and call(out=-8) == ARG
+    assert call(inp=(1 << 30) + 16) == ARG and call(out=(1 << 30) + 1) == ARG
+    assert call(ws=256 * 128 - 8) == ARG and call(wo=8) == ARG and call(wo=-8) == ARG and call(ws=256 * 128 + 4) == ARG
+    assert call(st=256 * 128) == ARG                       # no room for the scales
+    assert call(st=256 * 128 + 8) == ARG and call(co=8) == ARG and call(so=256 * 128 + 2) == ARG
+    assert call(so=256 * 128 - 4) == ARG and call(co=-16) == ARG and call(so=-4) == ARG  # windows that overlap, or start before
+    assert call(co=1 << 40) == ARG and call(so=1 << 40) == ARG
+    assert call(w=None) == NULL and call(w8=None) == NULL
+    assert call(w=vp(FAKE + 8)) == MISALIGNED and call(w8=vp(FAKE * 2 + 8)) == MISALIGNED
+    assert call(w8=vp(FAKE + 1024)) == ALIAS
+
+
+@pytest.mark.parametrize("glu", [False, True], ids=["gemm", "glu"])
+def test_product_refusals(L, glu):
+    s = mx.Shape(4, 16, 8, 2, 64)
+    n = 256 * 128
+
+    def call(plan=at(0), ws=at(1), Bs=2, inp=256, out=128, x8=at(2), xs=at(3), wh=at(4), pool=at(5), st=2 * (n + 16),
+             co=0, so=2 * n, y=at(6), hs=at(7), sh=s):
+        if not glu:
+            return L.moonep_expert_gemm_quant(B(sh), plan, ws, Bs, inp, out, x8, xs, wh, pool, i64(st), i64(co), i64(so),
+                                              y, None)
+        # the window under test is up's; gate's is sound
+        return L.moonep_expert_glu_quant(B(sh), plan, ws, Bs, inp, out, x8, xs, wh, pool, i64(st), i64(n), i64(2 * n + 16),
+                                         i64(co), i64(so), y, hs, None)
+
+    assert call(sh=mx.Shape(3, 16, 8, 2, 64)) == SHAPE
+    assert call(Bs=-1) == ARG and call(Bs=1 << 30) == ARG
+    assert call(inp=0) == ARG and call(inp=200) == ARG and call(out=0) == ARG and call(out=120) == ARG
+    assert call(inp=(1 << 22) + 16, st=1 << 40) == ARG
+    assert call(st=0) == ARG and call(st=2 * (n + 16) + 8) == ARG
+    assert call(co=4) == ARG and call(co=-16) == ARG and call(co=n + 48) == ARG
+    assert call(so=2 * n + 2) == ARG and call(so=2 * n + 32) == ARG and call(so=n - 4) == ARG
+    for k in ("plan", "ws", "x8", "xs", "wh", "pool", "y"):
+        assert call(**{k: None}) == NULL, k
+    assert call(x8=vp(FAKE * 3 + 8)) == MISALIGNED and call(xs=vp(FAKE * 4 + 2)) == MISALIGNED
+    assert call(y=vp(FAKE * 7 + 8)) == MISALIGNED and call(wh=vp(FAKE * 5 + 8)) == MISALIGNED
+    assert call(y=at(2)) == ALIAS and call(y=vp(FAKE * 5 + 64)) == ALIAS and call(y=at(5)) == ALIAS and call(y=at(3)) == ALIAS
+    if glu:
+        assert call(hs=None) == NULL and call(hs=vp(FAKE * 8 + 2)) == MISALIGNED
+        assert call(hs=at(6)) == ALIAS and call(hs=at(2)) == ALIAS
+    # nothing to do: accepted without a launch
+    empty = mx.Shape(4, 16, 0, 2, 64)
+    assert call(sh=empty, x8=None, xs=None, y=None, hs=None) == OK
+
+
+def test_reference_quantisation():
+    """The tests' own rounding: least scale, exact at its border, codes within half a step."""
+    assert scale_of(np.array([448.0, 448.0001, 224.0, 1.75, 1.7500001, 0.0, 2.0 ** -140])).tolist() == \
+        [127, 128, 126, 119, 120, 127, 1]
+    rng = np.random.default_rng(0)
+    y = (rng.standard_normal((7, 300)) * 2.0 ** rng.integers(-20, 20, (7, 300))).astype(np.float32).astype(np.float64)
+    c, s = quantise(y)
+    step = np.repeat(np.ldexp(1.0, s.astype(int) - 127), 128, axis=1)[:, :300]
+    assert (np.abs(values(c, s) - y) <= np.maximum(np.abs(y) * 2.0 ** -4, step * 2.0 ** -10)).all()
