@@ -119,8 +119,8 @@ __global__ __launch_bounds__((GemmCfg<BM, BN, WM, WN, BK, S>::kThreads)) void ex
         const int32_t mt = t - seg_start[s];
         int64_t wrow;
         bool pooled;
-        const int64_t row0 = a.seg.first_row(s, &wrow, &pooled);
-        const int32_t len = a.seg.rows(s);
+        int32_t len;
+        const int64_t row0 = a.seg.segment(s, &len, &wrow, &pooled);
         const uint16_t *wbase = (pooled ? a.pool : a.w_home) + wrow * a.w_stride;
         wbase += a.w_offset;
         const int64_t m0 = row0 + (int64_t)mt * BM;

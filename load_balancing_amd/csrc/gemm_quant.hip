@@ -45,19 +45,25 @@ struct QCfg {
     static constexpr int kAInstr = BM / 8 / kWavesG;  // 8 rows (1 KiB) per LDS-DMA load
     static constexpr int kBInstr = BN / 8 / kWavesG;
     static constexpr int kPerStage = kAInstr + kBInstr + 1;
-    static constexpr int kScaleAt = (BM + BN) * kBK;
+    static constexpr int kBBlocks = GLU ? 2 : (BN + kQuantBlock - 1) / kQuantBlock;
+    static constexpr int kScaleAt = (BM + BN) * kBK;  // [BM] row scales, then the weights'
     static constexpr int kStageBytes = kScaleAt + kThreads * 4;
     static constexpr int kOutCols = GLU ? BN / 2 : BN;
-    static constexpr int kLdo = GLU ? kOutCols + 4 : kOutCols + 8;  // epilogue row, elements
-    static constexpr int kOutBytes = GLU ? 4 : 2;
-    static constexpr int kOutVec = 8;                     // columns per thread of the epilogue
-    static constexpr int kOIter = WM * kOutCols / kOutVec / kThreads;
+    // Epilogue, in the stage that was computed last: GLU all rows of codes and
+    // the waves' row maxima; else a band of rows in bf16.
+    static constexpr int kBands = GLU ? 1 : kWM;
+    static constexpr int kBandRows = BM / kBands;
+    static constexpr int kOutBytes = GLU ? 1 : 2;
+    static constexpr int kLdoBytes = kOutCols * kOutBytes + 16;
+    static constexpr int kMaxAt = kBandRows * kLdoBytes;
+    static constexpr int kVecPerRow = kOutCols * kOutBytes / 16;
+    static constexpr int kOIter = kBandRows * kVecPerRow / kThreads;
     static_assert(BM % (8 * kWavesG) == 0 && BN % (8 * kWavesG) == 0, "rows per DMA round");
-    static_assert(BM <= kThreads, "one scale dword per thread");
-    static_assert(WM * kLdo * kOutBytes <= S * kStageBytes, "an epilogue band must fit the ring");
+    static_assert(BM + kBBlocks <= kThreads, "a thread for every scale");
+    static_assert(kMaxAt + (GLU ? BM * kWN * 4 : 0) <= kStageBytes, "the epilogue fits one stage");
     static_assert((S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
     static_assert(!GLU || (kOutCols == kQuantBlock && kTN == 2), "gate and up in one wave, one block");
-    static_assert(kOIter >= 1 && WM * kOutCols % (kOutVec * kThreads) == 0, "epilogue split");
+    static_assert(kOIter >= 1 && kBandRows * kVecPerRow % kThreads == 0, "epilogue split");
     __device__ static constexpr int swz(int r) { return (r >> 1) & 7; }
 };
 
@@ -78,6 +84,28 @@ __device__ __forceinline__ void wait_vm()
     __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
 }
 
+// One LDS-DMA load: kBytes of each lane to dst + lane * kBytes.
+template <int kBytes>
+__device__ __forceinline__ void dma(const uint8_t *src, char *dst)
+{
+    auto *to = (__attribute__((address_space(3))) void *)dst;
+    if constexpr (kBytes == 16)
+        __builtin_amdgcn_global_load_lds((const void *)src, to, 16, 0, 0);
+    else
+        __builtin_amdgcn_global_load_lds((const void *)src, to, 4, 0, 0);
+}
+
+// A workgroup barrier that waits for this wave's LDS operations only: a
+// __syncthreads would also wait for every load in flight, which leaves a ring
+// of any depth with one stage.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 }  // namespace
 
 template <int BM, int BN, int WM, int WN, int S, bool GLU>
@@ -89,7 +117,8 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
     int32_t *seg_start = (int32_t *)(lds_b + S * G::kStageBytes);
     __shared__ int scan_tmp[G::kWavesG];
 
-    const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / G::kWN, wn = wave % G::kWN;
     const int32_t nseg = a.seg.E + a.seg.n_rep();
     const int32_t tiles = scan_tiles<BM, G::kWavesG>(a.seg, nseg, seg_start, scan_tmp);
@@ -99,93 +128,123 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
     const int32_t SB = scale_row_bytes(a.in_dim), SO = scale_row_bytes(a.out_dim);
     const bool k_tail = a.in_dim % G::kBK != 0;
 
-    for (int64_t it = xcd_slot((int)blockIdx.x, (int)gridDim.x); it < items; it += gridDim.x) {
-        int32_t t, nb;
+    // ---- the loads: items and their k-steps in one sequence ------------------
+    // LDS-DMA: lane i of a load brings chunk (i % 8) ^ swz(row) of row 8 g + i / 8
+    // to byte 16 i of the load's KiB.  Row r of the B tile is column r of the
+    // block, or for gate and up column (r / 64) * 32 + r % 32 of gate (r / 32
+    // even) or up, which one load never mixes.
+    struct Load {
+        int64_t it, m0;
+        int32_t kt, mrows, n0;
+        const uint8_t *a_base, *w_base;
+        const uint8_t *scale;  // this thread's
+        uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
+    };
+    Load ld;
+    ld.it = xcd_slot((int)blockIdx.x, (int)gridDim.x);
+    if (ld.it >= items)
+        return;
+    const int dma_row = lane >> 3, dma_pos = lane & 7;
+    auto a_row = [&](int v) { return (v * G::kWavesG + wave) * 8 + dma_row; };
+    auto b_mat = [&](int v) { return GLU ? (v * G::kWavesG + wave) / 4 % 2 : 0; };
+    auto chunk = [&](int v) { return (dma_pos ^ G::swz(a_row(v))) << 4; };
+    // First row and column of an item, its rows and its weights.
+    auto locate = [&](int64_t it, int64_t *m0, int32_t *mrows, int32_t *n0) -> const uint8_t * {
+        int32_t t, nb, n;
         item_of<kTileGroup>(it, tiles, nbn, &t, &nb);
         const int32_t s = find_segment(seg_start, nseg, t);
+        const int32_t mt = t - __builtin_amdgcn_readfirstlane(seg_start[s]);
         int64_t wrow;
         bool pooled;
-        const int32_t mt = t - seg_start[s];
-        const int64_t m0 = a.seg.first_row(s, &wrow, &pooled) + (int64_t)mt * BM;
-        const int32_t left = a.seg.rows(s) - mt * BM;
-        const int32_t mrows = left < BM ? left : BM;
-        const uint8_t *wbase = (pooled ? a.pool : a.w_home) + wrow * a.w_stride;
-        const int32_t n0 = nb * G::kOutCols;
-
-        // Row of the B tile -> matrix and column: for gate and up, 32 of one and
-        // 32 of the other in turn.
-        auto b_col = [&](int row) { return n0 + (GLU ? (row >> 6) * 32 + (row & 31) : row); };
-        auto b_mat = [&](int row) { return GLU ? (row >> 5) & 1 : 0; };
-
-        // LDS-DMA: lane i of a load brings chunk (i % 8) ^ swz(row) of row
-        // 8 g + i / 8 to byte 16 i of the load's KiB.
-        const int dma_row = lane >> 3, dma_pos = lane & 7;
-        uint32_t a_off[G::kAInstr];
-        const uint8_t *b_ptr[G::kBInstr];
+        *m0 = a.seg.segment(s, &n, &wrow, &pooled) + (int64_t)mt * BM;
+        *mrows = n - mt * BM < BM ? n - mt * BM : BM;
+        *n0 = nb * G::kOutCols;
+        return (pooled ? a.pool : a.w_home) + wrow * a.w_stride;
+    };
+    auto begin_item = [&]() {
+        ld.w_base = locate(ld.it, &ld.m0, &ld.mrows, &ld.n0);
+        ld.kt = 0;
+        ld.a_base = a.x8 + ld.m0 * a.in_dim;
 #pragma unroll
-        for (int v = 0; v < G::kAInstr; ++v) {
-            const int row = (v * G::kWavesG + wave) * 8 + dma_row;
-            a_off[v] = (uint32_t)((row < mrows ? row : 0) * a.in_dim + ((dma_pos ^ G::swz(row)) << 4));
-        }
+        for (int v = 0; v < G::kAInstr; ++v)
+            ld.a_off[v] = (uint32_t)((a_row(v) < ld.mrows ? a_row(v) : 0) * a.in_dim + chunk(v));
 #pragma unroll
         for (int v = 0; v < G::kBInstr; ++v) {
-            const int row = (v * G::kWavesG + wave) * 8 + dma_row;
-            const int32_t col = b_col(row) < a.out_dim ? b_col(row) : n0;
-            b_ptr[v] = wbase + a.code[b_mat(row)] + (int64_t)col * a.in_dim + ((dma_pos ^ G::swz(row)) << 4);
+            const int r = a_row(v), c = GLU ? (r >> 6) * 32 + (r & 31) : r;
+            // columns past the end are not stored: the block's first serves them
+            ld.b_off[v] = (uint32_t)((ld.n0 + c < a.out_dim ? c : 0) * a.in_dim + chunk(v));
         }
-        const uint8_t *a_base = a.x8 + m0 * a.in_dim;
-        const int srow = tid % BM;
-        const uint8_t *as_base = a.xs + (m0 + (srow < mrows ? srow : 0)) * SB;
-        auto dma16 = [&](const uint8_t *src, char *dst) {
-            __builtin_amdgcn_global_load_lds((const void *)src,
-                                             (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-        };
-        auto issue = [&](int32_t kt) {
-            char *dst = lds_b + (kt % S) * G::kStageBytes;
-            const int64_t k0 = (int64_t)kt * G::kBK;
-            const bool tail = k_tail && kt == nk - 1;
-#pragma unroll
-            for (int v = 0; v < G::kAInstr; ++v) {
-                const int row = (v * G::kWavesG + wave) * 8 + dma_row;
-                const uint8_t *src = a_base + k0 + a_off[v];
-                if (tail && k0 + ((dma_pos ^ G::swz(row)) << 4) >= a.in_dim)
-                    src = kZeros;
-                dma16(src, dst + (v * G::kWavesG + wave) * 1024);
-            }
-#pragma unroll
-            for (int v = 0; v < G::kBInstr; ++v) {
-                const int row = (v * G::kWavesG + wave) * 8 + dma_row;
-                const uint8_t *src = b_ptr[v] + k0;
-                if (tail && k0 + ((dma_pos ^ G::swz(row)) << 4) >= a.in_dim)
-                    src = kZeros;
-                dma16(src, dst + BM * G::kBK + (v * G::kWavesG + wave) * 1024);
-            }
-            __builtin_amdgcn_global_load_lds(
-                (const void *)(as_base + (kt >> 2) * 4),
-                (__attribute__((address_space(3))) void *)(dst + G::kScaleAt + wave * 256), 4, 0, 0);
-        };
-        const int fr = lane & 31, fsw = G::swz(lane & 31), fhalf = lane >> 5;
-        auto frag = [&](const char *base, int row0, int ks) -> i32x8 {
-            const char *p = base + (row0 + fr) * G::kBK;
-            const u32x4 lo = *(const u32x4 *)(p + (((4 * ks + fhalf) ^ fsw) << 4));
-            const u32x4 hi = *(const u32x4 *)(p + (((4 * ks + 2 + fhalf) ^ fsw) << 4));
-            i32x8 r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                r[j] = (int)lo[j];
-                r[4 + j] = (int)hi[j];
-            }
-            return r;
-        };
-        // scale row of this wave's B columns (column tile j of gate and up: its
-        // matrix); columns past the end are not stored, any row serves them
-        auto b_scales = [&](int j) -> const uint32_t * {
+        if (tid < BM) {
+            ld.scale = a.xs + (ld.m0 + (tid < ld.mrows ? tid : 0)) * SB;
+        } else {
+            // weights: block q of the tile's columns, or gate's and up's block
+            const int q = tid - BM < G::kBBlocks ? tid - BM : 0;
             const int32_t last_block = (a.out_dim - 1) / kQuantBlock;
-            const int32_t col = n0 + (GLU ? 0 : wn * WN + j * 32);
-            const int32_t block = col / kQuantBlock < last_block ? col / kQuantBlock : last_block;
-            return (const uint32_t *)(wbase + a.scale[GLU ? j & 1 : 0] + (int64_t)block * SB);
-        };
+            const int32_t block = ld.n0 / kQuantBlock + (GLU ? 0 : q);
+            ld.scale = ld.w_base + a.scale[GLU ? q : 0] +
+                       (int64_t)(block < last_block ? block : last_block) * SB;
+        }
+    };
+    // Issues the next stage into slot `slot`, and moves on to the next item behind
+    // an item's last.
+    auto issue = [&](int slot) {
+        char *dst = lds_b + slot * G::kStageBytes;
+        const int64_t k0 = (int64_t)ld.kt * G::kBK;
+        const uint8_t *ap = ld.a_base + k0;
+        const uint8_t *bp[2] = {ld.w_base + a.code[0] + (int64_t)ld.n0 * a.in_dim + k0,
+                                ld.w_base + a.code[1] + (int64_t)ld.n0 * a.in_dim + k0};
+        if (k_tail && ld.kt == nk - 1) {
+            const int32_t left = a.in_dim - (int32_t)k0;
+#pragma unroll
+            for (int v = 0; v < G::kAInstr; ++v)
+                dma<16>(chunk(v) < left ? ap + ld.a_off[v] : kZeros,
+                        dst + (v * G::kWavesG + wave) * 1024);
+#pragma unroll
+            for (int v = 0; v < G::kBInstr; ++v)
+                dma<16>(chunk(v) < left ? bp[b_mat(v)] + ld.b_off[v] : kZeros,
+                        dst + BM * G::kBK + (v * G::kWavesG + wave) * 1024);
+        } else {
+#pragma unroll
+            for (int v = 0; v < G::kAInstr; ++v)
+                dma<16>(ap + ld.a_off[v], dst + (v * G::kWavesG + wave) * 1024);
+#pragma unroll
+            for (int v = 0; v < G::kBInstr; ++v)
+                dma<16>(bp[b_mat(v)] + ld.b_off[v], dst + BM * G::kBK + (v * G::kWavesG + wave) * 1024);
+        }
+        dma<4>(ld.scale + (ld.kt >> 2) * 4, dst + G::kScaleAt + wave * 256);
+        if (++ld.kt == nk) {
+            ld.it += gridDim.x;
+            if (ld.it < items)
+                begin_item();
+        }
+    };
 
+    // ---- the products ---------------------------------------------------------
+    const int fr = lane & 31, fsw = G::swz(lane & 31), fhalf = lane >> 5;
+    auto frag = [&](const char *base, int row0, int ks) -> i32x8 {
+        const char *p = base + (row0 + fr) * G::kBK;
+        const u32x4 lo = *(const u32x4 *)(p + (((4 * ks + fhalf) ^ fsw) << 4));
+        const u32x4 hi = *(const u32x4 *)(p + (((4 * ks + 2 + fhalf) ^ fsw) << 4));
+        i32x8 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r[j] = (int)lo[j];
+            r[4 + j] = (int)hi[j];
+        }
+        return r;
+    };
+    begin_item();
+    int slot = 0;  // of the stage computed next; the ring runs on across items
+#pragma unroll
+    for (int st = 0; st + 1 < S; ++st)
+        if (ld.it < items)
+            issue(st);
+
+    for (int64_t it = xcd_slot((int)blockIdx.x, (int)gridDim.x); it < items; it += gridDim.x) {
+        int64_t m0 = ld.m0;
+        int32_t mrows = ld.mrows, n0 = ld.n0;
+        if (ld.it != it)
+            locate(it, &m0, &mrows, &n0);  // few k-steps: the loads are at a later item already
         f32x16 acc[G::kTM][G::kTN];
 #pragma unroll
         for (int i = 0; i < G::kTM; ++i)
@@ -195,104 +254,121 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
                 for (int q = 0; q < 16; ++q)
                     acc[i][j][q] = 0.0f;
 
-#pragma unroll
-        for (int st = 0; st + 1 < S; ++st)
-            if (st < nk)
-                issue(st);
         for (int32_t kt = 0; kt < nk; ++kt) {
-            if (kt + S - 2 < nk)
+            // This stage's loads have landed once only what was issued after them is
+            // outstanding: those of S - 2 stages at least (and the stores of the
+            // epilogue before, if any), as long as there are stages to issue.
+            if (ld.it < items)
                 wait_vm<(S - 2) * G::kPerStage>();
             else
                 wait_vm<0>();
-            __syncthreads();  // every wave's part of stage kt is there; slot (kt - 1) % S is free
-            if (kt + S - 1 < nk)
-                issue(kt + S - 1);
-            const char *sa = lds_b + (kt % S) * G::kStageBytes;
+            lds_barrier();  // every wave's part of the stage is there, and the one before is free
+            const int cur = slot;
+            slot = slot + 1 == S ? 0 : slot + 1;
+            if (ld.it < items)
+                issue(cur == 0 ? S - 1 : cur - 1);
+            const char *sa = lds_b + cur * G::kStageBytes;
             const char *sb = sa + BM * G::kBK;
+            const uint32_t *sc = (const uint32_t *)(sa + G::kScaleAt);
             const int shift = (kt & 3) * 8;
             int sca[G::kTM], scb[G::kTN];
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i)
-                sca[i] = (int)(*(const uint32_t *)(sa + G::kScaleAt + (wm * WM + i * 32 + fr) * 4) >> shift);
+                sca[i] = (int)(sc[wm * WM + i * 32 + fr] >> shift);
 #pragma unroll
             for (int j = 0; j < G::kTN; ++j)
-                scb[j] = (int)(b_scales(j)[kt >> 2] >> shift);
+                scb[j] = (int)(sc[BM + (GLU ? j : (wn * WN + j * 32) / kQuantBlock)] >> shift);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 i32x8 fa[G::kTM], fb[G::kTN];
-#pragma unroll
-                for (int i = 0; i < G::kTM; ++i)
-                    fa[i] = frag(sa, wm * WM + i * 32, ks);
 #pragma unroll
                 for (int j = 0; j < G::kTN; ++j)
                     fb[j] = frag(sb, wn * WN + j * 32, ks);
 #pragma unroll
                 for (int i = 0; i < G::kTM; ++i)
-#pragma unroll
-                    for (int j = 0; j < G::kTN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            fa[i], fb[j], acc[i][j], 0, 0, 0, sca[i], 0, scb[j]);
-            }
-        }
-        __syncthreads();  // the ring is free for the epilogue
-
-        // ---- epilogue, one band of wave rows at a time through LDS -------------
-#pragma unroll
-        for (int band = 0; band < G::kWM; ++band) {
-            if (wm == band) {
+                    fa[i] = frag(sa, wm * WM + i * 32, ks);
 #pragma unroll
                 for (int i = 0; i < G::kTM; ++i)
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const int row = i * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3);
-                        if (GLU) {
-                            const float g = acc[i][0][q], u = acc[i][G::kTN - 1][q];
-                            const float h = g / (1.0f + __expf(-g)) * u;
-                            ((float *)lds_b)[row * G::kLdo + wn * 32 + fr] = h;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < G::kTN; ++j)
-                                ((uint16_t *)lds_b)[row * G::kLdo + wn * WN + j * 32 + fr] =
-                                    (uint16_t)(pack_bf16(acc[i][j][q], 0.0f) & 0xFFFFu);
-                        }
-                    }
+                    for (int j = 0; j < G::kTN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            fb[j], fa[i], acc[i][j], 0, 0, 0, scb[j], 0, sca[i]);
             }
-            __syncthreads();
+        }
+        lds_barrier();  // the stage computed last is free for the epilogue
+
+        // ---- epilogue: lane l holds row l % 32 of tile i, and of each column tile
+        // the columns 8 (q / 4) + 4 (l / 32) + q % 4 ------------------------------
+        char *so = lds_b + (slot == 0 ? S - 1 : slot - 1) * G::kStageBytes;
+        if constexpr (GLU) {
+            float *row_max = (float *)(so + G::kMaxAt);  // [BM][kWN]
+#pragma unroll
+            for (int i = 0; i < G::kTM; ++i) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const float g = acc[i][0][q], u = acc[i][G::kTN - 1][q];
+                    const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+                    acc[i][0][q] = h;
+                    m = max(m, n0 + wn * 32 + (q >> 2) * 8 + fhalf * 4 < a.out_dim ? abs_bits(h) : 0u);
+                }
+                m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                if (fhalf == 0)
+                    row_max[(wm * WM + i * 32 + fr) * G::kWN + wn] = __uint_as_float(m);
+            }
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < G::kTM; ++i) {
+                const int row = wm * WM + i * 32 + fr;
+                uint32_t m = 0;
+#pragma unroll
+                for (int q = 0; q < G::kWN; ++q)
+                    m = max(m, __float_as_uint(row_max[row * G::kWN + q]));
+                const uint32_t byte = scale_byte(m);
+                const float inv = inverse_scale(byte);
+#pragma unroll
+                for (int q = 0; q < 16; q += 4)
+                    *(uint32_t *)(so + row * G::kLdoBytes + wn * 32 + q * 2 + fhalf * 4) =
+                        pack_e4m3(acc[i][0][q], acc[i][0][q + 1], acc[i][0][q + 2], acc[i][0][q + 3],
+                                  inv, byte);
+                if (wn == 0 && fhalf == 0 && row < mrows) {
+                    uint8_t *dst = a.out_scales + (m0 + row) * SO;
+                    const int32_t nb = n0 / kQuantBlock;
+                    dst[nb] = (uint8_t)byte;
+                    if (nb == nbn - 1)
+                        for (int32_t p = nbn; p < SO; ++p)
+                            dst[p] = 127;
+                }
+            }
+        }
+#pragma unroll
+        for (int band = 0; band < G::kBands; ++band) {
+            if (!GLU) {
+                if (band)
+                    lds_barrier();  // the band before has been read
+                if (wm == band) {
+#pragma unroll
+                    for (int i = 0; i < G::kTM; ++i)
+#pragma unroll
+                        for (int j = 0; j < G::kTN; ++j)
+#pragma unroll
+                            for (int q = 0; q < 16; q += 4)
+                                *(u32x2 *)(so + (i * 32 + fr) * G::kLdoBytes +
+                                           (wn * WN + j * 32 + q * 2 + fhalf * 4) * 2) =
+                                    u32x2{pack_bf16(acc[i][j][q], acc[i][j][q + 1]),
+                                          pack_bf16(acc[i][j][q + 2], acc[i][j][q + 3])};
+                }
+            }
+            lds_barrier();
 #pragma unroll
             for (int v = 0; v < G::kOIter; ++v) {
                 const int idx = tid + v * G::kThreads;
-                const int row = idx / (G::kOutCols / 8), c = idx % (G::kOutCols / 8) * 8;
-                const int grow = band * WM + row;
-                const bool in = grow < mrows && n0 + c < a.out_dim;
-                const int64_t at = (m0 + grow) * a.out_dim + n0 + c;
-                if (GLU) {
-                    const float *src = (const float *)lds_b + row * G::kLdo + c;
-                    float f[8];
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        f[j] = src[j];
-                        m = max(m, n0 + c < a.out_dim ? abs_bits(f[j]) : 0u);
-                    }
-                    const uint32_t byte = scale_byte(row16_max(m));
-                    const float inv = inverse_scale(byte);
-                    if (in)
-                        *(u32x2 *)((uint8_t *)a.out + at) =
-                            u32x2{pack_e4m3(f[0], f[1], f[2], f[3], inv, byte),
-                                  pack_e4m3(f[4], f[5], f[6], f[7], inv, byte)};
-                    if (grow < mrows && c == 0) {
-                        uint8_t *dst = a.out_scales + (m0 + grow) * SO;
-                        dst[nb] = (uint8_t)byte;
-                        if (nb == nbn - 1)
-                            for (int32_t p = nbn; p < SO; ++p)
-                                dst[p] = 127;
-                    }
-                } else if (in) {
-                    *(u32x4 *)((uint16_t *)a.out + at) =
-                        *(const u32x4 *)((const uint16_t *)lds_b + row * G::kLdo + c);
-                }
+                const int row = idx / G::kVecPerRow, c = idx % G::kVecPerRow;
+                const int grow = band * G::kBandRows + row;
+                if (grow < mrows && n0 + c * (16 / G::kOutBytes) < a.out_dim)
+                    *(u32x4 *)((char *)a.out + ((m0 + grow) * a.out_dim + n0) * G::kOutBytes + c * 16) =
+                        *(const u32x4 *)(so + row * G::kLdoBytes + c * 16);
             }
-            __syncthreads();
         }
     }
 }
@@ -320,10 +396,7 @@ int run_quant(const QuantGemmArgs &a, hipStream_t st)
         if (dev >= 0 && dev < 64)
             raised[dev] = true;
     }
-    int per_cu = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, G::kThreads, lds) != hipSuccess)
-        return MOONEP_ERR_HIP;
-    hipLaunchKernelGGL(kernel, dim3(cus * (per_cu > 0 ? per_cu : 1)), dim3(G::kThreads), lds, st, a);
+    hipLaunchKernelGGL(kernel, dim3(cus), dim3(G::kThreads), lds, st, a);
     return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP;
 }
 
@@ -355,8 +428,8 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
     a.out = out;
     a.out_scales = out_scales;
     if (rows <= (int64_t)32 * s.E)
-        return glu ? run_quant<32, 256, 32, 64, 3, true>(a, st)
-                   : run_quant<32, 128, 32, 32, 4, false>(a, st);
+        return glu ? run_quant<32, 256, 32, 64, 4, true>(a, st)
+                   : run_quant<32, 128, 32, 32, 7, false>(a, st);
     return glu ? run_quant<256, 256, 128, 64, 2, true>(a, st)
                : run_quant<256, 256, 128, 64, 2, false>(a, st);
 }

@@ -16,6 +16,14 @@ struct SegTables {
     const int32_t *wslot;
     int32_t R, E, L, C, nslots;
 
+    // A word of the tables at a uniform address: a scalar load, which does not
+    // wait for the vector loads in flight.  The tables are not written by the
+    // kernels that read them.
+    __device__ static __forceinline__ int32_t word(const int32_t *p)
+    {
+        return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+    }
+
     __device__ __forceinline__ int32_t n_rep() const
     {
         const int32_t n = plan[pl.header + MOONEP_PLAN_H_N_REP];
@@ -36,19 +44,23 @@ struct SegTables {
         return (h >= 0 && h < R && e >= 0 && e < E && off >= 0 && n >= 0 && off <= C - n) ? n : 0;
     }
 
-    // First buffer row of a segment that has rows, and its weight row: of the
-    // pool if *pooled, else of the home weights.
-    __device__ __forceinline__ int64_t first_row(int32_t s, int64_t *weight_row, bool *pooled) const
+    // First buffer row of a segment that has rows, its row count, and its weight
+    // row: of the pool if *pooled, else of the home weights.  s is uniform.
+    __device__ __forceinline__ int64_t segment(int32_t s, int32_t *n, int64_t *weight_row,
+                                               bool *pooled) const
     {
+        s = __builtin_amdgcn_readfirstlane(s);
         *pooled = false;
         if (s < E) {
             *weight_row = s;
-            return (int64_t)(s / L) * C + plan[pl.home_row_off + s];
+            *n = word(plan + pl.keep + s);
+            return (int64_t)(s / L) * C + word(plan + pl.home_row_off + s);
         }
-        const int32_t j = s - E, ws = wslot[j];
+        const int32_t j = s - E, ws = word(wslot + j);
         *pooled = ws >= 0 && ws < nslots;
-        *weight_row = *pooled ? ws : plan[pl.rep_expert + j];
-        return (int64_t)plan[pl.rep_host + j] * C + plan[pl.rep_row_off + j];
+        *weight_row = *pooled ? ws : word(plan + pl.rep_expert + j);
+        *n = word(plan + pl.rep_count + j);
+        return (int64_t)word(plan + pl.rep_host + j) * C + word(plan + pl.rep_row_off + j);
     }
 };
 
@@ -116,19 +128,18 @@ __device__ __forceinline__ int32_t scan_tiles(const SegTables &t, int32_t nseg, 
     return total;
 }
 
-// Segment that holds tile t: the last s with seg_start[s] <= t.
+// Segment that holds tile t: the last s with seg_start[s] <= t, for nseg <=
+// 4096 and every lane of the wave active (uniform).  Two rounds of 64
+// comparisons at once: every step-th segment, then the step after the last of
+// those.
 __device__ __forceinline__ int32_t find_segment(const int32_t *seg_start, int32_t nseg, int32_t t)
 {
-    int log_nseg = 0;
-    while ((1 << log_nseg) < nseg + 1)
-        ++log_nseg;
-    int32_t s = 0;
-    for (int b = log_nseg - 1; b >= 0; --b) {
-        const int32_t c = s + (1 << b);
-        if (c < nseg && seg_start[c] <= t)
-            s = c;
-    }
-    return s;
+    const int lane = lane_id();
+    const int32_t step = (nseg + 63) / 64;
+    const int32_t c = lane * step;
+    const int32_t s0 = (__popcll(ballot(c < nseg && seg_start[c < nseg ? c : 0] <= t)) - 1) * step;
+    const int32_t d = s0 + lane;
+    return s0 + __popcll(ballot(lane < step && d < nseg && seg_start[d < nseg ? d : 0] <= t)) - 1;
 }
 
 // Position of workgroup b among all of them when each XCD (workgroup b runs on
