@@ -33,38 +33,52 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // What rows and chunks past the ends read: codes of 0.
 __device__ __align__(16) const uint8_t kZeros[16] = {};
 
+constexpr int kCuLds = 160 * 1024;
+constexpr int kSegBytesMax = (2 * kMaxExperts + kMaxRanks + 1) * 4;  // seg_start of the largest shape
 constexpr int kTileGroup = 8;  // row tiles per item group, as in the bf16 product
 
-template <int BM, int BN, int WM, int WN, int S, bool GLU>
+template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU>
 struct QCfg {
-    static constexpr int kBK = 128;
+    static constexpr int kBK = BK;                    // k per stage, in bytes
+    static constexpr int kCpr = BK / 16;              // 16-byte chunks of a row
+    static constexpr int kRpi = 64 / kCpr;            // rows (1 KiB) per LDS-DMA load
     static constexpr int kTM = WM / 32, kTN = WN / 32;
     static constexpr int kWM = BM / WM, kWN = BN / WN;
     static constexpr int kWavesG = kWM * kWN;
     static constexpr int kThreads = kWavesG * 64;
-    static constexpr int kAInstr = BM / 8 / kWavesG;  // 8 rows (1 KiB) per LDS-DMA load
-    static constexpr int kBInstr = BN / 8 / kWavesG;
-    static constexpr int kPerStage = kAInstr + kBInstr + 1;
+    static constexpr int kAInstr = BM / kRpi / kWavesG;
+    static constexpr int kBInstr = BN / kRpi / kWavesG;
+    static constexpr int kPerStage = kAInstr + kBInstr;
+    static constexpr int kStageBytes = (BM + BN) * BK;
+    // Scales: a dword holds four blocks of a row, so a slot of a ring of its own
+    // serves 4 * 128 / BK stages of an item: [BM] rows, then the weights' blocks.
+    // At most S stages are loading or in use, so S slots do.
     static constexpr int kBBlocks = GLU ? 2 : (BN + kQuantBlock - 1) / kQuantBlock;
-    static constexpr int kScaleAt = (BM + BN) * kBK;  // [BM] row scales, then the weights'
-    static constexpr int kStageBytes = kScaleAt + kThreads * 4;
+    static constexpr int kScaleStages = 4 * kQuantBlock / BK;
+    static constexpr int kScaleWaves = (BM + kBBlocks + 63) / 64;
+    static constexpr int kScaleBytes = kScaleWaves * 256;
+    static constexpr int kScaleAt = S * kStageBytes;
     static constexpr int kOutCols = GLU ? BN / 2 : BN;
-    // Epilogue, in the stage that was computed last: GLU all rows of codes and
-    // the waves' row maxima; else a band of rows in bf16.
-    static constexpr int kBands = GLU ? 1 : kWM;
-    static constexpr int kBandRows = BM / kBands;
+    // Epilogue: for an 8-bit output the waves' row maxima, and a band of EB rows
+    // on its way out, apart from the ring, which is loading the next item.
     static constexpr int kOutBytes = GLU ? 1 : 2;
     static constexpr int kLdoBytes = kOutCols * kOutBytes + 16;
-    static constexpr int kMaxAt = kBandRows * kLdoBytes;
+    static constexpr int kOutAt = kScaleAt + S * kScaleBytes;
+    static constexpr int kMaxAt = kOutAt + EB * kLdoBytes;
+    static constexpr int kSegAt = kMaxAt + (GLU ? BM * kWN * 4 : 0);
+    static constexpr int kBandRows = EB, kBands = BM / EB;
     static constexpr int kVecPerRow = kOutCols * kOutBytes / 16;
     static constexpr int kOIter = kBandRows * kVecPerRow / kThreads;
-    static_assert(BM % (8 * kWavesG) == 0 && BN % (8 * kWavesG) == 0, "rows per DMA round");
-    static_assert(BM + kBBlocks <= kThreads, "a thread for every scale");
-    static_assert(kMaxAt + (GLU ? BM * kWN * 4 : 0) <= kStageBytes, "the epilogue fits one stage");
-    static_assert((S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
+    static_assert(BK == 64 || BK == 128, "one or two matrix instructions, one scale");
+    static_assert(BM % (kRpi * kWavesG) == 0 && BN % (kRpi * kWavesG) == 0, "rows per DMA round");
+    static_assert(kScaleWaves <= kWavesG, "a thread for every scale");
+    static_assert(kBandRows % 32 == 0 && WM % kBandRows == 0, "bands of whole row tiles");
+    static_assert((S - 1) * kPerStage <= 63, "outstanding loads must fit vmcnt");
     static_assert(!GLU || (kOutCols == kQuantBlock && kTN == 2), "gate and up in one wave, one block");
+    static_assert(kSegAt + kSegBytesMax <= kCuLds, "LDS");
     static_assert(kOIter >= 1 && kBandRows * kVecPerRow % kThreads == 0, "epilogue split");
-    __device__ static constexpr int swz(int r) { return (r >> 1) & 7; }
+    // rows whose chunks share the banks: two of 128 bytes, four of 64
+    __device__ static constexpr int swz(int r) { return BK == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
 };
 
 struct QuantGemmArgs {
@@ -108,13 +122,13 @@ __device__ __forceinline__ void lds_barrier()
 
 }  // namespace
 
-template <int BM, int BN, int WM, int WN, int S, bool GLU>
-__global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expert_quant_kernel(
+template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU, bool TAIL>
+__global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) void expert_quant_kernel(
     QuantGemmArgs a)
 {
-    using G = QCfg<BM, BN, WM, WN, S, GLU>;
+    using G = QCfg<BM, BN, WM, WN, BK, S, EB, GLU>;
     extern __shared__ __align__(16) char lds_b[];
-    int32_t *seg_start = (int32_t *)(lds_b + S * G::kStageBytes);
+    int32_t *seg_start = (int32_t *)(lds_b + G::kSegAt);
     __shared__ int scan_tmp[G::kWavesG];
 
     const int tid = (int)threadIdx.x, lane = lane_id();
@@ -126,17 +140,16 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
     const int64_t items = (int64_t)tiles * nbn;
     const int32_t nk = (a.in_dim + G::kBK - 1) / G::kBK;
     const int32_t SB = scale_row_bytes(a.in_dim), SO = scale_row_bytes(a.out_dim);
-    const bool k_tail = a.in_dim % G::kBK != 0;
 
     // ---- the loads: items and their k-steps in one sequence ------------------
-    // LDS-DMA: lane i of a load brings chunk (i % 8) ^ swz(row) of row 8 g + i / 8
-    // to byte 16 i of the load's KiB.  Row r of the B tile is column r of the
+    // LDS-DMA: lane i of a load brings chunk (i % kCpr) ^ swz(row) of row kRpi g +
+    // i / kCpr to byte 16 i of the load's KiB.  Row r of the B tile is column r of the
     // block, or for gate and up column (r / 64) * 32 + r % 32 of gate (r / 32
     // even) or up, which one load never mixes.
     struct Load {
         int64_t it, m0;
         int32_t kt, mrows, n0;
-        const uint8_t *a_base, *w_base;
+        const uint8_t *a_base, *b_base[2];  // the item's first row; first column, of each matrix
         const uint8_t *scale;  // this thread's
         uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
     };
@@ -144,9 +157,9 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
     ld.it = xcd_slot((int)blockIdx.x, (int)gridDim.x);
     if (ld.it >= items)
         return;
-    const int dma_row = lane >> 3, dma_pos = lane & 7;
-    auto a_row = [&](int v) { return (v * G::kWavesG + wave) * 8 + dma_row; };
-    auto b_mat = [&](int v) { return GLU ? (v * G::kWavesG + wave) / 4 % 2 : 0; };
+    const int dma_row = lane / G::kCpr, dma_pos = lane % G::kCpr;
+    auto a_row = [&](int v) { return (v * G::kWavesG + wave) * G::kRpi + dma_row; };
+    auto b_mat = [&](int v) { return GLU ? (v * G::kWavesG + wave) * G::kRpi / 32 % 2 : 0; };
     auto chunk = [&](int v) { return (dma_pos ^ G::swz(a_row(v))) << 4; };
     // First row and column of an item, its rows and its weights.
     auto locate = [&](int64_t it, int64_t *m0, int32_t *mrows, int32_t *n0) -> const uint8_t * {
@@ -162,9 +175,11 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
         return (pooled ? a.pool : a.w_home) + wrow * a.w_stride;
     };
     auto begin_item = [&]() {
-        ld.w_base = locate(ld.it, &ld.m0, &ld.mrows, &ld.n0);
-        ld.kt = 0;
+        const uint8_t *w = locate(ld.it, &ld.m0, &ld.mrows, &ld.n0);
         ld.a_base = a.x8 + ld.m0 * a.in_dim;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            ld.b_base[m] = w + a.code[m] + (int64_t)ld.n0 * a.in_dim;
 #pragma unroll
         for (int v = 0; v < G::kAInstr; ++v)
             ld.a_off[v] = (uint32_t)((a_row(v) < ld.mrows ? a_row(v) : 0) * a.in_dim + chunk(v));
@@ -181,42 +196,40 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
             const int q = tid - BM < G::kBBlocks ? tid - BM : 0;
             const int32_t last_block = (a.out_dim - 1) / kQuantBlock;
             const int32_t block = ld.n0 / kQuantBlock + (GLU ? 0 : q);
-            ld.scale = ld.w_base + a.scale[GLU ? q : 0] +
+            ld.scale = w + a.scale[GLU ? q : 0] +
                        (int64_t)(block < last_block ? block : last_block) * SB;
         }
     };
-    // Issues the next stage into slot `slot`, and moves on to the next item behind
-    // an item's last.
-    auto issue = [&](int slot) {
-        char *dst = lds_b + slot * G::kStageBytes;
-        const int64_t k0 = (int64_t)ld.kt * G::kBK;
-        const uint8_t *ap = ld.a_base + k0;
-        const uint8_t *bp[2] = {ld.w_base + a.code[0] + (int64_t)ld.n0 * a.in_dim + k0,
-                                ld.w_base + a.code[1] + (int64_t)ld.n0 * a.in_dim + k0};
-        if (k_tail && ld.kt == nk - 1) {
-            const int32_t left = a.in_dim - (int32_t)k0;
-#pragma unroll
-            for (int v = 0; v < G::kAInstr; ++v)
-                dma<16>(chunk(v) < left ? ap + ld.a_off[v] : kZeros,
-                        dst + (v * G::kWavesG + wave) * 1024);
-#pragma unroll
-            for (int v = 0; v < G::kBInstr; ++v)
-                dma<16>(chunk(v) < left ? bp[b_mat(v)] + ld.b_off[v] : kZeros,
-                        dst + BM * G::kBK + (v * G::kWavesG + wave) * 1024);
-        } else {
-#pragma unroll
-            for (int v = 0; v < G::kAInstr; ++v)
-                dma<16>(ap + ld.a_off[v], dst + (v * G::kWavesG + wave) * 1024);
-#pragma unroll
-            for (int v = 0; v < G::kBInstr; ++v)
-                dma<16>(bp[b_mat(v)] + ld.b_off[v], dst + BM * G::kBK + (v * G::kWavesG + wave) * 1024);
-        }
-        dma<4>(ld.scale + (ld.kt >> 2) * 4, dst + G::kScaleAt + wave * 256);
-        if (++ld.kt == nk) {
+    // Issues the next stage into slot `to`; an item's every kScaleStages-th with the
+    // scales of as many.  After the last item the loads go on with its first
+    // stages again, which nobody computes: so every stage is followed by as many.
+    int scale_to = 0;
+    auto issue = [&](int to) {
+        if (ld.kt == nk) {
+            ld.kt = 0;
             ld.it += gridDim.x;
             if (ld.it < items)
                 begin_item();
         }
+        char *dst = lds_b + to * G::kStageBytes;
+        const int64_t k0 = (int64_t)ld.kt * G::kBK;
+        if (ld.kt % G::kScaleStages == 0) {
+            if (wave < G::kScaleWaves)
+                dma<4>(ld.scale + ld.kt / G::kScaleStages * 4,
+                       lds_b + G::kScaleAt + scale_to * G::kScaleBytes + wave * 256);
+            scale_to = scale_to + 1 == S ? 0 : scale_to + 1;
+        }
+#pragma unroll
+        for (int v = 0; v < G::kPerStage; ++v) {
+            const bool rows = v < G::kAInstr;
+            const int w = rows ? v : v - G::kAInstr;
+            const uint8_t *src = rows ? ld.a_base + k0 + ld.a_off[w]
+                                      : (b_mat(w) ? ld.b_base[1] : ld.b_base[0]) + k0 + ld.b_off[w];
+            if (TAIL)
+                src = chunk(w) < a.in_dim - (int32_t)k0 ? src : kZeros;
+            dma<16>(src, dst + (rows ? 0 : BM * G::kBK) + (w * G::kWavesG + wave) * 1024);
+        }
+        ++ld.kt;
     };
 
     // ---- the products ---------------------------------------------------------
@@ -233,12 +246,12 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
         }
         return r;
     };
+    ld.kt = 0;
     begin_item();
-    int slot = 0;  // of the stage computed next; the ring runs on across items
+    int slot = 0, scale_slot = 0;  // of the stage computed next; the rings run on across items
 #pragma unroll
-    for (int st = 0; st + 1 < S; ++st)
-        if (ld.it < items)
-            issue(st);
+    for (int st = 0; st < S; ++st)
+        issue(st);
 
     for (int64_t it = xcd_slot((int)blockIdx.x, (int)gridDim.x); it < items; it += gridDim.x) {
         int64_t m0 = ld.m0;
@@ -256,21 +269,24 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
 
         for (int32_t kt = 0; kt < nk; ++kt) {
             // This stage's loads have landed once only what was issued after them is
-            // outstanding: those of S - 2 stages at least (and the stores of the
-            // epilogue before, if any), as long as there are stages to issue.
-            if (ld.it < items)
-                wait_vm<(S - 2) * G::kPerStage>();
+            // outstanding: S - 2 stages, S - 1 at an item's start (the slot of the
+            // item before's last stage is loading already), and some more scales
+            // and stores, if any.
+            if (kt == 0)
+                wait_vm<(S - 1) * G::kPerStage>();
             else
-                wait_vm<0>();
+                wait_vm<(S - 2) * G::kPerStage>();
             lds_barrier();  // every wave's part of the stage is there, and the one before is free
             const int cur = slot;
             slot = slot + 1 == S ? 0 : slot + 1;
-            if (ld.it < items)
+            if (kt)
                 issue(cur == 0 ? S - 1 : cur - 1);
             const char *sa = lds_b + cur * G::kStageBytes;
             const char *sb = sa + BM * G::kBK;
-            const uint32_t *sc = (const uint32_t *)(sa + G::kScaleAt);
-            const int shift = (kt & 3) * 8;
+            const uint32_t *sc = (const uint32_t *)(lds_b + G::kScaleAt + scale_slot * G::kScaleBytes);
+            const int shift = (kt * G::kBK / kQuantBlock & 3) * 8;
+            if (kt % G::kScaleStages == G::kScaleStages - 1 || kt == nk - 1)
+                scale_slot = scale_slot + 1 == S ? 0 : scale_slot + 1;
             int sca[G::kTM], scb[G::kTN];
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i)
@@ -278,30 +294,39 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
 #pragma unroll
             for (int j = 0; j < G::kTN; ++j)
                 scb[j] = (int)(sc[BM + (GLU ? j : (wn * WN + j * 32) / kQuantBlock)] >> shift);
+            // Steps of one row tile and 64 k: each reads the next step's rows under its
+            // own matrix instructions.
+            constexpr int kSteps = G::kBK / 64 * G::kTM;
+            i32x8 fa[2], fb[2][G::kTN];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                i32x8 fa[G::kTM], fb[G::kTN];
+            for (int j = 0; j < G::kTN; ++j)
+                fb[0][j] = frag(sb, wn * WN + j * 32, 0);
+            fa[0] = frag(sa, wm * WM, 0);
+#pragma unroll
+            for (int n = 0; n < kSteps; ++n) {
+                const int i = n % G::kTM, ks = n / G::kTM, p = n + 1;
+                if (p < kSteps) {
+                    fa[p & 1] = frag(sa, wm * WM + p % G::kTM * 32, p / G::kTM);
+                    if (p % G::kTM == 0)
+#pragma unroll
+                        for (int j = 0; j < G::kTN; ++j)
+                            fb[(ks + 1) & 1][j] = frag(sb, wn * WN + j * 32, ks + 1);
+                }
 #pragma unroll
                 for (int j = 0; j < G::kTN; ++j)
-                    fb[j] = frag(sb, wn * WN + j * 32, ks);
-#pragma unroll
-                for (int i = 0; i < G::kTM; ++i)
-                    fa[i] = frag(sa, wm * WM + i * 32, ks);
-#pragma unroll
-                for (int i = 0; i < G::kTM; ++i)
-#pragma unroll
-                    for (int j = 0; j < G::kTN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            fb[j], fa[i], acc[i][j], 0, 0, 0, scb[j], 0, sca[i]);
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fb[ks & 1][j], fa[n & 1], acc[i][j], 0, 0, 0, scb[j], 0, sca[i]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        lds_barrier();  // the stage computed last is free for the epilogue
+        lds_barrier();  // the stage computed last is free
+        issue(slot == 0 ? S - 1 : slot - 1);
 
         // ---- epilogue: lane l holds row l % 32 of tile i, and of each column tile
         // the columns 8 (q / 4) + 4 (l / 32) + q % 4 ------------------------------
-        char *so = lds_b + (slot == 0 ? S - 1 : slot - 1) * G::kStageBytes;
+        char *so = lds_b + G::kOutAt;
+        float *row_max = (float *)(lds_b + G::kMaxAt);  // [BM][kWN]
         if constexpr (GLU) {
-            float *row_max = (float *)(so + G::kMaxAt);  // [BM][kWN]
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i) {
                 uint32_t m = 0;
@@ -317,46 +342,45 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
                     row_max[(wm * WM + i * 32 + fr) * G::kWN + wn] = __uint_as_float(m);
             }
             lds_barrier();
-#pragma unroll
-            for (int i = 0; i < G::kTM; ++i) {
-                const int row = wm * WM + i * 32 + fr;
-                uint32_t m = 0;
-#pragma unroll
-                for (int q = 0; q < G::kWN; ++q)
-                    m = max(m, __float_as_uint(row_max[row * G::kWN + q]));
-                const uint32_t byte = scale_byte(m);
-                const float inv = inverse_scale(byte);
-#pragma unroll
-                for (int q = 0; q < 16; q += 4)
-                    *(uint32_t *)(so + row * G::kLdoBytes + wn * 32 + q * 2 + fhalf * 4) =
-                        pack_e4m3(acc[i][0][q], acc[i][0][q + 1], acc[i][0][q + 2], acc[i][0][q + 3],
-                                  inv, byte);
-                if (wn == 0 && fhalf == 0 && row < mrows) {
-                    uint8_t *dst = a.out_scales + (m0 + row) * SO;
-                    const int32_t nb = n0 / kQuantBlock;
-                    dst[nb] = (uint8_t)byte;
-                    if (nb == nbn - 1)
-                        for (int32_t p = nbn; p < SO; ++p)
-                            dst[p] = 127;
-                }
-            }
         }
 #pragma unroll
         for (int band = 0; band < G::kBands; ++band) {
-            if (!GLU) {
-                if (band)
-                    lds_barrier();  // the band before has been read
-                if (wm == band) {
+            if (band)
+                lds_barrier();  // the band before has been read
 #pragma unroll
-                    for (int i = 0; i < G::kTM; ++i)
+            for (int i = 0; i < G::kTM; ++i) {
+                if (wm * (WM / G::kBandRows) + i * 32 / G::kBandRows != band)
+                    continue;
+                const int row = wm * WM + i * 32 + fr;
+                char *to = so + (row - band * G::kBandRows) * G::kLdoBytes;
+                if constexpr (GLU) {
+                    uint32_t m = 0;
 #pragma unroll
-                        for (int j = 0; j < G::kTN; ++j)
+                    for (int q = 0; q < G::kWN; ++q)
+                        m = max(m, __float_as_uint(row_max[row * G::kWN + q]));
+                    const uint32_t byte = scale_byte(m);
+                    const float inv = inverse_scale(byte);
 #pragma unroll
-                            for (int q = 0; q < 16; q += 4)
-                                *(u32x2 *)(so + (i * 32 + fr) * G::kLdoBytes +
-                                           (wn * WN + j * 32 + q * 2 + fhalf * 4) * 2) =
-                                    u32x2{pack_bf16(acc[i][j][q], acc[i][j][q + 1]),
-                                          pack_bf16(acc[i][j][q + 2], acc[i][j][q + 3])};
+                    for (int q = 0; q < 16; q += 4)
+                        *(uint32_t *)(to + wn * 32 + q * 2 + fhalf * 4) =
+                            pack_e4m3(acc[i][0][q], acc[i][0][q + 1], acc[i][0][q + 2],
+                                      acc[i][0][q + 3], inv, byte);
+                    if (wn == 0 && fhalf == 0 && row < mrows) {
+                        uint8_t *dst = a.out_scales + (m0 + row) * SO;
+                        const int32_t nb = n0 / kQuantBlock;
+                        dst[nb] = (uint8_t)byte;
+                        if (nb == nbn - 1)
+                            for (int32_t p = nbn; p < SO; ++p)
+                                dst[p] = 127;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < G::kTN; ++j)
+#pragma unroll
+                        for (int q = 0; q < 16; q += 4)
+                            *(u32x2 *)(to + (wn * WN + j * 32 + q * 2 + fhalf * 4) * 2) =
+                                u32x2{pack_bf16(acc[i][j][q], acc[i][j][q + 1]),
+                                      pack_bf16(acc[i][j][q + 2], acc[i][j][q + 3])};
                 }
             }
             lds_barrier();
@@ -371,17 +395,17 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, S, GLU>::kThreads)) void expe
             }
         }
     }
+    wait_vm<0>();  // the loads that nobody computes, before the LDS goes to another workgroup
 }
 
 namespace {
 
-template <int BM, int BN, int WM, int WN, int S, bool GLU>
+template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU, bool TAIL>
 int run_quant(const QuantGemmArgs &a, hipStream_t st)
 {
-    using G = QCfg<BM, BN, WM, WN, S, GLU>;
-    const auto kernel = expert_quant_kernel<BM, BN, WM, WN, S, GLU>;
-    const size_t ring = (size_t)S * G::kStageBytes;
-    const size_t lds = ring + (size_t)(a.seg.E + a.seg.pl.cap + 1) * 4;
+    using G = QCfg<BM, BN, WM, WN, BK, S, EB, GLU>;
+    const auto kernel = expert_quant_kernel<BM, BN, WM, WN, BK, S, EB, GLU, TAIL>;
+    const size_t lds = G::kSegAt + (size_t)(a.seg.E + a.seg.pl.cap + 1) * 4;
     int dev = 0, cus = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
@@ -389,15 +413,23 @@ int run_quant(const QuantGemmArgs &a, hipStream_t st)
     // Raised once per device, to what the largest allowed E and R need.
     static bool raised[64] = {};
     if (dev < 0 || dev >= 64 || !raised[dev]) {
-        const size_t most = ring + (size_t)(2 * kMaxExperts + kMaxRanks + 1) * 4;
         if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)most) != hipSuccess)
+                                G::kSegAt + kSegBytesMax) != hipSuccess)
             return MOONEP_ERR_HIP;
         if (dev >= 0 && dev < 64)
             raised[dev] = true;
     }
-    hipLaunchKernelGGL(kernel, dim3(cus), dim3(G::kThreads), lds, st, a);
+    const int per_cu = 2 * lds <= kCuLds ? 2 : 1;
+    hipLaunchKernelGGL(kernel, dim3(cus * per_cu), dim3(G::kThreads), lds, st, a);
     return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP;
+}
+
+// TAIL: the last k-step is part of one.
+template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU>
+int run_tail(const QuantGemmArgs &a, bool tail, hipStream_t st)
+{
+    return tail ? run_quant<BM, BN, WM, WN, BK, S, EB, GLU, true>(a, st)
+                : run_quant<BM, BN, WM, WN, BK, S, EB, GLU, false>(a, st);
 }
 
 }  // namespace
@@ -427,11 +459,12 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
     }
     a.out = out;
     a.out_scales = out_scales;
+    const bool tail = in_dim % kQuantBlock != 0;
     if (rows <= (int64_t)32 * s.E)
-        return glu ? run_quant<32, 256, 32, 64, 4, true>(a, st)
-                   : run_quant<32, 128, 32, 32, 7, false>(a, st);
-    return glu ? run_quant<256, 256, 128, 64, 2, true>(a, st)
-               : run_quant<256, 256, 128, 64, 2, false>(a, st);
+        return glu ? run_tail<32, 256, 32, 64, 128, 3, 32, true>(a, tail, st)
+                   : run_tail<32, 128, 32, 32, 128, 6, 32, false>(a, tail, st);
+    return glu ? run_tail<256, 256, 128, 64, 128, 2, 64, true>(a, tail, st)
+               : run_tail<256, 256, 128, 64, 128, 2, 32, false>(a, tail, st);
 }
 
 }  // namespace moonep
