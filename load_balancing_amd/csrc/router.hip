@@ -6,8 +6,12 @@
 // 64 i + 4 c .. + 3, so that rows of E % 4 == 0 are read as whole vectors.  Sums
 // and maxima over a token are four DPP steps for four tokens at once.
 //
-// Choosing: K rounds of the row's maximum and the least expert id that has it,
-// on integer keys ordered as the logits are.
+// Choosing: K rounds of the row's largest key below the last one.  A key is one
+// word, the leading bits of the logit in integer order above the expert id
+// (counted down, so that ties go to the lower id): unique, so a round is one
+// subtraction and maximum per element.  bf16 logits fit whole; where two of the
+// K + 1 largest fp32 logits share their leading bits, or the row holds a NaN,
+// the wave chooses again on whole keys, two words' worth of work.
 //
 // The shares of a workgroup's tokens are summed in registers (each lane keeps
 // its experts), then over its rows and waves, into one partial row of E sums
@@ -25,13 +29,13 @@ constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;
 
 // Workgroups of the loss's first pass: enough to fill the chip, few enough that
 // their partial rows stay small beside the logits.
-constexpr int64_t kLossBlocks = 2048;
-constexpr int kJoinThreads = 1024, kJoinExperts = 16, kJoinRows = kJoinThreads / kJoinExperts;
+constexpr int64_t kLossBlocks = 1024;
+constexpr int kJoinThreads = 1024, kJoinExperts = 64, kJoinRows = kJoinThreads / kJoinExperts;
 
 struct RouterLayout {
     int64_t per_group;   // workgroups of one group
     int64_t tokens;      // tokens of each of them
-    size_t prob_off, count_off, loss_off, ticket_off, bytes;
+    size_t count_off, loss_off, bytes;  // the shares' partial rows come first
 };
 
 RouterLayout router_layout(const moonep_shape &s, int32_t groups)
@@ -46,29 +50,17 @@ RouterLayout router_layout(const moonep_shape &s, int32_t groups)
     l.per_group = l.tokens ? (n + l.tokens - 1) / l.tokens : 1;
     const size_t rows = (size_t)l.per_group * groups * s.E * 4;
     const size_t nchunk = (size_t)(s.E + kJoinExperts - 1) / kJoinExperts;
-    l.prob_off = 256;
-    l.count_off = l.prob_off + rows;
-    l.loss_off = (l.count_off + rows + 15) & ~(size_t)15;
-    l.ticket_off = 0;
+    l.count_off = rows;
+    l.loss_off = (2 * rows + 15) & ~(size_t)15;
     l.bytes = l.loss_off + nchunk * groups * 8;
     return l;
 }
 
-// exp(x) for x <= 0 or any x that the caller lets overflow to infinity: 2^(x
-// log2 e), the product's rounding error carried as a correction so that large
-// |x| keeps its digits.  The hardware's exponential is good to one unit.
-__device__ __forceinline__ float exp_of(float x)
-{
-    constexpr float kHi = 1.44269502e+00f, kLo = 1.92596303e-08f, kLn2 = 0.693147181f;
-    const float t = x * kHi;
-    const float err = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
-    const float p = __builtin_amdgcn_exp2f(t);
-    const float q = __builtin_fmaf(p, err * kLn2, p);
-    // past the exponent's range p is 0 or infinite, and its correction inf - inf
-    return __builtin_fabsf(t) < 127.0f ? q : p;
-}
+// 2^(x log2 e): the product's rounding makes it (|x| + 2) 2^-24 relative, as the
+// rounding of a difference of logits does anyway.  0 and infinity at the ends.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
-__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + exp_of(-l)); }
+__device__ __forceinline__ float sigmoid_of(float l) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-l)); }
 
 __device__ __forceinline__ int32_t key_of(float l)
 {
@@ -76,10 +68,15 @@ __device__ __forceinline__ int32_t key_of(float l)
     return l != l ? kNanKey : b ^ ((b >> 31) & 0x7FFFFFFF);
 }
 
-__device__ __forceinline__ float value_of(int32_t key)
+// One word per element for the rounds: leading bits of the logit in unsigned
+// order, then the id counted down in kIdBits; below 2^31, and 0 for no expert.
+template <int kIdBits>
+__device__ __forceinline__ uint32_t packed_key(float l, int32_t e, int32_t E)
 {
-    return key == kNanKey ? __uint_as_float(0x7FC00000u)
-                          : __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF));
+    const uint32_t b = __float_as_uint(l + 0.0f);  // -0 -> +0
+    const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    const uint32_t id = (1u << kIdBits) - 1u - (uint32_t)e;
+    return e < E ? ((u >> 1) & ~((1u << kIdBits) - 1u)) | id : 0u;
 }
 
 // Expert of element i in the row's lane c.
@@ -179,7 +176,6 @@ struct RouterArgs {
     float *gates;
     float *prob_part;      // [blocks, E]
     int32_t *count_part;   // [blocks, E]
-    uint32_t *ticket;
     int64_t N, n, per_group, tokens;
     int32_t E, K, score, normalize, vec;
     float scale;
@@ -199,68 +195,127 @@ __global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
     const int64_t g = (int64_t)blockIdx.x / a.per_group;
     const int64_t first = g * a.n + ((int64_t)blockIdx.x - g * a.per_group) * a.tokens;
     const int64_t end = first + a.tokens < (g + 1) * a.n ? first + a.tokens : (g + 1) * a.n;
+    constexpr int kIdBits = kV == 4 ? 6 : kV == 8 ? 7 : kV == 16 ? 8 : kV == 32 ? 9 : 10;
+    // Expert e of round k0 + c in lane c: its id, its score for the gates.  (Keys of
+    // a row with a NaN may have run out, before it is chosen again.)
+    auto put = [&](int64_t tok, bool on, int32_t k0, int32_t kn, int c, int32_t e, float base, float *mine,
+                   float *wsum) {
+        const bool in = on && c < kn;
+        e = e < a.E ? e : a.E - 1;
+        float v = 0.0f;
+        if (in)
+            v = kBf16 ? bf16_lo(((const uint16_t *)a.logits)[tok * a.E + e])
+                      : ((const float *)a.logits)[tok * a.E + e];
+        *mine = !in ? 0.0f : a.score == MOONEP_SCORE_SOFTMAX ? exp_of(v - base) : sigmoid_of(v);
+        *wsum += *mine;
+        if (in) {
+            a.topk_idx[tok * a.K + k0 + c] = e;
+            if (a.K > kRowLanes)
+                a.gates[tok * a.K + k0 + c] = *mine;
+        }
+        return e;
+    };
     float acc[kV];
     if (kLoss) {
         for (int32_t e = (int32_t)threadIdx.x; e < a.E; e += kBlock)
             hist[e] = 0;
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            *a.ticket = 0;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kV; ++i)
             acc[i] = 0.0f;
     }
+    float nxt[kV];  // the next tokens' logits, on their way
+    if (first < end) {
+        const int64_t tok = first + wave * kRowsPerWave + r;
+        load_row<kV, kBf16>(a.logits, tok < end ? tok : first, a.E, c, a.vec != 0, tok < end, nxt);
+    }
     for (int64_t t0 = first + wave * kRowsPerWave; t0 < end; t0 += kRowsPerBlock) {
-        const int64_t tok = t0 + r;
+        const int64_t tok = t0 + r, tok2 = tok + kRowsPerBlock;
         const bool on = tok < end;
         float l[kV];
-        load_row<kV, kBf16>(a.logits, on ? tok : first, a.E, c, a.vec != 0, on, l);
-        int32_t key[kV];
+        uint32_t key[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-            key[i] = expert_of(i, c) < a.E ? key_of(l[i]) : kNoKey;
+        for (int i = 0; i < kV; ++i) {
+            l[i] = nxt[i];
+            key[i] = packed_key<kIdBits>(l[i], expert_of(i, c), a.E);
+        }
+        load_row<kV, kBf16>(a.logits, tok2 < end ? tok2 : first, a.E, c, a.vec != 0, tok2 < end, nxt);
         const float top = row_top(l);
         const float rz = scores(l, a.score, top);
         if (kLoss) {
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                acc[i] += on ? l[i] * rz : 0.0f;
+                acc[i] = __builtin_fmaf(l[i], on ? rz : 0.0f, acc[i]);
         }
         // K rounds; lane k % 16 keeps round k's expert and score, and a chunk of
         // 16 rounds is written at once
         const float base = top == -__builtin_huge_valf() ? 0.0f : top;
         float wsum = 0.0f, mine = 0.0f;
+        bool again = rz != rz;  // a NaN in the row
+        int32_t chosen = 0;     // the last chunk's expert of this lane
+        auto next_key = [&](uint32_t last) {
+            // key - last wraps to 2^31 and above for keys below last, and the
+            // largest of those differences is the largest of those keys
+            uint32_t d = 0;
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                d = max(d, key[i] - last);
+            return last + row16_max(d);
+        };
+        uint32_t m = 0x80000000u;  // the last round's key: those at it and above are chosen
         for (int32_t k0 = 0; k0 < a.K; k0 += kRowLanes) {
             const int32_t kn = a.K - k0 < kRowLanes ? a.K - k0 : kRowLanes;
-            int32_t my_key = kNoKey, my_e = 0;
+            uint32_t my_key = 0;
             for (int32_t k = 0; k < kn; ++k) {
-                int32_t m = key[0];
-#pragma unroll
-                for (int i = 1; i < kV; ++i)
-                    m = max(m, key[i]);
-                m = row16_imax(m);
-                uint32_t e = 0xFFFFu;
-#pragma unroll
-                for (int i = kV - 1; i >= 0; --i)
-                    e = key[i] == m ? (uint32_t)((i >> 2) * 64 + (i & 3)) : e;
-                e = row16_min(e + (uint32_t)c * 4);
-                const int32_t rel = (int32_t)e - c * 4;
-#pragma unroll
-                for (int i = 0; i < kV; ++i)
-                    key[i] = rel == (i >> 2) * 64 + (i & 3) ? kNoKey : key[i];
+                const uint32_t was = m;
+                m = next_key(was);
+                if (!kBf16)
+                    again |= (m ^ was) >> kIdBits == 0;
                 my_key = c == k ? m : my_key;
-                my_e = c == k ? (int32_t)e : my_e;
             }
-            const float v = value_of(my_key);
-            mine = c < kn ? (a.score == MOONEP_SCORE_SOFTMAX ? exp_of(v - base) : sigmoid_of(v)) : 0.0f;
-            wsum += mine;
-            if (on && c < kn) {
-                a.topk_idx[tok * a.K + k0 + c] = my_e;
-                if (a.K > kRowLanes)
-                    a.gates[tok * a.K + k0 + c] = mine;
-                if (kLoss)
-                    atomicAdd(hist + my_e, 1);
+            if (!kBf16 && k0 + kn == a.K && a.K < a.E)
+                again |= (next_key(m) ^ m) >> kIdBits == 0;
+            chosen = put(tok, on, k0, kn, c,
+                         (int32_t)((1u << kIdBits) - 1u - (my_key & ((1u << kIdBits) - 1u))), base,
+                         &mine, &wsum);
+        }
+        if (ballot(again && on)) {
+            // whole keys: the row's maximum, and the least id that has it
+            int32_t whole[kV];
+            load_row<kV, kBf16>(a.logits, on ? tok : first, a.E, c, a.vec != 0, on, l);
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                whole[i] = expert_of(i, c) < a.E ? key_of(l[i]) : kNoKey;
+            wsum = 0.0f;
+            for (int32_t k0 = 0; k0 < a.K; k0 += kRowLanes) {
+                const int32_t kn = a.K - k0 < kRowLanes ? a.K - k0 : kRowLanes;
+                int32_t my_e = 0;
+                for (int32_t k = 0; k < kn; ++k) {
+                    int32_t w = whole[0];
+#pragma unroll
+                    for (int i = 1; i < kV; ++i)
+                        w = max(w, whole[i]);
+                    w = row16_imax(w);
+                    uint32_t e = 0xFFFFu;
+#pragma unroll
+                    for (int i = kV - 1; i >= 0; --i)
+                        e = whole[i] == w ? (uint32_t)((i >> 2) * 64 + (i & 3)) : e;
+                    e = row16_min(e + (uint32_t)c * 4);
+                    const int32_t rel = (int32_t)e - c * 4;
+#pragma unroll
+                    for (int i = 0; i < kV; ++i)
+                        whole[i] = rel == (i >> 2) * 64 + (i & 3) ? kNoKey : whole[i];
+                    my_e = c == k ? (int32_t)e : my_e;
+                }
+                chosen = put(tok, on, k0, kn, c, my_e, base, &mine, &wsum);
             }
+        }
+        if (kLoss && on) {
+            if (a.K > kRowLanes)
+                for (int32_t k = c; k < a.K; k += kRowLanes)
+                    atomicAdd(hist + a.topk_idx[tok * a.K + k], 1);
+            else if (c < a.K)
+                atomicAdd(hist + chosen, 1);
         }
         float f = a.scale;
         if (a.normalize) {
@@ -298,66 +353,72 @@ __global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
     }
 }
 
-// Joins the partial rows of one group and 16 experts: 64 rows at a time, 16
-// lanes each, then over the 64 in LDS.  The workgroup that finishes last sums
-// the (group, chunk) losses in their order.
+// Joins the partial rows of one group and 64 experts: 16 rows at a time, then
+// over the 16 in LDS.
 __global__ __launch_bounds__(kJoinThreads) void router_join_kernel(
     const float *__restrict__ prob_part, const int32_t *__restrict__ count_part, int64_t per_group,
-    int32_t E, int32_t nchunk, int32_t groups, double factor, int32_t *__restrict__ counts,
-    float *__restrict__ prob_sum, double *losses, uint32_t *ticket, float *__restrict__ loss)
+    int32_t E, int32_t nchunk, int32_t *__restrict__ counts, float *__restrict__ prob_sum,
+    double *__restrict__ losses)
 {
     __shared__ double prob[kJoinThreads];
     __shared__ int32_t cnt[kJoinThreads];
-    __shared__ bool is_last;
     const int t = (int)threadIdx.x;
-    const int64_t total = (int64_t)groups * nchunk;
     const int64_t g = (int64_t)blockIdx.x / nchunk;
-    const int32_t chunk = (int32_t)((int64_t)blockIdx.x - g * nchunk);
-    const int32_t e = chunk * kJoinExperts + t % kJoinExperts;
+    const int32_t e = (int32_t)((int64_t)blockIdx.x - g * nchunk) * kJoinExperts + t % kJoinExperts;
     double p = 0.0;
     int32_t n = 0;
-    if (e < E)
+    if (e < E) {
+#pragma unroll 8
         for (int64_t b = t / kJoinExperts; b < per_group; b += kJoinRows) {
             const int64_t at = (g * per_group + b) * E + e;
             p += (double)prob_part[at];
             n += count_part[at];
         }
+    }
     prob[t] = p;
     cnt[t] = n;
-    for (int w = kJoinThreads / 2; w >= kJoinExperts; w >>= 1) {
-        __syncthreads();
-        if (t < w) {
-            prob[t] += prob[t + w];
-            cnt[t] += cnt[t + w];
-        }
-    }
-    if (t < kJoinExperts && e < E) {
-        counts[g * E + e] = cnt[t];
-        prob_sum[g * E + e] = (float)prob[t];
-    }
-    if (t == 0) {
-        double s = 0.0;
-        for (int j = 0; j < kJoinExperts && chunk * kJoinExperts + j < E; ++j)
-            s += (double)cnt[j] * prob[j];
-        losses[blockIdx.x] = s;
-        __threadfence();
-        is_last = atomicAdd(ticket, 1u) == (uint32_t)(total - 1);
-        __threadfence();
-    }
     __syncthreads();
-    if (!is_last)
-        return;
+    if (t < kJoinExperts) {
+#pragma unroll
+        for (int q = 1; q < kJoinRows; ++q) {
+            p += prob[t + q * kJoinExperts];
+            n += cnt[t + q * kJoinExperts];
+        }
+        if (e < E) {
+            counts[g * E + e] = n;
+            prob_sum[g * E + e] = (float)p;
+        }
+        double s = e < E ? (double)n * p : 0.0;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            s += __shfl_xor(s, d, 64);
+        if (t == 0)
+            losses[blockIdx.x] = s;
+    }
+}
+
+// The loss: the (group, chunk) sums, in an order of their number alone.
+__global__ __launch_bounds__(kJoinThreads) void router_loss_kernel(const double *__restrict__ losses,
+                                                                   int64_t total, double factor,
+                                                                   float *__restrict__ loss)
+{
+    __shared__ double part[kJoinThreads / 64];
+    const int t = (int)threadIdx.x;
     double s = 0.0;
     for (int64_t i = t; i < total; i += kJoinThreads)
-        s += __hip_atomic_load(losses + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    prob[t] = s;
-    for (int w = kJoinThreads / 2; w >= 1; w >>= 1) {
-        __syncthreads();
-        if (t < w)
-            prob[t] += prob[t + w];
+        s += losses[i];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        s += __shfl_xor(s, d, 64);
+    if (t % 64 == 0)
+        part[t / 64] = s;
+    __syncthreads();
+    if (t == 0) {
+        s = 0.0;
+        for (int q = 0; q < kJoinThreads / 64; ++q)
+            s += part[q];
+        loss[0] = (float)(s * factor);
     }
-    if (t == 0)
-        loss[0] = (float)(prob[0] * factor);
 }
 
 namespace {
@@ -567,9 +628,8 @@ int launch_router(const moonep_shape &s, const moonep_router_opts &o, const void
     a.logits = logits;
     a.topk_idx = topk_idx;
     a.gates = gates;
-    a.prob_part = with_loss ? (float *)(base + lay.prob_off) : nullptr;
+    a.prob_part = with_loss ? (float *)base : nullptr;
     a.count_part = with_loss ? (int32_t *)(base + lay.count_off) : nullptr;
-    a.ticket = with_loss ? (uint32_t *)(base + lay.ticket_off) : nullptr;
     a.N = (int64_t)s.R * s.S;
     a.E = s.E;
     a.K = s.K;
@@ -595,9 +655,11 @@ int launch_router(const moonep_shape &s, const moonep_router_opts &o, const void
     const int32_t nchunk = (s.E + kJoinExperts - 1) / kJoinExperts;
     const double n = (double)a.n;
     const double factor = a.n ? (double)s.E / ((double)s.K * n * n * o.groups) : 0.0;
-    hipLaunchKernelGGL(router_join_kernel, dim3((uint32_t)((int64_t)nchunk * o.groups)),
-                       dim3(kJoinThreads), 0, st, a.prob_part, a.count_part, a.per_group, s.E, nchunk,
-                       o.groups, factor, counts, prob_sum, (double *)(base + lay.loss_off), a.ticket,
+    double *losses = (double *)(base + lay.loss_off);
+    const int64_t parts = (int64_t)nchunk * o.groups;
+    hipLaunchKernelGGL(router_join_kernel, dim3((uint32_t)parts), dim3(kJoinThreads), 0, st,
+                       a.prob_part, a.count_part, a.per_group, s.E, nchunk, counts, prob_sum, losses);
+    hipLaunchKernelGGL(router_loss_kernel, dim3(1), dim3(kJoinThreads), 0, st, losses, parts, factor,
                        loss);
     return last();
 }

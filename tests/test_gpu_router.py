@@ -329,3 +329,22 @@ def test_backward_ignores_bad_ids():
     sg = 1 / (1 + np.exp(-l))
     off = np.abs(d_l.double().cpu().numpy() - want * sg * (1 - sg))
     assert (off <= mag * sg * (1 - sg) * (2 * np.abs(l).max() + 40) * 2.0 ** -24).all()
+
+
+def test_shared_leading_bits():
+    """fp32 logits that agree in the leading bits the fast rounds compare: at the border of the chosen, among them, in
+    one row of a wave, and with a NaN elsewhere."""
+    rng = np.random.default_rng(14)
+    for E, K in ((40, 4), (128, 8), (256, 8), (512, 20), (1024, 8)):
+        print(f"[case] leading bits E={E} K={K}", flush=True)
+        l = rng.standard_normal((37, E)).astype(np.float32)
+        for i in range(0, 37, 3):
+            # a cluster of K + 2 values around 3, in the last bits only, in random places
+            at = rng.permutation(E)[:K + 2]
+            l[i, at] = (np.float32(3).view(np.int32) + rng.integers(0, 3, at.size).astype(np.int32)).view(np.float32)
+        for i in range(1, 37, 6):
+            o = np.argsort(-l[i])
+            l[i, o[K]] = l[i, o[K - 1]]  # the border alone
+        for score in (SOFT, SIG):
+            got = forward(mx.Shape(1, E, 37, K, 16), mx.RouterOpts(score, True), torch.from_numpy(l).cuda())
+            np.testing.assert_array_equal(got["ids"].reshape(37, K), order(l.astype(np.float64), K))
