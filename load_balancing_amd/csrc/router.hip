@@ -29,26 +29,37 @@ constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;
 
 // Workgroups of the loss's first pass: enough to fill the chip, few enough that
 // their partial rows stay small beside the logits.
-constexpr int64_t kLossBlocks = 1024;
+constexpr int64_t kLossBlocks = 1024, kBwdBlocks = 2048;
 constexpr int kJoinThreads = 1024, kJoinExperts = 64, kJoinRows = kJoinThreads / kJoinExperts;
 
+// Workgroups of one group of n tokens, and the tokens of each: about `blocks` in
+// all, two rounds of rows each at least.
+struct Split {
+    int64_t per_group, tokens;
+};
+
+Split split_tokens(int64_t n, int64_t groups, int64_t blocks)
+{
+    int64_t per = blocks / groups;
+    const int64_t most = (n + 2 * kRowsPerBlock - 1) / (2 * kRowsPerBlock);
+    per = per < most ? per : most;
+    per = per < 1 ? 1 : per;
+    Split s;
+    s.tokens = (n + per - 1) / per;
+    s.per_group = s.tokens ? (n + s.tokens - 1) / s.tokens : 1;
+    return s;
+}
+
 struct RouterLayout {
-    int64_t per_group;   // workgroups of one group
-    int64_t tokens;      // tokens of each of them
+    Split split;
     size_t count_off, loss_off, bytes;  // the shares' partial rows come first
 };
 
 RouterLayout router_layout(const moonep_shape &s, int32_t groups)
 {
     RouterLayout l{};
-    const int64_t n = (int64_t)s.R * s.S / groups;
-    int64_t per = kLossBlocks / groups;
-    const int64_t most = (n + 2 * kRowsPerBlock - 1) / (2 * kRowsPerBlock);
-    per = per < most ? per : most;
-    per = per < 1 ? 1 : per;
-    l.tokens = (n + per - 1) / per;
-    l.per_group = l.tokens ? (n + l.tokens - 1) / l.tokens : 1;
-    const size_t rows = (size_t)l.per_group * groups * s.E * 4;
+    l.split = split_tokens((int64_t)s.R * s.S / groups, groups, kLossBlocks);
+    const size_t rows = (size_t)l.split.per_group * groups * s.E * 4;
     const size_t nchunk = (size_t)(s.E + kJoinExperts - 1) / kJoinExperts;
     l.count_off = rows;
     l.loss_off = (2 * rows + 15) & ~(size_t)15;
@@ -69,58 +80,62 @@ __device__ __forceinline__ int32_t key_of(float l)
 }
 
 // One word per element for the rounds: leading bits of the logit in unsigned
-// order, then the id counted down in kIdBits; below 2^31, and 0 for no expert.
+// order, then the id counted down in kIdBits.  The lane's part of the id, 4 c, is
+// left to be subtracted, so that element i's part is a constant.  Elements past E
+// hold -inf and the highest ids, so every expert comes before them.
 template <int kIdBits>
-__device__ __forceinline__ uint32_t packed_key(float l, int32_t e, int32_t E)
+__device__ __forceinline__ uint32_t packed_key(float l, int i)
 {
+    constexpr uint32_t kIds = (1u << kIdBits) - 1u;
     const uint32_t b = __float_as_uint(l + 0.0f);  // -0 -> +0
     const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-    const uint32_t id = (1u << kIdBits) - 1u - (uint32_t)e;
-    return e < E ? ((u >> 1) & ~((1u << kIdBits) - 1u)) | id : 0u;
+    return (u & ~kIds) | (kIds - (uint32_t)((i >> 2) * 64 + (i & 3)));
 }
 
 // Expert of element i in the row's lane c.
 __device__ __forceinline__ int32_t expert_of(int i, int c) { return (i >> 2) * 64 + c * 4 + (i & 3); }
 
-// One token's logits in fp32; experts past E are -inf (score 0).
+// Four tokens' logits in fp32, one per row of lanes, from `rows` (uniform) on; a
+// row past the last reads the first.  Experts past E are -inf (score 0): their
+// lanes read the row's last experts and drop them, so that no branch splits the
+// loads.
 template <int kV, bool kBf16>
-__device__ __forceinline__ void load_row(const void *logits, int64_t tok, int32_t E, int c, bool vec,
-                                         bool on, float (&l)[kV])
+__device__ __forceinline__ void load_rows(const char *rows, int32_t row, int32_t E, int c, bool vec,
+                                          float (&l)[kV])
 {
+    constexpr int kSize = kBf16 ? 2 : 4;
     constexpr float kNone = -__builtin_huge_valf();
+    if (vec) {
 #pragma unroll
-    for (int i = 0; i < kV; i += 4) {
-        const int32_t e = expert_of(i, c);
-        const int64_t at = tok * E + e;
-        if (vec) {
-            const bool in = on && e < E;
+        for (int i = 0; i < kV; i += 4) {
+            const int32_t e = expert_of(i, c), from = e < E ? e : E - 4;
+            const char *p = rows + (uint32_t)((row * E + from) * kSize);
             if (kBf16) {
-                u32x2 w = {0xFF80FF80u, 0xFF80FF80u};
-                if (in)
-                    w = *(const u32x2 *)((const uint16_t *)logits + at);
+                const u32x2 w = *(const u32x2 *)p;
                 l[i] = bf16_lo(w[0]);
                 l[i + 1] = bf16_hi(w[0]);
                 l[i + 2] = bf16_lo(w[1]);
                 l[i + 3] = bf16_hi(w[1]);
             } else {
-                f32x4 w = {kNone, kNone, kNone, kNone};
-                if (in)
-                    w = *(const f32x4 *)((const float *)logits + at);
+                const f32x4 w = *(const f32x4 *)p;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     l[i + j] = w[j];
             }
-        } else {
+        }
+        if (E == kV * kRowLanes)
+            return;
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v = kNone;
-                if (on && e + j < E)
-                    v = kBf16 ? bf16_lo(((const uint16_t *)logits)[at + j])
-                              : ((const float *)logits)[at + j];
-                l[i + j] = v;
-            }
+        for (int i = 0; i < kV; ++i) {
+            const int32_t e = expert_of(i, c), from = e < E ? e : E - 1;
+            const char *p = rows + (uint32_t)((row * E + from) * kSize);
+            l[i] = kBf16 ? bf16_lo(*(const uint16_t *)p) : *(const float *)p;
         }
     }
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+        l[i] = expert_of(i, c) < E ? l[i] : kNone;
 }
 
 // Scores of the row in place of the logits, and 1 / Z (0 for a row with no
@@ -224,22 +239,24 @@ __global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
         for (int i = 0; i < kV; ++i)
             acc[i] = 0.0f;
     }
+    const char *logits = (const char *)a.logits;
+    constexpr int kSize = kBf16 ? 2 : 4;
     float nxt[kV];  // the next tokens' logits, on their way
-    if (first < end) {
-        const int64_t tok = first + wave * kRowsPerWave + r;
-        load_row<kV, kBf16>(a.logits, tok < end ? tok : first, a.E, c, a.vec != 0, tok < end, nxt);
-    }
-    for (int64_t t0 = first + wave * kRowsPerWave; t0 < end; t0 += kRowsPerBlock) {
-        const int64_t tok = t0 + r, tok2 = tok + kRowsPerBlock;
+    int64_t t0 = first + wave * kRowsPerWave;
+    if (t0 < end)
+        load_rows<kV, kBf16>(logits + t0 * a.E * kSize, t0 + r < end ? r : 0, a.E, c, a.vec != 0, nxt);
+    for (; t0 < end; t0 += kRowsPerBlock) {
+        const int64_t tok = t0 + r;
         const bool on = tok < end;
         float l[kV];
         uint32_t key[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             l[i] = nxt[i];
-            key[i] = packed_key<kIdBits>(l[i], expert_of(i, c), a.E);
+            key[i] = packed_key<kIdBits>(l[i], i);
         }
-        load_row<kV, kBf16>(a.logits, tok2 < end ? tok2 : first, a.E, c, a.vec != 0, tok2 < end, nxt);
+        const int64_t t2 = t0 + kRowsPerBlock < end ? t0 + kRowsPerBlock : t0;
+        load_rows<kV, kBf16>(logits + t2 * a.E * kSize, t2 + r < end ? r : 0, a.E, c, a.vec != 0, nxt);
         const float top = row_top(l);
         const float rz = scores(l, a.score, top);
         if (kLoss) {
@@ -254,35 +271,38 @@ __global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
         bool again = rz != rz;  // a NaN in the row
         int32_t chosen = 0;     // the last chunk's expert of this lane
         auto next_key = [&](uint32_t last) {
-            // key - last wraps to 2^31 and above for keys below last, and the
-            // largest of those differences is the largest of those keys
-            uint32_t d = 0;
+            // last - 1 - (key - 4 c) wraps above last for the keys chosen already,
+            // and is least for the largest of the others
+            const uint32_t mine_last = last + (uint32_t)c * 4;
+            uint32_t d = 0xFFFFFFFFu;
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                d = max(d, key[i] - last);
-            return last + row16_max(d);
+                d = min(d, mine_last + ~key[i]);
+            return last - 1u - row16_min(d);
         };
-        uint32_t m = 0x80000000u;  // the last round's key: those at it and above are chosen
+        uint32_t least = 0xFFFFFFFFu;  // difference of two keys in turn, bit by bit
+        uint32_t m = 0xFFFFFF00u;  // the last round's key: those at it and above are chosen
         for (int32_t k0 = 0; k0 < a.K; k0 += kRowLanes) {
             const int32_t kn = a.K - k0 < kRowLanes ? a.K - k0 : kRowLanes;
             uint32_t my_key = 0;
             for (int32_t k = 0; k < kn; ++k) {
                 const uint32_t was = m;
                 m = next_key(was);
-                if (!kBf16)
-                    again |= (m ^ was) >> kIdBits == 0;
+                if (!kBf16 && k0 + k)
+                    least = min(least, m ^ was);
                 my_key = c == k ? m : my_key;
             }
             if (!kBf16 && k0 + kn == a.K && a.K < a.E)
-                again |= (next_key(m) ^ m) >> kIdBits == 0;
+                least = min(least, next_key(m) ^ m);
             chosen = put(tok, on, k0, kn, c,
                          (int32_t)((1u << kIdBits) - 1u - (my_key & ((1u << kIdBits) - 1u))), base,
                          &mine, &wsum);
         }
+        again |= least >> kIdBits == 0;
         if (ballot(again && on)) {
             // whole keys: the row's maximum, and the least id that has it
             int32_t whole[kV];
-            load_row<kV, kBf16>(a.logits, on ? tok : first, a.E, c, a.vec != 0, on, l);
+            load_rows<kV, kBf16>(logits + t0 * a.E * kSize, on ? r : 0, a.E, c, a.vec != 0, l);
 #pragma unroll
             for (int i = 0; i < kV; ++i)
                 whole[i] = expert_of(i, c) < a.E ? key_of(l[i]) : kNoKey;
@@ -428,7 +448,7 @@ struct RouterBwdArgs {
     const int32_t *topk_idx, *counts;
     const float *d_gates, *d_loss;
     void *d_logits;
-    int64_t N, n;
+    int64_t n, per_group, tokens;
     int32_t E, K, score, normalize, vec;
     float scale, factor;
 };
@@ -445,14 +465,41 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
     const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
     const int c = lane % kRowLanes, r = lane / kRowLanes;
     float *own = (float *)lds + (wave * kRowsPerWave + r) * (kV * kRowLanes);
-    const float dl = a.d_loss ? a.d_loss[0] * a.factor : 0.0f;
     const float tiny = a.score == MOONEP_SCORE_SIGMOID ? 1e-20f : 0.0f;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kRowsPerWave; t0 < a.N;
-         t0 += (int64_t)gridDim.x * kRowsPerBlock) {
+    const int64_t g = (int64_t)blockIdx.x / a.per_group;
+    const int64_t first = g * a.n + ((int64_t)blockIdx.x - g * a.per_group) * a.tokens;
+    const int64_t end = first + a.tokens < (g + 1) * a.n ? first + a.tokens : (g + 1) * a.n;
+    float la[kV];  // the loss's gradient at p_e
+    if (a.counts) {
+        const float dl = a.d_loss[0] * a.factor;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int32_t e = expert_of(i, c);
+            la[i] = e < a.E ? dl * (float)a.counts[g * a.E + e] : 0.0f;
+        }
+    }
+    const char *logits = (const char *)a.logits;
+    constexpr int kSize = kBf16 ? 2 : 4;
+    float nxt[kV];  // the next tokens' logits, on their way
+    int64_t t0 = first + wave * kRowsPerWave;
+    if (t0 < end)
+        load_rows<kV, kBf16>(logits + t0 * a.E * kSize, t0 + r < end ? r : 0, a.E, c, a.vec != 0, nxt);
+    for (; t0 < end; t0 += kRowsPerBlock) {
         const int64_t tok = t0 + r;
-        const bool on = tok < a.N;
+        const bool on = tok < end;
+        // the first 16 entries of the token, one a lane; others are read again
+        uint32_t e0 = 0xFFFFFFFFu;
+        float d0 = 0.0f;
+        if (a.d_gates && on && c < a.K) {
+            e0 = (uint32_t)a.topk_idx[tok * a.K + c];
+            d0 = a.d_gates[tok * a.K + c];
+        }
         float l[kV], s[kV], part[kV];
-        load_row<kV, kBf16>(a.logits, on ? tok : 0, a.E, c, a.vec != 0, on, l);
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            l[i] = nxt[i];
+        const int64_t t2 = t0 + kRowsPerBlock < end ? t0 + kRowsPerBlock : t0;
+        load_rows<kV, kBf16>(logits + t2 * a.E * kSize, t2 + r < end ? r : 0, a.E, c, a.vec != 0, nxt);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             s[i] = l[i];
@@ -466,13 +513,16 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
                 *(f32x4 *)(own + expert_of(i, c)) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
             wave_sync();
             float w = 0.0f, gs = 0.0f;
-            for (int32_t k = c; k < a.K; k += kRowLanes) {
-                const uint32_t e = on ? (uint32_t)a.topk_idx[tok * a.K + k] : 0xFFFFFFFFu;
+            auto chosen = [&](uint32_t e, float d) {
                 if (e < (uint32_t)a.E) {
                     w += own[e];
-                    gs = __builtin_fmaf(a.d_gates[tok * a.K + k], own[e], gs);
+                    gs = __builtin_fmaf(d, own[e], gs);
                 }
-            }
+            };
+            chosen(e0, d0);
+            if (a.K > kRowLanes && on)
+                for (int32_t k = c + kRowLanes; k < a.K; k += kRowLanes)
+                    chosen((uint32_t)a.topk_idx[tok * a.K + k], a.d_gates[tok * a.K + k]);
             w = row16_sum(w) + tiny;
             gs = row16_sum(gs);
             float mul = a.scale, sub = 0.0f;
@@ -489,11 +539,14 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             for (int i = 0; i < kV; i += 4)
                 *(f32x4 *)(own + expert_of(i, c)) = f32x4{0, 0, 0, 0};
             wave_sync();
-            for (int32_t k = c; k < a.K; k += kRowLanes) {
-                const uint32_t e = on ? (uint32_t)a.topk_idx[tok * a.K + k] : 0xFFFFFFFFu;
+            auto spread = [&](uint32_t e, float d) {
                 if (e < (uint32_t)a.E)
-                    atomicAdd(own + e, mul * (a.d_gates[tok * a.K + k] - sub));
-            }
+                    atomicAdd(own + e, mul * (d - sub));
+            };
+            spread(e0, d0);
+            if (a.K > kRowLanes && on)
+                for (int32_t k = c + kRowLanes; k < a.K; k += kRowLanes)
+                    spread((uint32_t)a.topk_idx[tok * a.K + k], a.d_gates[tok * a.K + k]);
             wave_sync();
 #pragma unroll
             for (int i = 0; i < kV; i += 4) {
@@ -505,15 +558,10 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             wave_sync();
         }
         if (a.counts) {
-            // the loss: its gradient at p_e is dl * T_e
-            const int32_t *cnt = a.counts + (on ? tok / a.n : 0) * a.E;
-            float la[kV], dot = 0.0f;
+            float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int32_t e = expert_of(i, c);
-                la[i] = e < a.E ? dl * (float)cnt[e] : 0.0f;
+            for (int i = 0; i < kV; ++i)
                 dot = __builtin_fmaf(la[i], s[i], dot);
-            }
             dot = row16_sum(dot) * rz;
 #pragma unroll
             for (int i = 0; i < kV; ++i)
@@ -524,7 +572,7 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             float slope = s[i];
             if (a.score == MOONEP_SCORE_SIGMOID) {
                 // s (1 - s) without the difference, which loses the digits of s near 1
-                const float d = exp_of(-__builtin_fabsf(l[i])), q = 1.0f / (1.0f + d);
+                const float d = exp_of(-__builtin_fabsf(l[i])), q = __builtin_amdgcn_rcpf(1.0f + d);
                 slope = d * q * q;
             }
             s[i] = (part[i] - all) * slope;
@@ -647,9 +695,9 @@ int launch_router(const moonep_shape &s, const moonep_router_opts &o, const void
         return by_experts<RunRouter>(s.E, a, bf16, false, a.per_group, st);
     }
     a.n = a.N / o.groups;
-    a.tokens = lay.tokens;
-    a.per_group = lay.per_group;
-    const int rc = by_experts<RunRouter>(s.E, a, bf16, true, lay.per_group * o.groups, st);
+    a.tokens = lay.split.tokens;
+    a.per_group = lay.split.per_group;
+    const int rc = by_experts<RunRouter>(s.E, a, bf16, true, a.per_group * o.groups, st);
     if (rc != MOONEP_OK)
         return rc;
     const int32_t nchunk = (s.E + kJoinExperts - 1) / kJoinExperts;
@@ -675,10 +723,15 @@ int launch_router_bwd(const moonep_shape &s, const moonep_router_opts &o, const 
     a.d_gates = d_gates;
     a.d_loss = d_loss;
     a.d_logits = d_logits;
-    a.N = (int64_t)s.R * s.S;
-    if (a.N == 0)
+    const int64_t N = (int64_t)s.R * s.S;
+    if (N == 0)
         return MOONEP_OK;
-    a.n = a.N / o.groups;
+    // without the loss no group matters
+    const int64_t groups = counts ? o.groups : 1;
+    const Split split = split_tokens(N / groups, groups, kBwdBlocks);
+    a.n = N / groups;
+    a.per_group = split.per_group;
+    a.tokens = split.tokens;
     a.E = s.E;
     a.K = s.K;
     a.score = o.score;
@@ -687,8 +740,7 @@ int launch_router_bwd(const moonep_shape &s, const moonep_router_opts &o, const 
     a.vec = row_vectors(logits, d_logits, s.E, bf16);
     a.scale = o.scale;
     a.factor = (float)((double)s.E / ((double)s.K * (double)a.n * (double)a.n * o.groups));
-    const int64_t need = (a.N + kRowsPerBlock - 1) / kRowsPerBlock;
-    return by_experts<RunRouterBwd>(s.E, a, bf16, need < 8192 ? need : 8192, st);
+    return by_experts<RunRouterBwd>(s.E, a, bf16, split.per_group * groups, st);
 }
 
 }  // namespace moonep
