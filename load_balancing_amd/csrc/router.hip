@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kRowLanes = 16, kRowsPerWave = 64 / kRowLanes;
 constexpr int kRowsPerBlock = kWaves * kRowsPerWave;
-constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;
+constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;  // nothing; a NaN, below -inf
 
 // Workgroups of the loss's first pass: enough to fill the chip, few enough that
 // their partial rows stay small beside the logits.
@@ -105,6 +105,9 @@ __device__ __forceinline__ void load_rows(const char *rows, int32_t row, int32_t
 {
     constexpr int kSize = kBf16 ? 2 : 4;
     constexpr float kNone = -__builtin_huge_valf();
+    // Offsets and bounds are cheaper to compute again than to keep across the
+    // rows: as loop invariants they take a register or a mask each.
+    asm volatile("" : "+v"(c));
     if (vec) {
 #pragma unroll
         for (int i = 0; i < kV; i += 4) {
@@ -200,7 +203,7 @@ struct RouterArgs {
 
 // Workgroup b takes `tokens` consecutive tokens of group b / per_group.
 template <int kV, bool kBf16, bool kLoss>
-__global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
+__global__ __launch_bounds__(kBlock, (kV <= 16 ? 4 : 1)) void router_kernel(RouterArgs a)
 {
     extern __shared__ __align__(16) uint32_t lds[];
     int32_t *hist = (int32_t *)lds;        // [E]
@@ -299,35 +302,48 @@ __global__ __launch_bounds__(kBlock) void router_kernel(RouterArgs a)
                          &mine, &wsum);
         }
         again |= least >> kIdBits == 0;
-        if (ballot(again && on)) {
-            // whole keys: the row's maximum, and the least id that has it
-            int32_t whole[kV];
-            load_rows<kV, kBf16>(logits + t0 * a.E * kSize, on ? r : 0, a.E, c, a.vec != 0, l);
+        // Whole keys, for one token at a time over all lanes (rare: so that it takes
+        // few registers from the other rows): the largest, and the least id that
+        // has it.
+        const uint64_t tied = ballot(again && on);
+        for (int q = 0; q < kRowsPerWave && tied; ++q) {
+            if (!((tied >> (q * kRowLanes)) & 1))
+                continue;
+            const char *row = logits + (t0 + q) * a.E * kSize;
+            int32_t whole[kV / 4];
 #pragma unroll
-            for (int i = 0; i < kV; ++i)
-                whole[i] = expert_of(i, c) < a.E ? key_of(l[i]) : kNoKey;
-            wsum = 0.0f;
+            for (int i = 0; i < kV / 4; ++i) {
+                const int32_t e = i * 64 + lane, from = e < a.E ? e : 0;
+                const int32_t w = key_of(kBf16 ? bf16_lo(((const uint16_t *)row)[from])
+                                               : ((const float *)row)[from]);
+                whole[i] = e < a.E ? w : kNoKey;
+            }
+            wsum = r == q ? 0.0f : wsum;
             for (int32_t k0 = 0; k0 < a.K; k0 += kRowLanes) {
                 const int32_t kn = a.K - k0 < kRowLanes ? a.K - k0 : kRowLanes;
                 int32_t my_e = 0;
                 for (int32_t k = 0; k < kn; ++k) {
                     int32_t w = whole[0];
 #pragma unroll
-                    for (int i = 1; i < kV; ++i)
+                    for (int i = 1; i < kV / 4; ++i)
                         w = max(w, whole[i]);
                     w = row16_imax(w);
+                    w = max(w, __shfl_xor(w, 16, 64));
+                    w = max(w, __shfl_xor(w, 32, 64));
                     uint32_t e = 0xFFFFu;
 #pragma unroll
-                    for (int i = kV - 1; i >= 0; --i)
-                        e = whole[i] == w ? (uint32_t)((i >> 2) * 64 + (i & 3)) : e;
-                    e = row16_min(e + (uint32_t)c * 4);
-                    const int32_t rel = (int32_t)e - c * 4;
+                    for (int i = kV / 4 - 1; i >= 0; --i)
+                        e = whole[i] == w ? (uint32_t)(i * 64 + lane) : e;
+                    e = row16_min(e);
+                    e = min(e, (uint32_t)__shfl_xor((int)e, 16, 64));
+                    e = min(e, (uint32_t)__shfl_xor((int)e, 32, 64));
 #pragma unroll
-                    for (int i = 0; i < kV; ++i)
-                        whole[i] = rel == (i >> 2) * 64 + (i & 3) ? kNoKey : whole[i];
+                    for (int i = 0; i < kV / 4; ++i)
+                        whole[i] = e == (uint32_t)(i * 64 + lane) ? kNoKey : whole[i];
                     my_e = c == k ? (int32_t)e : my_e;
                 }
-                chosen = put(tok, on, k0, kn, c, my_e, base, &mine, &wsum);
+                if (r == q)
+                    chosen = put(tok, on, k0, kn, c, my_e, base, &mine, &wsum);
             }
         }
         if (kLoss && on) {
