@@ -12,6 +12,7 @@ If libmoonep.so is not built, importing works but the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -149,12 +150,26 @@ def _check(rc: int, what: str):
 # marshalling helpers
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 _BF16_OK = ("bfloat16", "int16", "uint16")
+_dtype_names = {}  # torch.dtype -> its name
+
+
+def _dtype_name(dtype):
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
+    return name
 
 
 def _dev(t, what, numel, kinds):
@@ -167,7 +182,7 @@ def _dev(t, what, numel, kinds):
         return t
     if not t.is_cuda:
         raise ValueError(f"{what}: tensor must be on a GPU")
-    if str(t.dtype).replace("torch.", "") not in kinds:
+    if _dtype_name(t.dtype) not in kinds:
         raise ValueError(f"{what}: dtype {t.dtype} not in {kinds}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: tensor must be contiguous")
@@ -178,7 +193,9 @@ def _dev(t, what, numel, kinds):
 
 def _stream(stream):
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        # the current stream's handle, without building a Stream object for it
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -186,6 +203,33 @@ def _stream(stream):
 
 def _nbytes(t):
     return t.numel() * t.element_size()
+
+
+def _current_device():
+    return _torch().cuda.current_device()
+
+
+def _arg(dev, t, what, numel, kinds):
+    """_dev for a tensor that has to be on device dev, the current one, whose
+    stream the call takes; kinds None: numel bytes of any dtype."""
+    if t is None or type(t) is int:
+        return _dev(t, what, numel, kinds)
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, must be on a GPU, the current device")
+    if kinds is None:
+        return _dev_bytes(t, what, numel)
+    if _dtype_names.get(t.dtype) not in kinds or not t.is_contiguous() or t.numel() != numel:
+        return _dev(t, what, numel, kinds)  # says what is wrong (or has not seen the dtype yet)
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=None)
+def _plan_words(E, R):
+    return moonep_plan_bytes(Shape(R, E, 0, 1, 8)) // 4
+
+
+def _scale_row(cols):
+    return 4 * -(-cols // 512)
 
 
 # ---------------------------------------------------------------------------
@@ -351,16 +395,18 @@ def moonep_router(shape, opts, logits, topk_idx, gates, counts=None, prob_sum=No
                   workspace=None, stream=None):
     """topk_idx and gates [R*S*K] of logits [R*S, E]; with counts and prob_sum
     [groups, E], loss [1] and a workspace also the balance loss."""
-    some = any(t is not None for t in (counts, prob_sum, loss, workspace))
+    dev = _current_device()
+    some = not (counts is None and prob_sum is None and loss is None and workspace is None)
     tab = opts.groups * shape.E if some else 0
     _check(lib().moonep_router(
         ctypes.byref(shape), ctypes.byref(opts),
-        _dev(logits, "logits", shape.N * shape.E, _logit_kinds(opts)),
-        _dev(topk_idx, "topk_idx", shape.NK, ("int32",)),
-        _dev(gates, "gates", shape.NK, ("float32",)), _dev(counts, "counts", tab, ("int32",)),
-        _dev(prob_sum, "prob_sum", tab, ("float32",)),
-        _dev(loss, "loss", 1 if some else 0, ("float32",)),
-        _dev(workspace, "workspace", workspace.numel() if workspace is not None else int(some),
+        _arg(dev, logits, "logits", shape.N * shape.E, _logit_kinds(opts)),
+        _arg(dev, topk_idx, "topk_idx", shape.NK, ("int32",)),
+        _arg(dev, gates, "gates", shape.NK, ("float32",)),
+        _arg(dev, counts, "counts", tab, ("int32",)),
+        _arg(dev, prob_sum, "prob_sum", tab, ("float32",)),
+        _arg(dev, loss, "loss", 1 if some else 0, ("float32",)),
+        _arg(dev, workspace, "workspace", workspace.numel() if workspace is not None else int(some),
              ("uint8",)),
         _nbytes(workspace) if workspace is not None else 0, _stream(stream)), "moonep_router")
 
@@ -369,14 +415,16 @@ def moonep_router_bwd(shape, opts, logits, topk_idx, counts, d_gates, d_loss, d_
                       stream=None):
     """d_logits [R*S, E] from d_gates [R*S*K] (None: 0) and d_loss [1] with the
     forward's counts (both None: no loss)."""
+    dev = _current_device()
     n = shape.N * shape.E
     _check(lib().moonep_router_bwd(
-        ctypes.byref(shape), ctypes.byref(opts), _dev(logits, "logits", n, _logit_kinds(opts)),
-        _dev(topk_idx, "topk_idx", shape.NK, ("int32",)),
-        _dev(counts, "counts", 0 if counts is None else opts.groups * shape.E, ("int32",)),
-        _dev(d_gates, "d_gates", 0 if d_gates is None else shape.NK, ("float32",)),
-        _dev(d_loss, "d_loss", 0 if d_loss is None else 1, ("float32",)),
-        _dev(d_logits, "d_logits", n, _logit_kinds(opts)), _stream(stream)), "moonep_router_bwd")
+        ctypes.byref(shape), ctypes.byref(opts), _arg(dev, logits, "logits", n, _logit_kinds(opts)),
+        _arg(dev, topk_idx, "topk_idx", shape.NK, ("int32",)),
+        _arg(dev, counts, "counts", 0 if counts is None else opts.groups * shape.E, ("int32",)),
+        _arg(dev, d_gates, "d_gates", 0 if d_gates is None else shape.NK, ("float32",)),
+        _arg(dev, d_loss, "d_loss", 0 if d_loss is None else 1, ("float32",)),
+        _arg(dev, d_logits, "d_logits", n, _logit_kinds(opts)), _stream(stream)),
+        "moonep_router_bwd")
 
 
 _CODES = ("float8_e4m3fn", "uint8")
@@ -391,24 +439,29 @@ def moonep_scale_bytes(cols: int) -> int:
 def moonep_rmsnorm_quant(shape, x, res, weight, eps, res_out, y_out, y8, ys, stream=None):
     """res_out = x + res (both None: x alone), y8 and ys its RMS norm times weight
     [H] as 8-bit rows, y_out (or None) the same in bf16."""
+    dev = _current_device()
     n = shape.N * shape.H
     _check(lib().moonep_rmsnorm_quant(
-        ctypes.byref(shape), _dev(x, "x", n, _BF16_OK),
-        _dev(res, "res", 0 if res is None else n, _BF16_OK),
-        _dev(weight, "weight", shape.H, _BF16_OK), float(eps),
-        _dev(res_out, "res_out", 0 if res_out is None else n, _BF16_OK),
-        _dev(y_out, "y_out", 0 if y_out is None else n, _BF16_OK), _dev(y8, "y8", n, _CODES),
-        _dev(ys, "ys", shape.N * moonep_scale_bytes(shape.H), _SCALES), _stream(stream)),
+        ctypes.byref(shape), _arg(dev, x, "x", n, _BF16_OK),
+        _arg(dev, res, "res", 0 if res is None else n, _BF16_OK),
+        _arg(dev, weight, "weight", shape.H, _BF16_OK), float(eps),
+        _arg(dev, res_out, "res_out", 0 if res_out is None else n, _BF16_OK),
+        _arg(dev, y_out, "y_out", 0 if y_out is None else n, _BF16_OK),
+        _arg(dev, y8, "y8", n, _CODES),
+        _arg(dev, ys, "ys", shape.N * _scale_row(shape.H), _SCALES), _stream(stream)),
         "moonep_rmsnorm_quant")
 
 
 def moonep_dispatch_quant(shape, x8, xs, slot_of, buf8, bufs, stream=None):
     """buf8 [R*S*K, H] and bufs get every token's codes and scales at its slots."""
-    sb = moonep_scale_bytes(shape.H)
+    dev = _current_device()
+    sb = _scale_row(shape.H)
     _check(lib().moonep_dispatch_quant(
-        ctypes.byref(shape), _dev(x8, "x8", shape.N * shape.H, _CODES),
-        _dev(xs, "xs", shape.N * sb, _SCALES), _dev(slot_of, "slot_of", shape.NK, ("int32",)),
-        _dev(buf8, "buf8", shape.NK * shape.H, _CODES), _dev(bufs, "bufs", shape.NK * sb, _SCALES),
+        ctypes.byref(shape), _arg(dev, x8, "x8", shape.N * shape.H, _CODES),
+        _arg(dev, xs, "xs", shape.N * sb, _SCALES),
+        _arg(dev, slot_of, "slot_of", shape.NK, ("int32",)),
+        _arg(dev, buf8, "buf8", shape.NK * shape.H, _CODES),
+        _arg(dev, bufs, "bufs", shape.NK * sb, _SCALES),
         _stream(stream)), "moonep_dispatch_quant")
 
 
@@ -416,10 +469,11 @@ def moonep_quant_weights(shape, in_dim, out_dim, w, w_stride, w_offset, w8, w8_s
                          scale_offset, stream=None):
     """The [out_dim, in_dim] bf16 matrices at element w_offset of w [E, w_stride]
     to codes and scales inside the weight rows of w8 [E, w8_stride] bytes."""
+    dev = _current_device()
     _check(lib().moonep_quant_weights(
         ctypes.byref(shape), int(in_dim), int(out_dim),
-        _dev_bytes(w, "w", shape.E * w_stride * 2), int(w_stride), int(w_offset),
-        _dev_bytes(w8, "w8", shape.E * w8_stride), int(w8_stride), int(code_offset),
+        _arg(dev, w, "w", shape.E * w_stride * 2, None), int(w_stride), int(w_offset),
+        _arg(dev, w8, "w8", shape.E * w8_stride, None), int(w8_stride), int(code_offset),
         int(scale_offset), _stream(stream)), "moonep_quant_weights")
 
 
@@ -427,14 +481,15 @@ def moonep_expert_gemm_quant(shape, plan, wslot, B, in_dim, out_dim, x8, xs, w_h
                              code_offset, scale_offset, y, stream=None):
     """y [R*S*K, out_dim] bf16 = each 8-bit buffer row times its segment's 8-bit
     weights; w_home [E, w_stride] and pool [R*B, w_stride] bytes."""
+    dev = _current_device()
     _check(lib().moonep_expert_gemm_quant(
-        ctypes.byref(shape), _dev(plan, "plan", moonep_plan_bytes(shape) // 4, ("int32",)),
-        _dev(wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(out_dim),
-        _dev(x8, "x8", shape.NK * in_dim, _CODES),
-        _dev(xs, "xs", shape.NK * moonep_scale_bytes(in_dim), _SCALES),
-        _dev_bytes(w_home, "w_home", shape.E * w_stride),
-        _dev_bytes(pool, "pool", shape.R * B * w_stride), int(w_stride), int(code_offset),
-        int(scale_offset), _dev(y, "y", shape.NK * out_dim, _BF16_OK), _stream(stream)),
+        ctypes.byref(shape), _arg(dev, plan, "plan", _plan_words(shape.E, shape.R), ("int32",)),
+        _arg(dev, wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(out_dim),
+        _arg(dev, x8, "x8", shape.NK * in_dim, _CODES),
+        _arg(dev, xs, "xs", shape.NK * _scale_row(in_dim), _SCALES),
+        _arg(dev, w_home, "w_home", shape.E * w_stride, None),
+        _arg(dev, pool, "pool", shape.R * B * w_stride, None), int(w_stride), int(code_offset),
+        int(scale_offset), _arg(dev, y, "y", shape.NK * out_dim, _BF16_OK), _stream(stream)),
         "moonep_expert_gemm_quant")
 
 
@@ -443,16 +498,17 @@ def moonep_expert_glu_quant(shape, plan, wslot, B, in_dim, mid_dim, x8, xs, w_ho
                             h8, hs, stream=None):
     """h8 [R*S*K, mid_dim] and hs: silu of the gate projection times the up
     projection of each 8-bit buffer row, as 8-bit rows."""
+    dev = _current_device()
     _check(lib().moonep_expert_glu_quant(
-        ctypes.byref(shape), _dev(plan, "plan", moonep_plan_bytes(shape) // 4, ("int32",)),
-        _dev(wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(mid_dim),
-        _dev(x8, "x8", shape.NK * in_dim, _CODES),
-        _dev(xs, "xs", shape.NK * moonep_scale_bytes(in_dim), _SCALES),
-        _dev_bytes(w_home, "w_home", shape.E * w_stride),
-        _dev_bytes(pool, "pool", shape.R * B * w_stride), int(w_stride), int(gate_code_offset),
+        ctypes.byref(shape), _arg(dev, plan, "plan", _plan_words(shape.E, shape.R), ("int32",)),
+        _arg(dev, wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(mid_dim),
+        _arg(dev, x8, "x8", shape.NK * in_dim, _CODES),
+        _arg(dev, xs, "xs", shape.NK * _scale_row(in_dim), _SCALES),
+        _arg(dev, w_home, "w_home", shape.E * w_stride, None),
+        _arg(dev, pool, "pool", shape.R * B * w_stride, None), int(w_stride), int(gate_code_offset),
         int(gate_scale_offset), int(up_code_offset), int(up_scale_offset),
-        _dev(h8, "h8", shape.NK * mid_dim, _CODES),
-        _dev(hs, "hs", shape.NK * moonep_scale_bytes(mid_dim), _SCALES), _stream(stream)),
+        _arg(dev, h8, "h8", shape.NK * mid_dim, _CODES),
+        _arg(dev, hs, "hs", shape.NK * _scale_row(mid_dim), _SCALES), _stream(stream)),
         "moonep_expert_glu_quant")
 
 
