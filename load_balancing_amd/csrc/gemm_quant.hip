@@ -109,17 +109,6 @@ __device__ __forceinline__ void dma(const uint8_t *src, char *dst)
         __builtin_amdgcn_global_load_lds((const void *)src, to, 4, 0, 0);
 }
 
-// A workgroup barrier that waits for this wave's LDS operations only: a
-// __syncthreads would also wait for every load in flight, which leaves a ring
-// of any depth with one stage.
-__device__ __forceinline__ void lds_barrier()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 }  // namespace
 
 template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU, bool TAIL>

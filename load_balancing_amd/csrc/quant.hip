@@ -23,6 +23,16 @@ __device__ __forceinline__ void unpack8(const u32x4 &w, float (&f)[8])
     }
 }
 
+// Eight scaled values as codes.  Non-temporal, as every other store here: in the
+// norm of 131072 x 4096 rows write-back stores of the codes alone cost 835 us
+// against 808.
+__device__ __forceinline__ void store_codes(void *to, const float (&f)[8], float inv, uint32_t byte)
+{
+    __builtin_nontemporal_store(u32x2{pack_e4m3(f[0], f[1], f[2], f[3], inv, byte),
+                                      pack_e4m3(f[4], f[5], f[6], f[7], inv, byte)},
+                                (u32x2 *)to);
+}
+
 __device__ __forceinline__ float wave_sum(float v)
 {
     v = row16_sum(v);
@@ -36,19 +46,20 @@ __device__ __forceinline__ float wave_sum(float v)
 // groups of eight columns per thread in registers: every input is read once.
 // Sum of squares in fp32 per thread, then over the wave and the waves.
 template <int kTeam, int kIter>
-__global__ __launch_bounds__((kTeam < kBlock ? kBlock : kTeam)) void rmsnorm_quant_kernel(
+__global__ __launch_bounds__((kTeam == 64 ? kBlock : kTeam)) void rmsnorm_quant_kernel(
     const u32x4 *x, const u32x4 *res, const u32x4 *__restrict__ weight, float eps,
     u32x4 *res_out, u32x4 *__restrict__ y_out, u32x2 *__restrict__ y8, uint32_t *__restrict__ ys,
     int64_t N, int32_t V, int32_t H)
 {
-    constexpr int kThreads = kTeam < kBlock ? kBlock : kTeam;
+    constexpr int kThreads = kTeam == 64 ? kBlock : kTeam;  // several waves of one row each
     constexpr int kTeams = kThreads / kTeam, kTeamWaves = kTeam / 64;
     __shared__ float part[2][kTeamWaves];
     const int t = (int)threadIdx.x % kTeam, lane = lane_id();
     const int32_t SD = scale_row_bytes(H) / 4;
+    constexpr bool kKeepWeight = kIter <= 4;  // else read again each row, from the L2
     u32x4 w[kIter];
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
+    for (int i = 0; i < kIter && kKeepWeight; ++i) {
         const int32_t v = i * kTeam + t;
         w[i] = v < V ? weight[v] : u32x4{0, 0, 0, 0};
     }
@@ -101,6 +112,8 @@ __global__ __launch_bounds__((kTeam < kBlock ? kBlock : kTeam)) void rmsnorm_qua
             const int32_t v = i * kTeam + t;
             float f[8], g[8];
             unpack8(r[i], f);
+            if (!kKeepWeight)
+                w[i] = v < V ? weight[v] : u32x4{0, 0, 0, 0};
             unpack8(w[i], g);
             uint32_t m = 0;
 #pragma unroll
@@ -112,8 +125,7 @@ __global__ __launch_bounds__((kTeam < kBlock ? kBlock : kTeam)) void rmsnorm_qua
             const float inv = inverse_scale(byte);
             const uint32_t dword = gather_scale_dword(byte);
             if (v < V) {
-                y8[row * V + v] = u32x2{pack_e4m3(f[0], f[1], f[2], f[3], inv, byte),
-                                        pack_e4m3(f[4], f[5], f[6], f[7], inv, byte)};
+                store_codes(y8 + row * V + v, f, inv, byte);
                 if (y_out)
                     store_nt(y_out + row * V + v,
                              u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
@@ -161,49 +173,61 @@ __global__ __launch_bounds__(kBlock) void dispatch_quant_kernel(
     }
 }
 
-// One workgroup per 128 rows x 512 columns (four blocks): wave w holds rows
-// w, w + 16, .. of it, so the matrix is read once.
+// An item is 128 rows x 512 columns (four blocks): wave w holds rows w, w + 16,
+// .. of it in registers between the blocks' magnitudes and their codes, and the
+// next item's rows are on their way meanwhile (the barrier waits for LDS alone).
+// On 64 experts of 1408 x 2048: 112-114 us, 4.9 TB/s; without the next item's
+// loads 124, one block of 128 x 128 per workgroup (256-byte row pieces) 177,
+// write-back code stores 131.
 constexpr int kWqWaves = 16, kWqRows = kQuantBlock / kWqWaves;
+constexpr int64_t kWqGrid = 512;
 
 __global__ __launch_bounds__(kWqWaves * 64) void quant_weights_kernel(
     const uint16_t *__restrict__ w, int64_t w_stride, int64_t w_offset, uint8_t *__restrict__ w8,
     int64_t w8_stride, int64_t code_offset, int64_t scale_offset, int64_t items, int32_t out_dim,
     int32_t in_dim, int32_t nrb, int32_t ncb)
 {
-    __shared__ uint32_t part[kWqWaves][4];
+    __shared__ uint32_t part[2][kWqWaves][4];
     const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
+    int flip = 0;
+    // Rows of item `it` into r; rows and columns past the matrix are 0.
+    auto load = [&](int64_t it, u32x4 (&r)[kWqRows]) {
+        const int32_t cb = (int32_t)(it % ncb), rb = (int32_t)(it / ncb % nrb);
+        const int32_t col = cb * 512 + lane * 8, row0 = rb * kQuantBlock + wave;
+        const uint16_t *src = w + it / ncb / nrb * w_stride + w_offset + (int64_t)row0 * in_dim + col;
+#pragma unroll
+        for (int i = 0; i < kWqRows; ++i) {
+            r[i] = u32x4{0, 0, 0, 0};
+            if (row0 + i * kWqWaves < out_dim && col < in_dim)
+                r[i] = load_nt((const u32x4 *)(src + (int64_t)(i * kWqWaves) * in_dim));
+        }
+    };
+    u32x4 nxt[kWqRows];
+    load(blockIdx.x, nxt);
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int32_t cb = (int32_t)(it % ncb);
-        const int64_t rest = it / ncb;
-        const int32_t rb = (int32_t)(rest % nrb);
-        const int64_t e = rest / nrb;
-        const int32_t col = cb * 512 + lane * 8;
-        const uint16_t *src = w + e * w_stride + w_offset;
-        uint8_t *dst = w8 + e * w8_stride;
+        const int32_t cb = (int32_t)(it % ncb), rb = (int32_t)(it / ncb % nrb);
+        const int32_t col = cb * 512 + lane * 8, row0 = rb * kQuantBlock + wave;
+        uint8_t *dst = w8 + it / ncb / nrb * w8_stride;
+        uint8_t *code = dst + code_offset + (int64_t)row0 * in_dim + col;
         u32x4 r[kWqRows];
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kWqRows; ++i) {
-            const int32_t row = rb * kQuantBlock + i * kWqWaves + wave;
-            r[i] = u32x4{0, 0, 0, 0};
-            if (row < out_dim && col < in_dim)
-                r[i] = load_nt((const u32x4 *)(src + (int64_t)row * in_dim + col));
-        }
+            r[i] = nxt[i];
 #pragma unroll
-        for (int i = 0; i < kWqRows; ++i) {
-            float f[8];
-            unpack8(r[i], f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = max(m, abs_bits(f[j]));
+            for (int j = 0; j < 4; ++j)
+                m = max(m, max((r[i][j] << 16) & 0x7FFF0000u, r[i][j] & 0x7FFF0000u));
         }
+        if (it + gridDim.x < items)
+            load(it + gridDim.x, nxt);
         m = row16_max(m);
         if ((lane & 15) == 0)
-            part[wave][lane >> 4] = m;
-        __syncthreads();
+            part[flip][wave][lane >> 4] = m;
+        lds_barrier();
 #pragma unroll
         for (int q = 0; q < kWqWaves; ++q)
-            m = max(m, part[q][lane >> 4]);
+            m = max(m, part[flip][q][lane >> 4]);
+        flip ^= 1;
         const uint32_t byte = scale_byte(m);
         const float inv = inverse_scale(byte);
         const uint32_t dword = gather_scale_dword(byte);
@@ -211,15 +235,11 @@ __global__ __launch_bounds__(kWqWaves * 64) void quant_weights_kernel(
             *(uint32_t *)(dst + scale_offset + ((int64_t)rb * ncb + cb) * 4) = dword;
 #pragma unroll
         for (int i = 0; i < kWqRows; ++i) {
-            const int32_t row = rb * kQuantBlock + i * kWqWaves + wave;
             float f[8];
             unpack8(r[i], f);
-            if (row < out_dim && col < in_dim)
-                *(u32x2 *)(dst + code_offset + (int64_t)row * in_dim + col) =
-                    u32x2{pack_e4m3(f[0], f[1], f[2], f[3], inv, byte),
-                          pack_e4m3(f[4], f[5], f[6], f[7], inv, byte)};
+            if (row0 + i * kWqWaves < out_dim && col < in_dim)
+                store_codes(code + (int64_t)(i * kWqWaves) * in_dim, f, inv, byte);
         }
-        __syncthreads();  // part is free again
     }
 }
 
@@ -232,7 +252,7 @@ int run_rmsnorm(const moonep_shape &s, const uint16_t *x, const uint16_t *res,
                 const uint16_t *weight, float eps, uint16_t *res_out, uint16_t *y_out, uint8_t *y8,
                 uint8_t *ys, hipStream_t st)
 {
-    constexpr int kThreads = kTeam < kBlock ? kBlock : kTeam;
+    constexpr int kThreads = kTeam == 64 ? kBlock : kTeam;
     const int64_t N = (int64_t)s.R * s.S, per = kThreads / kTeam;
     const int64_t blocks = (N + per - 1) / per;
     const dim3 grid((uint32_t)(blocks < kRowGrid ? blocks : kRowGrid));
@@ -251,16 +271,25 @@ int launch_rmsnorm_quant(const moonep_shape &s, const uint16_t *x, const uint16_
 {
     if ((int64_t)s.R * s.S == 0)
         return MOONEP_OK;
+    // Threads of a row, and groups of eight columns of each: a wave without a
+    // barrier up to 1024 columns, then two to four groups a thread.  Measured with
+    // residual and bf16 output, TB/s: H = 1024 6.0 (256 threads, one group: 5.5),
+    // 2048 6.1 (256 x 1: 5.9), 4096 6.0 (512 x 1: 6.1, 512 x 2: 5.6), 7168 6.0
+    // (512 x 2: 5.9, 1024 x 1: 6.0).
     if (s.H <= 512)
         return run_rmsnorm<64, 1>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
+    if (s.H <= 1024)
+        return run_rmsnorm<64, 2>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
     if (s.H <= 2048)
-        return run_rmsnorm<256, 1>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
+        return run_rmsnorm<128, 2>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
     if (s.H <= 4096)
         return run_rmsnorm<256, 2>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
     if (s.H <= 8192)
-        return run_rmsnorm<512, 2>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
+        return run_rmsnorm<256, 4>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
     if (s.H <= 16384)
         return run_rmsnorm<1024, 2>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
+    if (s.H <= 32768)  // 512 threads: twice the registers a thread
+        return run_rmsnorm<512, 8>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
     return run_rmsnorm<1024, 8>(s, x, res, weight, eps, res_out, y_out, y8, ys, st);
 }
 
@@ -286,7 +315,7 @@ int launch_quant_weights(const moonep_shape &s, int32_t in_dim, int32_t out_dim,
     const int32_t nrb = (out_dim - 1) / kQuantBlock + 1;
     const int32_t ncb = scale_row_bytes(in_dim) / 4;
     const int64_t items = (int64_t)s.E * nrb * ncb;
-    const dim3 grid((uint32_t)(items < kRowGrid ? items : kRowGrid));
+    const dim3 grid((uint32_t)(items < kWqGrid ? items : kWqGrid));
     hipLaunchKernelGGL(quant_weights_kernel, grid, dim3(kWqWaves * 64), 0, st, w, w_stride,
                        w_offset, w8, w8_stride, code_offset, scale_offset, items, out_dim, in_dim,
                        nrb, ncb);

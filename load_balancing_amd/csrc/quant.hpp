@@ -89,4 +89,14 @@ __device__ __forceinline__ uint32_t gather_scale_dword(uint32_t byte)
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// A workgroup barrier that waits for this wave's LDS operations only: a
+// __syncthreads would also wait for every load in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 }  // namespace moonep
