@@ -471,7 +471,7 @@ int moonep_quant_weights(const moonep_shape *shape, int32_t in_dim, int32_t out_
  * moonep_expert_gemm):
  *   y[r, n] = bf16( sum_k x[r, k] * W[n, k] )  (fp32 accumulation on the matrix
  *             cores, one rounding to nearest even), y: bf16 [R*S*K, out_dim].
- * Limits (MOONEP_ERR_ARG): in_dim % 16 == 0, in_dim <= 2^22, out_dim % 16 == 0,
+ * Limits (MOONEP_ERR_ARG): in_dim and out_dim multiples of 16 and at most 2^22,
  * w_stride and code_offset multiples of 16, scale_offset of 4, windows inside
  * the weight row.  x8, y, w_home, pool 16-byte aligned; y must not overlap an
  * input.

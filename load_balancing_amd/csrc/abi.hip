@@ -470,10 +470,10 @@ int expert_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *
     const int rc = shape_status(shape);
     if (rc != MOONEP_OK)
         return rc;
-    // the kernel addresses a row of a tile by a 32-bit byte offset
+    // the kernel addresses a row of a tile, in and out, by a 32-bit byte offset
     constexpr int32_t kMaxDim = 1 << 22;
     if (B < 0 || (int64_t)shape->R * B >= ((int64_t)1 << 31) || in_dim <= 0 || in_dim % 16 != 0 ||
-        in_dim > kMaxDim || out_dim <= 0 || out_dim % 16 != 0 || out_dim > (1 << 30) ||
+        in_dim > kMaxDim || out_dim <= 0 || out_dim % 16 != 0 || out_dim > kMaxDim ||
         w_stride <= 0 || w_stride % 16 != 0)
         return MOONEP_ERR_ARG;
     for (int m = 0; m < nmat; ++m)

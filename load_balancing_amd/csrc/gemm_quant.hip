@@ -73,7 +73,8 @@ struct QCfg {
     static_assert(BM % (kRpi * kWavesG) == 0 && BN % (kRpi * kWavesG) == 0, "rows per DMA round");
     static_assert(kScaleWaves <= kWavesG, "a thread for every scale");
     static_assert(kBandRows % 32 == 0 && WM % kBandRows == 0, "bands of whole row tiles");
-    static_assert((S - 1) * kPerStage <= 63, "outstanding loads must fit vmcnt");
+    static constexpr int kStores = kBands * kOIter;  // of rows, per wave and item
+    static_assert((S - 1) * kPerStage + kStores <= 63, "outstanding accesses must fit vmcnt");
     static_assert(!GLU || (kOutCols == kQuantBlock && kTN == 2), "gate and up in one wave, one block");
     static_assert(kSegAt + kSegBytesMax <= kCuLds, "LDS");
     static_assert(kOIter >= 1 && kBandRows * kVecPerRow % kThreads == 0, "epilogue split");
@@ -96,6 +97,14 @@ template <int n>
 __device__ __forceinline__ void wait_vm()
 {
     __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
+}
+
+// A value that every lane holds alike, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 // One LDS-DMA load: kBytes of each lane to dst + lane * kBytes.
@@ -143,9 +152,10 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
         uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
     };
     Load ld;
-    ld.it = xcd_slot((int)blockIdx.x, (int)gridDim.x);
-    if (ld.it >= items)
+    const int64_t first = xcd_slot((int)blockIdx.x, (int)gridDim.x);
+    if (first >= items)
         return;
+    ld.it = first;
     const int dma_row = lane / G::kCpr, dma_pos = lane % G::kCpr;
     auto a_row = [&](int v) { return (v * G::kWavesG + wave) * G::kRpi + dma_row; };
     auto b_mat = [&](int v) { return GLU ? (v * G::kWavesG + wave) * G::kRpi / 32 % 2 : 0; };
@@ -242,7 +252,7 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
     for (int st = 0; st < S; ++st)
         issue(st);
 
-    for (int64_t it = xcd_slot((int)blockIdx.x, (int)gridDim.x); it < items; it += gridDim.x) {
+    for (int64_t it = first; it < items; it += gridDim.x) {
         int64_t m0 = ld.m0;
         int32_t mrows = ld.mrows, n0 = ld.n0;
         if (ld.it != it)
@@ -259,12 +269,14 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
         for (int32_t kt = 0; kt < nk; ++kt) {
             // This stage's loads have landed once only what was issued after them is
             // outstanding: S - 2 stages, S - 1 at an item's start (the slot of the
-            // item before's last stage is loading already), and some more scales
-            // and stores, if any.
-            if (kt == 0)
-                wait_vm<(S - 1) * G::kPerStage>();
+            // item before's last stage is loading already).  The first S stages
+            // were issued ahead of the stores of the item before, which so need
+            // not be waited for; scales and their stores come on top, if any.
+            if (kt >= S || it == first)
+                kt == 0 ? wait_vm<(S - 1) * G::kPerStage>() : wait_vm<(S - 2) * G::kPerStage>();
             else
-                wait_vm<(S - 2) * G::kPerStage>();
+                kt == 0 ? wait_vm<(S - 1) * G::kPerStage + G::kStores>()
+                        : wait_vm<(S - 2) * G::kPerStage + G::kStores>();
             lds_barrier();  // every wave's part of the stage is there, and the one before is free
             const int cur = slot;
             slot = slot + 1 == S ? 0 : slot + 1;
@@ -313,19 +325,33 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
 
         // ---- epilogue: lane l holds row l % 32 of tile i, and of each column tile
         // the columns 8 (q / 4) + 4 (l / 32) + q % 4 ------------------------------
+        m0 = uniform(m0);
+        mrows = __builtin_amdgcn_readfirstlane(mrows);
+        n0 = __builtin_amdgcn_readfirstlane(n0);
         char *so = lds_b + G::kOutAt;
+        // the tile's rows, from its first column to the end of its last row
+        const auto out = __builtin_amdgcn_make_buffer_rsrc(
+            (char *)a.out + (m0 * a.out_dim + n0) * G::kOutBytes, 0,
+            (int)((uint32_t)(mrows * a.out_dim - n0) * G::kOutBytes), 0x00020000);
         float *row_max = (float *)(lds_b + G::kMaxAt);  // [BM][kWN]
         if constexpr (GLU) {
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i) {
-                uint32_t m = 0;
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const float g = acc[i][0][q], u = acc[i][G::kTN - 1][q];
-                    const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-                    acc[i][0][q] = h;
-                    m = max(m, n0 + wn * 32 + (q >> 2) * 8 + fhalf * 4 < a.out_dim ? abs_bits(h) : 0u);
+                    acc[i][0][q] = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
                 }
+                if (n0 + G::kOutCols > a.out_dim) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (n0 + wn * 32 + (q >> 2) * 8 + fhalf * 4 >= a.out_dim)
+                            acc[i][0][q] = 0.0f;
+                }
+                uint32_t m = 0;
+#pragma unroll
+                for (int q = 0; q < 16; ++q)
+                    m = max(m, abs_bits(acc[i][0][q]));
                 m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
                 if (fhalf == 0)
                     row_max[(wm * WM + i * 32 + fr) * G::kWN + wn] = __uint_as_float(m);
@@ -378,9 +404,13 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
                 const int idx = tid + v * G::kThreads;
                 const int row = idx / G::kVecPerRow, c = idx % G::kVecPerRow;
                 const int grow = band * G::kBandRows + row;
-                if (grow < mrows && n0 + c * (16 / G::kOutBytes) < a.out_dim)
-                    *(u32x4 *)((char *)a.out + ((m0 + grow) * a.out_dim + n0) * G::kOutBytes + c * 16) =
-                        *(const u32x4 *)(so + row * G::kLdoBytes + c * 16);
+                // A buffer store drops what is out of bounds, so every wave issues
+                // the same number: rows past the tile end behind the buffer, and
+                // columns past the row are sent there.
+                const bool in = n0 + c * (16 / G::kOutBytes) < a.out_dim;
+                const uint32_t at = in ? (uint32_t)(grow * a.out_dim) * G::kOutBytes + c * 16 : 0xFFFFFFF0u;
+                __builtin_amdgcn_raw_buffer_store_b128(*(const u32x4 *)(so + row * G::kLdoBytes + c * 16),
+                                                       out, (int)at, 0, 0);
             }
         }
     }
@@ -449,11 +479,28 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
     a.out = out;
     a.out_scales = out_scales;
     const bool tail = in_dim % kQuantBlock != 0;
-    if (rows <= (int64_t)32 * s.E)
-        return glu ? run_tail<32, 256, 32, 64, 128, 3, 32, true>(a, tail, st)
-                   : run_tail<32, 128, 32, 32, 128, 6, 32, false>(a, tail, st);
-    return glu ? run_tail<256, 256, 128, 64, 128, 2, 64, true>(a, tail, st)
-               : run_tail<256, 256, 128, 64, 128, 2, 32, false>(a, tail, st);
+    // Tiles by the mean rows of an expert: few rows want few wasted ones and a deep
+    // ring of weights, many want the bytes that a large tile saves.  Measured at
+    // R = 8, E = 64, K = 8, 2048 x 1408, us by mean rows:
+    //   gate and up, tiles of 32 / 64 / 256 rows: 4: 77 / 79 / 108, 16: 97 / 88 /
+    //   120, 64: 149 / 118 / 142, 96: 181 / 134 / 143, 128: 220 / 160 / 146,
+    //   512: 627 / 418 / 256;
+    //   down, 32 x 128 / 128 x 128 / 256 x 256: 4: 42 / 45 / 57, 16: 48 / 55 / 77,
+    //   32: 58 / 59 / 80, 64: 76 / 59 / 83, 128: 118 / 75 / 83, 256: 201 / 110 /
+    //   106, 512: 370 / 184 / 153.
+    const int64_t mean = rows / s.E;
+    if (glu) {
+        if (mean <= 12)
+            return run_tail<32, 256, 32, 64, 128, 3, 32, true>(a, tail, st);
+        if (mean <= 96)
+            return run_tail<64, 256, 64, 64, 128, 3, 32, true>(a, tail, st);
+        return run_tail<256, 256, 128, 64, 128, 2, 64, true>(a, tail, st);
+    }
+    if (mean <= 24)
+        return run_tail<32, 128, 32, 32, 128, 6, 32, false>(a, tail, st);
+    if (mean <= 224)
+        return run_tail<128, 128, 64, 32, 128, 3, 32, false>(a, tail, st);
+    return run_tail<256, 256, 128, 64, 128, 2, 32, false>(a, tail, st);
 }
 
 }  // namespace moonep

@@ -125,7 +125,7 @@ __device__ __forceinline__ int32_t scan_tiles(const SegTables &t, int32_t nseg, 
     if (threadIdx.x == 0)
         seg_start[nseg] = total;
     __syncthreads();
-    return total;
+    return __builtin_amdgcn_readfirstlane(total);  // the same in every lane
 }
 
 // Segment that holds tile t: the last s with seg_start[s] <= t, for nseg <=
