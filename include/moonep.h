@@ -354,7 +354,8 @@ int moonep_expert_gemm(const moonep_shape *shape, const int32_t *plan, const int
  * order that the shape fixes: the same inputs give the same bits.
  *
  * workspace: moonep_router_workspace_bytes, 16-byte aligned, no initial
- * contents needed; one call at a time uses it.  Limits (MOONEP_ERR_ARG): an
+ * contents needed; one call at a time uses it.  The outputs and the workspace
+ * must not overlap the logits or each other.  Limits (MOONEP_ERR_ARG): an
  * unknown score or logits type, groups < 1, R*S % groups != 0,
  * groups > 2^20 or groups * E > 2^24, a scale that is not finite.
  */
@@ -391,7 +392,7 @@ int moonep_router(const moonep_shape *shape, const moonep_router_opts *opts, con
  *   d_logits_e = ds_e s_e (softmax) or ds_e s_e (1 - s_e) (sigmoid),
  * rounded once to the logits' type.  The counts are constants: choosing has no
  * gradient.  Masked experts and all-masked tokens get 0.  d_logits must not
- * overlap logits.
+ * overlap an input.
  */
 int moonep_router_bwd(const moonep_shape *shape, const moonep_router_opts *opts,
                       const void *logits, const int32_t *topk_idx, const int32_t *counts,

@@ -120,6 +120,26 @@ int shape_status(const moonep_shape *s)
 int64_t n_entries(const moonep_shape *s) { return (int64_t)s->R * s->S * s->K; }
 int64_t n_tokens(const moonep_shape *s) { return (int64_t)s->R * s->S; }
 
+struct Range {
+    const void *p;
+    size_t n;
+};
+
+// An output shares bytes with an input, or with another output.
+template <int NO, int NI>
+bool aliased(const Range (&out)[NO], const Range (&in)[NI])
+{
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+                return true;
+        for (int q = 0; q < o; ++q)
+            if (overlap(out[o].p, out[o].n, out[q].p, out[q].n))
+                return true;
+    }
+    return false;
+}
+
 // Pointers may be NULL only when the array they name is empty.
 bool present(const void *p, int64_t n) { return p != nullptr || n == 0; }
 
@@ -486,16 +506,15 @@ int expert_quant(const moonep_shape *shape, const int32_t *plan, const int32_t *
     if (!aligned(plan, 4) || !aligned(wslot, 4) || !aligned(x8, 16) || !aligned(xs, 4) ||
         !aligned(out, 16) || !aligned(out_scales, 4) || !aligned(w_home, 16) || !aligned(pool, 16))
         return MOONEP_ERR_MISALIGNED;
-    const void *in[] = {x8, xs, w_home, pool};
-    const size_t in_bytes[] = {(size_t)rows * in_dim, (size_t)rows * scale_row_bytes(in_dim),
-                               (size_t)shape->E * (size_t)w_stride,
-                               (size_t)pool_rows * (size_t)w_stride};
-    const size_t ob = (size_t)rows * (size_t)out_row;
-    const size_t sb = out_scales ? (size_t)rows * scale_row_bytes(out_dim) : 0;
-    for (int i = 0; i < 4; ++i)
-        if (overlap(out, ob, in[i], in_bytes[i]) || overlap(out_scales, sb, in[i], in_bytes[i]))
-            return MOONEP_ERR_ALIAS;
-    if (overlap(out, ob, out_scales, sb))
+    const Range out_r[] = {{out, (size_t)rows * (size_t)out_row},
+                           {out_scales, out_scales ? (size_t)rows * scale_row_bytes(out_dim) : 0}};
+    const Range in_r[] = {{x8, (size_t)rows * in_dim},
+                          {xs, (size_t)rows * scale_row_bytes(in_dim)},
+                          {w_home, (size_t)shape->E * (size_t)w_stride},
+                          {pool, (size_t)pool_rows * (size_t)w_stride},
+                          {plan, moonep_plan_bytes(shape)},
+                          {wslot, (size_t)(shape->E + shape->R) * 4}};
+    if (aliased(out_r, in_r))
         return MOONEP_ERR_ALIAS;
     if (rows == 0)
         return MOONEP_OK;
@@ -530,9 +549,13 @@ int moonep_router(const moonep_shape *shape, const moonep_router_opts *opts, con
         return MOONEP_ERR_MISALIGNED;
     if (some && workspace_bytes < router_workspace(*shape, opts->groups))
         return MOONEP_ERR_WORKSPACE;
-    const size_t lb = (size_t)n_tokens(shape) * shape->E * (opts->logits_type == MOONEP_BF16 ? 2 : 4);
-    if (overlap(topk_idx, nk * 4, logits, lb) || overlap(gates, nk * 4, logits, lb) ||
-        overlap(topk_idx, nk * 4, gates, nk * 4))
+    const size_t table = some ? (size_t)opts->groups * shape->E * 4 : 0;
+    const Range in[] = {{logits, (size_t)n_tokens(shape) * shape->E *
+                                     (opts->logits_type == MOONEP_BF16 ? 2 : 4)}};
+    const Range out[] = {{topk_idx, (size_t)nk * 4}, {gates, (size_t)nk * 4}, {counts, table},
+                         {prob_sum, table}, {loss, some ? (size_t)4 : 0},
+                         {workspace, some ? router_workspace(*shape, opts->groups) : 0}};
+    if (aliased(out, in))
         return MOONEP_ERR_ALIAS;
     return launch_router(*shape, *opts, logits, topk_idx, gates, counts, prob_sum, loss, workspace,
                          (hipStream_t)stream);
@@ -554,8 +577,11 @@ int moonep_router_bwd(const moonep_shape *shape, const moonep_router_opts *opts,
         !aligned(counts, 4) || !aligned(d_gates, 4) || !aligned(d_loss, 4))
         return MOONEP_ERR_MISALIGNED;
     const size_t lb = (size_t)n_tokens(shape) * shape->E * la;
-    if (overlap(d_logits, lb, logits, lb) || overlap(d_logits, lb, topk_idx, nk * 4) ||
-        overlap(d_logits, lb, d_gates, d_gates ? nk * 4 : 0))
+    const Range in[] = {{logits, lb}, {topk_idx, (size_t)nk * 4},
+                        {counts, counts ? (size_t)opts->groups * shape->E * 4 : 0},
+                        {d_gates, d_gates ? (size_t)nk * 4 : 0}, {d_loss, d_loss ? (size_t)4 : 0}};
+    const Range out[] = {{d_logits, lb}};
+    if (aliased(out, in))
         return MOONEP_ERR_ALIAS;
     return launch_router_bwd(*shape, *opts, logits, topk_idx, counts, d_gates, d_loss, d_logits,
                              (hipStream_t)stream);
@@ -580,20 +606,13 @@ int moonep_rmsnorm_quant(const moonep_shape *shape, const uint16_t *x, const uin
         !aligned(y_out, 16) || !aligned(y8, 16) || !aligned(ys, 4))
         return MOONEP_ERR_MISALIGNED;
     const size_t row = (size_t)n * shape->H * 2, wb = (size_t)shape->H * 2;
-    const void *in[] = {x, res, weight};
-    const size_t in_bytes[] = {row, res ? row : 0, wb};
-    const void *out[] = {res_out, y_out, y8, ys};
-    const size_t out_bytes[] = {res_out ? row : 0, y_out ? row : 0, row / 2,
-                                (size_t)n * scale_row_bytes(shape->H)};
-    for (int o = 0; o < 4; ++o) {
-        for (int i = 0; i < 3; ++i)
-            if (!(o == 0 && i < 2 && out[o] == in[i]) &&
-                overlap(out[o], out_bytes[o], in[i], in_bytes[i]))
-                return MOONEP_ERR_ALIAS;
-        for (int p = 0; p < o; ++p)
-            if (overlap(out[o], out_bytes[o], out[p], out_bytes[p]))
-                return MOONEP_ERR_ALIAS;
-    }
+    // the sum may go over x or res, whole rows over themselves
+    const Range in[] = {{res_out == x ? nullptr : x, res_out == x ? 0 : row},
+                        {res, res && res_out != res ? row : 0}, {weight, wb}};
+    const Range out[] = {{res_out, res_out ? row : 0}, {y_out, y_out ? row : 0}, {y8, row / 2},
+                         {ys, (size_t)n * scale_row_bytes(shape->H)}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
     return launch_rmsnorm_quant(*shape, x, res, weight, eps, res_out, y_out, y8, ys,
                                 (hipStream_t)stream);
 }
@@ -614,12 +633,9 @@ int moonep_dispatch_quant(const moonep_shape *shape, const uint8_t *x8, const ui
         !aligned(slot_of, 4))
         return MOONEP_ERR_MISALIGNED;
     const size_t row = (size_t)shape->H, sr = (size_t)scale_row_bytes(shape->H);
-    const void *in[] = {x8, xs, slot_of};
-    const size_t in_bytes[] = {nt * row, nt * sr, (size_t)nk * 4};
-    for (int i = 0; i < 3; ++i)
-        if (overlap(buf8, nk * row, in[i], in_bytes[i]) || overlap(bufs, nk * sr, in[i], in_bytes[i]))
-            return MOONEP_ERR_ALIAS;
-    if (overlap(buf8, nk * row, bufs, nk * sr))
+    const Range in[] = {{x8, nt * row}, {xs, nt * sr}, {slot_of, (size_t)nk * 4}};
+    const Range out[] = {{buf8, nk * row}, {bufs, nk * sr}};
+    if (aliased(out, in))
         return MOONEP_ERR_ALIAS;
     return launch_dispatch_quant(*shape, x8, xs, slot_of, buf8, bufs, (hipStream_t)stream);
 }

@@ -483,3 +483,50 @@ def test_products_full_size():
             assert not torch.isnan(y).any()
             off = np.abs(f64(bits(y[rd])) - want)
             assert (off <= np.abs(want) * 2.0 ** -8 + 2 * inp * 2.0 ** -23 * a).all()
+
+
+def test_far_rows():
+    """Rows more than 2^32 bytes into their arrays: norm, dispatch and a product, on the first, some middle and the
+    last rows."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    N, K, H, F = (1 << 20) + 5, 2, 2064, 16
+    s = mx.Shape(1, 2, N, K, H)
+    rows = torch.tensor([0, 1, N // 2, N - 2, N - 1], device="cuda")
+    print("[case] far rows", flush=True)
+    x = torch.randn((N, H), generator=g, device="cuda", dtype=torch.bfloat16)      # 4.3 GB
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    y8 = torch.zeros((N, H), dtype=torch.uint8, device="cuda")
+    ys = torch.zeros((N, scale_bytes(H)), dtype=torch.uint8, device="cuda")
+    mx.moonep_rmsnorm_quant(s, x, None, w, 1e-6, None, None, y8, ys)
+    v = x[rows].double().cpu().numpy()
+    want = v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6)
+    check_rows(host(y8[rows]), host(ys[rows]), want, np.abs(want) * (H + 8) * 2.0 ** -24)
+    del x
+    # every token to both experts, in either order
+    topk = torch.stack([torch.arange(N, device="cuda") % 2, (torch.arange(N, device="cuda") + 1) % 2], 1).int().reshape(-1)
+    b = mx.allocate(mx.Shape(1, 2, N, K, 8))
+    mx.plan_step(b, topk.contiguous())
+    buf8 = torch.zeros((N * K, H), dtype=torch.uint8, device="cuda")               # 4.3 GB
+    bufs = torch.zeros((N * K, scale_bytes(H)), dtype=torch.uint8, device="cuda")
+    mx.moonep_dispatch_quant(s, y8, ys, b.slot_of, buf8, bufs)
+    assert int(b.slot_of.max()) == N * K - 1
+    for k in range(K):
+        at = b.slot_of.view(N, K)[rows, k].long()
+        assert torch.equal(buf8[at], y8[rows]) and torch.equal(bufs[at], ys[rows])
+    rng = np.random.default_rng(7)
+    w_home, wins = weight_rows(rng, 2, [(F, H)], False)
+    ws = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    y = torch.full((N * K, F), float("nan"), dtype=torch.bfloat16, device="cuda")
+    mx.moonep_expert_gemm_quant(s, b.plan, ws, 0, H, F, buf8, bufs, to_dev(w_home), None, w_home.shape[1], *wins[0], y)
+    torch.cuda.synchronize()
+    assert not torch.isnan(y).any()
+    code, scale = wins[0]
+    for k in range(K):
+        at = b.slot_of.view(N, K)[rows, k].long()
+        got = f64(bits(y[at]))
+        xv = values(host(buf8[at]), host(bufs[at]))
+        for i, e in enumerate(topk.view(N, K)[rows, k].cpu().tolist()):
+            wv = weight_values(w_home[e, code:code + F * H].reshape(F, H),
+                               w_home[e, scale:scale + scale_bytes(H)].reshape(1, -1))
+            o, a = wv @ xv[i], np.abs(wv) @ np.abs(xv[i])
+            assert (np.abs(got[i] - o) <= np.abs(o) * 2.0 ** -8 + 2 * H * 2.0 ** -23 * a).all()

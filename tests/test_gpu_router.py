@@ -348,3 +348,55 @@ def test_shared_leading_bits():
         for score in (SOFT, SIG):
             got = forward(mx.Shape(1, E, 37, K, 16), mx.RouterOpts(score, True), torch.from_numpy(l).cuda())
             np.testing.assert_array_equal(got["ids"].reshape(37, K), order(l.astype(np.float64), K))
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+def test_unaligned_logits(bf16):
+    """Rows that start on no vector: logits and d_logits one element into their allocations."""
+    rng = np.random.default_rng(15)
+    s, opts = mx.Shape(2, 64, 21, 6, 16), mx.RouterOpts(SOFT, True, 2, int(bf16))
+    t, l = logits_for(rng, s.N, s.E, bf16)
+    dg = to_dev(rng.standard_normal(s.NK).astype(np.float32))
+
+    def both(shift):
+        buf = torch.zeros(s.N * s.E + 8, dtype=t.dtype, device="cuda")
+        out = torch.full_like(buf, float("nan"))
+        d, o = buf[shift:shift + s.N * s.E].view(s.N, s.E), out[shift:shift + s.N * s.E].view(s.N, s.E)
+        d.copy_(t)
+        got = forward(s, opts, d)
+        mx.moonep_router_bwd(s, opts, d, to_dev(got["ids"]), to_dev(got["counts"]), dg, torch.ones(1, device="cuda"), o)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[:shift]).all() and torch.isnan(out[shift + s.N * s.E:]).all()
+        return got, o.float().cpu().numpy()
+
+    a, b = both(0), both(1)
+    for k in a[0]:
+        np.testing.assert_array_equal(a[0][k], b[0][k], err_msg=k)
+    np.testing.assert_array_equal(a[1], b[1])
+
+
+def test_logits_far_into_memory():
+    """More than 2^31 elements of logits: offsets past 32 bits, checked on the last rows."""
+    s, opts = mx.Shape(1, 1024, (1 << 21) + 77, 2, 16), mx.RouterOpts(SOFT, False, 1, mx.BF16)
+    d = torch.zeros((s.N, s.E), dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1 << 20, s.N - 2, s.N - 1]
+    rng = np.random.default_rng(16)
+    v = rng.standard_normal((len(rows), s.E)).astype(np.float32)
+    for r, x in zip(rows, v):
+        d[r] = torch.from_numpy(x).cuda()
+    ids = torch.empty(s.NK, dtype=torch.int32, device="cuda")
+    gates = torch.empty(s.NK, device="cuda")
+    mx.moonep_router(s, opts, d, ids, gates)
+    d_l = torch.empty_like(d)
+    dg = torch.ones(s.NK, device="cuda")
+    mx.moonep_router_bwd(s, opts, d, ids, None, dg, None, d_l)
+    torch.cuda.synchronize()
+    l = d[rows].double().cpu().numpy()
+    want = order(l, 2)
+    np.testing.assert_array_equal(ids.view(-1, 2)[rows].cpu().numpy(), want)
+    assert (ids.view(-1, 2)[5].cpu().numpy() == [0, 1]).all()
+    ref = Ref(l, want, opts, 1)
+    np.testing.assert_allclose(gates.view(-1, 2)[rows].cpu().numpy(), ref.gates, rtol=2 * ref.rel)
+    g, mag = ref.grad(np.ones((len(rows), 2)), 0.0)
+    off = np.abs(d_l[rows].double().cpu().numpy() - g)
+    assert (off <= np.abs(g) * 2.0 ** -8 + mag * (4 * ref.rel + 32 * 2.0 ** -24) + 2.0 ** -126).all()

@@ -63,12 +63,15 @@ def test_router_refusals(L):
     assert call(ws=vp(FAKE * 7 + 8)) == MISALIGNED and call(g=vp(FAKE * 3 + 1)) == MISALIGNED
     assert call(n=need - 1) == WORKSPACE
     assert call(ids=vp(FAKE + 4 * 100)) == ALIAS and call(g=vp(FAKE * 2 + 4)) == ALIAS
+    assert call(c=vp(FAKE + 64)) == ALIAS and call(p=at(3)) == ALIAS and call(ls=at(4)) == ALIAS
+    assert call(ws=vp(FAKE + 4096)) == ALIAS and call(ws=vp(FAKE * 6)) == ALIAS
     back = lambda lg=at(0), ids=at(1), c=at(2), dg=at(3), dl=at(4), out=at(5): \
         L.moonep_router_bwd(B(s), B(o), lg, ids, c, dg, dl, out, None)  # noqa: E731
     assert back(lg=None) == NULL and back(ids=None) == NULL and back(out=None) == NULL
     assert back(c=None) == NULL and back(dl=None) == NULL
     assert back(out=vp(FAKE * 6 + 2)) == MISALIGNED
     assert back(out=at(0)) == ALIAS and back(out=at(3)) == ALIAS and back(out=at(1)) == ALIAS
+    assert back(out=at(2)) == ALIAS and back(out=at(4)) == ALIAS
 
 
 def test_norm_refusals(L):
@@ -84,7 +87,7 @@ def test_norm_refusals(L):
     assert call(x=vp(FAKE + 8)) == MISALIGNED and call(ys=vp(FAKE * 7 + 2)) == MISALIGNED
     assert call(y=at(0)) == ALIAS and call(y8=at(1)) == ALIAS and call(ys=vp(FAKE * 6 + 64)) == ALIAS
     assert call(ro=vp(FAKE + 128)) == ALIAS                    # over x, but not x itself
-    assert call(ro=at(2)) == ALIAS
+    assert call(ro=at(2)) == ALIAS and call(ro=at(4)) == ALIAS and call(ro=at(0), y=at(0)) == ALIAS
 
 
 def test_dispatch_refusals(L):
@@ -140,6 +143,8 @@ def test_product_refusals(L, glu):
         assert call(**{k: None}) == NULL, k
     assert call(x8=vp(FAKE * 3 + 8)) == MISALIGNED and call(xs=vp(FAKE * 4 + 2)) == MISALIGNED
     assert call(y=vp(FAKE * 7 + 8)) == MISALIGNED and call(wh=vp(FAKE * 5 + 8)) == MISALIGNED
+    assert call(out=(1 << 22) + 16, st=1 << 40) == ARG
+    assert call(y=at(0)) == ALIAS and call(y=at(1)) == ALIAS
     assert call(y=at(2)) == ALIAS and call(y=vp(FAKE * 5 + 64)) == ALIAS and call(y=at(5)) == ALIAS and call(y=at(3)) == ALIAS
     if glu:
         assert call(hs=None) == NULL and call(hs=vp(FAKE * 8 + 2)) == MISALIGNED
