@@ -37,7 +37,7 @@ constexpr int kCuLds = 160 * 1024;
 constexpr int kSegBytesMax = (2 * kMaxExperts + kMaxRanks + 1) * 4;  // seg_start of the largest shape
 constexpr int kTileGroup = 8;  // row tiles per item group, as in the bf16 product
 
-template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU>
+template <int BM, int BN, int WM, int WN, int BK, int S, bool GLU>
 struct QCfg {
     static constexpr int kBK = BK;                    // k per stage, in bytes
     static constexpr int kCpr = BK / 16;              // 16-byte chunks of a row
@@ -59,25 +59,21 @@ struct QCfg {
     static constexpr int kScaleBytes = kScaleWaves * 256;
     static constexpr int kScaleAt = S * kStageBytes;
     static constexpr int kOutCols = GLU ? BN / 2 : BN;
-    // Epilogue: for an 8-bit output the waves' row maxima, and a band of EB rows
-    // on its way out, apart from the ring, which is loading the next item.
+    // Epilogue, apart from the ring, which is loading the next item: for an 8-bit
+    // output the waves' row maxima, for bf16 a band of 32 rows on its way out.
     static constexpr int kOutBytes = GLU ? 1 : 2;
-    static constexpr int kLdoBytes = kOutCols * kOutBytes + 16;
+    static constexpr int kBands = BM / 32, kBandRowBytes = BN * 2 + 16;
+    static constexpr int kBandStores = 32 * (BN / 8) / kThreads;
     static constexpr int kOutAt = kScaleAt + S * kScaleBytes;
-    static constexpr int kMaxAt = kOutAt + EB * kLdoBytes;
-    static constexpr int kSegAt = kMaxAt + (GLU ? BM * kWN * 4 : 0);
-    static constexpr int kBandRows = EB, kBands = BM / EB;
-    static constexpr int kVecPerRow = kOutCols * kOutBytes / 16;
-    static constexpr int kOIter = kBandRows * kVecPerRow / kThreads;
+    static constexpr int kSegAt = kOutAt + (GLU ? BM * kWN * 4 : 32 * kBandRowBytes);
     static_assert(BK == 64 || BK == 128, "one or two matrix instructions, one scale");
     static_assert(BM % (kRpi * kWavesG) == 0 && BN % (kRpi * kWavesG) == 0, "rows per DMA round");
     static_assert(kScaleWaves <= kWavesG, "a thread for every scale");
-    static_assert(kBandRows % 32 == 0 && WM % kBandRows == 0, "bands of whole row tiles");
-    static constexpr int kStores = kBands * kOIter;  // of rows, per wave and item
+    static constexpr int kStores = GLU ? kTM : kBands * kBandStores;  // of rows, per wave and item
     static_assert((S - 1) * kPerStage + kStores <= 63, "outstanding accesses must fit vmcnt");
+    static_assert(GLU || (kBandStores >= 1 && 32 * (BN / 8) % kThreads == 0), "whole stores of a band");
     static_assert(!GLU || (kOutCols == kQuantBlock && kTN == 2), "gate and up in one wave, one block");
     static_assert(kSegAt + kSegBytesMax <= kCuLds, "LDS");
-    static_assert(kOIter >= 1 && kBandRows * kVecPerRow % kThreads == 0, "epilogue split");
     // rows whose chunks share the banks: two of 128 bytes, four of 64
     __device__ static constexpr int swz(int r) { return BK == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
 };
@@ -107,6 +103,14 @@ __device__ __forceinline__ int64_t uniform(int64_t v)
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// Lanes 32 .. 63 of `a` for lanes 0 .. 31 of `b`.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
 // One LDS-DMA load: kBytes of each lane to dst + lane * kBytes.
 template <int kBytes>
 __device__ __forceinline__ void dma(const uint8_t *src, char *dst)
@@ -120,11 +124,11 @@ __device__ __forceinline__ void dma(const uint8_t *src, char *dst)
 
 }  // namespace
 
-template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU, bool TAIL>
-__global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) void expert_quant_kernel(
+template <int BM, int BN, int WM, int WN, int BK, int S, bool GLU, bool TAIL>
+__global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void expert_quant_kernel(
     QuantGemmArgs a)
 {
-    using G = QCfg<BM, BN, WM, WN, BK, S, EB, GLU>;
+    using G = QCfg<BM, BN, WM, WN, BK, S, GLU>;
     extern __shared__ __align__(16) char lds_b[];
     int32_t *seg_start = (int32_t *)(lds_b + G::kSegAt);
     __shared__ int scan_tmp[G::kWavesG];
@@ -328,13 +332,20 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
         m0 = uniform(m0);
         mrows = __builtin_amdgcn_readfirstlane(mrows);
         n0 = __builtin_amdgcn_readfirstlane(n0);
-        char *so = lds_b + G::kOutAt;
         // the tile's rows, from its first column to the end of its last row
         const auto out = __builtin_amdgcn_make_buffer_rsrc(
             (char *)a.out + (m0 * a.out_dim + n0) * G::kOutBytes, 0,
             (int)((uint32_t)(mrows * a.out_dim - n0) * G::kOutBytes), 0x00020000);
-        float *row_max = (float *)(lds_b + G::kMaxAt);  // [BM][kWN]
+        // 16 bytes of row `row` from column `col` of the item on.  A buffer store
+        // drops what is out of bounds, so every wave issues the same number: rows
+        // past the tile end behind the buffer, and columns past the row are sent there.
+        auto store = [&](int row, int col, const u32x4 &v) {
+            const uint32_t at = n0 + col < a.out_dim ? (uint32_t)(row * a.out_dim + col) * G::kOutBytes
+                                                     : 0xFFFFFFF0u;
+            __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)at, 0, 0);
+        };
         if constexpr (GLU) {
+            float *row_max = (float *)(lds_b + G::kOutAt);  // [BM][kWN]
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i) {
 #pragma unroll
@@ -357,60 +368,57 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
                     row_max[(wm * WM + i * 32 + fr) * G::kWN + wn] = __uint_as_float(m);
             }
             lds_barrier();
-        }
-#pragma unroll
-        for (int band = 0; band < G::kBands; ++band) {
-            if (band)
-                lds_barrier();  // the band before has been read
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i) {
-                if (wm * (WM / G::kBandRows) + i * 32 / G::kBandRows != band)
-                    continue;
                 const int row = wm * WM + i * 32 + fr;
-                char *to = so + (row - band * G::kBandRows) * G::kLdoBytes;
-                if constexpr (GLU) {
-                    uint32_t m = 0;
+                uint32_t m = 0;
 #pragma unroll
-                    for (int q = 0; q < G::kWN; ++q)
-                        m = max(m, __float_as_uint(row_max[row * G::kWN + q]));
-                    const uint32_t byte = scale_byte(m);
-                    const float inv = inverse_scale(byte);
+                for (int q = 0; q < G::kWN; ++q)
+                    m = max(m, __float_as_uint(row_max[row * G::kWN + q]));
+                const uint32_t byte = scale_byte(m);
+                const float inv = inverse_scale(byte);
+                uint32_t d[4];
 #pragma unroll
-                    for (int q = 0; q < 16; q += 4)
-                        *(uint32_t *)(to + wn * 32 + q * 2 + fhalf * 4) =
-                            pack_e4m3(acc[i][0][q], acc[i][0][q + 1], acc[i][0][q + 2],
-                                      acc[i][0][q + 3], inv, byte);
-                    if (wn == 0 && fhalf == 0 && row < mrows) {
-                        uint8_t *dst = a.out_scales + (m0 + row) * SO;
-                        const int32_t nb = n0 / kQuantBlock;
-                        dst[nb] = (uint8_t)byte;
-                        if (nb == nbn - 1)
-                            for (int32_t p = nbn; p < SO; ++p)
-                                dst[p] = 127;
-                    }
-                } else {
+                for (int q = 0; q < 4; ++q)
+                    d[q] = pack_e4m3(acc[i][0][4 * q], acc[i][0][4 * q + 1], acc[i][0][4 * q + 2],
+                                     acc[i][0][4 * q + 3], inv, byte);
+                // the lower lanes take the row's columns 0 .. 15, the upper 16 .. 31
+                swap_halves(d[0], d[2]);
+                swap_halves(d[1], d[3]);
+                store(row, wn * 32 + fhalf * 16, u32x4{d[0], d[2], d[1], d[3]});
+                if (wn == 0 && fhalf == 0 && row < mrows) {
+                    uint8_t *dst = a.out_scales + (m0 + row) * SO;
+                    const int32_t nb = n0 / kQuantBlock;
+                    dst[nb] = (uint8_t)byte;
+                    if (nb == nbn - 1)
+                        for (int32_t p = nbn; p < SO; ++p)
+                            dst[p] = 127;
+                }
+            }
+        } else {
+            char *so = lds_b + G::kOutAt;
+#pragma unroll
+            for (int band = 0; band < G::kBands; ++band) {
+                if (band)
+                    lds_barrier();  // the band before has been read
+#pragma unroll
+                for (int i = 0; i < G::kTM; ++i) {
+                    if (wm * G::kTM + i != band)
+                        continue;
 #pragma unroll
                     for (int j = 0; j < G::kTN; ++j)
 #pragma unroll
                         for (int q = 0; q < 16; q += 4)
-                            *(u32x2 *)(to + (wn * WN + j * 32 + q * 2 + fhalf * 4) * 2) =
+                            *(u32x2 *)(so + fr * G::kBandRowBytes + (wn * WN + j * 32 + q * 2 + fhalf * 4) * 2) =
                                 u32x2{pack_bf16(acc[i][j][q], acc[i][j][q + 1]),
                                       pack_bf16(acc[i][j][q + 2], acc[i][j][q + 3])};
                 }
-            }
-            lds_barrier();
+                lds_barrier();
 #pragma unroll
-            for (int v = 0; v < G::kOIter; ++v) {
-                const int idx = tid + v * G::kThreads;
-                const int row = idx / G::kVecPerRow, c = idx % G::kVecPerRow;
-                const int grow = band * G::kBandRows + row;
-                // A buffer store drops what is out of bounds, so every wave issues
-                // the same number: rows past the tile end behind the buffer, and
-                // columns past the row are sent there.
-                const bool in = n0 + c * (16 / G::kOutBytes) < a.out_dim;
-                const uint32_t at = in ? (uint32_t)(grow * a.out_dim) * G::kOutBytes + c * 16 : 0xFFFFFFF0u;
-                __builtin_amdgcn_raw_buffer_store_b128(*(const u32x4 *)(so + row * G::kLdoBytes + c * 16),
-                                                       out, (int)at, 0, 0);
+                for (int v = 0; v < G::kBandStores; ++v) {
+                    const int idx = tid + v * G::kThreads, row = idx / (BN / 8), c = idx % (BN / 8);
+                    store(band * 32 + row, c * 8, *(const u32x4 *)(so + row * G::kBandRowBytes + c * 16));
+                }
             }
         }
     }
@@ -419,11 +427,11 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, EB, GLU>::kThreads)) v
 
 namespace {
 
-template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU, bool TAIL>
+template <int BM, int BN, int WM, int WN, int BK, int S, bool GLU, bool TAIL>
 int run_quant(const QuantGemmArgs &a, hipStream_t st)
 {
-    using G = QCfg<BM, BN, WM, WN, BK, S, EB, GLU>;
-    const auto kernel = expert_quant_kernel<BM, BN, WM, WN, BK, S, EB, GLU, TAIL>;
+    using G = QCfg<BM, BN, WM, WN, BK, S, GLU>;
+    const auto kernel = expert_quant_kernel<BM, BN, WM, WN, BK, S, GLU, TAIL>;
     const size_t lds = G::kSegAt + (size_t)(a.seg.E + a.seg.pl.cap + 1) * 4;
     int dev = 0, cus = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
@@ -444,11 +452,11 @@ int run_quant(const QuantGemmArgs &a, hipStream_t st)
 }
 
 // TAIL: the last k-step is part of one.
-template <int BM, int BN, int WM, int WN, int BK, int S, int EB, bool GLU>
+template <int BM, int BN, int WM, int WN, int BK, int S, bool GLU>
 int run_tail(const QuantGemmArgs &a, bool tail, hipStream_t st)
 {
-    return tail ? run_quant<BM, BN, WM, WN, BK, S, EB, GLU, true>(a, st)
-                : run_quant<BM, BN, WM, WN, BK, S, EB, GLU, false>(a, st);
+    return tail ? run_quant<BM, BN, WM, WN, BK, S, GLU, true>(a, st)
+                : run_quant<BM, BN, WM, WN, BK, S, GLU, false>(a, st);
 }
 
 }  // namespace
@@ -491,16 +499,16 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
     const int64_t mean = rows / s.E;
     if (glu) {
         if (mean <= 12)
-            return run_tail<32, 256, 32, 64, 128, 3, 32, true>(a, tail, st);
+            return run_tail<32, 256, 32, 64, 128, 3, true>(a, tail, st);
         if (mean <= 96)
-            return run_tail<64, 256, 64, 64, 128, 3, 32, true>(a, tail, st);
-        return run_tail<256, 256, 128, 64, 128, 2, 64, true>(a, tail, st);
+            return run_tail<64, 256, 64, 64, 128, 3, true>(a, tail, st);
+        return run_tail<256, 256, 128, 64, 128, 2, true>(a, tail, st);
     }
     if (mean <= 24)
-        return run_tail<32, 128, 32, 32, 128, 6, 32, false>(a, tail, st);
+        return run_tail<32, 128, 32, 32, 128, 6, false>(a, tail, st);
     if (mean <= 224)
-        return run_tail<128, 128, 64, 32, 128, 3, 32, false>(a, tail, st);
-    return run_tail<256, 256, 128, 64, 128, 2, 32, false>(a, tail, st);
+        return run_tail<128, 128, 64, 32, 128, 3, false>(a, tail, st);
+    return run_tail<256, 256, 128, 64, 128, 2, false>(a, tail, st);
 }
 
 }  // namespace moonep
