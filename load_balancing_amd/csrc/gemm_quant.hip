@@ -139,7 +139,12 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
     const int32_t nseg = a.seg.E + a.seg.n_rep();
     const int32_t tiles = scan_tiles<BM, G::kWavesG>(a.seg, nseg, seg_start, scan_tmp);
     const int32_t nbn = (a.out_dim + G::kOutCols - 1) / G::kOutCols;
-    const int64_t items = (int64_t)tiles * nbn;
+    // Items of whole tiles; those of the last round are halves of a tile's rows where
+    // that still makes one round.  (32 bits: 2^31 items of 32 x 128 values at
+    // least would be over 8 TB of output.)
+    const uint32_t tile_items = (uint32_t)tiles * (uint32_t)nbn, rest = tile_items % gridDim.x;
+    const uint32_t halves = G::kWM == 2 && 2 * rest <= gridDim.x ? rest : 0;
+    const uint32_t whole = tile_items - halves, items = tile_items + halves;
     const int32_t nk = (a.in_dim + G::kBK - 1) / G::kBK;
     const int32_t SB = scale_row_bytes(a.in_dim), SO = scale_row_bytes(a.out_dim);
 
@@ -149,14 +154,15 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
     // block, or for gate and up column (r / 64) * 32 + r % 32 of gate (r / 32
     // even) or up, which one load never mixes.
     struct Load {
-        int64_t it, m0;
+        uint32_t it;
+        int64_t m0;
         int32_t kt, mrows, n0;
         const uint8_t *a_base, *b_base[2];  // the item's first row; first column, of each matrix
         const uint8_t *scale;  // this thread's
         uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
     };
     Load ld;
-    const int64_t first = xcd_slot((int)blockIdx.x, (int)gridDim.x);
+    const uint32_t first = (uint32_t)xcd_slot((int)blockIdx.x, (int)gridDim.x);
     if (first >= items)
         return;
     ld.it = first;
@@ -165,15 +171,22 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
     auto b_mat = [&](int v) { return GLU ? (v * G::kWavesG + wave) * G::kRpi / 32 % 2 : 0; };
     auto chunk = [&](int v) { return (dma_pos ^ G::swz(a_row(v))) << 4; };
     // First row and column of an item, its rows and its weights.
-    auto locate = [&](int64_t it, int64_t *m0, int32_t *mrows, int32_t *n0) -> const uint8_t * {
-        int32_t t, nb, n;
+    auto locate = [&](uint32_t it, int64_t *m0, int32_t *mrows, int32_t *n0) -> const uint8_t * {
+        int32_t t, nb, n, row0 = 0, most = BM;
+        if (it >= whole) {
+            row0 = (it - whole) % 2 * (BM / 2);
+            most = BM / 2;
+            it = whole + (it - whole) / 2;
+        }
         item_of<kTileGroup>(it, tiles, nbn, &t, &nb);
         const int32_t s = find_segment(seg_start, nseg, t);
         const int32_t mt = t - __builtin_amdgcn_readfirstlane(seg_start[s]);
         int64_t wrow;
         bool pooled;
         *m0 = a.seg.segment(s, &n, &wrow, &pooled) + (int64_t)mt * BM;
-        *mrows = n - mt * BM < BM ? n - mt * BM : BM;
+        const int32_t left = n - mt * BM - row0;
+        *mrows = left < 0 ? 0 : left < most ? left : most;  // 0: a short tile's second half
+        *m0 += left > 0 ? row0 : 0;
         *n0 = nb * G::kOutCols;
         return (pooled ? a.pool : a.w_home) + wrow * a.w_stride;
     };
@@ -256,11 +269,14 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
     for (int st = 0; st < S; ++st)
         issue(st);
 
-    for (int64_t it = first; it < items; it += gridDim.x) {
+    for (uint32_t it = first; it < items; it += gridDim.x) {
         int64_t m0 = ld.m0;
         int32_t mrows = ld.mrows, n0 = ld.n0;
         if (ld.it != it)
             locate(it, &m0, &mrows, &n0);  // few k-steps: the loads are at a later item already
+        m0 = uniform(m0);
+        mrows = __builtin_amdgcn_readfirstlane(mrows);
+        n0 = __builtin_amdgcn_readfirstlane(n0);
         f32x16 acc[G::kTM][G::kTN];
 #pragma unroll
         for (int i = 0; i < G::kTM; ++i)
@@ -292,6 +308,8 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
             const int shift = (kt * G::kBK / kQuantBlock & 3) * 8;
             if (kt % G::kScaleStages == G::kScaleStages - 1 || kt == nk - 1)
                 scale_slot = scale_slot + 1 == S ? 0 : scale_slot + 1;
+            if (G::kWM > 1 && wm * WM >= mrows)
+                continue;  // none of this wave's rows
             int sca[G::kTM], scb[G::kTN];
 #pragma unroll
             for (int i = 0; i < G::kTM; ++i)
@@ -329,13 +347,10 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
 
         // ---- epilogue: lane l holds row l % 32 of tile i, and of each column tile
         // the columns 8 (q / 4) + 4 (l / 32) + q % 4 ------------------------------
-        m0 = uniform(m0);
-        mrows = __builtin_amdgcn_readfirstlane(mrows);
-        n0 = __builtin_amdgcn_readfirstlane(n0);
         // the tile's rows, from its first column to the end of its last row
         const auto out = __builtin_amdgcn_make_buffer_rsrc(
             (char *)a.out + (m0 * a.out_dim + n0) * G::kOutBytes, 0,
-            (int)((uint32_t)(mrows * a.out_dim - n0) * G::kOutBytes), 0x00020000);
+            mrows ? (int)((uint32_t)(mrows * a.out_dim - n0) * G::kOutBytes) : 0, 0x00020000);
         // 16 bytes of row `row` from column `col` of the item on.  A buffer store
         // drops what is out of bounds, so every wave issues the same number: rows
         // past the tile end behind the buffer, and columns past the row are sent there.

@@ -155,11 +155,11 @@ __device__ __forceinline__ int xcd_slot(int b, int P)
 
 // Item -> (row tile, column block): groups of GM row tiles, the row tile
 // running fastest inside a group (fewer in the last one).
-template <int GM>
-__device__ __forceinline__ void item_of(int64_t it, int32_t tiles, int32_t nbn, int32_t *t, int32_t *nb)
+template <int GM, class Item>
+__device__ __forceinline__ void item_of(Item it, int32_t tiles, int32_t nbn, int32_t *t, int32_t *nb)
 {
-    const int64_t gi = it / ((int64_t)GM * nbn);
-    const int32_t within = (int32_t)(it - gi * ((int64_t)GM * nbn));
+    const Item gi = it / ((Item)GM * nbn);
+    const int32_t within = (int32_t)(it - gi * ((Item)GM * nbn));
     const int32_t gleft = tiles - (int32_t)gi * GM;
     const int32_t gm = gleft < GM ? gleft : GM;
     *t = (int32_t)gi * GM + within % gm;
