@@ -10,12 +10,32 @@
 //   l % 32, 32 k values each (which 32 is free, as long as A and B agree), and
 //   the byte that scales them; the 32 x 32 result as in the bf16 kernel: lane
 //   l, register q holds row (q / 4) * 8 + (l / 32) * 4 + q % 4, column l % 32.
+// The weights are the first operand, so that a lane holds one token row.
+//
+// Rounding: the accumulators are fp32, but inside one instruction the 8-bit forms
+// (scaled or not, both shapes) cut the sum of their products short: on random
+// codes an rms error of 2^-19 (k = 128) to 2^-21 (k = 2048) of sum |a| |b|, and
+// 2^-18.5 towards zero where all products are positive; bf16 instructions do
+// not.  That is far below the half steps of the outputs (2^-4 of an e4m3 code,
+// 2^-8 of a bf16 value), so no partial sums are taken apart to avoid it.
 //
 // Structure: persistent workgroups walk (row tile, column block) items; K
 // advances 128 at a time (one scale block) through a ring of S LDS stages
 // filled by LDS-DMA, rows of 128 bytes with their 16-byte chunks XOR-swizzled
-// so that 16 consecutive rows' reads fall on different banks; each stage also
-// carries the dword of A scales that its block's byte is taken from.
+// so that 16 consecutive rows' reads fall on different banks; scales go through a
+// ring of their own, a dword for four blocks.  The rings run on from one item to
+// the next, under the epilogue.
+//
+// What bounds it, gate and up of 262144 rows, 2048 -> 2 x 1408 (1424 us, 2.12
+// PFLOP/s; a library product in 8 bits without block scales and segments takes
+// 1264): the tile's loads from the L2 (12.3 GB; alone 1259 us) and the matrix
+// products (without loads 987 us), which overlap but share the power: 1.9 GHz
+// with both, 2.13 without the loads.  Deeper rings of smaller stages, other
+// schedules of the LDS reads and tiles of 128 rows (two workgroups per CU) were all
+// no faster.  At 4 rows an expert (77 us) it is bound by the weights' bytes, 5.6
+// TB/s of them.  One projection of 32576 rows, 1408 -> 2048 (141 us): 20% of the
+// tiles' rows are empty, and the bf16 stores take 25 us that the next item's loads,
+// which return in order behind them, do not hide.
 //
 // Gate and up: the column tile interleaves 32 gate and 32 up columns, so one
 // wave holds both products of an output, and 128 output columns -- one block of
@@ -351,13 +371,12 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
         const auto out = __builtin_amdgcn_make_buffer_rsrc(
             (char *)a.out + (m0 * a.out_dim + n0) * G::kOutBytes, 0,
             mrows ? (int)((uint32_t)(mrows * a.out_dim - n0) * G::kOutBytes) : 0, 0x00020000);
-        // 16 bytes of row `row` from column `col` of the item on.  A buffer store
-        // drops what is out of bounds, so every wave issues the same number: rows
-        // past the tile end behind the buffer, and columns past the row are sent there.
-        auto store = [&](int row, int col, const u32x4 &v) {
-            const uint32_t at = n0 + col < a.out_dim ? (uint32_t)(row * a.out_dim + col) * G::kOutBytes
-                                                     : 0xFFFFFFF0u;
-            __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)at, 0, 0);
+        // Offset of row `row` and column `col` of the item.  A buffer store drops what
+        // is out of bounds, so every wave issues the same number: rows past the tile
+        // end behind the buffer, and columns past the row are sent there.
+        auto place = [&](int row, int col) -> int {
+            const bool in = n0 + col < a.out_dim;
+            return (int)(in ? (uint32_t)(row * a.out_dim) * G::kOutBytes + col * G::kOutBytes : 0xFFFFFFF0u);
         };
         if constexpr (GLU) {
             float *row_max = (float *)(lds_b + G::kOutAt);  // [BM][kWN]
@@ -400,7 +419,8 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
                 // the lower lanes take the row's columns 0 .. 15, the upper 16 .. 31
                 swap_halves(d[0], d[2]);
                 swap_halves(d[1], d[3]);
-                store(row, wn * 32 + fhalf * 16, u32x4{d[0], d[2], d[1], d[3]});
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{d[0], d[2], d[1], d[3]}, out,
+                                                       place(row, wn * 32 + fhalf * 16), 0, 0);
                 if (wn == 0 && fhalf == 0 && row < mrows) {
                     uint8_t *dst = a.out_scales + (m0 + row) * SO;
                     const int32_t nb = n0 / kQuantBlock;
@@ -432,7 +452,9 @@ __global__ __launch_bounds__((QCfg<BM, BN, WM, WN, BK, S, GLU>::kThreads)) void 
 #pragma unroll
                 for (int v = 0; v < G::kBandStores; ++v) {
                     const int idx = tid + v * G::kThreads, row = idx / (BN / 8), c = idx % (BN / 8);
-                    store(band * 32 + row, c * 8, *(const u32x4 *)(so + row * G::kBandRowBytes + c * 16));
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        *(const u32x4 *)(so + row * G::kBandRowBytes + c * 16), out,
+                        place(band * 32 + row, c * 8), 0, 0);
                 }
             }
         }
@@ -504,24 +526,26 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
     const bool tail = in_dim % kQuantBlock != 0;
     // Tiles by the mean rows of an expert: few rows want few wasted ones and a deep
     // ring of weights, many want the bytes that a large tile saves.  Measured at
-    // R = 8, E = 64, K = 8, 2048 x 1408, us by mean rows:
-    //   gate and up, tiles of 32 / 64 / 256 rows: 4: 77 / 79 / 108, 16: 97 / 88 /
-    //   120, 64: 149 / 118 / 142, 96: 181 / 134 / 143, 128: 220 / 160 / 146,
-    //   512: 627 / 418 / 256;
-    //   down, 32 x 128 / 128 x 128 / 256 x 256: 4: 42 / 45 / 57, 16: 48 / 55 / 77,
-    //   32: 58 / 59 / 80, 64: 76 / 59 / 83, 128: 118 / 75 / 83, 256: 201 / 110 /
-    //   106, 512: 370 / 184 / 153.
+    // R = 8, E = 64, K = 8, us by mean rows:
+    //   gate and up, tiles of 32 / 64 / 256 rows, 2048 -> 1408: 4: 77 / 78 / 101, 12:
+    //   86 / 89 / 111, 16: 96 / 87 / 111, 64: 147 / 117 / 131, 80: 166 / 127 / 132,
+    //   96: 178 / 133 / 131, 128: 219 / 159 / 135, 512: 624 / 412 / 246;
+    //   4096 -> 4096: 64: 565 / 466 / 490, 96: 700 / 544 / 529;
+    //   one projection, 32 x 128 / 128 x 128 / 256 x 256, 1408 -> 2048: 4: 41 / 45 / 55,
+    //   16: 48 / 52 / 70, 24: 53 / 53 / 70, 64: 74 / 59 / 74, 128: 115 / 74 / 78, 192:
+    //   155 / 93 / 86, 512: 365 / 192 / 149; 4096 -> 4096: 96: 385 / 283 / 282, 128:
+    //   482 / 316 / 297.
     const int64_t mean = rows / s.E;
     if (glu) {
         if (mean <= 12)
             return run_tail<32, 256, 32, 64, 128, 3, true>(a, tail, st);
-        if (mean <= 96)
+        if (mean <= 88)
             return run_tail<64, 256, 64, 64, 128, 3, true>(a, tail, st);
         return run_tail<256, 256, 128, 64, 128, 2, true>(a, tail, st);
     }
     if (mean <= 24)
         return run_tail<32, 128, 32, 32, 128, 6, false>(a, tail, st);
-    if (mean <= 224)
+    if (mean <= 144)
         return run_tail<128, 128, 64, 32, 128, 3, false>(a, tail, st);
     return run_tail<256, 256, 128, 64, 128, 2, false>(a, tail, st);
 }
