@@ -421,7 +421,8 @@ size_t moonep_scale_bytes(int32_t cols); /* 4 * ceil(cols / 512); 0 if cols < 1 
  * its token rows before the router and the dispatch.  x, res: bf16 [R*S, H];
  * weight: bf16 [H]; H % 16 == 0, H <= 65536 (MOONEP_ERR_ARG).
  *   r = bf16(x + res) (x itself if res is NULL), written to res_out;
- *   y = r * (1 / sqrt(mean over the row of r^2 + eps)) * weight, in fp32;
+ *   y = r * (1 / sqrt(mean over the row of r^2 + eps)) * weight, in fp32 (a row
+ *       whose sum of squares is beyond fp32 becomes 0);
  *   y8, ys = the 8-bit row of y: codes [R*S, H], scales
  *            [R*S, moonep_scale_bytes(H)];
  *   y_out  = bf16(y), [R*S, H], for the router and a shared expert; NULL to
@@ -472,6 +473,8 @@ int moonep_quant_weights(const moonep_shape *shape, int32_t in_dim, int32_t out_
  * moonep_expert_gemm):
  *   y[r, n] = bf16( sum_k x[r, k] * W[n, k] )  (fp32 accumulation on the matrix
  *             cores, one rounding to nearest even), y: bf16 [R*S*K, out_dim].
+ *             The 8-bit matrix instructions drop bits inside a sum of 64
+ *             products: of the order of 2^-18 of sum |x| |W|.
  * Limits (MOONEP_ERR_ARG): in_dim and out_dim multiples of 16 and at most 2^22,
  * w_stride and code_offset multiples of 16, scale_offset of 4, windows inside
  * the weight row.  x8, y, w_home, pool 16-byte aligned; y must not overlap an

@@ -9,14 +9,22 @@
 // Choosing: K rounds of the row's largest key below the last one.  A key is one
 // word, the leading bits of the logit in integer order above the expert id
 // (counted down, so that ties go to the lower id): unique, so a round is one
-// subtraction and maximum per element.  bf16 logits fit whole; where two of the
-// K + 1 largest fp32 logits share their leading bits, or the row holds a NaN,
-// the wave chooses again on whole keys, two words' worth of work.
+// addition and half a three-way minimum per element.  bf16 logits fit whole; where
+// two of the K + 1 largest fp32 logits share their leading bits, or the row holds
+// a NaN, that row is chosen again on whole keys, over all 64 lanes of its wave.
 //
 // The shares of a workgroup's tokens are summed in registers (each lane keeps
 // its experts), then over its rows and waves, into one partial row of E sums
-// per workgroup; a second kernel joins the partials in fp64 in a fixed order.
-// Counts are integer atomics in LDS.
+// per workgroup; a second kernel joins the partials in fp64 in a fixed order, and
+// a third the loss.  Counts are integer atomics in LDS.
+//
+// Measured: 131072 x 256 fp32, sigmoid, K = 8, with the loss: 57 us, of which the
+// first kernel 47, the joins 5 each; its vector instructions (some 700 for four
+// tokens, the exponentials and reciprocals at a quarter of the rate) alone take
+// about 43 us, its bytes 24.  131072 x 128 bf16, softmax, backward: 22 us, its bytes
+// 13; 64 tokens of 64 experts: 3.4 us, a launch.  Sixteen lanes a token are a
+// balance: fewer would not hold 1024 experts in registers, more would spend the
+// reductions' steps on fewer tokens.
 #include "quant.hpp"
 
 namespace moonep {
@@ -202,6 +210,8 @@ struct RouterArgs {
 }  // namespace
 
 // Workgroup b takes `tokens` consecutive tokens of group b / per_group.
+// Four waves per SIMD up to 256 experts: without the bound 16 experts a lane take
+// more registers than that, and the loads of fewer waves are waited for.
 template <int kV, bool kBf16, bool kLoss>
 __global__ __launch_bounds__(kBlock, (kV <= 16 ? 4 : 1)) void router_kernel(RouterArgs a)
 {
