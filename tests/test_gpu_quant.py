@@ -385,6 +385,49 @@ def test_glu_within_bound(case):
     check_rows(h8, hs, h, err)
 
 
+# Hundreds of rows an expert, so the tile of 256 rows: fewer k-steps than the ring has stages, all items halves of
+# a tile, and one or two rounds of whole tiles before a round of halves.
+TALL = [
+    (synth.Workload("one_step", 1, 2, 1500, 1, 16, "zipf"), 16, 48, 0),
+    (synth.Workload("two_steps", 2, 4, 700, 2, 16, "zipf", alpha=1.0), 144, 272, 1),
+    (synth.Workload("half_round", 1, 4, 4400, 1, 16, "zipf", alpha=0.5), 32, 4096, 0),
+]
+
+
+@pytest.mark.parametrize("case", TALL, ids=lambda c: c[0].name)
+def test_gemm_large_tiles(case):
+    w, inp, out, B = case
+    print(f"[case] gemm {w.name} in={inp} out={out} B={B}", flush=True)
+    rng = np.random.default_rng(6)
+    b, ws, segs = product_setup(w, B)
+    w_home, wins = weight_rows(rng, w.E, [(out, inp)], True)
+    pool, _ = weight_rows(rng, w.R * B, [(out, inp)], True)
+    x8, xs = x_rows(rng, w.NK, inp, True)
+    y = run_gemm(w, b, ws, B, inp, out, x8, xs, w_home, pool, wins[0])
+    (want, _), = reference(segs, x8, xs, w_home, pool, [(out, inp)], wins)
+    np.testing.assert_array_equal(bits(y), bf16_of(want))
+
+
+@pytest.mark.parametrize("case", TALL, ids=lambda c: c[0].name)
+def test_glu_large_tiles(case):
+    w, inp, out, B = case
+    print(f"[case] glu {w.name}", flush=True)
+    rng = np.random.default_rng(7)
+    b, ws, segs = product_setup(w, B)
+    mats = [(out, inp), (out, inp)]
+    w_home, wins = weight_rows(rng, w.E, mats, False)
+    pool, _ = weight_rows(rng, w.R * B, mats, False)
+    x8, xs = x_rows(rng, w.NK, inp, False)
+    h8, hs = run_glu(w, b, ws, B, inp, out, x8, xs, w_home, pool, wins)
+    (g, ga), (u, ua) = reference(segs, x8, xs, w_home, pool, mats, wins)
+    silu = g / (1 + np.exp(-g))
+    # fp32 sums, and 2^-16 of the magnitudes for what the matrix instruction drops inside itself
+    dg, du = (inp * 2.0 ** -23 + 2.0 ** -16) * ga, (inp * 2.0 ** -23 + 2.0 ** -16) * ua
+    h = silu * u
+    err = 1.1 * dg * np.abs(u) + (np.abs(silu) + 1.1 * dg) * du + np.abs(h) * (np.abs(g) + 4) * 2.0 ** -22
+    check_rows(h8, hs, h, err)
+
+
 def test_products_of_non_finite_rows():
     """A NaN code or scale in a row makes that row's outputs NaN and no other's."""
     w, inp, out, B = PRODUCTS[4]
