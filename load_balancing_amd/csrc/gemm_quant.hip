@@ -26,14 +26,14 @@
 // ring of their own, a dword for four blocks.  The rings run on from one item to
 // the next, under the epilogue.
 //
-// What bounds it, gate and up of 262144 rows, 2048 -> 2 x 1408 (1424 us, 2.12
+// What bounds it, gate and up of 262144 rows, 2048 -> 2 x 1408 (1424-1441 us, 2.1
 // PFLOP/s; a library product in 8 bits without block scales and segments takes
 // 1264): the tile's loads from the L2 (12.3 GB; alone 1259 us) and the matrix
 // products (without loads 987 us), which overlap but share the power: 1.9 GHz
 // with both, 2.13 without the loads.  Deeper rings of smaller stages, other
 // schedules of the LDS reads and tiles of 128 rows (two workgroups per CU) were all
 // no faster.  At 4 rows an expert (77 us) it is bound by the weights' bytes, 5.6
-// TB/s of them.  One projection of 32576 rows, 1408 -> 2048 (141 us): 20% of the
+// TB/s of them.  One projection of 32576 rows, 1408 -> 2048 (141-148 us): 20% of the
 // tiles' rows are empty, and the bf16 stores take 25 us that the next item's loads,
 // which return in order behind them, do not hide.
 //

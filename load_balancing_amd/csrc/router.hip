@@ -21,7 +21,7 @@
 // Measured: 131072 x 256 fp32, sigmoid, K = 8, with the loss: 57 us, of which the
 // first kernel 47, the joins 5 each; its vector instructions (some 700 for four
 // tokens, the exponentials and reciprocals at a quarter of the rate) alone take
-// about 43 us, its bytes 24.  131072 x 128 bf16, softmax, backward: 22 us, its bytes
+// about 43 us, its bytes 24.  131072 x 128 bf16, softmax, backward: 21 us, its bytes
 // 13; 64 tokens of 64 experts: 3.4 us, a launch.  Sixteen lanes a token are a
 // balance: fewer would not hold 1024 experts in registers, more would spend the
 // reductions' steps on fewer tokens.
@@ -35,9 +35,14 @@ constexpr int kRowLanes = 16, kRowsPerWave = 64 / kRowLanes;
 constexpr int kRowsPerBlock = kWaves * kRowsPerWave;
 constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;  // nothing; a NaN, below -inf
 
+// Workgroups of the backward: what is on the chip at once.  131072 tokens, us at 1024 /
+// 2048: E = 64 bf16 16.7 / 15.2, 128 bf16 21.1 / 22.6, 128 fp32 33.5 / 37.2, 256 bf16
+// 38.0 / 43.6, 256 fp32 62.9 / 63.1.
+int64_t bwd_blocks(int32_t E) { return E <= 64 ? 2048 : 1024; }
+
 // Workgroups of the loss's first pass: enough to fill the chip, few enough that
 // their partial rows stay small beside the logits.
-constexpr int64_t kLossBlocks = 1024, kBwdBlocks = 2048;
+constexpr int64_t kLossBlocks = 1024;
 constexpr int kJoinThreads = 1024, kJoinExperts = 64, kJoinRows = kJoinThreads / kJoinExperts;
 
 // Workgroups of one group of n tokens, and the tokens of each: about `blocks` in
@@ -754,7 +759,7 @@ int launch_router_bwd(const moonep_shape &s, const moonep_router_opts &o, const 
         return MOONEP_OK;
     // without the loss no group matters
     const int64_t groups = counts ? o.groups : 1;
-    const Split split = split_tokens(N / groups, groups, kBwdBlocks);
+    const Split split = split_tokens(N / groups, groups, bwd_blocks(s.E));
     a.n = N / groups;
     a.per_group = split.per_group;
     a.tokens = split.tokens;
