@@ -275,7 +275,7 @@ __global__ __launch_bounds__(kBlock, (kV <= 16 ? 4 : 1)) void router_kernel(Rout
         }
         const int64_t t2 = t0 + kRowsPerBlock < end ? t0 + kRowsPerBlock : t0;
         load_rows<kV, kBf16>(logits + t2 * a.E * kSize, t2 + r < end ? r : 0, a.E, c, a.vec != 0, nxt);
-        const float top = row_top(l);
+        const float top = a.score == MOONEP_SCORE_SOFTMAX ? row_top(l) : 0.0f;
         const float rz = scores(l, a.score, top);
         if (kLoss) {
 #pragma unroll
@@ -536,7 +536,7 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             s[i] = l[i];
             part[i] = 0.0f;
         }
-        const float rz = scores(s, a.score, row_top(l));
+        const float rz = scores(s, a.score, a.score == MOONEP_SCORE_SOFTMAX ? row_top(l) : 0.0f);
         float all = 0.0f;  // what every expert's ds loses to the gates
         if (a.d_gates) {
 #pragma unroll
