@@ -481,6 +481,7 @@ struct RouterBwdArgs {
     void *d_logits;
     int64_t n, per_group, tokens;
     int32_t E, K, score, normalize, vec;
+    int32_t mean;  // of a group's counts, to the nearest integer
     float scale, factor;
 };
 
@@ -500,13 +501,17 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
     const int64_t g = (int64_t)blockIdx.x / a.per_group;
     const int64_t first = g * a.n + ((int64_t)blockIdx.x - g * a.per_group) * a.tokens;
     const int64_t end = first + a.tokens < (g + 1) * a.n ? first + a.tokens : (g + 1) * a.n;
-    float la[kV];  // the loss's gradient at p_e
+    // The loss's gradient at p_e, less that of a mean count: a_e - sum_j a_j p_j takes no
+    // constant into account but for a tiny / Z of it (as sum_j p_j = 1 - tiny / Z), and
+    // counts near their mean, where the loss drives them, would cancel to rounding.
+    float la[kV], la_tiny = 0.0f;
     if (a.counts) {
         const float dl = a.d_loss[0] * a.factor;
+        la_tiny = dl * (float)a.mean * tiny;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const int32_t e = expert_of(i, c);
-            la[i] = e < a.E ? dl * (float)a.counts[g * a.E + e] : 0.0f;
+            la[i] = e < a.E ? dl * (float)(a.counts[g * a.E + e] - a.mean) : 0.0f;
         }
     }
     const char *logits = (const char *)a.logits;
@@ -593,7 +598,7 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
 #pragma unroll
             for (int i = 0; i < kV; ++i)
                 dot = __builtin_fmaf(la[i], s[i], dot);
-            dot = row16_sum(dot) * rz;
+            dot = (row16_sum(dot) - la_tiny) * rz;
 #pragma unroll
             for (int i = 0; i < kV; ++i)
                 part[i] += (la[i] - dot) * rz;
@@ -770,6 +775,7 @@ int launch_router_bwd(const moonep_shape &s, const moonep_router_opts &o, const 
     const bool bf16 = o.logits_type == MOONEP_BF16;
     a.vec = row_vectors(logits, d_logits, s.E, bf16);
     a.scale = o.scale;
+    a.mean = (int32_t)((a.n * s.K + s.E / 2) / s.E);
     a.factor = (float)((double)s.E / ((double)s.K * (double)a.n * (double)a.n * o.groups));
     return by_experts<RunRouterBwd>(s.E, a, bf16, split.per_group * groups, st);
 }
