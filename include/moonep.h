@@ -390,7 +390,10 @@ int moonep_router(const moonep_shape *shape, const moonep_router_opts *opts, con
  *          + scale (dg_e - sum_j dg_j p_j) / Z      softmax, every e;
  *          + scale dg_e                             sigmoid;
  *   d_logits_e = ds_e s_e (softmax) or ds_e s_e (1 - s_e) (sigmoid),
- * rounded once to the logits' type.  The counts are constants: choosing has no
+ * rounded once to the logits' type.  The differences of a and of the normalised
+ * gates are taken with the mean count and the token's first d_gates off every
+ * term, so that what cancels in them (one chosen expert, one that dominates, even
+ * counts) leaves no rounding noise.  The counts are constants: choosing has no
  * gradient.  Masked experts and all-masked tokens get 0.  d_logits must not
  * overlap an input.
  */

@@ -77,6 +77,14 @@ __device__ __forceinline__ float row16_sum(float v)
     return v + __uint_as_float(dpp<kDppRowRor1>(__float_as_uint(v)));
 }
 
+// The first lane's value in all 16 lanes of a DPP row (row_newbcast:0).
+constexpr int kDppRowBcast0 = 0x150;
+
+__device__ __forceinline__ float row16_first(float v)
+{
+    return __uint_as_float(dpp<kDppRowBcast0>(__float_as_uint(v)));
+}
+
 // The scale bytes of the four 16-lane rows of a wave as one dword (uniform).
 __device__ __forceinline__ uint32_t gather_scale_dword(uint32_t byte)
 {

@@ -548,11 +548,16 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             for (int i = 0; i < kV; i += 4)
                 *(f32x4 *)(own + expert_of(i, c)) = f32x4{s[i], s[i + 1], s[i + 2], s[i + 3]};
             wave_sync();
+            // dg_k - sum_j dg_j s_j / W (normalised) takes no constant into account but
+            // for a tiny / W of it.  The first entry's comes off, that of the largest
+            // score: with one expert chosen nothing is left, and where one dominates
+            // its own term is the others' small ones, not what is left of two equal ones.
+            const float d_first = a.normalize ? row16_first(e0 < (uint32_t)a.E ? d0 : 0.0f) : 0.0f;
             float w = 0.0f, gs = 0.0f;
             auto chosen = [&](uint32_t e, float d) {
                 if (e < (uint32_t)a.E) {
                     w += own[e];
-                    gs = __builtin_fmaf(d, own[e], gs);
+                    gs = __builtin_fmaf(d - d_first, own[e], gs);
                 }
             };
             chosen(e0, d0);
@@ -565,7 +570,7 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             if (a.normalize) {
                 const float rw = w == 0.0f ? 0.0f : 1.0f / w;
                 mul = a.scale * rw;
-                sub = gs * rw;
+                sub = (gs - d_first * tiny) * rw;
             } else if (a.score == MOONEP_SCORE_SOFTMAX) {
                 mul = a.scale * rz;
                 all = mul * gs * rz;
@@ -577,7 +582,7 @@ __global__ __launch_bounds__(kBlock) void router_bwd_kernel(RouterBwdArgs a)
             wave_sync();
             auto spread = [&](uint32_t e, float d) {
                 if (e < (uint32_t)a.E)
-                    atomicAdd(own + e, mul * (d - sub));
+                    atomicAdd(own + e, mul * (d - d_first - sub));
             };
             spread(e0, d0);
             if (a.K > kRowLanes && on)

@@ -61,6 +61,63 @@ def check(got, want, mag, ref, bf16):
     assert (off <= allowed).all(), f"{(off / allowed).max()} of what is allowed"
 
 
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
+def test_one_chosen_expert_normalised(score, bf16):
+    """The gate is the constant `scale`: no gradient with softmax, and with sigmoid what tiny leaves."""
+    rng = np.random.default_rng(21)
+    for N, E, spread in ((700, 16, 1.0), (33, 1, 1.0), (129, 130, 4.0)):
+        print(f"[case] K=1 N={N} E={E} score={score} bf16={bf16}", flush=True)
+        t = as_type(spread * rng.standard_normal((N, E)), bf16)
+        l = t.double().numpy()
+        opts = mx.RouterOpts(score, True, 1, int(bf16), 2.5)
+        ids = order(l, 1)
+        dg = rng.standard_normal((N, 1)).astype(np.float32)
+        got = backward(mx.Shape(1, E, N, 1, 16), opts, t.cuda(), ids, None, dg, None)
+        if score == SOFT:
+            assert (got == 0).all()
+            continue
+        s = np.take_along_axis(1 / (1 + np.exp(-l)), ids, 1)
+        allowed = np.zeros((N, E))
+        np.put_along_axis(allowed, ids, 2.5 * np.abs(dg) * 1e-20 / (s + 1e-20) ** 2 * s * (1 - s), 1)
+        assert (np.abs(got) <= 1.01 * allowed + 2.0 ** -126).all()
+
+
+# tokens, experts, K, groups, score, factor of the gates, how far the first choice stands above the others
+TRAINING = [
+    ("k1", 7300, 16, 1, 1, SIG, 2.5, 0.0),
+    ("k1_wide", 32768, 64, 1, 1, SIG, 2.5, 0.0),
+    ("k1_two", 65536, 2, 1, 1, SIG, 1.0, 0.0),
+    ("k1_softmax", 8192, 64, 1, 4, SOFT, 1.0, 0.0),
+    ("dominant", 4096, 64, 8, 1, SIG, 1.0, 17.0),
+    ("dominant_softmax", 4096, 130, 6, 2, SOFT, 2.5, 17.0),
+    ("many_chosen", 2048, 64, 20, 1, SIG, 1.0, 16.0),
+    ("even", 16384, 32, 4, 8, SOFT, 1.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("case", TRAINING, ids=lambda c: c[0])
+def test_training_proportions(case, bf16):
+    """d_gates of 0.1 beside a loss weight of 0.01, spread over all tokens: the loss's gradient is far below
+    2^-24 of a single gate's."""
+    name, N, E, K, G, score, scale, above = case
+    print(f"[case] {name} bf16={bf16}", flush=True)
+    rng = np.random.default_rng(22)
+    l = rng.standard_normal((N, E)) - above
+    l[np.arange(N), rng.integers(0, E, N)] += 2 * above if score == SIG else above
+    t = as_type(l, bf16)
+    l = t.double().numpy()
+    ids = order(l, K)
+    opts = mx.RouterOpts(score, True, G, int(bf16), scale)
+    ref = Ref(l, ids, opts, G)
+    dg = (0.1 * rng.standard_normal((N, K))).astype(np.float32)
+    dl = np.float32(0.01)
+    for use in (dg, np.zeros_like(dg)):
+        got = backward(mx.Shape(1, E, N, K, 16), opts, t.cuda(), ids, ref.T, use, dl)
+        check(got, *left(ref, use.astype(np.float64), float(dl), ref.T), ref, bf16)
+
+
 @pytest.mark.parametrize("score", [SOFT, SIG], ids=["softmax", "sigmoid"])
 def test_even_counts(score):
     """Counts that are all equal leave no gradient of the loss (with sigmoid, tiny's); counts a few apart leave theirs."""
@@ -81,3 +138,32 @@ def test_even_counts(score):
     T = T + rng.integers(-2, 3, (1, E))
     zero = np.zeros((N, K))
     check(backward(shape, opts, t.cuda(), ids, T, None, 1.0), *left(ref, zero, 1.0, T), ref, False)
+
+
+def test_first_id_refused_normalised():
+    """A token whose first ids are outside [0, E): they contribute nothing, the others as if alone."""
+    rng = np.random.default_rng(24)
+    N, E, K = 40, 20, 4
+    t = as_type(rng.standard_normal((N, E)), False)
+    l = t.double().numpy()
+    ids = order(l, K)
+    dg = rng.standard_normal((N, K)).astype(np.float32)
+    bad = ids.copy()
+    bad[::3, 0], bad[1::5, 1], bad[7] = -1, E, E + 3
+    for score in (SOFT, SIG):
+        opts = mx.RouterOpts(score, True, 1, mx.F32, 1.5)
+        got = backward(mx.Shape(1, E, N, K, 16), opts, t.cuda(), bad, None, dg, None)
+        s = np.exp(l - l.max(1, keepdims=True)) if score == SOFT else 1 / (1 + np.exp(-l))
+        slope = s if score == SOFT else s * (1 - s)
+        ok = (bad >= 0) & (bad < E)
+        sk = np.where(ok, np.take_along_axis(s, np.where(ok, bad, 0), 1), 0)
+        W = sk.sum(1, keepdims=True)
+        W[W == 0] = 1
+        want, mag = np.zeros((N, E)), np.zeros((N, E))
+        for out, v in ((want, dg - (dg * sk).sum(1, keepdims=True) / W),
+                       (mag, np.abs(dg) + (np.abs(dg) * sk).sum(1, keepdims=True) / W)):
+            for k in range(K):
+                np.add.at(out, (np.arange(N), np.where(ok[:, k], bad[:, k], 0)), np.where(ok, 1.5 * v / W, 0)[:, k])
+        rel = (2 * np.abs(l - l.max(1, keepdims=True)).max() + E / 8 + 32) * 2.0 ** -24
+        allowed = (np.abs(want) * 2.0 ** -24 + mag * (4 * rel + (K + 16) * 2.0 ** -24)) * slope + 2.0 ** -126
+        assert (np.abs(got - want * slope) <= allowed).all()
