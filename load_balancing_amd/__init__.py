@@ -472,7 +472,7 @@ def moonep_quant_weights(shape, in_dim, out_dim, w, w_stride, w_offset, w8, w8_s
     dev = _current_device()
     _check(lib().moonep_quant_weights(
         ctypes.byref(shape), int(in_dim), int(out_dim),
-        _arg(dev, w, "w", shape.E * w_stride * 2, None), int(w_stride), int(w_offset),
+        _arg(dev, w, "w", shape.E * w_stride, _BF16_OK), int(w_stride), int(w_offset),
         _arg(dev, w8, "w8", shape.E * w8_stride, None), int(w8_stride), int(code_offset),
         int(scale_offset), _stream(stream)), "moonep_quant_weights")
 
