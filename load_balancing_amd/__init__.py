@@ -193,9 +193,13 @@ def _dev(t, what, numel, kinds):
 
 def _stream(stream):
     if stream is None:
-        # the current stream's handle, without building a Stream object for it
         torch = _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # The current stream's handle without a Stream object built for it, where torch
+        # has its internal accessor; that one is no public name.
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -63,3 +63,20 @@ def test_quant_weights_takes_bf16(one_gpu, calls):
     with pytest.raises(ValueError, match="elements"):
         call(OnGpu(E * n - 8, torch.bfloat16))
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("internal", [True, False], ids=["internal", "public"])
+def test_current_stream(monkeypatch, internal):
+    """The current stream of the current device, also from a torch without its internal accessor of the handle."""
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    if internal:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 70 + device, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert mx._stream(None) == (73 if internal else 77)
+    assert mx._stream(5) == 5 and mx._stream(Stream()) == 77
