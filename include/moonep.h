@@ -350,8 +350,9 @@ int moonep_expert_gemm(const moonep_shape *shape, const int32_t *plan, const int
  *   prob_sum[g, e] = P_ge = sum of p_e over its tokens, fp32 [groups, E];
  *   loss[0] = mean over g of E / (K n^2) * sum_e T_ge P_ge, fp32: 1 when
  *             counts or shares are uniform.  0 when there are no tokens.
- * Sums over tokens are fp32 within a workgroup's few and fp64 beyond, in an
- * order that the shape fixes: the same inputs give the same bits.
+ * Sums over tokens are fp32 within a workgroup's (2048 at most, 128 of them one
+ * after the other) and fp64 beyond, in an order that the shape fixes: the same
+ * inputs give the same bits.
  *
  * workspace: moonep_router_workspace_bytes, 16-byte aligned, no initial
  * contents needed; one call at a time uses it.  The outputs and the workspace

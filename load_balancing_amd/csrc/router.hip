@@ -41,8 +41,11 @@ constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;  // nothing; a Na
 int64_t bwd_blocks(int32_t E) { return E <= 64 ? 2048 : 1024; }
 
 // Workgroups of the loss's first pass: enough to fill the chip, few enough that
-// their partial rows stay small beside the logits.
-constexpr int64_t kLossBlocks = 1024;
+// their partial rows stay small beside the logits; and no more tokens for one than
+// that each lane adds 128 shares in fp32 (shares that are all alike, so that every
+// addition rounds the same way, then are 2e-6 off at most; without the limit 2^24
+// tokens of 3 experts were 1.5e-5 off).
+constexpr int64_t kLossBlocks = 1024, kLossTokens = 2048;
 constexpr int kJoinThreads = 1024, kJoinExperts = 64, kJoinRows = kJoinThreads / kJoinExperts;
 
 // Workgroups of one group of n tokens, and the tokens of each: about `blocks` in
@@ -71,7 +74,8 @@ struct RouterLayout {
 RouterLayout router_layout(const moonep_shape &s, int32_t groups)
 {
     RouterLayout l{};
-    l.split = split_tokens((int64_t)s.R * s.S / groups, groups, kLossBlocks);
+    const int64_t n = (int64_t)s.R * s.S / groups, least = groups * ((n + kLossTokens - 1) / kLossTokens);
+    l.split = split_tokens(n, groups, least < kLossBlocks ? kLossBlocks : least);
     const size_t rows = (size_t)l.split.per_group * groups * s.E * 4;
     const size_t nchunk = (size_t)(s.E + kJoinExperts - 1) / kJoinExperts;
     l.count_off = rows;
