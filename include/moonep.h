@@ -325,8 +325,9 @@ int moonep_expert_gemm(const moonep_shape *shape, const int32_t *plan, const int
  * The router: scores of the experts, the K experts and gates of every token,
  * and a balance loss that keeps maxvio low in training.
  *
- * logits: [R*S, E], fp32 or bf16 by opts->logits_type; computed in fp32.  With
- * l the logits of one token,
+ * logits: [R*S, E], fp32 or bf16 by opts->logits_type; computed in fp32, scores
+ * s_e to (2.5 |x| + 8) 2^-24 relative, x = l_e - max l (softmax) or l_e (sigmoid),
+ * and to 0 below 2^-126.  With l the logits of one token,
  *   softmax (MOONEP_SCORE_SOFTMAX): s_e = exp(l_e - max l), Z = sum_e s_e;
  *   sigmoid (MOONEP_SCORE_SIGMOID): s_e = 1 / (1 + exp(-l_e)),
  *                                   Z = sum_e s_e + 1e-20;

@@ -19,8 +19,8 @@
 // accumulator are then added within 2^-24 of the largest.  Products of codes have
 // eight bits, so those within 2^-7 of the largest are whole.  On normal codes that is
 // an rms of 2^-19 (k = 128) to 2^-21 (k = 2048) of sum |a| |b|, 2^-14.5 at most, and
-// 2^-18.5 towards zero where all products are positive; codes of every size alike,
-// 2^-12 at most.  All 8-bit forms do this (scaled or not, both shapes), bf16 ones do
+// 2^-18.5 towards zero where all products are positive; on codes of every size alike
+// 2^-11 at most.  All 8-bit forms do this (scaled or not, both shapes), bf16 ones do
 // not and take twice the time; the outputs' half steps are 2^-4 of an e4m3 code and
 // 2^-8 of a bf16 value, so it is accepted.
 //

@@ -84,10 +84,16 @@ RouterLayout router_layout(const moonep_shape &s, int32_t groups)
     return l;
 }
 
-// 2^(x log2 e): the product's rounding makes it (|x| + 2) 2^-24 relative, as the
-// rounding of a difference of logits does anyway.  0 and infinity at the ends.
+// 2^(x log2 e) with the product rounded once: (1.25 |x| + 2) 2^-24 relative (the
+// constant's rounding is the quarter), 1.6e-6 at |x| = 20; for fp32 logits under
+// softmax the rounding of their difference costs |x| 2^-24 as well, for sigmoid and
+// bf16 logits there is nothing else.  The choice does not go through it.  With the
+// product's dropped part taken along, as four more operations an element, 131072 x 256
+// forward takes 63.8 us instead of 59.8 and the backward of x 128 bf16 24.0 instead of
+// 22.1, so it is left out.  0 and infinity at the ends; results below 2^-126 are 0.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
+// v_rcp is good to one unit in the last place; 0 below 2^-126 (logits under -87.3).
 __device__ __forceinline__ float sigmoid_of(float l) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-l)); }
 
 __device__ __forceinline__ int32_t key_of(float l)
