@@ -427,7 +427,8 @@ size_t moonep_scale_bytes(int32_t cols); /* 4 * ceil(cols / 512); 0 if cols < 1 
  * weight: bf16 [H]; H % 16 == 0, H <= 65536 (MOONEP_ERR_ARG).
  *   r = bf16(x + res) (x itself if res is NULL), written to res_out;
  *   y = r * (1 / sqrt(mean over the row of r^2 + eps)) * weight, in fp32 (a row
- *       whose sum of squares is beyond fp32 becomes 0);
+ *       whose sum of squares is beyond fp32 becomes 0; with eps = 0 a row of
+ *       zeros, or of values whose squares are all 0 in fp32, is not finite);
  *   y8, ys = the 8-bit row of y: codes [R*S, H], scales
  *            [R*S, moonep_scale_bytes(H)];
  *   y_out  = bf16(y), [R*S, H], for the router and a shared expert; NULL to

@@ -10,8 +10,8 @@ import load_balancing_amd as mx
 import synth
 from gpu_harness import bf16_dev, bits, to_dev
 from quant_ref import check_rows, host, scale_bytes
-from test_gpu_quant import (bf16_of, f64, product_setup, quantise_matrix, reference, run_gemm, run_glu, weight_rows,
-                            x_rows)
+from test_gpu_quant import (bf16_of, f64, product_setup, quantise_matrix, reference, run_gemm, run_glu, run_norm,
+                            weight_rows, x_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,18 @@ def test_norm_and_dispatch_rows_past_one_grid():
     bufs = torch.full((N, 4), 0xA5, dtype=torch.uint8, device="cuda")
     mx.moonep_dispatch_quant(s, y8, ys, slot, buf8, bufs)
     assert torch.equal(buf8, y8.flip(0)) and torch.equal(bufs, ys.flip(0))
+
+
+def test_norm_rows_without_squares():
+    """With eps = 0, rows of zeros or of values of 2^-80 have no norm in fp32: codes and scales say so, the rows beside
+    them are as ever.  Any eps gives them one."""
+    x = np.ones((4, 256))
+    x[1], x[2] = 0, 2.0 ** -80
+    w = bf16_of(np.ones(256))
+    _, y, y8, ys = run_norm(bf16_of(x), None, w, 0.0)
+    assert (ys[1:3, :2] == 255).all() and (y8[1:3] == 0x7F).all() and not np.isfinite(f64(bits(y))[1:3]).any()
+    assert (f64(bits(y))[[0, 3]] == 1).all()
+    _, y, y8, ys = run_norm(bf16_of(x), None, w, 1e-30)
+    assert (f64(bits(y))[1] == 0).all() and (ys[1] == 127).all()
+    want = 2.0 ** -80 / np.sqrt(1e-30)
+    assert (np.abs(f64(bits(y))[2] - want) <= want * 2.0 ** -7).all()
