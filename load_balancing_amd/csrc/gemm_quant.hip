@@ -33,14 +33,19 @@
 //
 // What bounds it, gate and up of 262144 rows, 2048 -> 2 x 1408 (1424-1441 us, 2.1
 // PFLOP/s; a library product in 8 bits without block scales and segments takes
-// 1264): the tile's loads from the L2 (12.3 GB; alone 1259 us) and the matrix
-// products (without loads 987 us), which overlap but share the power: 1.9 GHz
-// with both, 2.13 without the loads.  Deeper rings of smaller stages, other
-// schedules of the LDS reads and tiles of 128 rows (two workgroups per CU) were all
-// no faster.  At 4 rows an expert (77 us) it is bound by the weights' bytes, 5.6
-// TB/s of them.  One projection of 32576 rows, 1408 -> 2048 (141-148 us): 20% of the
-// tiles' rows are empty, and the bf16 stores take 25 us that the next item's loads,
-// which return in order behind them, do not hide.
+// 1264): the tile's loads (12.3 GB; alone 1259 us) and the matrix products (without
+// loads 987 us), which overlap but share the power: 1.9-2.0 GHz with both, 2.13 without
+// the loads.  The loads' limit is no bandwidth.  19% of the L2's requests miss, 3.3 GB
+// come from beyond it (2.3 TB/s; rows and weights once are 0.95 GB), and with all of
+// them made to hit the loads alone take 736 us, 16.7 TB/s, where LDS-DMA of resident
+// data reaches 38: it is a stage's round trip, with one stage in flight, and half
+// of it the misses'.  Deeper rings of smaller stages (the loads alone 1323 us with 96
+// KB in flight), other schedules of the LDS reads and tiles of 128 rows (two
+// workgroups per CU) were all no faster; an item order with fewer misses is untried.  At 4 rows an expert (77 us) it is bound by the weights' bytes, 5.6
+// TB/s of them.  One projection of 32576 rows, 1408 -> 2048 (141-148 us, its products
+// 64): 20% of the tiles' rows are empty, the bf16 stores take 25 us that the next
+// item's loads, which return in order behind them, do not hide, and an item is
+// eleven k-steps with one stage in flight.
 //
 // Gate and up: the column tile interleaves 32 gate and 32 up columns, so one
 // wave holds both products of an output, and 128 output columns -- one block of
@@ -542,6 +547,14 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
     //   16: 48 / 52 / 70, 24: 53 / 53 / 70, 64: 74 / 59 / 74, 128: 115 / 74 / 78, 192:
     //   155 / 93 / 86, 512: 365 / 192 / 149; 4096 -> 4096: 96: 385 / 283 / 282, 128:
     //   482 / 316 / 297.
+    // With other experts and skews the tile chosen is within 6% of the best (one
+    // projection of skewed short segments, the last line: 10-14%): E = 128, K = 4, gate and up 2048 -> 1408: 8: 148 / 152 / 206, 12: 166 /
+    //   154 / 207, 64: 267 / 221 / 232, 88: 325 / 249 / 238; one projection 1408 -> 2048:
+    //   24: 99 / 102 / 125, 128: 218 / 144 / 144, 200: 316 / 181 / 164;
+    //   E = 32, 4096 -> 4096: 24: 224 / 224 / 256 and 115 / 116 / 155, 88: 344 / 269 / 270
+    //   and 191 / 142 / 164, 128: 430 / 331 / 282 and 245 / 163 / 166;
+    //   E = 256, skewed, 2048 -> 768: 8: 118 / 111 / 147, 88: 326 / 241 / 230; 768 -> 2048:
+    //   8: 57 / 70 / 81, 24: 83 / 91 / 101, 88: 182 / 143 / 130, 144: 269 / 179 / 157.
     const int64_t mean = rows / s.E;
     if (glu) {
         if (mean <= 12)

@@ -21,8 +21,9 @@
 // Measured: 131072 x 256 fp32, sigmoid, K = 8, with the loss: 57 us, of which the
 // first kernel 47, the joins 5 each; its vector instructions (some 700 for four
 // tokens, the exponentials and reciprocals at a quarter of the rate) alone take
-// about 43 us, its bytes 24.  131072 x 128 bf16, softmax, backward: 21 us, its bytes
-// 13; 64 tokens of 64 experts: 3.4 us, a launch.  Sixteen lanes a token are a
+// about 43 us, its bytes 24; bf16 46 us, its bytes 13.  131072 x 128 bf16, softmax,
+// backward: 21 us, its bytes 13 (normalised sigmoid 24: its slope has an exponential
+// of its own); 64 tokens of 64 experts: 3.4 us, a launch.  Sixteen lanes a token are a
 // balance: fewer would not hold 1024 experts in registers, more would spend the
 // reductions' steps on fewer tokens.
 #include "quant.hpp"
@@ -35,9 +36,11 @@ constexpr int kRowLanes = 16, kRowsPerWave = 64 / kRowLanes;
 constexpr int kRowsPerBlock = kWaves * kRowsPerWave;
 constexpr int32_t kNoKey = INT32_MIN, kNanKey = INT32_MIN + 1;  // nothing; a NaN, below -inf
 
-// Workgroups of the backward: what is on the chip at once.  131072 tokens, us at 1024 /
-// 2048: E = 64 bf16 16.7 / 15.2, 128 bf16 21.1 / 22.6, 128 fp32 33.5 / 37.2, 256 bf16
-// 38.0 / 43.6, 256 fp32 62.9 / 63.1.
+// Workgroups of the backward: about what is on the chip at once (2048 of kV = 4, 1024
+// to 1792 of kV = 8 and 16, fewer above).  131072 tokens, us at 1024 / 2048, bf16 and
+// fp32: E = 32 16.7 / 15.0 and 16.7 / 15.1, 64 16.2 / 15.2 and 16.0 / 15.7, 96 21.3 /
+// 21.9 and 27.4 / 30.7, 128 21.0 / 22.2 and 33.5 / 37.5, 256 37.1 / 43.2 and 63.3 /
+// 62.9, 512 78.3 / 92.0 and 122 / 124; 65536 of 1024 133 / 170 and 147 / 204.
 int64_t bwd_blocks(int32_t E) { return E <= 64 ? 2048 : 1024; }
 
 // Workgroups of the loss's first pass: enough to fill the chip, few enough that
