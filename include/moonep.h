@@ -25,9 +25,15 @@
  * moonep_prefetch_weights (the replicas' weights), moonep_dispatch, the expert
  * computation over the buffer (moonep_expert_gemm per projection, with the
  * caller's activation between projections), moonep_combine.  Backward:
- * moonep_combine_bwd, the expert's backward (the caller's), moonep_dispatch_bwd,
- * moonep_router_bwd (d_gates and the loss to the logits), and
- * moonep_replica_grad_reduce for the replicas' weight-gradients.
+ * moonep_combine_bwd, the expert's backward (moonep_expert_gemm_dx and
+ * moonep_expert_gemm_dw per projection, with the caller's backward of the
+ * activation in between), moonep_dispatch_bwd, moonep_router_bwd (d_gates and the
+ * loss to the logits), moonep_replica_grad_reduce for the replicas'
+ * weight-gradients, and moonep_grad_clip over all gradients.
+ *
+ * Low-rank adapters of many requests or tenants stand beside any projection that
+ * all rows share: moonep_adapter adds them to its output, moonep_adapter_bwd
+ * gives their gradients.
  *
  * An 8-bit forward, for serving: moonep_rmsnorm_quant (the residual stream to
  * 8-bit token rows, with the bf16 rows for the router), moonep_router,
@@ -512,6 +518,159 @@ int moonep_expert_glu_quant(const moonep_shape *shape, const int32_t *plan, cons
                             int64_t w_stride, int64_t gate_code_offset, int64_t gate_scale_offset,
                             int64_t up_code_offset, int64_t up_scale_offset, uint8_t *h8,
                             uint8_t *hs, void *stream);
+
+/*
+ * Backward of moonep_expert_gemm for the rows: with W as there (the same
+ * arguments and limits),
+ *   d_x[r, k] = bf16( sum_n d_y[r, n] * W[n, k] )  (fp32 accumulation on the
+ *               matrix cores, one rounding to nearest even).
+ * d_y: bf16 [R*S*K, out_dim]; d_x: bf16 [R*S*K, in_dim], must not overlap d_y,
+ * w_home or pool.  out_dim is at most 2^22 as well.
+ */
+int moonep_expert_gemm_dx(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
+                          int32_t B, int32_t in_dim, int32_t out_dim, const uint16_t *d_y,
+                          const uint16_t *w_home, const uint16_t *pool, int64_t w_stride,
+                          int64_t w_offset, uint16_t *d_x, void *stream);
+
+/*
+ * Backward of moonep_expert_gemm for the weights, into the rows that
+ * moonep_replica_grad_reduce reduces.  home_grads: fp32 [E, G]; replica_grads:
+ * fp32 [E + R, G], row j = replica j of `plan`.  With g the [out_dim, in_dim]
+ * window at element g_offset of the row of home expert e or of replica j < n_rep,
+ *   g[n, k] = sum over the buffer rows r of that expert's or replica's segment of
+ *             d_y[r, n] * x[r, k]
+ * in fp32 on the matrix cores, added to what g holds if accumulate is nonzero.
+ * A segment without rows gives zeros (or leaves g as it is).  Nothing else of the
+ * rows is touched, nor rows j >= n_rep.  x: bf16 [R*S*K, in_dim], d_y: bf16
+ * [R*S*K, out_dim].
+ * Limits (MOONEP_ERR_ARG): in_dim % 64 == 0, out_dim % 128 == 0, both at most
+ * 2^22, g_offset >= 0, g_offset + out_dim*in_dim <= G.  x and d_y 16-byte
+ * aligned, the gradients 4-byte; they must not overlap x, d_y or each other.
+ */
+int moonep_expert_gemm_dw(const moonep_shape *shape, const int32_t *plan, int32_t in_dim,
+                          int32_t out_dim, const uint16_t *x, const uint16_t *d_y,
+                          int32_t accumulate, int64_t G, int64_t g_offset, float *home_grads,
+                          float *replica_grads, void *stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that all rows
+ * share.  Rows r < R*S*K of `shape`, where R = K = 1 (MOONEP_ERR_ARG): S rows, and
+ * adapters take the place of experts, so that moonep_route_stats and moonep_plan
+ * on `ids` group the rows by adapter (E - 1 adapters, say, and id E - 1 for rows
+ * without one).  H is not used.
+ *
+ * A bank holds the adapters: row m of bank [n, stride] (bf16) is adapter m, its
+ * matrices A [rank, in_dim] at element a_offset and B [out_dim, rank] at
+ * b_offset, row-major, so that one row may hold the adapter's matrices of every
+ * layer.  scale: fp32 [n].  ids: int32 [S]; a row whose id is outside [0, n) has no
+ * adapter.  An adapter of a lower rank has zeros in the rows of A and the columns
+ * of B past it; their gradients are then zeros too.
+ *   u[r] = x[r] A^T,  y[r] = bf16(base[r] + scale * u[r] B^T)
+ * x: bf16 [S, in_dim]; base, y: bf16 [S, out_dim], base being the shared
+ * projection's output and y possibly the same array; u: fp32 [S, rank], which
+ * moonep_adapter_bwd takes.  u is summed in fp32 on the matrix cores; scale * u
+ * enters the second product with 16 bits (2^-17 relative), and y is rounded once.
+ * A row without an adapter has u = 0 and y = base, bit for bit.
+ * order: int32 [S] or NULL, the rows in the order to work in: moonep_plan's
+ * src_of_slot.  Rows of one adapter that stand together share its loads, so NULL
+ * (the rows as they are) is right for few rows or whole prompts one after the
+ * other.  The result does not depend on it; a row that is not in it is left out.
+ *
+ * workspace: moonep_adapter_workspace_bytes, 16-byte aligned, no initial contents
+ * needed; one call at a time uses it.
+ * Limits (MOONEP_ERR_ARG): 1 <= n <= E, rank, in_dim and out_dim multiples of 8,
+ * rank at most 128, in_dim and out_dim at most 2^22, stride and offsets multiples
+ * of 8, windows inside the row and apart.  bf16 arrays, u and workspace 16-byte
+ * aligned.  Outputs and the workspace must not overlap inputs or each other,
+ * except y = base.
+ */
+typedef struct moonep_adapters {
+    int32_t n;        /* adapters in the bank */
+    int32_t rank;     /* the largest rank */
+    int32_t in_dim, out_dim;
+    int64_t stride;   /* elements of a bank row */
+    int64_t a_offset; /* A [rank, in_dim] in it */
+    int64_t b_offset; /* B [out_dim, rank] in it */
+} moonep_adapters;
+
+/* Bytes of scratch; 0 for an invalid shape or adapters. */
+size_t moonep_adapter_workspace_bytes(const moonep_shape *shape, const moonep_adapters *ad);
+size_t moonep_adapter_bwd_workspace_bytes(const moonep_shape *shape, const moonep_adapters *ad);
+
+int moonep_adapter(const moonep_shape *shape, const moonep_adapters *ad, const int32_t *ids,
+                   const int32_t *order, const uint16_t *x, const uint16_t *bank,
+                   const float *scale, const uint16_t *base, float *u, uint16_t *y,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Adapter backward.  With u as moonep_adapter wrote it, d_y: bf16 [S, out_dim],
+ *   du[r]  = scale * d_y[r] B                       (fp32)
+ *   d_x[r] = bf16(dx_base[r] + du[r] A)
+ *   dA     = sum over the adapter's rows of du[r]^T x[r]
+ *   dB     = sum over the adapter's rows of scale * d_y[r]^T u[r]
+ * dx_base, d_x: bf16 [S, in_dim], dx_base being the shared projection's part and
+ * d_x possibly the same array; d_x = dx_base, bit for bit, without an adapter.  Both
+ * NULL: not computed.  d_bank: fp32 [n, stride], its windows laid out as bank's;
+ * the sums are written there, or added to what it holds if accumulate is nonzero;
+ * an adapter without rows gets zeros (or stays as it is), and the rest of a row is
+ * not touched.  d_bank NULL: not computed, and plan, x and u may be NULL too.
+ * Every product is summed in fp32, du and u entering the gradients' with all their
+ * bits; sums over rows are taken in an order that the shape and the plan fix.
+ * order and plan: moonep_plan's src_of_slot and plan for `shape` and ids (order
+ * may be NULL where d_bank is).  With another plan's tables d_bank is unspecified,
+ * but every access stays in bounds.  The other arguments and the limits are
+ * moonep_adapter's; workspace: moonep_adapter_bwd_workspace_bytes; d_bank 16-byte
+ * aligned.
+ */
+int moonep_adapter_bwd(const moonep_shape *shape, const moonep_adapters *ad, const int32_t *ids,
+                       const int32_t *order, const int32_t *plan, const uint16_t *x, const float *u,
+                       const uint16_t *d_y, const uint16_t *bank, const float *scale,
+                       const uint16_t *dx_base, uint16_t *d_x, int32_t accumulate, float *d_bank,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The norm over many gradient tensors, and their clipping.  The tensors are named
+ * by a device table of runs, int64 [entries, 4]: address of the gradient, address
+ * of the clipped one (may be the same), elements, type (MOONEP_F32 or MOONEP_BF16,
+ * of both).  moonep_grad_table writes it, on the host, for the caller to copy to
+ * the device: tensor i, counts[i] elements at src[i], in runs of at most
+ * MOONEP_GRAD_RUN (a run is one workgroup's work; longer ones are right as well).
+ * dst NULL: dst[i] = src[i].  It refuses (MOONEP_ERR_ARG) a negative count or an unknown
+ * type, (MOONEP_ERR_MISALIGNED) an address that is no multiple of the element,
+ * (MOONEP_ERR_NULL_PTR) a NULL address of a tensor with elements,
+ * (MOONEP_ERR_WORKSPACE) more entries than `entries`, and (MOONEP_ERR_ALIAS)
+ * tensors that overlap each other, or an output that overlaps a gradient other than
+ * by being it.  The table holds addresses: the tensors have to live as long as it
+ * is used.
+ */
+enum { MOONEP_GRAD_RUN = 16384, MOONEP_GRAD_WORKSPACE_BYTES = 16384 };
+
+/* Entries of the table; -1 for a negative n or count. */
+int64_t moonep_grad_entries(int64_t n, const int64_t *counts);
+int moonep_grad_table(int64_t n, const uint64_t *src, const uint64_t *dst, const int64_t *counts,
+                      const int32_t *types, int64_t entries, int64_t *table);
+
+/*
+ * norm[0] = fp32(sqrt(sum of g^2)) over every element of the table; sumsq[0], if
+ * given, the sum itself in fp64 (to be added up over ranks).  Squares and sums are
+ * fp64, in an order that the table fixes: not finite only if an element is not
+ * (or, for norm, beyond fp32).  workspace: MOONEP_GRAD_WORKSPACE_BYTES, 8-byte
+ * aligned, no initial contents needed; one call at a time uses it.
+ */
+int moonep_grad_norm(int64_t entries, const int64_t *table, double *sumsq, float *norm,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same norm (of sumsq[0] if it is given: the sum over all ranks), and
+ *   dst = g * fp32(max_norm / norm)   if norm > max_norm and norm is finite,
+ *   dst = g                           otherwise (nothing is written where dst is
+ *                                     the gradient itself),
+ * rounded once to the gradient's type.  An infinity or a NaN among the gradients
+ * leaves them all as they are, and norm says so.  max_norm is finite and >= 0
+ * (MOONEP_ERR_ARG).  workspace may be NULL where sumsq is given.
+ */
+int moonep_grad_clip(int64_t entries, const int64_t *table, double max_norm, const double *sumsq,
+                     float *norm, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Reads the sticky device error word of a workspace into *host_code, then

@@ -36,7 +36,10 @@ EXPORTS = ("moonep_check_shape", "moonep_workspace_bytes", "moonep_plan_layout_o
            "moonep_plan_noalloc", "moonep_router_workspace_bytes", "moonep_router",
            "moonep_router_bwd", "moonep_scale_bytes", "moonep_rmsnorm_quant",
            "moonep_dispatch_quant", "moonep_quant_weights", "moonep_expert_gemm_quant",
-           "moonep_expert_glu_quant")
+           "moonep_expert_glu_quant", "moonep_expert_gemm_dx", "moonep_expert_gemm_dw",
+           "moonep_adapter_workspace_bytes", "moonep_adapter_bwd_workspace_bytes",
+           "moonep_adapter", "moonep_adapter_bwd", "moonep_grad_entries", "moonep_grad_table",
+           "moonep_grad_norm", "moonep_grad_clip")
 
 
 class MoonepError(RuntimeError):
@@ -80,6 +83,20 @@ class RouterOpts(ctypes.Structure):
         super().__init__(int(score), int(normalize), int(groups), int(logits_type), float(scale))
 
 
+class Adapters(ctypes.Structure):
+    """moonep_adapters: n adapters of a bank of rows of `stride` elements, A [rank,
+    in_dim] at a_offset and B [out_dim, rank] at b_offset of each (by default a row
+    holds just the two)."""
+    _fields_ = [("n", ctypes.c_int32), ("rank", ctypes.c_int32), ("in_dim", ctypes.c_int32),
+                ("out_dim", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("a_offset", ctypes.c_int64), ("b_offset", ctypes.c_int64)]
+
+    def __init__(self, n, rank, in_dim, out_dim, stride=None, a_offset=0, b_offset=None):
+        super().__init__(int(n), int(rank), int(in_dim), int(out_dim),
+                         int(rank * (in_dim + out_dim) if stride is None else stride), int(a_offset),
+                         int(a_offset + rank * in_dim if b_offset is None else b_offset))
+
+
 class PlanLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "words", "cap", "header", "rep_expert", "rep_host", "rep_count", "rep_spill_off",
@@ -99,7 +116,7 @@ def lib():
                                "`python -m load_balancing_amd.build` (there is no fallback)")
         L = ctypes.CDLL(LIB_PATH)
         P, VP, SZ, I64 = ctypes.POINTER(Shape), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
-        I32, RO = ctypes.c_int32, ctypes.POINTER(RouterOpts)
+        I32, RO, AD = ctypes.c_int32, ctypes.POINTER(RouterOpts), ctypes.POINTER(Adapters)
         sig = {
             "moonep_check_shape": (ctypes.c_int, [P]),
             "moonep_workspace_bytes": (SZ, [P]),
@@ -132,6 +149,19 @@ def lib():
                                                         I64, I64, I64, VP, VP]),
             "moonep_expert_glu_quant": (ctypes.c_int, [P, VP, VP, I32, I32, I32, VP, VP, VP, VP,
                                                        I64, I64, I64, I64, I64, VP, VP, VP]),
+            "moonep_expert_gemm_dx": (ctypes.c_int, [P, VP, VP, I32, I32, I32, VP, VP, VP, I64, I64,
+                                                     VP, VP]),
+            "moonep_expert_gemm_dw": (ctypes.c_int, [P, VP, I32, I32, VP, VP, I32, I64, I64, VP, VP,
+                                                     VP]),
+            "moonep_adapter_workspace_bytes": (SZ, [P, AD]),
+            "moonep_adapter_bwd_workspace_bytes": (SZ, [P, AD]),
+            "moonep_adapter": (ctypes.c_int, [P, AD, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+            "moonep_adapter_bwd": (ctypes.c_int, [P, AD, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, I32,
+                                                  VP, VP, SZ, VP]),
+            "moonep_grad_entries": (I64, [I64, VP]),
+            "moonep_grad_table": (ctypes.c_int, [I64, VP, VP, VP, VP, I64, VP]),
+            "moonep_grad_norm": (ctypes.c_int, [I64, VP, VP, VP, VP, SZ, VP]),
+            "moonep_grad_clip": (ctypes.c_int, [I64, VP, ctypes.c_double, VP, VP, VP, SZ, VP]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -514,6 +544,153 @@ def moonep_expert_glu_quant(shape, plan, wslot, B, in_dim, mid_dim, x8, xs, w_ho
         _arg(dev, h8, "h8", shape.NK * mid_dim, _CODES),
         _arg(dev, hs, "hs", shape.NK * _scale_row(mid_dim), _SCALES), _stream(stream)),
         "moonep_expert_glu_quant")
+
+
+def moonep_expert_gemm_dx(shape, plan, wslot, B, in_dim, out_dim, d_y, w_home, pool, w_stride,
+                          w_offset, d_x, stream=None):
+    """d_x [R*S*K, in_dim] = each buffer row of d_y [R*S*K, out_dim] times its
+    segment's weights, transposed; w_home [E, w_stride] and pool [R*B, w_stride] bf16."""
+    dev = _current_device()
+    _check(lib().moonep_expert_gemm_dx(
+        ctypes.byref(shape), _arg(dev, plan, "plan", _plan_words(shape.E, shape.R), ("int32",)),
+        _arg(dev, wslot, "wslot", shape.E + shape.R, ("int32",)), int(B), int(in_dim), int(out_dim),
+        _arg(dev, d_y, "d_y", shape.NK * out_dim, _BF16_OK),
+        _arg(dev, w_home, "w_home", shape.E * w_stride, _BF16_OK),
+        _arg(dev, pool, "pool", shape.R * B * w_stride, _BF16_OK), int(w_stride), int(w_offset),
+        _arg(dev, d_x, "d_x", shape.NK * in_dim, _BF16_OK), _stream(stream)),
+        "moonep_expert_gemm_dx")
+
+
+def moonep_expert_gemm_dw(shape, plan, in_dim, out_dim, x, d_y, accumulate, G, g_offset, home_grads,
+                          replica_grads, stream=None):
+    """The [out_dim, in_dim] windows at element g_offset of home_grads [E, G] and
+    of the replicas' rows of replica_grads [E + R, G]: each segment's d_y^T x, added
+    to what they hold if accumulate."""
+    dev = _current_device()
+    _check(lib().moonep_expert_gemm_dw(
+        ctypes.byref(shape), _arg(dev, plan, "plan", _plan_words(shape.E, shape.R), ("int32",)),
+        int(in_dim), int(out_dim), _arg(dev, x, "x", shape.NK * in_dim, _BF16_OK),
+        _arg(dev, d_y, "d_y", shape.NK * out_dim, _BF16_OK), int(bool(accumulate)), int(G),
+        int(g_offset), _arg(dev, home_grads, "home_grads", shape.E * G, ("float32",)),
+        _arg(dev, replica_grads, "replica_grads", (shape.E + shape.R) * G, ("float32",)),
+        _stream(stream)), "moonep_expert_gemm_dw")
+
+
+def moonep_adapter_workspace_bytes(shape, ad: Adapters) -> int:
+    return lib().moonep_adapter_workspace_bytes(ctypes.byref(shape), ctypes.byref(ad))
+
+
+def moonep_adapter_bwd_workspace_bytes(shape, ad: Adapters) -> int:
+    return lib().moonep_adapter_bwd_workspace_bytes(ctypes.byref(shape), ctypes.byref(ad))
+
+
+def moonep_adapter(shape, ad, ids, order, x, bank, scale, base, u, y, workspace, stream=None):
+    """y [S, out_dim] = base + each row's adapter on x [S, in_dim]; u [S, rank] fp32
+    for the backward.  ids [S]: outside [0, n) none; order [S] or None; bank [n,
+    stride] bf16, scale [n]; y may be base."""
+    dev = _current_device()
+    S = shape.S
+    _check(lib().moonep_adapter(
+        ctypes.byref(shape), ctypes.byref(ad), _arg(dev, ids, "ids", S, ("int32",)),
+        _arg(dev, order, "order", 0 if order is None else S, ("int32",)),
+        _arg(dev, x, "x", S * ad.in_dim, _BF16_OK),
+        _arg(dev, bank, "bank", ad.n * ad.stride, _BF16_OK),
+        _arg(dev, scale, "scale", ad.n, ("float32",)),
+        _arg(dev, base, "base", S * ad.out_dim, _BF16_OK),
+        _arg(dev, u, "u", S * ad.rank, ("float32",)), _arg(dev, y, "y", S * ad.out_dim, _BF16_OK),
+        _arg(dev, workspace, "workspace", workspace.numel(), ("uint8",)), _nbytes(workspace),
+        _stream(stream)), "moonep_adapter")
+
+
+def moonep_adapter_bwd(shape, ad, ids, order, plan, x, u, d_y, bank, scale, dx_base, d_x, accumulate,
+                       d_bank, workspace, stream=None):
+    """d_x [S, in_dim] = dx_base + the adapters' part (both None: left out), and the
+    adapters' gradients into d_bank [n, stride] fp32, added if accumulate (None: left
+    out, with plan, order, x and u)."""
+    dev = _current_device()
+    S = shape.S
+    _check(lib().moonep_adapter_bwd(
+        ctypes.byref(shape), ctypes.byref(ad), _arg(dev, ids, "ids", S, ("int32",)),
+        _arg(dev, order, "order", 0 if order is None else S, ("int32",)),
+        _arg(dev, plan, "plan", 0 if plan is None else _plan_words(shape.E, shape.R), ("int32",)),
+        _arg(dev, x, "x", 0 if x is None else S * ad.in_dim, _BF16_OK),
+        _arg(dev, u, "u", 0 if u is None else S * ad.rank, ("float32",)),
+        _arg(dev, d_y, "d_y", S * ad.out_dim, _BF16_OK),
+        _arg(dev, bank, "bank", ad.n * ad.stride, _BF16_OK),
+        _arg(dev, scale, "scale", ad.n, ("float32",)),
+        _arg(dev, dx_base, "dx_base", 0 if dx_base is None else S * ad.in_dim, _BF16_OK),
+        _arg(dev, d_x, "d_x", 0 if d_x is None else S * ad.in_dim, _BF16_OK), int(bool(accumulate)),
+        _arg(dev, d_bank, "d_bank", 0 if d_bank is None else ad.n * ad.stride, ("float32",)),
+        _arg(dev, workspace, "workspace", workspace.numel(), ("uint8",)), _nbytes(workspace),
+        _stream(stream)), "moonep_adapter_bwd")
+
+
+GRAD_RUN, GRAD_WORKSPACE_BYTES = 16384, 16384
+
+
+def moonep_grad_entries(counts) -> int:
+    """Entries of the table of tensors of these sizes; -1 for a negative one."""
+    n = len(counts)
+    return lib().moonep_grad_entries(n, (ctypes.c_int64 * n)(*counts))
+
+
+def moonep_grad_table(grads, out=None):
+    """The table [entries, 4] of moonep_grad_norm and moonep_grad_clip, on the
+    current device: contiguous fp32 and bf16 tensors, and where their clipped values
+    go (out None: in place).  The tensors have to live as long as it is used."""
+    torch = _torch()
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
+    dev, n = _current_device(), len(grads)
+    kinds = {"float32": F32, "bfloat16": BF16}
+    types = []
+    for i, (g, o) in enumerate(zip(grads, out)):
+        name = _dtype_name(g.dtype)
+        if name not in kinds:
+            raise ValueError(f"grads[{i}]: dtype {g.dtype} not in {tuple(kinds)}")
+        _arg(dev, g, f"grads[{i}]", g.numel(), (name,))
+        _arg(dev, o, f"out[{i}]", g.numel(), (name,))
+        types.append(kinds[name])
+    counts = [g.numel() for g in grads]
+    entries = moonep_grad_entries(counts)
+    words = torch.empty((entries, 4), dtype=torch.int64)
+    _check(lib().moonep_grad_table(
+        n, (ctypes.c_uint64 * n)(*[g.data_ptr() for g in grads]),
+        (ctypes.c_uint64 * n)(*[o.data_ptr() for o in out]), (ctypes.c_int64 * n)(*counts),
+        (ctypes.c_int32 * n)(*types), entries, words.data_ptr()), "moonep_grad_table")
+    return words.to(torch.device("cuda", dev))
+
+
+def _grad_table(dev, table):
+    if table.dim() != 2 or table.shape[1] != 4:
+        raise ValueError(f"table: shape {tuple(table.shape)}, needs [entries, 4]")
+    return table.shape[0], _arg(dev, table, "table", table.numel(), ("int64",))
+
+
+def moonep_grad_norm(table, norm, workspace, sumsq=None, stream=None):
+    """norm [1] fp32 of every element of the table's tensors, and the sum of their
+    squares (sumsq [1] fp64)."""
+    dev = _current_device()
+    n, at = _grad_table(dev, table)
+    _check(lib().moonep_grad_norm(
+        n, at, _arg(dev, sumsq, "sumsq", 0 if sumsq is None else 1, ("float64",)),
+        _arg(dev, norm, "norm", 1, ("float32",)),
+        _arg(dev, workspace, "workspace", workspace.numel(), ("uint8",)), _nbytes(workspace),
+        _stream(stream)), "moonep_grad_norm")
+
+
+def moonep_grad_clip(table, max_norm, norm, workspace, sumsq=None, stream=None):
+    """The table's tensors scaled to a norm of at most max_norm (of the norm that
+    sumsq [1] fp64 gives, if it is given; workspace may be None then)."""
+    dev = _current_device()
+    n, at = _grad_table(dev, table)
+    size = 0 if workspace is None else workspace.numel()
+    _check(lib().moonep_grad_clip(
+        n, at, float(max_norm), _arg(dev, sumsq, "sumsq", 0 if sumsq is None else 1, ("float64",)),
+        _arg(dev, norm, "norm", 1, ("float32",)), _arg(dev, workspace, "workspace", size, ("uint8",)),
+        size, _stream(stream)), "moonep_grad_clip")
 
 
 def moonep_read_error(workspace, stream=None) -> int:

@@ -4,8 +4,10 @@
 // described, with the pages that define them, in include/moonep.h.
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "quant.hpp"
@@ -57,6 +59,28 @@ int launch_expert_quant(const moonep_shape &s, const int32_t *plan, const int32_
                         const uint8_t *w_home, const uint8_t *pool, int64_t w_stride,
                         const int64_t *code, const int64_t *scale, void *out, uint8_t *out_scales,
                         hipStream_t st);
+int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *wslot, int32_t B,
+                     int32_t in_dim, int32_t out_dim, const uint16_t *d_y, const uint16_t *w_home,
+                     const uint16_t *pool, int64_t w_stride, int64_t w_offset, uint16_t *d_x,
+                     hipStream_t st);
+int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim, int32_t out_dim,
+                     const uint16_t *x, const uint16_t *d_y, int accumulate, int64_t G,
+                     int64_t g_offset, float *home, float *rep, hipStream_t st);
+size_t adapter_workspace(int64_t rows, const moonep_adapters &ad);
+size_t adapter_bwd_workspace(int64_t rows, const moonep_adapters &ad);
+int launch_adapter(int32_t rows, const moonep_adapters &ad, const int32_t *ids, const int32_t *order,
+                   const uint16_t *x, const uint16_t *bank, const float *scale, const uint16_t *base,
+                   float *u, uint16_t *y, void *ws, hipStream_t st);
+int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const int32_t *ids,
+                       const int32_t *order, const int32_t *plan, const uint16_t *x, const float *u,
+                       const uint16_t *dy, const uint16_t *bank, const float *scale,
+                       const uint16_t *dx_base, uint16_t *dx, int accumulate, float *d_bank, void *ws,
+                       hipStream_t st);
+size_t grad_workspace();
+int launch_grad_norm(const void *table, int64_t n, double *sumsq, float *norm, void *ws,
+                     hipStream_t st);
+int launch_grad_clip(const void *table, int64_t n, double max_norm, const double *sumsq, float *norm,
+                     void *ws, hipStream_t st);
 }  // namespace moonep
 
 using namespace moonep;
@@ -138,6 +162,40 @@ bool aliased(const Range (&out)[NO], const Range (&in)[NI])
                 return true;
     }
     return false;
+}
+
+// Elements of an array that byte sizes in 64 bits are formed of.
+constexpr int64_t kMostElements = (int64_t)1 << 58;
+
+// The sizes of a projection that the grouped products take.
+bool gemm_dims_ok(int32_t in_dim, int32_t out_dim)
+{
+    // the kernels address a row of a tile by a 32-bit byte offset: 256 rows of bf16
+    constexpr int32_t kMost = 1 << 22;
+    return in_dim > 0 && in_dim % 64 == 0 && in_dim <= kMost && out_dim > 0 &&
+           out_dim % gemm_out_align() == 0 && out_dim <= kMost;
+}
+
+// The rules of moonep_adapters and of the shape that goes with it.
+int adapter_status(const moonep_shape *s, const moonep_adapters *ad)
+{
+    const int rc = shape_status(s);
+    if (rc != MOONEP_OK)
+        return rc;
+    if (!ad)
+        return MOONEP_ERR_NULL_PTR;
+    constexpr int32_t kMostDim = 1 << 22, kMostRows = 1 << 30;
+    if (s->R != 1 || s->K != 1 || s->S > kMostRows || ad->n < 1 || ad->n > s->E || ad->rank < 8 ||
+        ad->rank > 128 || ad->rank % 8 || ad->in_dim < 8 || ad->in_dim > kMostDim || ad->in_dim % 8 ||
+        ad->out_dim < 8 || ad->out_dim > kMostDim || ad->out_dim % 8 || ad->stride % 8 ||
+        ad->stride > kMostElements / kMaxExperts || ad->a_offset < 0 || ad->a_offset % 8 ||
+        ad->b_offset < 0 || ad->b_offset % 8)
+        return MOONEP_ERR_ARG;
+    const int64_t a = (int64_t)ad->rank * ad->in_dim, b = (int64_t)ad->rank * ad->out_dim;
+    if (ad->a_offset > ad->stride - a || ad->b_offset > ad->stride - b ||
+        (ad->a_offset < ad->b_offset + b && ad->b_offset < ad->a_offset + a))
+        return MOONEP_ERR_ARG;
+    return MOONEP_OK;
 }
 
 // Pointers may be NULL only when the array they name is empty.
@@ -686,6 +744,251 @@ int moonep_expert_glu_quant(const moonep_shape *shape, const int32_t *plan, cons
     const int64_t scale[2] = {gate_scale_offset, up_scale_offset};
     return expert_quant(shape, plan, wslot, B, in_dim, mid_dim, x8, xs, w_home, pool, w_stride, 2,
                         code, scale, h8, mid_dim, hs, stream);
+}
+
+int moonep_expert_gemm_dx(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
+                          int32_t B, int32_t in_dim, int32_t out_dim, const uint16_t *d_y,
+                          const uint16_t *w_home, const uint16_t *pool, int64_t w_stride,
+                          int64_t w_offset, uint16_t *d_x, void *stream)
+{
+    int rc = shape_status(shape);
+    if (rc != MOONEP_OK)
+        return rc;
+    if (B < 0 || (int64_t)shape->R * B >= ((int64_t)1 << 31) || !gemm_dims_ok(in_dim, out_dim) ||
+        w_stride % 8 != 0 || w_offset < 0 || w_offset % 8 != 0 ||
+        w_offset > w_stride - (int64_t)out_dim * in_dim)
+        return MOONEP_ERR_ARG;
+    const int64_t rows = n_entries(shape);
+    const int64_t pool_rows = (int64_t)shape->R * B;
+    if (!plan || !wslot || !w_home || !present(d_y, rows) || !present(d_x, rows) ||
+        !present(pool, pool_rows))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(plan, 4) || !aligned(wslot, 4) || !aligned(d_y, 16) || !aligned(d_x, 16) ||
+        !aligned(w_home, 16) || !aligned(pool, 16))
+        return MOONEP_ERR_MISALIGNED;
+    const Range out[] = {{d_x, (size_t)rows * in_dim * 2}};
+    const Range in[] = {{d_y, (size_t)rows * out_dim * 2},
+                        {w_home, (size_t)shape->E * (size_t)w_stride * 2},
+                        {pool, (size_t)pool_rows * (size_t)w_stride * 2}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
+    return launch_expert_dx(*shape, plan, wslot, B, in_dim, out_dim, d_y, w_home, pool, w_stride,
+                            w_offset, d_x, (hipStream_t)stream);
+}
+
+int moonep_expert_gemm_dw(const moonep_shape *shape, const int32_t *plan, int32_t in_dim,
+                          int32_t out_dim, const uint16_t *x, const uint16_t *d_y,
+                          int32_t accumulate, int64_t G, int64_t g_offset, float *home_grads,
+                          float *replica_grads, void *stream)
+{
+    int rc = shape_status(shape);
+    if (rc != MOONEP_OK)
+        return rc;
+    if (!gemm_dims_ok(in_dim, out_dim) || g_offset < 0 || g_offset > G - (int64_t)out_dim * in_dim ||
+        G > kMostElements / (2 * kMaxExperts))
+        return MOONEP_ERR_ARG;
+    const int64_t rows = n_entries(shape);
+    if (!plan || !home_grads || !replica_grads || !present(x, rows) || !present(d_y, rows))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(plan, 4) || !aligned(home_grads, 4) || !aligned(replica_grads, 4) ||
+        !aligned(x, 16) || !aligned(d_y, 16))
+        return MOONEP_ERR_MISALIGNED;
+    const Range out[] = {{home_grads, (size_t)shape->E * (size_t)G * 4},
+                         {replica_grads, (size_t)(shape->E + shape->R) * (size_t)G * 4}};
+    const Range in[] = {{x, (size_t)rows * in_dim * 2}, {d_y, (size_t)rows * out_dim * 2}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
+    return launch_expert_dw(*shape, plan, in_dim, out_dim, x, d_y, accumulate, G, g_offset,
+                            home_grads, replica_grads, (hipStream_t)stream);
+}
+
+size_t moonep_adapter_workspace_bytes(const moonep_shape *shape, const moonep_adapters *ad)
+{
+    return adapter_status(shape, ad) == MOONEP_OK ? adapter_workspace(shape->S, *ad) : 0;
+}
+
+size_t moonep_adapter_bwd_workspace_bytes(const moonep_shape *shape, const moonep_adapters *ad)
+{
+    return adapter_status(shape, ad) == MOONEP_OK ? adapter_bwd_workspace(shape->S, *ad) : 0;
+}
+
+int moonep_adapter(const moonep_shape *shape, const moonep_adapters *ad, const int32_t *ids,
+                   const int32_t *order, const uint16_t *x, const uint16_t *bank,
+                   const float *scale, const uint16_t *base, float *u, uint16_t *y,
+                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int rc = adapter_status(shape, ad);
+    if (rc != MOONEP_OK)
+        return rc;
+    const int64_t rows = shape->S;
+    if (!present(ids, rows) || !present(x, rows) || !present(base, rows) || !present(u, rows) ||
+        !present(y, rows) || !bank || !scale || !workspace)
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(scale, 4) || !aligned(x, 16) ||
+        !aligned(bank, 16) || !aligned(base, 16) || !aligned(u, 16) || !aligned(y, 16) ||
+        !aligned(workspace, 16))
+        return MOONEP_ERR_MISALIGNED;
+    if (workspace_bytes < adapter_workspace(rows, *ad))
+        return MOONEP_ERR_WORKSPACE;
+    const size_t wide = (size_t)rows * ad->out_dim * 2;
+    const Range out[] = {{u, (size_t)rows * ad->rank * 4}, {workspace, workspace_bytes}, {y, wide}};
+    const Range in[] = {{ids, (size_t)rows * 4}, {order, order ? (size_t)rows * 4 : 0},
+                        {x, (size_t)rows * ad->in_dim * 2}, {bank, (size_t)ad->n * ad->stride * 2},
+                        {scale, (size_t)ad->n * 4}, {base == y ? nullptr : base, base == y ? 0 : wide}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
+    return launch_adapter((int32_t)rows, *ad, ids, order, x, bank, scale, base, u, y, workspace,
+                          (hipStream_t)stream);
+}
+
+int moonep_adapter_bwd(const moonep_shape *shape, const moonep_adapters *ad, const int32_t *ids,
+                       const int32_t *order, const int32_t *plan, const uint16_t *x, const float *u,
+                       const uint16_t *d_y, const uint16_t *bank, const float *scale,
+                       const uint16_t *dx_base, uint16_t *d_x, int32_t accumulate, float *d_bank,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int rc = adapter_status(shape, ad);
+    if (rc != MOONEP_OK)
+        return rc;
+    const int64_t rows = shape->S;
+    const bool grads = d_bank != nullptr;
+    if (!present(ids, rows) || !present(d_y, rows) || !bank || !scale || !workspace ||
+        (dx_base == nullptr) != (d_x == nullptr) || (rows && !d_x && !grads) ||
+        (grads && (!plan || !present(order, rows) || !present(x, rows) || !present(u, rows))))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(plan, 4) || !aligned(scale, 4) ||
+        !aligned(x, 16) || !aligned(u, 16) || !aligned(d_y, 16) || !aligned(bank, 16) ||
+        !aligned(dx_base, 16) || !aligned(d_x, 16) || !aligned(d_bank, 16) || !aligned(workspace, 16))
+        return MOONEP_ERR_MISALIGNED;
+    if (workspace_bytes < adapter_bwd_workspace(rows, *ad))
+        return MOONEP_ERR_WORKSPACE;
+    const size_t wide = d_x ? (size_t)rows * ad->in_dim * 2 : 0;
+    const Range out[] = {{d_bank, grads ? (size_t)ad->n * ad->stride * 4 : 0},
+                         {workspace, workspace_bytes}, {d_x, wide}};
+    const Range in[] = {{ids, (size_t)rows * 4}, {order, order ? (size_t)rows * 4 : 0},
+                        {plan, plan ? (size_t)plan_layout(shape->E, 1).words * 4 : 0},
+                        {x, grads ? (size_t)rows * ad->in_dim * 2 : 0},
+                        {u, grads ? (size_t)rows * ad->rank * 4 : 0},
+                        {d_y, (size_t)rows * ad->out_dim * 2}, {bank, (size_t)ad->n * ad->stride * 2},
+                        {scale, (size_t)ad->n * 4},
+                        {dx_base == d_x ? nullptr : dx_base, dx_base == d_x ? 0 : wide}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
+    return launch_adapter_bwd((int32_t)rows, shape->E, *ad, ids, order, plan, x, u, d_y, bank, scale,
+                              dx_base, d_x, accumulate, d_bank, workspace, (hipStream_t)stream);
+}
+
+int64_t moonep_grad_entries(int64_t n, const int64_t *counts)
+{
+    if (n < 0 || (n && !counts))
+        return -1;
+    int64_t entries = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (counts[i] < 0 || counts[i] > kMostElements)
+            return -1;
+        entries += (counts[i] + MOONEP_GRAD_RUN - 1) / MOONEP_GRAD_RUN;
+    }
+    return entries;
+}
+
+int moonep_grad_table(int64_t n, const uint64_t *src, const uint64_t *dst, const int64_t *counts,
+                      const int32_t *types, int64_t entries, int64_t *table)
+{
+    if (n < 0)
+        return MOONEP_ERR_ARG;
+    if (n && (!src || !counts || !types))
+        return MOONEP_ERR_NULL_PTR;
+    int64_t need = 0, spans = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (counts[i] < 0 || counts[i] > kMostElements ||
+            (types[i] != MOONEP_F32 && types[i] != MOONEP_BF16))
+            return MOONEP_ERR_ARG;
+        if (!counts[i])
+            continue;
+        const uint64_t size = types[i] == MOONEP_BF16 ? 2 : 4, to = dst ? dst[i] : src[i];
+        if (!src[i] || !to)
+            return MOONEP_ERR_NULL_PTR;
+        if (src[i] % size || to % size)
+            return MOONEP_ERR_MISALIGNED;
+        need += (counts[i] + MOONEP_GRAD_RUN - 1) / MOONEP_GRAD_RUN;
+        spans += to == src[i] ? 1 : 2;
+    }
+    if (need > entries)
+        return MOONEP_ERR_WORKSPACE;
+    if (need && !table)
+        return MOONEP_ERR_NULL_PTR;
+    if (!need)
+        return MOONEP_OK;
+    // every span of memory in order of its address: none may begin inside another
+    struct Span {
+        uint64_t at, end;
+    };
+    Span *all = (Span *)malloc((size_t)spans * sizeof(Span));
+    if (!all)
+        return MOONEP_ERR_WORKSPACE;
+    int64_t k = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (!counts[i])
+            continue;
+        const uint64_t bytes = (uint64_t)counts[i] * (types[i] == MOONEP_BF16 ? 2 : 4);
+        all[k++] = {src[i], src[i] + bytes};
+        if (dst && dst[i] != src[i])
+            all[k++] = {dst[i], dst[i] + bytes};
+    }
+    std::sort(all, all + spans, [](const Span &a, const Span &b) { return a.at < b.at; });
+    bool shared = false;
+    for (int64_t i = 1; i < spans; ++i)
+        shared |= all[i].at < all[i - 1].end;
+    free(all);
+    if (shared)
+        return MOONEP_ERR_ALIAS;
+    int64_t *w = table;
+    for (int64_t i = 0; i < n; ++i) {
+        const uint64_t size = types[i] == MOONEP_BF16 ? 2 : 4, to = dst ? dst[i] : src[i];
+        for (int64_t at = 0; at < counts[i]; at += MOONEP_GRAD_RUN, w += 4) {
+            w[0] = (int64_t)(src[i] + at * size);
+            w[1] = (int64_t)(to + at * size);
+            w[2] = counts[i] - at < MOONEP_GRAD_RUN ? counts[i] - at : MOONEP_GRAD_RUN;
+            w[3] = types[i];
+        }
+    }
+    return MOONEP_OK;
+}
+
+int moonep_grad_norm(int64_t entries, const int64_t *table, double *sumsq, float *norm,
+                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (entries < 0)
+        return MOONEP_ERR_ARG;
+    if (!present(table, entries) || !norm || !workspace)
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(table, 8) || !aligned(sumsq, 8) || !aligned(norm, 4) || !aligned(workspace, 8))
+        return MOONEP_ERR_MISALIGNED;
+    if (workspace_bytes < grad_workspace())
+        return MOONEP_ERR_WORKSPACE;
+    const Range out[] = {{norm, 4}, {sumsq, sumsq ? 8u : 0u}, {workspace, workspace_bytes}};
+    const Range in[] = {{table, (size_t)entries * 32}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
+    return launch_grad_norm(table, entries, sumsq, norm, workspace, (hipStream_t)stream);
+}
+
+int moonep_grad_clip(int64_t entries, const int64_t *table, double max_norm, const double *sumsq,
+                     float *norm, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (entries < 0 || !isfinite(max_norm) || max_norm < 0)
+        return MOONEP_ERR_ARG;
+    if (!present(table, entries) || !norm || (!sumsq && !workspace))
+        return MOONEP_ERR_NULL_PTR;
+    if (!aligned(table, 8) || !aligned(sumsq, 8) || !aligned(norm, 4) || !aligned(workspace, 8))
+        return MOONEP_ERR_MISALIGNED;
+    if (!sumsq && workspace_bytes < grad_workspace())
+        return MOONEP_ERR_WORKSPACE;
+    const Range out[] = {{norm, 4}, {workspace, workspace ? workspace_bytes : 0}};
+    const Range in[] = {{table, (size_t)entries * 32}, {sumsq, sumsq ? 8u : 0u}};
+    if (aliased(out, in))
+        return MOONEP_ERR_ALIAS;
+    return launch_grad_clip(table, entries, max_norm, sumsq, norm, workspace, (hipStream_t)stream);
 }
 
 int moonep_read_error(void *workspace, size_t workspace_bytes, int32_t *host_code, void *stream)

@@ -44,6 +44,15 @@ struct SegTables {
         return (h >= 0 && h < R && e >= 0 && e < E && off >= 0 && n >= 0 && off <= C - n) ? n : 0;
     }
 
+    // First buffer row of a segment that has rows.  s is uniform.
+    __device__ __forceinline__ int64_t first_row(int32_t s) const
+    {
+        s = __builtin_amdgcn_readfirstlane(s);
+        if (s < E)
+            return (int64_t)(s / L) * C + word(plan + pl.home_row_off + s);
+        return (int64_t)word(plan + pl.rep_host + s - E) * C + word(plan + pl.rep_row_off + s - E);
+    }
+
     // First buffer row of a segment that has rows, its row count, and its weight
     // row: of the pool if *pooled, else of the home weights.  s is uniform.
     __device__ __forceinline__ int64_t segment(int32_t s, int32_t *n, int64_t *weight_row,
