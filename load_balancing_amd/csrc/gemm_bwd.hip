@@ -29,7 +29,9 @@ namespace moonep {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 namespace {
@@ -45,12 +47,69 @@ __device__ __forceinline__ int tr_offset(int lane)
     return row * RB + ((row & 3) << 6) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 }
 
-template <int RB>
-__device__ __forceinline__ bf16x8 tr_frag(const char *p)
+// LDS byte address of a generic pointer into it.
+__device__ __forceinline__ uint32_t lds_addr(const void *p)
 {
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(void *)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(void *)(p + 4 * RB));
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
+}
+
+__device__ __forceinline__ bf16x8 join(s16x4 lo, s16x4 hi)
+{
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The fragments at N LDS addresses, rows RB bytes apart.  In assembly, with its
+// wait inside: before the builtin of this read the compiler waits for every
+// LDS-DMA load in flight, the next stages' too, which leaves nothing to overlap.
+template <int RB, int N>
+__device__ __forceinline__ void tr_frags(const uint32_t (&at)[N], bf16x8 (&f)[N])
+{
+    static_assert(N == 2 || N == 4 || N == 6, "fragments a read");
+    s16x4 r[2 * N];
+    if constexpr (N == 2)
+        asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                     "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+                     "ds_read_b64_tr_b16 %2, %5\n\t"
+                     "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+                     : "v"(at[0]), "v"(at[1]), "n"(4 * RB)
+                     : "memory");
+    else if constexpr (N == 4)
+        asm volatile("ds_read_b64_tr_b16 %0, %8\n\t"
+                     "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                     "ds_read_b64_tr_b16 %2, %9\n\t"
+                     "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                     "ds_read_b64_tr_b16 %4, %10\n\t"
+                     "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                     "ds_read_b64_tr_b16 %6, %11\n\t"
+                     "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
+                       "=&v"(r[6]), "=&v"(r[7])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(4 * RB)
+                     : "memory");
+    else
+        asm volatile("ds_read_b64_tr_b16 %0, %12\n\t"
+                     "ds_read_b64_tr_b16 %1, %12 offset:%18\n\t"
+                     "ds_read_b64_tr_b16 %2, %13\n\t"
+                     "ds_read_b64_tr_b16 %3, %13 offset:%18\n\t"
+                     "ds_read_b64_tr_b16 %4, %14\n\t"
+                     "ds_read_b64_tr_b16 %5, %14 offset:%18\n\t"
+                     "ds_read_b64_tr_b16 %6, %15\n\t"
+                     "ds_read_b64_tr_b16 %7, %15 offset:%18\n\t"
+                     "ds_read_b64_tr_b16 %8, %16\n\t"
+                     "ds_read_b64_tr_b16 %9, %16 offset:%18\n\t"
+                     "ds_read_b64_tr_b16 %10, %17\n\t"
+                     "ds_read_b64_tr_b16 %11, %17 offset:%18\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
+                       "=&v"(r[6]), "=&v"(r[7]), "=&v"(r[8]), "=&v"(r[9]), "=&v"(r[10]), "=&v"(r[11])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]), "n"(4 * RB)
+                     : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = join(r[2 * i], r[2 * i + 1]);
 }
 
 __device__ __forceinline__ void dma16(const char *src, char *dst)
@@ -67,11 +126,21 @@ __device__ __forceinline__ void wait_vm()
     __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
+// A workgroup barrier that waits for this wave's LDS operations only: a
+// __syncthreads would also wait for every load in flight.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // d_x: rows of d_y against W, contracted over W's rows
 // ---------------------------------------------------------------------------
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN>
 struct DxCfg {
     static constexpr int kTM = WM / 32, kTN = WN / 32;
     static constexpr int kWM = BM / WM, kWN = BN / WN;
@@ -81,12 +150,15 @@ struct DxCfg {
     static constexpr int kStageA = BM * kRowA, kStageB = kBK * kRowB;
     static constexpr int kStageBytes = kStageA + kStageB;
     static constexpr int kAInstr = kStageA / 1024 / kWavesG, kBInstr = kStageB / 1024 / kWavesG;
-    static constexpr int kPerStage = kAInstr + kBInstr;
-    static constexpr int kLdo = BN + 8;
-    static constexpr int kOVec = WM * BN / 8 / kThreads;
-    static_assert(WM * kLdo * 2 <= S * kStageBytes, "an epilogue band must fit the ring");
+    // Epilogue: each wave's own 16 rows of WN columns, apart from the ring, which
+    // is loading the next item.
+    static constexpr int kOutRow = WN * 2 + 16, kOutAt = 2 * kStageBytes;
+    static constexpr int kPieces = WN / 8;  // 16-byte pieces of a row
+    static constexpr int kOVec = 16 * kPieces / 64;
+    static constexpr int kStores = kTM * 2 * kOVec;  // per wave and item
+    static constexpr int kSegAt = kOutAt + kWavesG * 16 * kOutRow;
     static_assert(kStageA % (1024 * kWavesG) == 0 && kStageB % (1024 * kWavesG) == 0, "DMA rounds");
-    static_assert((S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
+    static_assert(16 * kPieces % 64 == 0, "whole stores of 16 rows");
     // 16-byte chunk c of row r of the A part sits at c ^ swz(r), as in gemm.hip
     __device__ static constexpr int swz(int r) { return (r / 2) % 8; }
 };
@@ -101,160 +173,182 @@ struct DxArgs {
 
 constexpr int kGroupM = 8;  // row tiles per item group, as in gemm.hip
 
-template <int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__((DxCfg<BM, BN, WM, WN, S>::kThreads)) void expert_dx_kernel(DxArgs a)
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_kernel(DxArgs a)
 {
-    using G = DxCfg<BM, BN, WM, WN, S>;
+    using G = DxCfg<BM, BN, WM, WN>;
     extern __shared__ __align__(16) uint16_t lds[];
     char *ring = (char *)lds;
-    int32_t *seg_start = (int32_t *)(ring + S * G::kStageBytes);  // [E + cap + 1]
+    int32_t *seg_start = (int32_t *)(ring + G::kSegAt);  // [E + cap + 1]
     __shared__ int scan_tmp[G::kWavesG];
 
-    const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t nseg = a.seg.E + a.seg.n_rep();
-    const int32_t total_tiles = scan_tiles<BM, G::kWavesG>(a.seg, nseg, seg_start, scan_tmp);
+    const int32_t tiles = scan_tiles<BM, G::kWavesG>(a.seg, nseg, seg_start, scan_tmp);
     const int32_t nbn = (a.in_dim + BN - 1) / BN;  // the last block may be part-empty
-    const int64_t items = (int64_t)total_tiles * nbn;
+    const int64_t items = (int64_t)tiles * nbn;
     const int P = (int)gridDim.x;
-    const int slot = xcd_slot((int)blockIdx.x, P);
+    const int64_t first = xcd_slot((int)blockIdx.x, P);
+    if (first >= items)
+        return;
     const int32_t nk = a.out_dim / kBK;
     const int wm = wave / G::kWN, wn = wave % G::kWN;
 
-    for (int64_t it = slot; it < items; it += P) {
-        int32_t t, nb;
-        item_of<kGroupM>(it, total_tiles, nbn, &t, &nb);
+    struct Item {
+        int64_t m0;
+        int32_t mrows, n0;
+        const uint16_t *w;
+    };
+    auto locate = [&](int64_t it) -> Item {
+        Item i;
+        int32_t t, nb, len;
+        item_of<kGroupM>(it, tiles, nbn, &t, &nb);
         const int32_t s = find_segment(seg_start, nseg, t);
-        const int32_t mt = t - seg_start[s];
+        const int32_t mt = t - __builtin_amdgcn_readfirstlane(seg_start[s]);
         int64_t wrow;
         bool pooled;
-        int32_t len;
-        const int64_t row0 = a.seg.segment(s, &len, &wrow, &pooled);
-        const uint16_t *wbase = (pooled ? a.pool : a.w_home) + wrow * a.w_stride + a.w_offset;
-        const int64_t m0 = row0 + (int64_t)mt * BM;
-        const int32_t mrows = len - mt * BM < BM ? len - mt * BM : BM;
-        const int32_t n0 = nb * BN;
+        i.m0 = a.seg.segment(s, &len, &wrow, &pooled) + (int64_t)mt * BM;
+        i.mrows = len - mt * BM < BM ? len - mt * BM : BM;
+        i.n0 = nb * BN;
+        i.w = (pooled ? a.pool : a.w_home) + wrow * a.w_stride + a.w_offset;
+        return i;
+    };
 
-        uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
+    // ---- the loads: the stages of all items in one sequence -------------------
+    int64_t load_it = first;
+    int32_t load_kt = 0;
+    const char *a_base, *b_base;
+    uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
+    auto begin_item = [&]() {
+        const Item i = locate(load_it);
+        a_base = (const char *)(a.d_y + i.m0 * a.out_dim);
+        b_base = (const char *)(i.w + i.n0);
+        // rows and columns past the end are not stored: the first serve them
 #pragma unroll
         for (int v = 0; v < G::kAInstr; ++v) {
             const int row = (v * G::kWavesG + wave) * 8 + lane / 8;
             const int chunk = (lane % 8) ^ G::swz(row);
-            a_off[v] = (uint32_t)(row < mrows ? row : 0) * (uint32_t)a.out_dim * 2 + chunk * 16;
+            a_off[v] = (uint32_t)(row < i.mrows ? row : 0) * (uint32_t)a.out_dim * 2 + chunk * 16;
         }
 #pragma unroll
         for (int v = 0; v < G::kBInstr; ++v) {
             constexpr int kCpr = G::kRowB / 16;
             const int at = (v * G::kWavesG + wave) * 64 + lane;
             const int row = at / kCpr, chunk = (at % kCpr) ^ ((row & 3) << 2);
-            const int32_t col = n0 + chunk * 8;
-            b_off[v] = (uint32_t)row * (uint32_t)a.in_dim * 2 + (uint32_t)(col < a.in_dim ? col : 0) * 2;
+            b_off[v] = (uint32_t)row * (uint32_t)a.in_dim * 2 + (i.n0 + chunk * 8 < a.in_dim ? chunk * 16 : 0);
         }
-        const char *a_base = (const char *)(a.d_y + m0 * a.out_dim);
-        const char *b_base = (const char *)wbase;
-        const int64_t b_step = (int64_t)kBK * a.in_dim * 2;
-        auto issue = [&](int32_t kt, int st) {
-            char *dst = ring + st * G::kStageBytes + wave * 1024;
-            const char *ap = a_base + (int64_t)kt * G::kRowA;
-            const char *bp = b_base + kt * b_step;
+    };
+    // Issues the next stage into slot `to`, if one is left.
+    auto issue = [&](int to) {
+        if (load_kt == nk) {
+            load_kt = 0;
+            load_it += P;
+            if (load_it < items)
+                begin_item();
+        }
+        if (load_it >= items)
+            return;
+        char *dst = ring + to * G::kStageBytes + wave * 1024;
 #pragma unroll
-            for (int v = 0; v < G::kAInstr; ++v)
-                dma16(ap + a_off[v], dst + v * G::kWavesG * 1024);
+        for (int v = 0; v < G::kAInstr; ++v)
+            dma16(a_base + a_off[v], dst + v * G::kWavesG * 1024);
 #pragma unroll
-            for (int v = 0; v < G::kBInstr; ++v)
-                dma16(bp + b_off[v], dst + G::kStageA + v * G::kWavesG * 1024);
-        };
-        const int fr = lane & 31, fsw = G::swz(lane & 31), fhalf = lane >> 5;
-        auto frag_a = [&](const char *base, int row0, int ks) -> bf16x8 {
-            return *(const bf16x8 *)(base + (row0 + fr) * G::kRowA + (((2 * ks + fhalf) ^ fsw) << 4));
-        };
-        const int tr0 = tr_offset<G::kRowB>(lane);
-        auto frag_b = [&](const char *base, int tile, int ks) -> bf16x8 {
-            return tr_frag<G::kRowB>(base + (tr0 ^ (tile << 6)) + ks * 16 * G::kRowB);
-        };
+        for (int v = 0; v < G::kBInstr; ++v)
+            dma16(b_base + b_off[v], dst + G::kStageA + v * G::kWavesG * 1024);
+        a_base += G::kRowA;
+        b_base += (int64_t)kBK * a.in_dim * 2;
+        ++load_kt;
+    };
 
+    const int fr = lane & 31, fsw = G::swz(lane & 31), fhalf = lane >> 5;
+    auto frag_a = [&](const char *base, int row0, int ks) -> bf16x8 {
+        return *(const bf16x8 *)(base + (row0 + fr) * G::kRowA + (((2 * ks + fhalf) ^ fsw) << 4));
+    };
+    uint32_t b_at[G::kTN];
+#pragma unroll
+    for (int j = 0; j < G::kTN; ++j)
+        b_at[j] = lds_addr(ring) + G::kStageA + (tr_offset<G::kRowB>(lane) ^ ((wn * G::kTN + j) << 6));
+    char *mine = ring + G::kOutAt + wave * 16 * G::kOutRow;
+
+    begin_item();
+    issue(0);
+    int now = 0;               // slot of the stage computed next; the ring runs on across items
+    bool stores_ahead = false;  // of the loads of this item's first stage, kStores were issued
+    for (int64_t it = first; it < items; it += P) {
+        const Item i = locate(it);
         f32x16 acc[G::kTM][G::kTN];
 #pragma unroll
-        for (int i = 0; i < G::kTM; ++i)
+        for (int m = 0; m < G::kTM; ++m)
 #pragma unroll
-            for (int j = 0; j < G::kTN; ++j)
+            for (int n = 0; n < G::kTN; ++n)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    acc[i][j][r] = 0.0f;
-
-#pragma unroll
-        for (int st = 0; st + 1 < S; ++st)
-            if (st < nk)
-                issue(st, st);
+                    acc[m][n][r] = 0.0f;
         for (int32_t kt = 0; kt < nk; ++kt) {
-            // this wave's loads of stage kt have landed once at most the later
-            // stages' loads are outstanding
-            if (kt + S - 2 < nk)
-                wait_vm<(S - 2) * G::kPerStage>();
+            // An item's first stage was issued before the stores of the item
+            // before: where all of those were issued, they need not be waited for.
+            if (kt == 0 && stores_ahead)
+                wait_vm<G::kStores>();
             else
                 wait_vm<0>();
-            __syncthreads();  // stage kt is visible to all; slot (kt - 1) % S is free
-            if (kt + S - 1 < nk)
-                issue(kt + S - 1, (kt + S - 1) % S);
-            const char *sa = ring + (kt % S) * G::kStageBytes;
-            const char *sb = sa + G::kStageA;
-            bf16x8 fa[2][G::kTM], fb[2][G::kTN];
-#pragma unroll
-            for (int i = 0; i < G::kTM; ++i)
-                fa[0][i] = frag_a(sa, wm * WM + i * 32, 0);
-#pragma unroll
-            for (int j = 0; j < G::kTN; ++j)
-                fb[0][j] = frag_b(sb, wn * G::kTN + j, 0);
+            lds_barrier();  // the stage is visible to all; the other slot is free
+            issue(now ^ 1);
+            const char *sa = ring + now * G::kStageBytes;
 #pragma unroll
             for (int ks = 0; ks < kBK / 16; ++ks) {
-                const int cur = ks & 1, nxt = cur ^ 1;
-                if (ks + 1 < kBK / 16) {
+                bf16x8 fa[G::kTM], fb[G::kTN];
+                uint32_t at[G::kTN];
 #pragma unroll
-                    for (int i = 0; i < G::kTM; ++i)
-                        fa[nxt][i] = frag_a(sa, wm * WM + i * 32, ks + 1);
+                for (int m = 0; m < G::kTM; ++m)
+                    fa[m] = frag_a(sa, wm * WM + m * 32, ks);
 #pragma unroll
-                    for (int j = 0; j < G::kTN; ++j)
-                        fb[nxt][j] = frag_b(sb, wn * G::kTN + j, ks + 1);
-                }
+                for (int n = 0; n < G::kTN; ++n)
+                    at[n] = b_at[n] + now * G::kStageBytes + ks * 16 * G::kRowB;
+                tr_frags<G::kRowB>(at, fb);
+                // W's columns as the instruction's rows: a lane's results are four
+                // consecutive columns of one row of d_x
 #pragma unroll
-                for (int i = 0; i < G::kTM; ++i)
+                for (int m = 0; m < G::kTM; ++m)
 #pragma unroll
-                    for (int j = 0; j < G::kTN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[cur][i], fb[cur][j],
-                                                                            acc[i][j], 0, 0, 0);
+                    for (int n = 0; n < G::kTN; ++n)
+                        acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[n], fa[m], acc[m][n], 0, 0, 0);
             }
+            now ^= 1;
         }
-        __syncthreads();  // every wave is done with the ring before the epilogue reuses it
-
-        // epilogue: one band of wave rows at a time through LDS, as in gemm.hip
-        uint16_t *so = lds;
+        // Epilogue: 16 rows at a time through the wave's own LDS, to whole lines.
+        const bool full = i.mrows == BM && i.n0 + BN <= a.in_dim;
+        stores_ahead = full;
 #pragma unroll
-        for (int band = 0; band < G::kWM; ++band) {
-            if (wm == band) {
+        for (int m = 0; m < G::kTM; ++m)
 #pragma unroll
-                for (int i = 0; i < G::kTM; ++i)
+            for (int half = 0; half < 2; ++half) {
+                if ((lane >> 4 & 1) == half) {
+                    char *to = mine + (lane & 15) * G::kOutRow + (lane >> 5) * 8;
 #pragma unroll
-                    for (int j = 0; j < G::kTN; ++j)
+                    for (int n = 0; n < G::kTN; ++n)
 #pragma unroll
-                        for (int r = 0; r < 16; r += 2) {
-                            const int row = i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
-                            const int col = wn * WN + j * 32 + (lane & 31);
-                            const uint32_t p = pack_bf16(acc[i][j][r], acc[i][j][r + 1]);
-                            so[row * G::kLdo + col] = (uint16_t)(p & 0xFFFFu);
-                            so[(row + 1) * G::kLdo + col] = (uint16_t)(p >> 16);
+                        for (int q = 0; q < 4; ++q) {
+                            u32x2 v;
+                            v[0] = pack_bf16(acc[m][n][4 * q], acc[m][n][4 * q + 1]);
+                            v[1] = pack_bf16(acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]);
+                            *(u32x2 *)(to + n * 64 + q * 16) = v;
                         }
-            }
-            __syncthreads();
+                }
+                wave_sync();
 #pragma unroll
-            for (int v = 0; v < G::kOVec; ++v) {
-                const int idx = tid + v * G::kThreads;
-                const int row = idx / (BN / 8), c = idx % (BN / 8);
-                const int grow = band * WM + row;
-                if (grow < mrows && n0 + c * 8 < a.in_dim)
-                    *(u32x4 *)(a.d_x + (m0 + grow) * a.in_dim + n0 + c * 8) =
-                        *(const u32x4 *)(so + row * G::kLdo + c * 8);
+                for (int v = 0; v < G::kOVec; ++v) {
+                    const int idx = lane + v * 64, r = idx / G::kPieces, c = idx % G::kPieces;
+                    const u32x4 piece = *(const u32x4 *)(mine + r * G::kOutRow + c * 16);
+                    const int row = wm * WM + m * 32 + half * 16 + r, col = i.n0 + wn * WN + c * 8;
+                    u32x4 *p = (u32x4 *)(a.d_x + (i.m0 + row) * a.in_dim + col);
+                    if (full)
+                        *p = piece;
+                    else if (row < i.mrows && col < a.in_dim)
+                        *p = piece;
+                }
+                wave_sync();
             }
-            __syncthreads();
-        }
     }
 }
 
@@ -262,19 +356,19 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN, S>::kThreads)) void expert_d
 // g: both operands contracted over the segment's rows
 // ---------------------------------------------------------------------------
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int BK, int S>
 struct DwCfg {
     static constexpr int kTM = WM / 32, kTN = WN / 32;
     static constexpr int kWM = BM / WM, kWN = BN / WN;
     static constexpr int kWavesG = kWM * kWN;
     static constexpr int kThreads = kWavesG * 64;
     static constexpr int kRowA = BM * 2, kRowB = BN * 2;
-    static constexpr int kStageA = kBK * kRowA, kStageB = kBK * kRowB;
+    static constexpr int kStageA = BK * kRowA, kStageB = BK * kRowB;
     static constexpr int kStageBytes = kStageA + kStageB;
     static constexpr int kAInstr = kStageA / 1024 / kWavesG, kBInstr = kStageB / 1024 / kWavesG;
     static constexpr int kPerStage = kAInstr + kBInstr;
     static_assert(kStageA % (1024 * kWavesG) == 0 && kStageB % (1024 * kWavesG) == 0, "DMA rounds");
-    static_assert((S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
+    static_assert(S >= 2 && (S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
 };
 
 struct DwArgs {
@@ -289,72 +383,133 @@ struct DwArgs {
 // nothing whatever the buffer holds there.
 __device__ const uint32_t g_zero_row[4] = {0, 0, 0, 0};
 
-template <int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, S>::kThreads)) void expert_dw_kernel(DwArgs a)
+template <int BM, int BN, int WM, int WN, int BK, int S>
+__global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expert_dw_kernel(DwArgs a)
 {
-    using G = DwCfg<BM, BN, WM, WN, S>;
+    using G = DwCfg<BM, BN, WM, WN, BK, S>;
     extern __shared__ __align__(16) uint16_t lds[];
     char *ring = (char *)lds;
-    const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid >> 6;
+    const int tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t nseg = a.seg.E + a.seg.n_rep();
     const int32_t nbm = (a.out_dim + BM - 1) / BM, nbn = (a.in_dim + BN - 1) / BN;
     const int64_t per = (int64_t)nbm * nbn, items = nseg * per;
-    const int P = (int)gridDim.x;
+    const int P = (int)gridDim.x, slot = xcd_slot((int)blockIdx.x, P);
     const int wm = wave / G::kWN, wn = wave % G::kWN;
 
-    for (int64_t it = xcd_slot((int)blockIdx.x, P); it < items; it += P) {
-        const int32_t s = (int32_t)(it / per), within = (int32_t)(it - s * per);
-        const int32_t mb = within % nbm, nb = within / nbm;
-        const int32_t m0 = mb * BM, n0 = nb * BN;
-        const int32_t len = __builtin_amdgcn_readfirstlane(a.seg.rows(s));
-        const int64_t row0 = len ? a.seg.first_row(s) : 0;
-        float *out = s < a.seg.E ? a.home + s * a.G : a.rep + (int64_t)(s - a.seg.E) * a.G;
-        out += a.g_offset;
+    // The segments from the longest to the shortest (of equals the lower first):
+    // each one's place is the number of those before it.
+    int32_t *length = (int32_t *)(ring + S * G::kStageBytes);  // [nseg, padded to 4]
+    int32_t *by_length = length + (nseg + 3) / 4 * 4;          // [nseg]
+    for (int32_t i = tid; i < (nseg + 3) / 4 * 4; i += G::kThreads)
+        length[i] = i < nseg ? a.seg.rows(i) : -1;
+    __syncthreads();
+    for (int32_t i = tid; i < nseg; i += G::kThreads) {
+        const int32_t mine = length[i];
+        int32_t place = 0;
+        for (int32_t j = 0; j < nseg; j += 4) {
+            const i32x4 o = *(const i32x4 *)(length + j);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                place += o[q] > mine || (o[q] == mine && j + q < i);
+        }
+        by_length[place] = i;
+    }
+    __syncthreads();
 
+    // Rounds of P items, every other one backwards, so that whoever has a
+    // round's longest item has the next one's shortest.
+    const int64_t rounds = (items + P - 1) / P;
+    struct Item {
+        int32_t s, len, m0, n0;
+    };
+    auto locate = [&](int64_t round, Item *w) -> bool {
+        const int64_t it = round * P + (round & 1 ? P - 1 - slot : slot);
+        if (it >= items)
+            return false;
+        const int32_t at = (int32_t)(it / per), within = (int32_t)(it - at * per);
+        w->s = __builtin_amdgcn_readfirstlane(by_length[at]);
+        w->len = __builtin_amdgcn_readfirstlane(length[w->s]);
+        w->m0 = within % nbm * BM;
+        w->n0 = within / nbm * BN;
+        return true;
+    };
+
+    // ---- the loads: the stages of all items in one sequence -------------------
+    struct Load {
+        int64_t round;
+        int32_t left;  // rows from the next stage's first on
+        const char *a_base, *b_base;
         uint32_t a_off[G::kAInstr], b_off[G::kBInstr];
-        int a_row[G::kAInstr], b_row[G::kBInstr];
+    } ld;
+    auto a_row = [&](int v) { return ((v * G::kWavesG + wave) * 64 + lane) / (G::kRowA / 16); };
+    auto b_row = [&](int v) { return ((v * G::kWavesG + wave) * 64 + lane) / (G::kRowB / 16); };
+    auto begin_item = [&]() {  // the next one with rows; none leaves left = 0
+        Item w;
+        ld.left = 0;
+        while (++ld.round < rounds) {
+            if (!locate(ld.round, &w) || !w.len)
+                continue;
+            const int64_t row0 = a.seg.first_row(w.s);
+            ld.left = w.len;
+            ld.a_base = (const char *)(a.d_y + row0 * a.out_dim + w.m0);
+            ld.b_base = (const char *)(a.x + row0 * a.in_dim + w.n0);
+            // columns past the end are not stored: the block's first serve them
 #pragma unroll
-        for (int v = 0; v < G::kAInstr; ++v) {
-            constexpr int kCpr = G::kRowA / 16;
-            const int at = (v * G::kWavesG + wave) * 64 + lane;
-            const int row = at / kCpr, chunk = (at % kCpr) ^ ((row & 3) << 2);
-            const int32_t col = m0 + chunk * 8;
-            a_row[v] = row;
-            a_off[v] = (uint32_t)row * (uint32_t)a.out_dim * 2 + (uint32_t)(col < a.out_dim ? col : 0) * 2;
+            for (int v = 0; v < G::kAInstr; ++v) {
+                const int row = a_row(v), chunk = (lane % (G::kRowA / 16)) ^ ((row & 3) << 2);
+                ld.a_off[v] = (uint32_t)row * (uint32_t)a.out_dim * 2 +
+                              (w.m0 + chunk * 8 < a.out_dim ? chunk * 16 : 0);
+            }
+#pragma unroll
+            for (int v = 0; v < G::kBInstr; ++v) {
+                const int row = b_row(v), chunk = (lane % (G::kRowB / 16)) ^ ((row & 3) << 2);
+                ld.b_off[v] = (uint32_t)row * (uint32_t)a.in_dim * 2 +
+                              (w.n0 + chunk * 8 < a.in_dim ? chunk * 16 : 0);
+            }
+            return;
         }
+    };
+    const char *zero = (const char *)g_zero_row;
+    // Issues the next stage into slot `to`.  After the last item the loads go on
+    // with zeros, which nobody computes: so every stage is followed by as many.
+    auto issue = [&](int to) {
+        if (ld.left <= 0)
+            begin_item();
+        char *dst = ring + to * G::kStageBytes + wave * 1024;
 #pragma unroll
-        for (int v = 0; v < G::kBInstr; ++v) {
-            constexpr int kCpr = G::kRowB / 16;
-            const int at = (v * G::kWavesG + wave) * 64 + lane;
-            const int row = at / kCpr, chunk = (at % kCpr) ^ ((row & 3) << 2);
-            const int32_t col = n0 + chunk * 8;
-            b_row[v] = row;
-            b_off[v] = (uint32_t)row * (uint32_t)a.in_dim * 2 + (uint32_t)(col < a.in_dim ? col : 0) * 2;
-        }
-        const char *a_base = (const char *)(a.d_y + row0 * a.out_dim);
-        const char *b_base = (const char *)(a.x + row0 * a.in_dim);
-        const int64_t a_step = (int64_t)kBK * a.out_dim * 2, b_step = (int64_t)kBK * a.in_dim * 2;
-        const char *zero = (const char *)g_zero_row;
-        auto issue = [&](int32_t kt, int st) {
-            char *dst = ring + st * G::kStageBytes + wave * 1024;
-            const char *ap = a_base + kt * a_step;
-            const char *bp = b_base + kt * b_step;
-            const int32_t left = len - kt * kBK;
+        for (int v = 0; v < G::kAInstr; ++v)
+            dma16(a_row(v) < ld.left ? ld.a_base + ld.a_off[v] : zero, dst + v * G::kWavesG * 1024);
 #pragma unroll
-            for (int v = 0; v < G::kAInstr; ++v)
-                dma16(a_row[v] < left ? ap + a_off[v] : zero, dst + v * G::kWavesG * 1024);
-#pragma unroll
-            for (int v = 0; v < G::kBInstr; ++v)
-                dma16(b_row[v] < left ? bp + b_off[v] : zero, dst + G::kStageA + v * G::kWavesG * 1024);
-        };
-        const int tra = tr_offset<G::kRowA>(lane), trb = tr_offset<G::kRowB>(lane);
-        auto frag_a = [&](const char *base, int tile, int ks) -> bf16x8 {
-            return tr_frag<G::kRowA>(base + (tra ^ (tile << 6)) + ks * 16 * G::kRowA);
-        };
-        auto frag_b = [&](const char *base, int tile, int ks) -> bf16x8 {
-            return tr_frag<G::kRowB>(base + (trb ^ (tile << 6)) + ks * 16 * G::kRowB);
-        };
+        for (int v = 0; v < G::kBInstr; ++v)
+            dma16(b_row(v) < ld.left ? ld.b_base + ld.b_off[v] : zero,
+                  dst + G::kStageA + v * G::kWavesG * 1024);
+        ld.a_base += (int64_t)BK * a.out_dim * 2;
+        ld.b_base += (int64_t)BK * a.in_dim * 2;
+        ld.left -= BK;
+    };
 
+    // LDS addresses of this wave's fragments in slot 0, k-step 0
+    uint32_t frag_at[G::kTM + G::kTN];
+#pragma unroll
+    for (int i = 0; i < G::kTM; ++i)
+        frag_at[i] = lds_addr(ring) + (tr_offset<G::kRowA>(lane) ^ ((wm * G::kTM + i) << 6));
+#pragma unroll
+    for (int j = 0; j < G::kTN; ++j)
+        frag_at[G::kTM + j] =
+            lds_addr(ring) + G::kStageA + (tr_offset<G::kRowB>(lane) ^ ((wn * G::kTN + j) << 6));
+
+    ld.round = -1;
+    ld.left = 0;
+    ld.a_base = ld.b_base = zero;
+#pragma unroll
+    for (int st = 0; st + 1 < S; ++st)
+        issue(st);
+    int now = 0;  // slot of the stage computed next
+    for (int64_t round = 0; round < rounds; ++round) {
+        Item w;
+        if (!locate(round, &w))
+            continue;
         f32x16 acc[G::kTM][G::kTN];
 #pragma unroll
         for (int i = 0; i < G::kTM; ++i)
@@ -364,57 +519,44 @@ __global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, S>::kThreads)) void expert_d
                 for (int r = 0; r < 16; ++r)
                     acc[i][j][r] = 0.0f;
 
-        const int32_t nk = (len + kBK - 1) / kBK;
-        __syncthreads();  // the item before is done with the ring
-#pragma unroll
-        for (int st = 0; st + 1 < S; ++st)
-            if (st < nk)
-                issue(st, st);
+        const int32_t nk = (w.len + BK - 1) / BK;
         for (int32_t kt = 0; kt < nk; ++kt) {
-            if (kt + S - 2 < nk)
-                wait_vm<(S - 2) * G::kPerStage>();
-            else
-                wait_vm<0>();
-            __syncthreads();
-            if (kt + S - 1 < nk)
-                issue(kt + S - 1, (kt + S - 1) % S);
-            const char *sa = ring + (kt % S) * G::kStageBytes;
-            const char *sb = sa + G::kStageA;
-            bf16x8 fa[2][G::kTM], fb[2][G::kTN];
+            // this wave's loads of the stage have landed once only those of the S - 2
+            // later ones are outstanding
+            wait_vm<(S - 2) * G::kPerStage>();
+            lds_barrier();  // the stage is visible to all; the one before is free
+            issue(now ? now - 1 : S - 1);
+            const uint32_t stage = (uint32_t)(now * G::kStageBytes);
+            now = now + 1 == S ? 0 : now + 1;
 #pragma unroll
-            for (int i = 0; i < G::kTM; ++i)
-                fa[0][i] = frag_a(sa, wm * G::kTM + i, 0);
+            for (int ks = 0; ks < BK / 16; ++ks) {
+                static_assert(G::kRowA == G::kRowB, "one distance for all fragments");
+                uint32_t at[G::kTM + G::kTN];
+                bf16x8 f[G::kTM + G::kTN];
 #pragma unroll
-            for (int j = 0; j < G::kTN; ++j)
-                fb[0][j] = frag_b(sb, wn * G::kTN + j, 0);
-#pragma unroll
-            for (int ks = 0; ks < kBK / 16; ++ks) {
-                const int cur = ks & 1, nxt = cur ^ 1;
-                if (ks + 1 < kBK / 16) {
-#pragma unroll
-                    for (int i = 0; i < G::kTM; ++i)
-                        fa[nxt][i] = frag_a(sa, wm * G::kTM + i, ks + 1);
-#pragma unroll
-                    for (int j = 0; j < G::kTN; ++j)
-                        fb[nxt][j] = frag_b(sb, wn * G::kTN + j, ks + 1);
-                }
+                for (int i = 0; i < G::kTM + G::kTN; ++i)
+                    at[i] = frag_at[i] + stage + ks * 16 * G::kRowA;
+                tr_frags<G::kRowA>(at, f);
 #pragma unroll
                 for (int i = 0; i < G::kTM; ++i)
 #pragma unroll
                     for (int j = 0; j < G::kTN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[cur][i], fb[cur][j],
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i], f[G::kTM + j],
                                                                             acc[i][j], 0, 0, 0);
             }
         }
+        if (a.accumulate && !nk)
+            continue;
         // a register's 32 lanes hold 32 consecutive columns: whole 128-byte lines
+        float *out = w.s < a.seg.E ? a.home + w.s * a.G : a.rep + (int64_t)(w.s - a.seg.E) * a.G;
+        out += a.g_offset;
 #pragma unroll
         for (int i = 0; i < G::kTM; ++i)
 #pragma unroll
             for (int j = 0; j < G::kTN; ++j) {
-                const int32_t row = m0 + wm * WM + i * 32 + (lane >> 5) * 4;
-                const int32_t col = n0 + wn * WN + j * 32 + (lane & 31);
-                if (m0 + wm * WM + i * 32 < a.out_dim && n0 + wn * WN + j * 32 < a.in_dim) {
-                    float *p = out + (int64_t)row * a.in_dim + col;
+                const int32_t row = w.m0 + wm * WM + i * 32, col = w.n0 + wn * WN + j * 32;
+                if (row < a.out_dim && col < a.in_dim) {
+                    float *p = out + (int64_t)(row + (lane >> 5) * 4) * a.in_dim + col + (lane & 31);
                     if (a.accumulate) {
                         float old[16];
 #pragma unroll
@@ -430,6 +572,7 @@ __global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, S>::kThreads)) void expert_d
                 }
             }
     }
+    wait_vm<0>();  // nothing is on its way into the LDS when it is given back
 }
 
 // The device's compute units, and the kernel's dynamic-LDS limit raised once
@@ -451,37 +594,38 @@ int prepare_launch(Kernel kernel, size_t most, bool (&raised)[64], int *cus)
     return MOONEP_OK;
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN>
 int run_dx(const DxArgs &a, hipStream_t st)
 {
-    using G = DxCfg<BM, BN, WM, WN, S>;
-    constexpr size_t kRing = (size_t)S * G::kStageBytes;
+    using G = DxCfg<BM, BN, WM, WN>;
     static bool raised[64] = {};
     int cus = 0;
-    const int rc = prepare_launch(expert_dx_kernel<BM, BN, WM, WN, S>,
-                                  kRing + (size_t)(2 * kMaxExperts + kMaxRanks + 1) * 4, raised, &cus);
+    const int rc = prepare_launch(expert_dx_kernel<BM, BN, WM, WN>,
+                                  G::kSegAt + (size_t)(2 * kMaxExperts + kMaxRanks + 1) * 4, raised, &cus);
     if (rc != MOONEP_OK)
         return rc;
-    const size_t bytes = kRing + (size_t)(a.seg.E + a.seg.pl.cap + 1) * 4;
+    const size_t bytes = G::kSegAt + (size_t)(a.seg.E + a.seg.pl.cap + 1) * 4;
     const int per_cu = (int)((160u << 10) / bytes);
-    hipLaunchKernelGGL((expert_dx_kernel<BM, BN, WM, WN, S>), dim3(cus * (per_cu > 1 ? 2 : 1)),
+    hipLaunchKernelGGL((expert_dx_kernel<BM, BN, WM, WN>), dim3(cus * (per_cu > 1 ? per_cu : 1)),
                        dim3(G::kThreads), bytes, st, a);
     return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP;
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int BK, int S>
 int run_dw(const DwArgs &a, hipStream_t st)
 {
-    using G = DwCfg<BM, BN, WM, WN, S>;
+    using G = DwCfg<BM, BN, WM, WN, BK, S>;
     constexpr size_t kRing = (size_t)S * G::kStageBytes;
     static bool raised[64] = {};
     int cus = 0;
-    const int rc = prepare_launch(expert_dw_kernel<BM, BN, WM, WN, S>, kRing, raised, &cus);
+    const int rc = prepare_launch(expert_dw_kernel<BM, BN, WM, WN, BK, S>,
+                                  kRing + (size_t)(2 * (2 * kMaxExperts + kMaxRanks) + 4) * 4, raised, &cus);
     if (rc != MOONEP_OK)
         return rc;
-    const int per_cu = (int)((160u << 10) / kRing);
-    hipLaunchKernelGGL((expert_dw_kernel<BM, BN, WM, WN, S>), dim3(cus * (per_cu > 1 ? 2 : 1)),
-                       dim3(G::kThreads), kRing, st, a);
+    const size_t bytes = kRing + (size_t)(2 * (a.seg.E + a.seg.pl.cap) + 4) * 4;
+    const int per_cu = (int)((160u << 10) / bytes);
+    hipLaunchKernelGGL((expert_dw_kernel<BM, BN, WM, WN, BK, S>), dim3(cus * (per_cu > 1 ? per_cu : 1)),
+                       dim3(G::kThreads), bytes, st, a);
     return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP;
 }
 
@@ -496,7 +640,10 @@ int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *
         return MOONEP_OK;
     const DxArgs a{seg_tables(s, plan, wslot, B), in_dim, out_dim, d_y, w_home, pool,
                    w_stride, w_offset, d_x};
-    return run_dx<256, 256, 128, 64, 2>(a, st);
+#ifdef DXV
+    return run_dx<DXV>(a, st);
+#endif
+    return run_dx<256, 256, 128, 64>(a, st);
 }
 
 int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim, int32_t out_dim,
@@ -507,7 +654,10 @@ int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim,
         return MOONEP_OK;
     const DwArgs a{seg_tables(s, plan, nullptr, 0), in_dim, out_dim, accumulate, x, d_y, G, g_offset,
                    home, rep};
-    return run_dw<256, 256, 128, 64, 2>(a, st);
+#ifdef DWV
+    return run_dw<DWV>(a, st);
+#endif
+    return run_dw<256, 256, 128, 64, 32, 3>(a, st);
 }
 
 }  // namespace moonep
