@@ -9,23 +9,24 @@
 //
 // All of it is bound by memory: 4 rank operations or fewer for each element of
 // x, dy, base and y, which are read or written once (dy twice in the backward).
-// Three kernels, each in the two orders of its matrix:
+// Three products, on the 16 x 16 x 32 bf16 matrix instruction, each with its
+// matrix in either order:
 //   shrink  rows [D] against a matrix, to rank values in fp32 (u, du);
 //   expand  rank values against a matrix, added to base rows (y, dx);
 //   wgrad   rank values against rows [D], summed over an adapter's rows.
-// They use the 16 x 16 x 32 bf16 matrix instruction with operands loaded
-// straight into registers, without LDS: the rows of a 16-position tile are the
-// instruction's columns, so that every lane holds one row's results, and a tile
-// whose rows have several adapters is run once for each of them, each lane
-// keeping the results of its own row's adapter (what another adapter's matrix
-// holds, NaN or infinity, cannot reach it).  Positions are taken in `order`,
-// where rows of one adapter stand together, or as they are.
+// Rows are worked on in tiles of 16 or 64 positions, in `order`, where rows of one
+// adapter stand together, or as they are.  A tile whose rows have several
+// adapters is run once for each, every row keeping the results of its own (what
+// another adapter's matrix holds, NaN or infinity, cannot reach it).
 //
 // Lane layout of the instruction (m, n: 16; k: 32): operand A lane l holds row
 // m = l % 16, k = 8 (l / 16) .. + 7; operand B lane l column n = l % 16, same k;
-// the result's lane l holds column l % 16, rows 4 (l / 16) .. + 3.  The 16 rows
-// of tile t of T stand for indexes m T + t, so that a lane's results over T
-// tiles are 4 T consecutive indexes.
+// the result's lane l holds column l % 16, rows 4 (l / 16) .. + 3.  Loaded from rows
+// as they are, an operand's neighbouring lanes are in different rows, and the
+// vector-memory path serves one 64-byte piece after the other: such kernels ran at
+// half the bandwidth.  So whatever is read for every row comes in runs: rows of x
+// through LDS, base and y with 16 lanes along a row, and the rank values laid out by
+// their producer in the order of the lanes that take them (`parts`, `turned`).
 //
 // Rounding: u and du stay in fp32.  Where they enter a product they are split
 // into bf16 parts whose products the instruction sums in fp32: two parts (16
@@ -36,13 +37,14 @@
 namespace moonep {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 namespace {
 
 constexpr int kAdBlock = 256;  // four waves
-constexpr int kMostSplits = 16;
+constexpr int kMostSplits = 14, kMostSplitsBwd = 8;
 constexpr int kMostChunks = 64;
-constexpr int32_t kSplitRows = 2048;  // up to here a tile's contraction is split
+constexpr int32_t kFewRows = 256;  // up to here a tile's adapters are spread over waves
 
 union Frag {
     uint16_t h[8];
@@ -103,35 +105,297 @@ struct ShrinkArgs {
     AdRows r;
     AdMats w;
     const uint16_t *x;
-    const float *scale;  // per adapter, or NULL for 1
-    float *out;          // [splits][rows][rank]
+    const float *scale;     // per adapter: of the results, or of `parts` alone
+    float *out;             // [splits][rows][rank]
+    uint16_t *parts;        // or NULL: scale * result, see Parts
 };
 
-// T tiles of 16 of the rank; kNN: the matrix is [D][rank]; RT row tiles a wave.
-// kSplit: the four waves share a row tile, each a part of the contraction, of
-// which blockIdx.y is one of gridDim.y parts; their sums are joined in LDS.
-template <int T, bool kNN, int RT, bool kSplit>
+// Two bf16 parts of a pair of values, packed: 16 bits of each.  The second part
+// of an infinity is 0.
+__device__ __forceinline__ void split2(float a, float b, uint32_t *hi, uint32_t *lo)
+{
+    const uint32_t h = pack_bf16(a, b);
+    const float h0 = bf16_lo(h), h1 = bf16_hi(h);
+    *hi = h;
+    *lo = pack_bf16(__builtin_isfinite(h0) ? a - h0 : 0.0f, __builtin_isfinite(h1) ? b - h1 : 0.0f);
+}
+
+// The two bf16 parts of rank values in the order in which expand's lanes take them:
+// for each 16 positions, steps() steps of 64 lanes x 8 values.  Lane 16 g + m of step
+// s holds chunk c = 4 s + g of position m: values 8 (c % per) .. + 7 of part c / per.
+// Chunks past the rank are not written, nor used.
+struct Parts {
+    int32_t per;  // chunks of a part: whole steps, or half of one
+    __host__ __device__ explicit Parts(int32_t rank) : per(rank <= 16 ? 2 : rank <= 32 ? 4 : rank <= 64 ? 8 : 16) {}
+    __host__ __device__ int32_t steps() const { return per / 2; }
+    // Elements before chunk c of a position.
+    __device__ int64_t at(int64_t pos, int32_t c) const
+    {
+        return ((pos / 16 * (per * 2) + c) * 16 + pos % 16) * 8;
+    }
+    // Values c .. c + 3 of a position (c % 4 == 0).
+    __device__ __forceinline__ void put(uint16_t *parts, int64_t pos, int32_t c, f32x4 v) const
+    {
+        u32x2 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t h, l;
+            split2(v[2 * j], v[2 * j + 1], &h, &l);
+            hi[j] = h;
+            lo[j] = l;
+        }
+        *(u32x2 *)(parts + at(pos, c / 8) + c % 8) = hi;
+        *(u32x2 *)(parts + at(pos, per + c / 8) + c % 8) = lo;
+    }
+};
+
+__device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ void dma16(const void *src, char *dst)
+{
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N <= 63, "vmcnt");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// A workgroup barrier that waits for this wave's LDS operations only.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// N fragments whose 8 values of k are rows of LDS: 16 lanes read 4 rows x 16
+// columns, 8 bytes each, and lane d gets column d; `lo` for the first four rows and
+// `hi` for the others.  With its wait inside: see gemm_bwd.hip.
+template <int N>
+__device__ __forceinline__ void tr_frags(const uint32_t (&lo)[N], const uint32_t (&hi)[N], Frag (&f)[N])
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    static_assert(N == 1 || N == 2 || N == 4, "fragments a read");
+    s16x4 r[2 * N];
+    if constexpr (N == 1)
+        asm volatile("ds_read_b64_tr_b16 %0, %2\n\t"
+                     "ds_read_b64_tr_b16 %1, %3\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(r[0]), "=&v"(r[1])
+                     : "v"(lo[0]), "v"(hi[0])
+                     : "memory");
+    else if constexpr (N == 2)
+        asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                     "ds_read_b64_tr_b16 %1, %5\n\t"
+                     "ds_read_b64_tr_b16 %2, %6\n\t"
+                     "ds_read_b64_tr_b16 %3, %7\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+                     : "v"(lo[0]), "v"(hi[0]), "v"(lo[1]), "v"(hi[1])
+                     : "memory");
+    else
+        asm volatile("ds_read_b64_tr_b16 %0, %8\n\t"
+                     "ds_read_b64_tr_b16 %1, %9\n\t"
+                     "ds_read_b64_tr_b16 %2, %10\n\t"
+                     "ds_read_b64_tr_b16 %3, %11\n\t"
+                     "ds_read_b64_tr_b16 %4, %12\n\t"
+                     "ds_read_b64_tr_b16 %5, %13\n\t"
+                     "ds_read_b64_tr_b16 %6, %14\n\t"
+                     "ds_read_b64_tr_b16 %7, %15\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]),
+                       "=&v"(r[6]), "=&v"(r[7])
+                     : "v"(lo[0]), "v"(hi[0]), "v"(lo[1]), "v"(hi[1]), "v"(lo[2]), "v"(hi[2]), "v"(lo[3]),
+                       "v"(hi[3])
+                     : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i].v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(r[2 * i], r[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Many rows: 64 positions a workgroup, 16 a wave, rows and matrix through a ring of
+// LDS stages of 64 values of the contraction, filled by LDS-DMA.  blockIdx.y is one
+// of gridDim.y parts of the contraction.  The matrix's stage is [16 T][64], or
+// with kNN what memory has: 64 rows of rank.
+template <int T, bool kNN>
+struct ShrinkCfg {
+    static constexpr int kRows = 64, kStageX = kRows * 128, kStageW = T * 2048;
+    static constexpr int kStageBytes = kStageX + kStageW;
+    static constexpr int kWInstr = T < 4 ? 1 : T / 2;  // loads of a wave for the matrix's stage
+    static constexpr int kPerStage = 2 + kWInstr;
+    static constexpr int kStages = T == 8 ? 3 : 4;
+    static constexpr int kLds = kStages * kStageBytes;
+    // 16-byte chunk c of row r of a stage of 128-byte rows sits at c ^ swz(r)
+    __device__ static constexpr int swz(int r) { return (r / 2) % 8; }
+};
+
+template <int T, bool kNN>
 __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 {
-    constexpr int U = T * (kNN ? 2 : 1) + RT <= 4 ? 4 : (T <= 4 ? 2 : 1);  // steps in flight
+    using G = ShrinkCfg<T, kNN>;
+    extern __shared__ __align__(16) char ring[];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int m = lane & 15, g = lane >> 4;
+    const int32_t D = a.w.D, rank = a.w.rank;
+    const int64_t p0 = (int64_t)blockIdx.x * G::kRows;
+    const int32_t steps = (D + 63) / 64;
+    const int32_t k0 = (int32_t)((int64_t)steps * blockIdx.y / gridDim.y);
+    const int32_t nk = (int32_t)((int64_t)steps * (blockIdx.y + 1) / gridDim.y) - k0;
+
+    // this lane's chunk of two rows, of its wave's two loads of a stage of rows
+    const uint16_t *xp[2];
+    int xc[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const int r = (v * 4 + wave) * 8 + lane / 8;
+        const int32_t row = a.r.row(p0 + r);
+        xc[v] = (lane % 8) ^ G::swz(r);
+        xp[v] = a.x + (int64_t)(row < 0 ? 0 : row) * D + xc[v] * 8;
+    }
+    uint64_t todo = ballot(a.r.id(a.r.row(p0 + lane)) >= 0);  // the same in every wave
+    const int32_t id_all = a.r.id(a.r.row(p0 + lane));
+    const int64_t pos = p0 + wave * 16 + m;
+    const int32_t row = a.r.row(pos), id = a.r.id(row);
+    f32x4 res[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        res[t] = f32x4{0, 0, 0, 0};
+
+    while (todo) {
+        const int32_t cur = __builtin_amdgcn_readlane(id_all, __builtin_ctzll(todo));
+        todo &= ~ballot(id_all == cur);
+        const uint16_t *w = a.w.first + cur * a.w.stride;
+        const int32_t kn = kNN ? rank / 8 : 2 * T;  // KiB of the matrix's stage
+        const uint16_t *wp[G::kWInstr];
+        int wk[G::kWInstr];  // the value of the contraction that this lane's chunk begins at, in a stage
+#pragma unroll
+        for (int v = 0; v < G::kWInstr; ++v) {
+            const int at = (v * 4 + wave) % kn * 64 + lane;  // waves without a load of their own repeat one
+            if (kNN) {
+                wk[v] = at * 8 / rank;
+                wp[v] = w + at * 8;
+            } else {
+                const int r = at / 8;
+                wk[v] = ((at % 8) ^ G::swz(r)) * 8;
+                wp[v] = w + (int64_t)(r < rank ? r : 0) * D + wk[v];
+            }
+        }
+        auto issue = [&](int32_t kt, int st) {
+            char *to = ring + st * G::kStageBytes;
+            const int32_t k = (k0 + kt) * 64;
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                dma16(k + xc[v] * 8 < D ? (const void *)(xp[v] + k) : kZeros, to + (v * 4 + wave) * 1024);
+#pragma unroll
+            for (int v = 0; v < G::kWInstr; ++v)
+                dma16(k + wk[v] < D ? (const void *)(wp[v] + (kNN ? (int64_t)k * rank : k)) : kZeros,
+                      to + G::kStageX + (v * 4 + wave) % kn * 1024);
+        };
+        f32x4 acc[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+            acc[t] = f32x4{0, 0, 0, 0};
+        lds_barrier();  // the adapter before is done with the ring
+#pragma unroll
+        for (int st = 0; st + 1 < G::kStages; ++st)
+            if (st < nk)
+                issue(st, st);
+        const bool mine = ballot(id == cur) != 0;
+        int now = 0;
+        for (int32_t kt = 0; kt < nk; ++kt) {
+            if (kt + G::kStages - 2 < nk)
+                wait_vm<(G::kStages - 2) * G::kPerStage>();
+            else
+                wait_vm<0>();
+            lds_barrier();  // the stage is visible to all, the one before is free
+            if (kt + G::kStages - 1 < nk)
+                issue(kt + G::kStages - 1, now ? now - 1 : G::kStages - 1);
+            const char *x = ring + now * G::kStageBytes, *ws = x + G::kStageX;
+            now = now + 1 == G::kStages ? 0 : now + 1;
+            if (!mine)
+                continue;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                Frag xf, wf[T];
+                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * 128 + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                if constexpr (kNN) {
+                    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ws +
+                                        (ks * 32 + g * 8 + (m >> 2)) * rank * 2 + (m & 3) * 8;
+                    constexpr int N = T < 4 ? T : 4;
+#pragma unroll
+                    for (int t = 0; t < T; t += N) {
+                        uint32_t lo[N], hi[N];
+                        Frag f[N];
+#pragma unroll
+                        for (int q = 0; q < N; ++q) {
+                            lo[q] = at + (t + q) * 32;
+                            hi[q] = lo[q] + 8 * rank;
+                        }
+                        tr_frags<N>(lo, hi, f);
+#pragma unroll
+                        for (int q = 0; q < N; ++q)
+                            wf[t + q] = f[q];
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * 128 + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                }
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+                    acc[t] = mfma16(wf[t].v, xf.v, acc[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                res[t][j] = id == cur ? acc[t][j] : res[t][j];
+    }
+    if (row < 0)
+        return;
+    const float s = id >= 0 && a.scale ? a.scale[id] : 1.0f;
+    const Parts parts(rank);
+    float *o = a.out + ((int64_t)blockIdx.y * a.r.rows + row) * rank;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int32_t c = t * 16 + g * 4;
+        if (c >= rank)
+            continue;
+        *(f32x4 *)(o + c) = a.parts ? res[t] : res[t] * s;
+        if (a.parts)
+            parts.put(a.parts, pos, c, res[t] * s);
+    }
+}
+
+// Few rows: 16 positions a workgroup, operands straight into registers.  The four
+// waves share the rows, each with a part of the contraction, of which blockIdx.y
+// is one of gridDim.y parts; their sums are joined in LDS.  Of a tile's
+// adapters, workgroup blockIdx.z has every gridDim.z-th, and their rows.  The 16
+// rows of the instruction's tile t are indexes m T + t of the rank, so that a
+// lane's results are 4 T consecutive ones.
+template <int T, bool kNN>
+__global__ __launch_bounds__(kAdBlock) void shrink_few_kernel(ShrinkArgs a)
+{
+    constexpr int RT = 1;
+    constexpr int U = T <= 4 ? 4 : 2;  // steps in flight
     const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
     const int m = lane & 15, g = lane >> 4;
     const int32_t D = a.w.D, rank = a.w.rank;
-    const int64_t p0 = kSplit ? (int64_t)blockIdx.x * 16 : ((int64_t)blockIdx.x * 4 + wave) * 16 * RT;
+    const int64_t p0 = (int64_t)blockIdx.x * 16 * RT;
     const int32_t steps = (D + 31) / 32;
-    int32_t k0 = 0, k1 = steps;
-    if (kSplit) {
-        const int32_t parts = (int32_t)gridDim.y * 4, part = (int32_t)blockIdx.y * 4 + wave;
-        k0 = (int32_t)((int64_t)steps * part / parts);
-        k1 = (int32_t)((int64_t)steps * (part + 1) / parts);
-    } else if (p0 >= a.r.rows) {
-        return;
-    }
+    const int32_t cuts = (int32_t)gridDim.y * 4, cut = (int32_t)blockIdx.y * 4 + wave;
+    const int32_t k0 = (int32_t)((int64_t)steps * cut / cuts);
+    const int32_t k1 = (int32_t)((int64_t)steps * (cut + 1) / cuts);
     const int32_t full = k1 < D / 32 ? k1 : D / 32;  // steps before this have all 32
 
     int32_t row[RT], id[RT];
     const uint16_t *xp[RT];
-    uint64_t todo[RT];
+    uint64_t todo[RT], store[RT];
     f32x4 res[RT][T];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -139,13 +403,14 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
         id[i] = a.r.id(row[i]);
         xp[i] = a.x + (int64_t)(row[i] < 0 ? 0 : row[i]) * D + g * 8;
         todo[i] = ballot(id[i] >= 0);
+        store[i] = blockIdx.z == 0 ? ballot(row[i] >= 0 && id[i] < 0) : 0;
 #pragma unroll
         for (int t = 0; t < T; ++t)
             res[i][t] = f32x4{0, 0, 0, 0};
     }
     const int32_t r0 = m * T < rank ? m * T : 0;  // lanes past the rank repeat index 0: not stored
 
-    for (;;) {
+    for (uint32_t turn = 0;; turn = turn + 1 == gridDim.z ? 0 : turn + 1) {
         int32_t cur = -1;
 #pragma unroll
         for (int i = 0; i < RT; ++i)
@@ -153,14 +418,22 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 cur = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo[i]));
         if (cur < 0)
             break;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const uint64_t mine = ballot(id[i] == cur);
+            todo[i] &= ~mine;
+            store[i] |= turn == blockIdx.z ? mine : 0;
+        }
+        if (turn != blockIdx.z)
+            continue;
         const uint16_t *w = a.w.first + cur * a.w.stride;
         w += kNN ? (int64_t)g * 8 * rank + r0 : (int64_t)r0 * D + g * 8;
-        auto load_w = [&](int32_t k, bool in, Frag (&f)[T]) {
+        auto load_w = [&](int32_t k, Frag (&f)[T]) {
             if constexpr (kNN) {
                 Halves<T> v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[j] = load_halves<T>(w + (int64_t)((in ? k * 32 : 0) + j) * rank);
+                    v[j] = load_halves<T>(w + (int64_t)(k * 32 + j) * rank);
 #pragma unroll
                 for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -169,7 +442,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
             } else {
 #pragma unroll
                 for (int t = 0; t < T; ++t)
-                    f[t].v = *(const bf16x8 *)(w + (int64_t)t * D + (in ? k * 32 : 0));
+                    f[t].v = *(const bf16x8 *)(w + (int64_t)t * D + k * 32);
             }
         };
         f32x4 acc[RT][T];
@@ -182,12 +455,13 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
         for (; k + U <= full; k += U) {
             Frag x[U][RT], f[U][T];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
                     x[u][i].v = *(const bf16x8 *)(xp[i] + (k + u) * 32);
-                load_w(k + u, true, f[u]);
-            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                load_w(k + u, f[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -198,24 +472,22 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
         }
         for (; k < k1; ++k) {
             // the last step may end inside: chunks past D are zeros in both operands
-            const bool in = k * 32 + g * 8 < D;
             Frag x[RT], f[T];
 #pragma unroll
             for (int i = 0; i < RT; ++i)
-                x[i].v = *(const bf16x8 *)(in ? xp[i] + k * 32 : xp[i] - g * 8);
-            if (in) {
-                load_w(k, true, f);
-            } else {
 #pragma unroll
-                for (int t = 0; t < T; ++t)
+                for (int j = 0; j < 4; ++j)
+                    x[i].w[j] = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        f[t].w[j] = 0;
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    f[t].w[j] = 0;
+            if (k * 32 + g * 8 < D) {
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[i].w[j] = 0;
+                    x[i].v = *(const bf16x8 *)(xp[i] + k * 32);
+                load_w(k, f);
             }
 #pragma unroll
             for (int i = 0; i < RT; ++i)
@@ -223,49 +495,124 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 for (int t = 0; t < T; ++t)
                     acc[i][t] = mfma16(f[t].v, x[i].v, acc[i][t]);
         }
-        const float s = a.scale ? a.scale[cur] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const bool mine = id[i] == cur;
-            todo[i] &= ~ballot(mine);
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    res[i][t][j] = mine ? acc[i][t][j] * s : res[i][t][j];
-        }
+                    res[i][t][j] = id[i] == cur ? acc[i][t][j] : res[i][t][j];
     }
 
-    float *out = a.out + (kSplit ? (int64_t)blockIdx.y * a.r.rows * rank : 0);
-    if constexpr (kSplit) {
-        __shared__ f32x4 join[4][T][64];
+    // Row tile i is joined and written by wave i % 4.
+    __shared__ f32x4 join[RT][4][T][64];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int t = 0; t < T; ++t)
-            join[wave][t][lane] = res[0][t];
-        __syncthreads();
-        if (wave)
-            return;
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int v = 1; v < 4; ++v)
-                res[0][t] += join[v][t][lane];
-    }
+            join[i][wave][t][lane] = res[i][t];
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        if (row[i] < 0)
+        if ((i & 3) != wave || !(store[i] >> lane & 1))
             continue;
+        const float s = id[i] >= 0 && a.scale ? a.scale[id[i]] : 1.0f;
         float v[4 * T];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int t = 0; t < T; ++t) {
+            f32x4 sum = join[i][0][t][lane];
 #pragma unroll
-            for (int t = 0; t < T; ++t)
-                v[j * T + t] = res[i][t][j];
-        float *o = out + (int64_t)row[i] * rank + g * 4 * T;
+            for (int q = 1; q < 4; ++q)
+                sum += join[i][q][t][lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j * T + t] = sum[j] * s;
+        }
+        float *o = a.out + ((int64_t)blockIdx.y * a.r.rows + row[i]) * rank + g * 4 * T;
 #pragma unroll
         for (int q = 0; q < T; ++q)
             if (g * 4 * T + q * 4 < rank)
                 *(f32x4 *)(o + q * 4) = f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+    }
+}
+
+// ---------------------------------------------------------------------------
+// prepare: partial sums joined and cut into the parts that the products take
+// ---------------------------------------------------------------------------
+
+constexpr int kStep = 32;  // positions of one step of wgrad's contraction
+
+struct PrepArgs {
+    AdRows r;
+    const float *scale;
+    int32_t rank, tiles, splits;
+    const float *sums;   // [splits][rows][rank]
+    float *total;        // [rows][rank]: their sum, or NULL
+    uint16_t *parts;     // of scale_parts ? scale * sum : sum, or NULL
+    int32_t scale_parts;
+    const float *u;      // [rows][rank]
+    // For wgrad, or NULL: all bits of the sums, and of scale * u, as wgrad's lanes take
+    // them: for each 32 positions and each of three bf16 parts, `tiles` tiles of 64
+    // lanes x 8 values; lane 16 g + m of tile t holds index 16 t + m of the rank at
+    // positions 8 g .. + 7.  Zeros for positions without an adapter; indexes past the
+    // rank are not used.
+    uint16_t *t_sum, *t_u;
+};
+
+// The three bf16 parts of a value, all 24 bits; the later ones of an infinity are 0.
+__device__ __forceinline__ void split3(float a, uint16_t *p0, uint16_t *p1, uint16_t *p2)
+{
+    const uint32_t hi = pack_bf16(a, 0.0f);
+    const float h = bf16_lo(hi);
+    const float r = __builtin_isfinite(h) ? a - h : 0.0f;
+    const uint32_t mid = pack_bf16(r, 0.0f);
+    *p0 = (uint16_t)hi;
+    *p1 = (uint16_t)mid;
+    *p2 = (uint16_t)pack_bf16(r - bf16_lo(mid), 0.0f);
+}
+
+// One workgroup: 32 positions, 8 threads each.
+__global__ __launch_bounds__(kAdBlock) void adapter_prep_kernel(PrepArgs a)
+{
+    extern __shared__ __align__(16) uint16_t turned[];  // both arrays' step, as it leaves
+    const int p = (int)threadIdx.x & 31, part = (int)threadIdx.x >> 5;
+    const int32_t rank = a.rank, plane = a.tiles * 512;  // elements of one bf16 part of a step
+    const int64_t pos = (int64_t)blockIdx.x * kStep + p;
+    const int32_t row = a.r.row(pos), id = a.r.id(row);
+    const float s = id >= 0 ? a.scale[id] : 0.0f, by = a.scale_parts ? s : 1.0f;
+    const Parts parts(rank);
+    for (int32_t c = part * 4; c < rank; c += 32) {
+        f32x4 v = {0, 0, 0, 0}, w = {0, 0, 0, 0};
+        if (id >= 0) {
+            const float *q = a.sums + (int64_t)row * rank + c;
+            v = *(const f32x4 *)q;
+            for (int32_t i = 1; i < a.splits; ++i)
+                v += *(const f32x4 *)(q + i * ((int64_t)a.r.rows * rank));
+            if (a.t_u)
+                w = *(const f32x4 *)(a.u + (int64_t)row * rank + c) * s;
+        }
+        if (row >= 0 && a.total)
+            *(f32x4 *)(a.total + (int64_t)row * rank + c) = v;
+        if (row >= 0 && a.parts)
+            parts.put(a.parts, pos, c, v * by);
+        if (a.t_u) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t r = c + j;
+                uint16_t *t = turned + (r / 16 * 64 + p / 8 * 16 + r % 16) * 8 + p % 8;
+                split3(v[j], t, t + plane, t + 2 * plane);
+                t += 3 * plane;
+                split3(w[j], t, t + plane, t + 2 * plane);
+            }
+        }
+    }
+    if (!a.t_u)
+        return;
+    __syncthreads();
+    const int32_t words = 3 * plane / 8;
+    for (int32_t i = (int)threadIdx.x; i < 2 * words; i += kAdBlock) {
+        u32x4 *to = (u32x4 *)(i < words ? a.t_sum : a.t_u) + (int64_t)blockIdx.x * words;
+        to[i < words ? i : i - words] = ((const u32x4 *)turned)[i];
     }
 }
 
@@ -276,153 +623,317 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 struct ExpandArgs {
     AdRows r;
     AdMats w;
-    const float *u;      // [parts][rows][rank]
-    float *u_out;        // their sum, or NULL
-    const float *scale;  // per adapter, or NULL for 1
+    const uint16_t *parts;  // what is multiplied
     const uint16_t *base;
     uint16_t *y;
-    int32_t parts, tiles;  // row tiles a workgroup
+    int32_t tiles;          // row tiles a workgroup
+    // few rows: the parts are not made yet
+    const float *sums;      // [splits][rows][rank]
+    float *total;           // their sum
+    const float *scale;
+    int32_t splits;
 };
 
-// The contraction is over 2 rank: both bf16 parts of u in turn, 8 of a part in
-// one 8-value chunk, KS steps of four chunks; chunks past it are zeros.  A wave
-// has 16 CT columns, column m CT + t in row m of tile t, and walks row tiles.
-template <int KS, int CT, bool kNN>
-__global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
-{
-    const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
-    const int m = lane & 15, g = lane >> 4;
-    const int32_t D = a.w.D, rank = a.w.rank, rc = rank / 8;
-    const int32_t c0 = ((int32_t)blockIdx.x * 4 + wave) * 16 * CT;
-    if (c0 >= D)
-        return;
-    const int32_t wc = c0 + m * CT < D ? c0 + m * CT : 0;  // lanes past D repeat column 0: not stored
-    const int32_t oc = c0 + g * 4 * CT;                    // this lane's output columns
-    int chunk[KS];
-    bool low[KS], in[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        const int c = s * 4 + g;
-        in[s] = c < 2 * rc;
-        low[s] = c >= rc;
-        chunk[s] = in[s] ? (low[s] ? c - rc : c) * 8 : 0;
-    }
+template <int CT>
+struct Piece;  // CT bf16 values of a row
+template <>
+struct Piece<8> {
+    typedef u32x4 type;
+};
+template <>
+struct Piece<4> {
+    typedef u32x2 type;
+};
 
-    Frag wf[KS][CT];
-    int32_t have = -1;
-    const int64_t first = (int64_t)blockIdx.y * a.tiles * 16;
-    for (int32_t tile = 0; tile < a.tiles; ++tile) {
-        const int64_t p0 = first + tile * 16;
-        if (p0 >= a.r.rows)
-            break;
-        const int32_t row = a.r.row(p0 + m), id = a.r.id(row);
-        const bool mine_io = row >= 0 && (id >= 0 || a.y != a.base);
-        u32x4 b[CT / 2];
+// The contraction is over both parts, PS steps each (kHalf: both in one step).
+// Positions are the instruction's rows and columns its columns: a wave has 16 CT,
+// column n CT + t in column n of tile t, so that a lane's results are CT
+// consecutive columns of positions 4 g .. + 3, and 16 lanes write a run of a row.
+template <int PS, bool kHalf, int CT, bool kNN>
+struct Expand {
+    static constexpr int kSteps = kHalf ? 1 : 2 * PS;
+    typedef typename Piece<CT>::type piece;
+    int32_t D, rank, c0, col, wc;
+    int chunk[PS];  // values of the rank this lane has in step s of a part
+    bool in[PS];
+
+    __device__ __forceinline__ Expand(const AdMats &w, int32_t column)
+    {
+        const int n = lane_id() & 15, g = lane_id() >> 4;
+        D = w.D;
+        rank = w.rank;
+        c0 = column;
+        col = c0 + n * CT;
+        wc = col < D ? col : 0;  // lanes past D repeat column 0: not stored
 #pragma unroll
-        for (int q = 0; q < CT / 2; ++q)
-            b[q] = mine_io && oc + q * 8 < D ? *(const u32x4 *)(a.base + (int64_t)row * D + oc + q * 8)
-                                             : u32x4{0, 0, 0, 0};
-        Frag uf[KS];
-        const float s = a.scale ? (id >= 0 ? a.scale[id] : 0.0f) : 1.0f;
+        for (int s = 0; s < PS; ++s) {
+            const int c = (s * 4 + (kHalf ? g & 1 : g)) * 8;
+            in[s] = c < rank;
+            chunk[s] = in[s] ? c : 0;
+        }
+    }
+    __device__ __forceinline__ void load_w(const uint16_t *w, Frag (&f)[PS][CT]) const
+    {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            f32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
-            if (row >= 0 && in[k]) {
-                const float *u = a.u + (int64_t)row * rank + chunk[k];
-                v0 = *(const f32x4 *)u;
-                v1 = *(const f32x4 *)(u + 4);
-                for (int32_t q = 1; q < a.parts; ++q) {
-                    u += (int64_t)a.r.rows * rank;
-                    v0 += *(const f32x4 *)u;
-                    v1 += *(const f32x4 *)(u + 4);
-                }
-                if (a.u_out && c0 == 0 && !low[k]) {
-                    float *o = a.u_out + (int64_t)row * rank + chunk[k];
-                    *(f32x4 *)o = v0;
-                    *(f32x4 *)(o + 4) = v1;
-                }
-            }
+        for (int k = 0; k < PS; ++k) {
+            if constexpr (kNN) {
+                Halves<CT> v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float e0 = (j < 2 ? v0[2 * j] : v1[2 * j - 4]) * s;
-                const float e1 = (j < 2 ? v0[2 * j + 1] : v1[2 * j - 3]) * s;
-                const uint32_t hi = pack_bf16(e0, e1);
-                const float h0 = bf16_lo(hi), h1 = bf16_hi(hi);
-                // of an infinity the second part is 0
-                const float l0 = __builtin_isfinite(h0) ? e0 - h0 : 0.0f;
-                const float l1 = __builtin_isfinite(h1) ? e1 - h1 : 0.0f;
-                uf[k].w[j] = low[k] ? pack_bf16(l0, l1) : hi;
+                for (int j = 0; j < 8; ++j)
+                    v[j] = load_halves<CT>(w + (int64_t)(chunk[k] + j) * D + wc);
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        f[k][t].w[j] = (uint32_t)v[2 * j].h[t] | (uint32_t)v[2 * j + 1].h[t] << 16;
+            } else {
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+                    f[k][t].v = *(const bf16x8 *)(w + (int64_t)(wc + t) * rank + chunk[k]);
             }
         }
+#pragma unroll
+        for (int k = 0; k < PS; ++k)
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    f[k][t].w[j] = in[k] ? f[k][t].w[j] : 0;
+    }
+    // The tile's parts; positions past the last row read what is there, and are not stored.
+    __device__ __forceinline__ void load_parts(const uint16_t *parts, int64_t tile, Frag (&f)[kSteps]) const
+    {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[s].w[j] = 0;
+            if (in[kHalf ? 0 : s % PS])
+                f[s].v = *(const bf16x8 *)(parts + ((tile * kSteps + s) * 64 + lane_id()) * 8);
+        }
+    }
+    __device__ __forceinline__ void load_base(const uint16_t *base, const int32_t (&row)[4],
+                                              const bool (&wanted)[4], piece (&b)[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[i] = piece{};
+            if (wanted[i] && col < D)
+                b[i] = *(const piece *)(base + (int64_t)row[i] * D + col);
+        }
+    }
+    __device__ __forceinline__ void product(const Frag (&w)[PS][CT], const Frag (&u)[kSteps],
+                                            const bool (&mine)[4], f32x4 (&res)[CT]) const
+    {
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                acc = mfma16(u[s].v, w[kHalf ? 0 : s % PS][t].v, acc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                res[t][i] = mine[i] ? acc[i] : res[t][i];
+        }
+    }
+    // A row without an adapter is copied bit for bit.
+    __device__ __forceinline__ void store(uint16_t *y, const int32_t (&row)[4], const int32_t (&id)[4],
+                                          const bool (&wanted)[4], const piece (&b)[4],
+                                          const f32x4 (&res)[CT]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!wanted[i] || col >= D)
+                continue;
+            piece o;
+#pragma unroll
+            for (int t = 0; t < CT; t += 2) {
+                const uint32_t v = pack_bf16(bf16_lo(b[i][t / 2]) + res[t][i], bf16_hi(b[i][t / 2]) + res[t + 1][i]);
+                o[t / 2] = id[i] >= 0 ? v : b[i][t / 2];
+            }
+            *(piece *)(y + (int64_t)row[i] * D + col) = o;
+        }
+    }
+};
+
+// Many rows: a wave keeps its columns of one adapter's matrix in registers and
+// walks row tiles, the next tile's rows on their way while one is computed.
+template <int PS, bool kHalf, int CT, bool kNN>
+__global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
+{
+    using X = Expand<PS, kHalf, CT, kNN>;
+    const int wave = (int)threadIdx.x >> 6, g = lane_id() >> 4;
+    const X x(a.w, ((int32_t)blockIdx.x * 4 + wave) * 16 * CT);
+    if (x.c0 >= x.D)
+        return;
+    const bool copy = a.y != a.base;
+    const int64_t first = (int64_t)blockIdx.y * a.tiles;
+    const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
+    const int64_t end = first + a.tiles < tiles ? first + a.tiles : tiles;
+
+    struct Tile {
+        int32_t row[4], id[4];
+        bool wanted[4];
+        typename X::piece b[4];
+        Frag u[X::kSteps];
+    } now, next;
+    auto rows_of = [&](int64_t tile, int32_t (&row)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            row[i] = tile < end ? a.r.row(tile * 16 + g * 4 + i) : -1;
+    };
+    auto ids_of = [&](const int32_t (&row)[4], int32_t (&id)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            id[i] = a.r.id(row[i]);
+    };
+    auto load = [&](Tile &t, int64_t tile) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t.wanted[i] = t.row[i] >= 0 && (t.id[i] >= 0 || copy);
+        x.load_base(a.base, t.row, t.wanted, t.b);
+        x.load_parts(a.parts, tile, t.u);
+    };
+    rows_of(first, now.row);
+    rows_of(first + 1, next.row);
+    ids_of(now.row, now.id);
+    ids_of(next.row, next.id);
+    load(now, first);
+    Frag wf[PS][CT];
+    int32_t have = -1;
+    for (int64_t tile = first; tile < end; ++tile) {
+        int32_t row2[4], id2[4];
+        rows_of(tile + 2, row2);
+        if (tile + 1 < end)
+            load(next, tile + 1);
+        ids_of(row2, id2);
         f32x4 res[CT];
 #pragma unroll
         for (int t = 0; t < CT; ++t)
             res[t] = f32x4{0, 0, 0, 0};
-        uint64_t todo = ballot(id >= 0);
-        while (todo) {
-            const int32_t cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        bool left[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            left[i] = now.id[i] >= 0;
+        for (;;) {
+            int32_t cur = -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t some = ballot(left[i]);
+                if (cur < 0 && some)
+                    cur = __builtin_amdgcn_readlane(now.id[i], __builtin_ctzll(some));
+            }
+            if (cur < 0)
+                break;
             if (cur != have) {
                 have = cur;
-                const uint16_t *w = a.w.first + cur * a.w.stride;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    if constexpr (kNN) {
-                        Halves<CT> v[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            v[j] = load_halves<CT>(w + (int64_t)(chunk[k] + j) * D + wc);
-#pragma unroll
-                        for (int t = 0; t < CT; ++t)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                wf[k][t].w[j] = (uint32_t)v[2 * j].h[t] | (uint32_t)v[2 * j + 1].h[t] << 16;
-                    } else {
-#pragma unroll
-                        for (int t = 0; t < CT; ++t)
-                            wf[k][t].v = *(const bf16x8 *)(w + (int64_t)(wc + t) * rank + chunk[k]);
-                    }
-                    if (!in[k]) {
-#pragma unroll
-                        for (int t = 0; t < CT; ++t)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                wf[k][t].w[j] = 0;
-                    }
-                }
+                x.load_w(a.w.first + cur * a.w.stride, wf);
             }
-            const bool mine = id == cur;
-            todo &= ~ballot(mine);
+            bool mine[4];
 #pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    acc = mfma16(wf[k][t].v, uf[k].v, acc);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    res[t][j] = mine ? acc[j] : res[t][j];
+            for (int i = 0; i < 4; ++i) {
+                mine[i] = now.id[i] == cur;
+                left[i] = left[i] && !mine[i];
             }
+            x.product(wf, now.u, mine, res);
         }
-        if (mine_io) {
-            float v[4 * CT];
+        x.store(a.y, now.row, now.id, now.wanted, now.b, res);
+        now = next;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int t = 0; t < CT; ++t)
-                    v[j * CT + t] = res[t][j];
-#pragma unroll
-            for (int q = 0; q < CT / 2; ++q) {
-                if (oc + q * 8 >= D)
-                    continue;
-                u32x4 o;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[j] = pack_bf16(bf16_lo(b[q][j]) + v[q * 8 + 2 * j], bf16_hi(b[q][j]) + v[q * 8 + 2 * j + 1]);
-                // a row without an adapter is copied bit for bit
-                *(u32x4 *)(a.y + (int64_t)row * D + oc + q * 8) = id >= 0 ? o : b[q];
-            }
+        for (int i = 0; i < 4; ++i) {
+            next.row[i] = row2[i];
+            next.id[i] = id2[i];
         }
     }
+}
+
+// Few rows: the four waves of a workgroup and gridDim.z of them share a row tile
+// and its 16 CT columns, each with some of the tile's adapters and their rows.
+template <int PS, bool kHalf, int CT, bool kNN, bool kJoin>
+__global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
+{
+    using X = Expand<PS, kHalf, CT, kNN>;
+    const int wave = (int)threadIdx.x >> 6, m = lane_id() & 15, g = lane_id() >> 4;
+    const X x(a.w, (int32_t)blockIdx.x * 16 * CT);
+    const uint32_t share = blockIdx.z * 4 + wave, shares = gridDim.z * 4;
+    const int64_t p0 = (int64_t)blockIdx.y * 16;
+    // of position m, and of this lane's results
+    const int32_t u_row = a.r.row(p0 + m), u_id = a.r.id(u_row);
+    uint64_t left = ballot(u_id >= 0), taken = share == 0 ? ballot(u_row >= 0 && u_id < 0 && a.y != a.base) : 0;
+    uint64_t todo = 0;
+    for (uint32_t turn = 0; left; turn = turn + 1 == shares ? 0 : turn + 1) {
+        const uint64_t mine = ballot(u_id == __builtin_amdgcn_readlane(u_id, __builtin_ctzll(left)));
+        left &= ~mine;
+        todo |= turn == share ? mine : 0;
+    }
+    taken |= todo;
+    const bool write_total = kJoin && x.c0 == 0 && share == 0;
+    if (!taken && !write_total)
+        return;
+    int32_t row[4], id[4];
+    bool wanted[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        row[i] = __builtin_amdgcn_ds_bpermute((g * 4 + i) * 4, u_row);
+        id[i] = __builtin_amdgcn_ds_bpermute((g * 4 + i) * 4, u_id);
+        wanted[i] = taken >> (g * 4 + i) & 1;
+    }
+    typename X::piece b[4];
+    x.load_base(a.base, row, wanted, b);
+    Frag u[X::kSteps];
+    if constexpr (kJoin) {
+        const float s = u_id >= 0 ? a.scale[u_id] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < PS; ++k) {
+            f32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
+            if (u_row >= 0 && x.in[k] && (write_total || (todo >> m & 1))) {
+                const float *p = a.sums + (int64_t)u_row * x.rank + x.chunk[k];
+                v0 = *(const f32x4 *)p;
+                v1 = *(const f32x4 *)(p + 4);
+                for (int32_t q = 1; q < a.splits; ++q) {
+                    p += (int64_t)a.r.rows * x.rank;
+                    v0 += *(const f32x4 *)p;
+                    v1 += *(const f32x4 *)(p + 4);
+                }
+                if (write_total) {
+                    float *o = a.total + (int64_t)u_row * x.rank + x.chunk[k];
+                    *(f32x4 *)o = v0;
+                    *(f32x4 *)(o + 4) = v1;
+                }
+            }
+            v0 *= s;
+            v1 *= s;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t hi, lo;
+                split2(j < 2 ? v0[2 * j] : v1[2 * j - 4], j < 2 ? v0[2 * j + 1] : v1[2 * j - 3], &hi, &lo);
+                if (kHalf) {
+                    u[0].w[j] = g < 2 ? hi : lo;
+                } else {
+                    u[k].w[j] = hi;
+                    u[PS + k].w[j] = lo;
+                }
+            }
+        }
+    } else {
+        x.load_parts(a.parts, blockIdx.y, u);
+    }
+    f32x4 res[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+        res[t] = f32x4{0, 0, 0, 0};
+    while (todo) {
+        const int32_t cur = __builtin_amdgcn_readlane(u_id, __builtin_ctzll(todo));
+        Frag wf[PS][CT];
+        x.load_w(a.w.first + cur * a.w.stride, wf);
+        todo &= ~ballot(u_id == cur);
+        bool mine[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine[i] = id[i] == cur;
+        x.product(wf, u, mine, res);
+    }
+    x.store(a.y, row, id, wanted, b, res);
 }
 
 // ---------------------------------------------------------------------------
@@ -434,7 +945,7 @@ struct WgradArgs {
     const int32_t *off, *keep;
     int32_t rank, in_dim, out_dim, chunk, nchunks, blocks_a, accumulate;
     int64_t stride, a_off, b_off;
-    const float *du, *u, *scale;
+    const uint16_t *t_du, *t_u;  // as adapter_prep_kernel leaves them
     const uint16_t *x, *dy;
     float *part;  // [nchunks + n][rank * (in_dim + out_dim)]
     float *d_bank;
@@ -450,24 +961,13 @@ __device__ __forceinline__ int32_t adapter_rows(const int32_t *off, const int32_
     return o >= 0 && n >= 0 && o <= rows - n ? n : 0;
 }
 
-// The three bf16 parts of a value pair, packed.
-__device__ __forceinline__ void split3(float a, float b, uint32_t *p0, uint32_t *p1, uint32_t *p2)
-{
-    const uint32_t hi = pack_bf16(a, b);
-    const float h0 = bf16_lo(hi), h1 = bf16_hi(hi);
-    const float r0 = __builtin_isfinite(h0) ? a - h0 : 0.0f;
-    const float r1 = __builtin_isfinite(h1) ? b - h1 : 0.0f;
-    const uint32_t mid = pack_bf16(r0, r1);
-    *p0 = hi;
-    *p1 = mid;
-    *p2 = pack_bf16(r0 - bf16_lo(mid), r1 - bf16_hi(mid));
-}
-
 // T tiles of 16 of the rank against 16 CT columns a wave.  blockIdx.x: columns
-// of x (dA), then of dy (dB); blockIdx.y: a chunk of positions.  The sums of an
-// adapter whose rows lie in one chunk go to their place, those of a longer one
-// to a slot of the workspace: chunk + adapter, which no two pieces share, since
-// from one piece to the next the chunk or the adapter grows and neither falls.
+// of x (dA), then of dy (dB); blockIdx.y: a chunk of positions, whole steps of 32.
+// Positions of a step that belong to another adapter are zeros in both operands.
+// The sums of an adapter whose rows lie in one chunk go to their place, those of a
+// longer one to a slot of the workspace: chunk + adapter, which no two pieces
+// share, since from one piece to the next the chunk or the adapter grows and
+// neither falls.
 template <int T, int CT>
 __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
 {
@@ -480,14 +980,13 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
         return;
     const int32_t col = c0 + n * CT;
     const uint16_t *qp = (is_a ? a.x : a.dy) + (col < D ? col : 0);
-    const int32_t r0 = n * T < rank ? n * T : 0;
-    const float *pp = (is_a ? a.du : a.u) + r0;
+    const uint16_t *pp = (is_a ? a.t_du : a.t_u) + lane * 8;
     const int64_t window = (int64_t)rank * (a.in_dim + a.out_dim);
     int32_t p = (int32_t)blockIdx.y * a.chunk;
     const int32_t p_end = rows - p < a.chunk ? rows : p + a.chunk;
 
     while (p < p_end) {
-        int32_t row = a.r.order[p];
+        const int32_t row = a.r.order[p];
         if ((uint32_t)row >= (uint32_t)rows)
             return;
         const int32_t e = __builtin_amdgcn_readfirstlane(a.r.ids[row]);
@@ -498,7 +997,6 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
         if (p < first || p >= first + cnt)
             return;  // not this order's plan
         const int32_t end = first + cnt < p_end ? first + cnt : p_end;
-        const float s = is_a ? 1.0f : a.scale[e];
 
         f32x4 acc[T][CT];
 #pragma unroll
@@ -507,25 +1005,31 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
             for (int c = 0; c < CT; ++c)
                 acc[t][c] = f32x4{0, 0, 0, 0};
 
-        auto step = [&](int32_t at, bool whole) {
-            Halves<CT> q[8];
-            float v[8][T];
+        // The rows of the step at `at` (a multiple of 32); those outside [p, end)
+        // are some row inside.
+        auto rows_of = [&](int32_t at, int32_t (&r)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int32_t pos = at + g * 8 + j;
-                const bool in = whole || pos < end;
-                int32_t r = a.r.order[in ? pos : at];
-                r = (uint32_t)r < (uint32_t)rows ? r : 0;
-                q[j] = load_halves<CT>(qp + (int64_t)r * D);
-                __builtin_memcpy(v[j], __builtin_assume_aligned(pp + (int64_t)r * rank, T < 4 ? 4 * T : 16), 4 * T);
-                if (!in) {
+                const int32_t i = a.r.order[pos < p || pos >= end ? p : pos];
+                r[j] = (uint32_t)i < (uint32_t)rows ? i : 0;
+            }
+        };
+        auto load_q = [&](const int32_t (&r)[8], Halves<CT> (&q)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q[j] = load_halves<CT>(qp + (int64_t)r[j] * D);
+        };
+        auto step = [&](int32_t at, Halves<CT> (&q)[8]) {
+            const uint16_t *f = pp + (int64_t)(at / kStep) * 3 * T * 512;
+            const int32_t lo = p - at - g * 8, hi = end - at - g * 8;  // positions of this lane's 8
+            const bool edge = at < p || at + kStep > end;
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
-                        q[j].h[c] = 0;
-#pragma unroll
-                    for (int t = 0; t < T; ++t)
-                        v[j][t] = 0.0f;
-                }
+                        q[j].h[c] = j >= lo && j < hi ? q[j].h[c] : 0;
             }
             Frag qf[CT];
 #pragma unroll
@@ -534,24 +1038,37 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
                 for (int j = 0; j < 4; ++j)
                     qf[c].w[j] = (uint32_t)q[2 * j].h[c] | (uint32_t)q[2 * j + 1].h[c] << 16;
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                Frag f0, f1, f2;
+            for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    split3(v[2 * j][t] * s, v[2 * j + 1][t] * s, &f0.w[j], &f1.w[j], &f2.w[j]);
+                for (int b = 0; b < 3; ++b) {
+                    Frag pf;
+                    pf.v = *(const bf16x8 *)(f + (b * T + t) * 512);
+                    if (edge) {
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    acc[t][c] = mfma16(f0.v, qf[c].v, acc[t][c]);
-                    acc[t][c] = mfma16(f1.v, qf[c].v, acc[t][c]);
-                    acc[t][c] = mfma16(f2.v, qf[c].v, acc[t][c]);
+                        for (int j = 0; j < 8; ++j)
+                            pf.h[j] = j >= lo && j < hi ? pf.h[j] : 0;
+                    }
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        acc[t][c] = mfma16(pf.v, qf[c].v, acc[t][c]);
                 }
-            }
         };
-        int32_t at = p;
-        for (; at + 32 <= end; at += 32)
-            step(at, true);
-        if (at < end)
-            step(at, false);
+        int32_t at = p / kStep * kStep, r[8];
+        Halves<CT> q[8], q2[8];
+        rows_of(at, r);
+        load_q(r, q);
+        if (at + kStep < end)
+            rows_of(at + kStep, r);
+        for (; at < end; at += kStep) {
+            if (at + kStep < end)
+                load_q(r, q2);
+            if (at + 2 * kStep < end)
+                rows_of(at + 2 * kStep, r);
+            step(at, q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q[j] = q2[j];
+        }
 
         const int32_t ch = (int32_t)blockIdx.y;
         const bool direct = first / a.chunk == (first + cnt - 1) / a.chunk;
@@ -559,15 +1076,16 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
         float *o = direct ? a.d_bank + e * a.stride + (is_a ? a.a_off : a.b_off)
                           : a.part + (ch + e) * window + (is_a ? 0 : (int64_t)rank * a.in_dim);
         if (col < D) {
-            if (is_a) {
+            // a lane's results: indexes 16 t + 4 g .. + 3 of the rank, CT columns
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int t = 0; t < T; ++t) {
+                const int32_t at_r = t * 16 + g * 4;
+                if (at_r >= rank)
+                    continue;
+                if (is_a) {
 #pragma unroll
-                    for (int t = 0; t < T; ++t) {
-                        const int32_t r = (g * 4 + i) * T + t;
-                        if (r >= rank)
-                            continue;
-                        float *z = o + (int64_t)r * D + col;
+                    for (int i = 0; i < 4; ++i) {
+                        float *z = o + (int64_t)(at_r + i) * D + col;
 #pragma unroll
                         for (int c = 0; c < CT; c += 4) {
                             f32x4 val = {acc[t][c][i], acc[t][c + 1][i], acc[t][c + 2][i], acc[t][c + 3][i]};
@@ -576,24 +1094,11 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
                             *(f32x4 *)(z + c) = val;
                         }
                     }
-            } else {
+                } else {
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    float v[4 * T];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int t = 0; t < T; ++t)
-                            v[i * T + t] = acc[t][c][i];
-                    float *z = o + (int64_t)(col + c) * rank + g * 4 * T;
-#pragma unroll
-                    for (int q = 0; q < T; ++q) {
-                        if (g * 4 * T + q * 4 >= rank)
-                            continue;
-                        f32x4 val = {v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
-                        if (add)
-                            val += *(const f32x4 *)(z + q * 4);
-                        *(f32x4 *)(z + q * 4) = val;
+                    for (int c = 0; c < CT; ++c) {
+                        f32x4 *z = (f32x4 *)(o + (int64_t)(col + c) * rank + at_r);
+                        *z = add ? *z + acc[t][c] : acc[t][c];
                     }
                 }
             }
@@ -634,66 +1139,102 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_join_kernel(WgradArgs a)
 
 int status() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP; }
 
-int split_count(int32_t rows, int32_t D)
+// Parts of a contraction over workgroups: until there are about 512.
+int split_count(int32_t rows, int32_t D, int most)
 {
-    if (rows > kSplitRows)
-        return 1;
-    const int32_t tiles = (rows + 15) / 16, steps = (D + 31) / 32;
-    int32_t s = 512 / tiles;
-    s = s < kMostSplits ? s : kMostSplits;
-    s = s < (steps + 3) / 4 ? s : (steps + 3) / 4;
-    return s < 1 ? 1 : s;
+    const bool few = rows <= kFewRows;
+    const int64_t tiles = few ? (rows + 15) / 16 : ((int64_t)rows + 63) / 64;
+    const int32_t steps = (D + 127) / 128;  // two stages, or a step a wave
+    int64_t s = 512 / tiles;
+    s = s < most ? s : most;
+    s = s < steps ? s : steps;
+    return (int)(s < 1 ? 1 : s);
 }
 
+// Tiles of 16 that a rank takes, a power of two.
+int rank_tiles(int32_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
 template <int T, bool kNN>
-void shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
+int shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
 {
     const int32_t rows = a.r.rows;
-    if (rows <= kSplitRows)
-        hipLaunchKernelGGL((shrink_kernel<T, kNN, 1, true>), dim3((rows + 15) / 16, splits),
-                           dim3(kAdBlock), 0, st, a);
-    else
-        hipLaunchKernelGGL((shrink_kernel<T, kNN, 2, false>), dim3((rows + 127) / 128),
-                           dim3(kAdBlock), 0, st, a);
+    if (rows <= kFewRows) {
+        hipLaunchKernelGGL((shrink_few_kernel<T, kNN>), dim3((rows + 15) / 16, splits, 4), dim3(kAdBlock), 0,
+                           st, a);
+        return MOONEP_OK;
+    }
+    using G = ShrinkCfg<T, kNN>;
+    static_assert(G::kLds <= 160 * 1024, "LDS");
+    static bool raised[64] = {};
+    int dev = 0;
+    if (G::kLds > 64 * 1024) {
+        if (hipGetDevice(&dev) != hipSuccess)
+            return MOONEP_ERR_HIP;
+        if (dev < 0 || dev >= 64 || !raised[dev]) {
+            if (hipFuncSetAttribute((const void *)shrink_kernel<T, kNN>,
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds) != hipSuccess)
+                return MOONEP_ERR_HIP;
+            if (dev >= 0 && dev < 64)
+                raised[dev] = true;
+        }
+    }
+    hipLaunchKernelGGL((shrink_kernel<T, kNN>), dim3((unsigned)(((int64_t)rows + 63) / 64), splits),
+                       dim3(kAdBlock), G::kLds, st, a);
+    return MOONEP_OK;
 }
 
 template <bool kNN>
-void shrink(const ShrinkArgs &a, int splits, hipStream_t st)
+int shrink(const ShrinkArgs &a, int splits, hipStream_t st)
 {
-    if (a.w.rank <= 16)
-        shrink_as<1, kNN>(a, splits, st);
-    else if (a.w.rank <= 32)
-        shrink_as<2, kNN>(a, splits, st);
-    else if (a.w.rank <= 64)
-        shrink_as<4, kNN>(a, splits, st);
-    else
-        shrink_as<8, kNN>(a, splits, st);
+    switch (rank_tiles(a.w.rank)) {
+    case 1: return shrink_as<1, kNN>(a, splits, st);
+    case 2: return shrink_as<2, kNN>(a, splits, st);
+    case 4: return shrink_as<4, kNN>(a, splits, st);
+    default: return shrink_as<8, kNN>(a, splits, st);
+    }
 }
 
-template <int KS, int CT, bool kNN>
+void prepare(const PrepArgs &a, hipStream_t st)
+{
+    const size_t lds = a.t_u ? (size_t)2 * 3 * a.tiles * 512 * 2 : 0;
+    hipLaunchKernelGGL(adapter_prep_kernel, dim3((unsigned)(((int64_t)a.r.rows + kStep - 1) / kStep)),
+                       dim3(kAdBlock), lds, st, a);
+}
+
+template <int PS, bool kHalf, int CT, bool kNN>
 void expand_as(ExpandArgs a, hipStream_t st)
 {
-    const int64_t tiles = ((int64_t)a.r.rows + 15) / 16, blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
+    const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
+    if (a.r.rows <= kFewRows) {
+        const dim3 grid((unsigned)((a.w.D + 63) / 64), (unsigned)tiles, 4);
+        if constexpr (!kNN) {
+            if (a.sums) {
+                hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4, kNN, true>), grid, dim3(kAdBlock), 0, st, a);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4, kNN, false>), grid, dim3(kAdBlock), 0, st, a);
+        return;
+    }
+    const int64_t blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
     int64_t per = tiles * blocks / 1024;
-    per = per < 1 ? 1 : (per > 16 ? 16 : per);
+    per = per < 1 ? 1 : (per > 32 ? 32 : per);
     while ((tiles + per - 1) / per > 65535)
         per *= 2;
     a.tiles = (int32_t)per;
-    hipLaunchKernelGGL((expand_kernel<KS, CT, kNN>), dim3((unsigned)blocks, (unsigned)((tiles + per - 1) / per)),
-                       dim3(kAdBlock), 0, st, a);
+    hipLaunchKernelGGL((expand_kernel<PS, kHalf, CT, kNN>),
+                       dim3((unsigned)blocks, (unsigned)((tiles + per - 1) / per)), dim3(kAdBlock), 0, st, a);
 }
 
 template <bool kNN>
 void expand(const ExpandArgs &a, hipStream_t st)
 {
-    if (a.w.rank <= 16)
-        expand_as<1, 4, kNN>(a, st);
-    else if (a.w.rank <= 32)
-        expand_as<2, 4, kNN>(a, st);
-    else if (a.w.rank <= 64)
-        expand_as<4, 4, kNN>(a, st);
-    else
-        expand_as<8, 2, kNN>(a, st);
+    switch (rank_tiles(a.w.rank)) {
+    case 1: return expand_as<1, true, 8, kNN>(a, st);
+    case 2: return expand_as<1, false, 8, kNN>(a, st);
+    case 4: return expand_as<2, false, 8, kNN>(a, st);
+    default: return expand_as<4, false, 4, kNN>(a, st);
+    }
 }
 
 template <int T, int CT>
@@ -704,16 +1245,44 @@ void wgrad_as(WgradArgs a, hipStream_t st)
     hipLaunchKernelGGL((wgrad_kernel<T, CT>), dim3(blocks, a.nchunks), dim3(kAdBlock), 0, st, a);
 }
 
+// Consecutive arrays of the workspace, each at a multiple of 256 bytes.
+struct Carve {
+    char *at;
+    template <class X>
+    X *take(size_t n)
+    {
+        at = (char *)(((uintptr_t)at + 255) & ~(uintptr_t)255);
+        X *p = (X *)at;
+        at += n * sizeof(X);
+        return p;
+    }
+};
+
+size_t steps_of(int64_t rows) { return (size_t)((rows + kStep - 1) / kStep); }
+
+}  // namespace
+
+namespace {
+
+// Elements of expand's parts, and of one of wgrad's arrays.
+size_t parts_size(int64_t rows, int32_t rank) { return (size_t)((rows + 15) / 16) * Parts(rank).steps() * 512; }
+size_t turned_size(int64_t rows, int32_t rank) { return steps_of(rows) * 3 * rank_tiles(rank) * 512; }
+
 }  // namespace
 
 size_t adapter_workspace(int64_t rows, const moonep_adapters &ad)
 {
-    return (size_t)rows * ad.rank * 4 * kMostSplits + 65536;
+    // partial sums and the parts: 4 splits rank + 64 steps bytes a row, at most 64
+    // rank for every rank (rank 8: 448 + 64; 72: 4032 + 512), and 15 rows more of parts
+    return (size_t)rows * ad.rank * 64 + 65536;
 }
 
 size_t adapter_bwd_workspace(int64_t rows, const moonep_adapters &ad)
 {
-    return (size_t)rows * ad.rank * 4 * (kMostSplits + 1) +
+    // partial sums, the parts and wgrad's two arrays (192 bytes a row for each tile of
+    // the rank): at most 68 rank for every rank (rank 8: 256 + 64 + 192), and up to 31
+    // rows more; the pieces of the gradients take the place of the sums
+    return (size_t)rows * ad.rank * 68 +
            (size_t)(kMostChunks + ad.n) * ad.rank * ((size_t)ad.in_dim + ad.out_dim) * 4 + 65536;
 }
 
@@ -724,12 +1293,22 @@ int launch_adapter(int32_t rows, const moonep_adapters &ad, const int32_t *ids, 
     if (rows == 0)
         return MOONEP_OK;
     const AdRows r{ids, order, rows, ad.n};
-    const int splits = split_count(rows, ad.in_dim);
-    float *to = splits > 1 ? (float *)ws : u;
-    shrink<false>(ShrinkArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, x, nullptr, to},
-                  splits, st);
-    expand<false>(ExpandArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, to,
-                             splits > 1 ? u : nullptr, scale, base, y, splits, 0}, st);
+    const bool few = rows <= kFewRows;
+    const int splits = split_count(rows, ad.in_dim, kMostSplits);
+    Carve carve{(char *)ws};
+    float *sums = splits > 1 || few ? carve.take<float>((size_t)splits * rows * ad.rank) : u;
+    uint16_t *parts = few ? nullptr : carve.take<uint16_t>(parts_size(rows, ad.rank));
+    const bool ready = !few && splits == 1;  // shrink makes the parts itself
+    const int rc = shrink<false>(ShrinkArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, x,
+                                            ready ? scale : nullptr, sums, ready ? parts : nullptr},
+                                 splits, st);
+    if (rc != MOONEP_OK)
+        return rc;
+    if (!few && !ready)
+        prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, sums, u, parts, 1, nullptr, nullptr,
+                         nullptr}, st);
+    expand<false>(ExpandArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, parts, base, y, 0,
+                             few ? sums : nullptr, u, scale, splits}, st);
     return status();
 }
 
@@ -742,17 +1321,24 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
     if (rows == 0 && (!d_bank || accumulate))
         return MOONEP_OK;
     const AdRows r{ids, order, rows, ad.n};
-    const size_t plane = (size_t)rows * ad.rank;
-    float *du = (float *)ws, *parts = du + plane;
+    const size_t plane = (size_t)rows * ad.rank, turned = d_bank ? turned_size(rows, ad.rank) : 0;
+    Carve carve{(char *)ws};
+    uint16_t *parts = carve.take<uint16_t>(dx ? parts_size(rows, ad.rank) : 0);
+    uint16_t *t_du = carve.take<uint16_t>(turned);
+    uint16_t *t_u = carve.take<uint16_t>(turned);
     if (rows) {
-        // with one part, or nobody to join them, du is written at once
-        const int splits = dx ? split_count(rows, ad.out_dim) : 1;
-        float *to = splits > 1 ? parts : du;
-        shrink<true>(ShrinkArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, dy, scale, to},
-                     splits, st);
+        const int splits = split_count(rows, ad.out_dim, kMostSplitsBwd);
+        Carve sums = carve;  // done with before the gradients' pieces are made
+        float *du = sums.take<float>(splits * plane);
+        const int rc = shrink<true>(ShrinkArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, dy,
+                                               scale, du, nullptr}, splits, st);
+        if (rc != MOONEP_OK)
+            return rc;
+        prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, du, nullptr, dx ? parts : nullptr, 0,
+                         u, d_bank ? t_du : nullptr, d_bank ? t_u : nullptr}, st);
         if (dx)
-            expand<true>(ExpandArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, to,
-                                    splits > 1 ? du : nullptr, nullptr, dx_base, dx, splits, 0}, st);
+            expand<true>(ExpandArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts, dx_base,
+                                    dx, 0, nullptr, nullptr, nullptr, 0}, st);
     }
     if (d_bank) {
         const PlanLayout pl = plan_layout(E, 1);
@@ -767,33 +1353,32 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         a.a_off = ad.a_offset;
         a.b_off = ad.b_offset;
         a.accumulate = accumulate;
-        a.du = du;
-        a.u = u;
-        a.scale = scale;
+        a.t_du = t_du;
+        a.t_u = t_u;
         a.x = x;
         a.dy = dy;
-        a.part = (float *)(((uintptr_t)(parts + kMostSplits * plane) + 255) & ~(uintptr_t)255);
+        const int64_t window = (int64_t)ad.rank * ((int64_t)ad.in_dim + ad.out_dim);
+        a.part = carve.take<float>((size_t)(kMostChunks + ad.n) * window);
         a.d_bank = d_bank;
         // chunks of at least 128 positions, 64 at most, for about 1024 workgroups
-        const int32_t blocks = (ad.in_dim + ad.out_dim + 255) / 256;
+        const int32_t width = ad.rank <= 32 ? 512 : 256, blocks = (ad.in_dim + ad.out_dim + width - 1) / width;
         int32_t chunks = 1024 / blocks;
         chunks = chunks < 1 ? 1 : (chunks > kMostChunks ? kMostChunks : chunks);
         int64_t chunk = ((int64_t)rows + chunks - 1) / chunks;
-        chunk = (chunk + 31) / 32 * 32;
+        chunk = (chunk + kStep - 1) / kStep * kStep;
         chunk = chunk < 128 ? 128 : chunk;
         a.chunk = (int32_t)chunk;
         a.nchunks = (int32_t)(((int64_t)rows + chunk - 1) / chunk);
         if (rows) {
             if (ad.rank <= 16)
-                wgrad_as<1, 4>(a, st);
+                wgrad_as<1, 8>(a, st);
             else if (ad.rank <= 32)
-                wgrad_as<2, 4>(a, st);
+                wgrad_as<2, 8>(a, st);
             else if (ad.rank <= 64)
                 wgrad_as<4, 4>(a, st);
             else
                 wgrad_as<8, 4>(a, st);
         }
-        const int64_t window = (int64_t)ad.rank * ((int64_t)ad.in_dim + ad.out_dim);
         const int64_t nb = (window + kAdBlock * 4 - 1) / (kAdBlock * 4);
         hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(nb < 128 ? nb : 128), ad.n), dim3(kAdBlock),
                            0, st, a);

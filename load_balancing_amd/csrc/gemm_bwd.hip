@@ -631,6 +631,18 @@ int run_dw(const DwArgs &a, hipStream_t st)
 
 }  // namespace
 
+// Tiles of 256 x 256, eight waves, or of 128 x 128, four waves and two
+// workgroups per CU, measured on 64 experts, 2048 -> 1408 (d_x) and 1408 -> 2048
+// (g), us, large tile first:
+//   d_x, by mean rows of an expert:   32: 112, 92    61: 117, 95   128: 127, 123
+//     256: 172, 162   384: 224, 202   512: 248, 257   4096: 1486, 1716;
+//     2048 rows, 512 x 512, 16 experts (two rounds of items): 35, 33
+//   g, which the rows do not decide (61: 179, 190; 512: 324, 418) but the items
+//     do: 36: 23.5, 15.4   64: 98, 64   128: 41, 28   256: 44, 42   384: 55, 64   768: 105, 123.
+constexpr int64_t kLargeRows = 448;    // mean rows of an expert from which d_x takes large tiles
+constexpr int64_t kLargeItemsX = 512;  // and of those tiles
+constexpr int64_t kLargeItemsW = 320;  // large tiles from which g takes them
+
 int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *wslot, int32_t B,
                      int32_t in_dim, int32_t out_dim, const uint16_t *d_y, const uint16_t *w_home,
                      const uint16_t *pool, int64_t w_stride, int64_t w_offset, uint16_t *d_x,
@@ -643,7 +655,11 @@ int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *
 #ifdef DXV
     return run_dx<DXV>(a, st);
 #endif
-    return run_dx<256, 256, 128, 64>(a, st);
+    const int64_t rows = (int64_t)s.R * s.S * s.K;
+    const int64_t items = ((rows + 255) / 256 + s.E / 2) * ((in_dim + 255) / 256);
+    if (rows >= kLargeRows * s.E && items >= kLargeItemsX)
+        return run_dx<256, 256, 128, 64>(a, st);
+    return run_dx<128, 128, 64, 64>(a, st);
 }
 
 int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim, int32_t out_dim,
@@ -657,7 +673,10 @@ int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim,
 #ifdef DWV
     return run_dw<DWV>(a, st);
 #endif
-    return run_dw<256, 256, 128, 64, 32, 3>(a, st);
+    const int64_t items = (int64_t)s.E * ((in_dim + 255) / 256) * ((out_dim + 255) / 256);
+    if (items >= kLargeItemsW)
+        return run_dw<256, 256, 128, 64, 32, 3>(a, st);
+    return run_dw<128, 128, 64, 64, 64, 2>(a, st);
 }
 
 }  // namespace moonep

@@ -137,6 +137,17 @@ CASES = [
     (4100, 1, 64, 200, 64),
     (2113, 6, 128, 104, 72),
     (3000, 9, 56, 64, 128),
+    # either side of what a wave, a workgroup and a launch take at once
+    (256, 40, 64, 264, 520),
+    (257, 40, 16, 520, 264),
+    (250, 4, 128, 136, 72),
+    (1024, 12, 24, 2056, 328),
+    (4097, 90, 8, 64, 1096),
+    (16385, 7, 16, 72, 136),
+    (16500, 3, 128, 64, 72),
+    (32769, 5, 32, 136, 64),
+    (33000, 2, 64, 64, 200),
+    (32770, 3, 96, 72, 64),
 ]
 
 

@@ -42,6 +42,11 @@ CASES = [
     (4, 8, 513, 3, 576, 128, 2),
     (8, 32, 130, 4, 256, 640, 4),
     (2, 64, 9, 4, 1088, 256, 3),
+    # enough rows, and enough items, for the large tiles
+    (4, 4, 16384, 1, 320, 128, 1),
+    (8, 16, 4099, 2, 576, 128, 1),
+    (4, 64, 40, 2, 832, 384, 0),
+    (2, 32, 300, 4, 1088, 640, 1),
 ]
 
 
