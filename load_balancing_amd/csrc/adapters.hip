@@ -757,93 +757,138 @@ struct Expand {
 };
 
 // Many rows: a wave keeps its columns of one adapter's matrix in registers and
-// walks row tiles, the next tile's rows on their way while one is computed.
+// walks row tiles.  Base rows and parts come through the wave's own ring of LDS
+// slots, kAhead tiles ahead: so many bytes in flight would not fit the registers,
+// and no wave waits for another.
+constexpr int kAhead = 2;
+constexpr int kTileRun = 32;  // row tiles whose rows and adapters are looked up at once
+
+template <int PS, bool kHalf, int CT>
+struct ExpandRing {
+    static constexpr int kSteps = kHalf ? 1 : 2 * PS;
+    static constexpr int kLanesRow = 2 * CT;              // lanes, 16 bytes each, of a row
+    static constexpr int kBaseInstr = 16 * kLanesRow / 64;
+    static constexpr int kLoads = kBaseInstr + kSteps;    // of a tile
+    static constexpr int kBaseBytes = 16 * CT * 32;
+    static constexpr int kSlot = kBaseBytes + kSteps * 1024;
+    static constexpr int kLds = 4 * (kAhead + 1) * kSlot;
+    static_assert(kAhead * (kLoads + 4) <= 63, "outstanding accesses must fit vmcnt");
+};
+
 template <int PS, bool kHalf, int CT, bool kNN>
 __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 {
     using X = Expand<PS, kHalf, CT, kNN>;
-    const int wave = (int)threadIdx.x >> 6, g = lane_id() >> 4;
+    using G = ExpandRing<PS, kHalf, CT>;
+    typedef typename X::piece piece;
+    extern __shared__ __align__(16) char ring_all[];
+    __shared__ int32_t rows[kTileRun * 16], ids[kTileRun * 16];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 4;
     const X x(a.w, ((int32_t)blockIdx.x * 4 + wave) * 16 * CT);
-    if (x.c0 >= x.D)
-        return;
+    char *ring = ring_all + wave * (kAhead + 1) * G::kSlot;
     const bool copy = a.y != a.base;
-    const int64_t first = (int64_t)blockIdx.y * a.tiles;
     const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
-    const int64_t end = first + a.tiles < tiles ? first + a.tiles : tiles;
-
-    struct Tile {
-        int32_t row[4], id[4];
-        bool wanted[4];
-        typename X::piece b[4];
-        Frag u[X::kSteps];
-    } now, next;
-    auto rows_of = [&](int64_t tile, int32_t (&row)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            row[i] = tile < end ? a.r.row(tile * 16 + g * 4 + i) : -1;
-    };
-    auto ids_of = [&](const int32_t (&row)[4], int32_t (&id)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            id[i] = a.r.id(row[i]);
-    };
-    auto load = [&](Tile &t, int64_t tile) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            t.wanted[i] = t.row[i] >= 0 && (t.id[i] >= 0 || copy);
-        x.load_base(a.base, t.row, t.wanted, t.b);
-        x.load_parts(a.parts, tile, t.u);
-    };
-    rows_of(first, now.row);
-    rows_of(first + 1, next.row);
-    ids_of(now.row, now.id);
-    ids_of(next.row, next.id);
-    load(now, first);
+    const int64_t last = ((int64_t)blockIdx.y + 1) * a.tiles < tiles ? ((int64_t)blockIdx.y + 1) * a.tiles : tiles;
     Frag wf[PS][CT];
     int32_t have = -1;
-    for (int64_t tile = first; tile < end; ++tile) {
-        int32_t row2[4], id2[4];
-        rows_of(tile + 2, row2);
-        if (tile + 1 < end)
-            load(next, tile + 1);
-        ids_of(row2, id2);
-        f32x4 res[CT];
+    for (int64_t first = (int64_t)blockIdx.y * a.tiles; first < last; first += kTileRun) {
+        const int32_t n = (int32_t)(last - first < kTileRun ? last - first : kTileRun);
+        __syncthreads();
+        for (int32_t i = (int)threadIdx.x; i < n * 16; i += kAdBlock) {
+            const int32_t row = a.r.row(first * 16 + i), id = a.r.id(row);
+            rows[i] = id >= 0 || copy ? row : -1;  // neither read nor written
+            ids[i] = id;
+        }
+        __syncthreads();
+        if (x.c0 >= x.D)
+            continue;
+        // As many loads for every tile, also past the last one.
+        auto issue = [&](int32_t t, int slot) {
+            char *to = ring + slot * G::kSlot;
+            const int32_t c = x.c0 + lane % G::kLanesRow * 8;
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-            res[t] = f32x4{0, 0, 0, 0};
-        bool left[4];
+            for (int v = 0; v < G::kBaseInstr; ++v) {
+                const int32_t row = t < n ? rows[t * 16 + (v * 64 + lane) / G::kLanesRow] : -1;
+                dma16(row >= 0 && c < x.D ? (const void *)(a.base + (int64_t)row * x.D + c) : kZeros, to + v * 1024);
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            left[i] = now.id[i] >= 0;
-        for (;;) {
-            int32_t cur = -1;
+            for (int s = 0; s < G::kSteps; ++s)
+                dma16(t < n ? (const void *)(a.parts + (((first + t) * G::kSteps + s) * 64 + lane) * 8) : kZeros,
+                      to + G::kBaseBytes + s * 1024);
+        };
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t)
+            issue(t, t);
+        int slot = 0, stored = 0;  // stored: tiles just before this one whose four stores were issued, kAhead at most
+        for (int32_t t = 0; t < n; ++t) {
+            wave_sync();
+            issue(t + kAhead, slot ? slot - 1 : kAhead);
+            // the tile's loads have landed once only what was issued after them is
+            // outstanding: kAhead tiles' loads, and the stores in between
+            if (stored == 2)
+                wait_vm<kAhead * G::kLoads + 2 * 4>();
+            else if (stored == 1)
+                wait_vm<kAhead * G::kLoads + 4>();
+            else
+                wait_vm<kAhead * G::kLoads>();
+            asm volatile("" ::: "memory");
+            const char *at = ring + slot * G::kSlot;
+            slot = slot == kAhead ? 0 : slot + 1;
+            int32_t row[4], id[4];
+            piece b[4];
+            Frag u[G::kSteps];
+            bool left[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint64_t some = ballot(left[i]);
-                if (cur < 0 && some)
-                    cur = __builtin_amdgcn_readlane(now.id[i], __builtin_ctzll(some));
+                row[i] = rows[t * 16 + g * 4 + i];
+                id[i] = ids[t * 16 + g * 4 + i];
+                left[i] = id[i] >= 0;
+                b[i] = *(const piece *)(at + (g * 4 + i) * CT * 32 + (lane & 15) * CT * 2);
             }
-            if (cur < 0)
-                break;
-            if (cur != have) {
-                have = cur;
-                x.load_w(a.w.first + cur * a.w.stride, wf);
+#pragma unroll
+            for (int s = 0; s < G::kSteps; ++s) {
+                u[s].v = *(const bf16x8 *)(at + G::kBaseBytes + s * 1024 + lane * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    u[s].w[j] = x.in[kHalf ? 0 : s % PS] ? u[s].w[j] : 0;
             }
-            bool mine[4];
+            f32x4 res[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                res[c] = f32x4{0, 0, 0, 0};
+            for (;;) {
+                int32_t cur = -1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t some = ballot(left[i]);
+                    if (cur < 0 && some)
+                        cur = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(some));
+                }
+                if (cur < 0)
+                    break;
+                if (cur != have) {
+                    have = cur;
+                    x.load_w(a.w.first + cur * a.w.stride, wf);
+                }
+                bool mine[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mine[i] = id[i] == cur;
+                    left[i] = left[i] && !mine[i];
+                }
+                x.product(wf, u, mine, res);
+            }
+            bool wanted[4];
+            uint64_t all = ~(uint64_t)0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                mine[i] = now.id[i] == cur;
-                left[i] = left[i] && !mine[i];
+                wanted[i] = row[i] >= 0;
+                all &= ballot(wanted[i] && x.col < x.D);
             }
-            x.product(wf, now.u, mine, res);
+            x.store(a.y, row, id, wanted, b, res);
+            stored = all == ~(uint64_t)0 ? (stored < kAhead ? stored + 1 : kAhead) : 0;
         }
-        x.store(a.y, now.row, now.id, now.wanted, now.b, res);
-        now = next;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            next.row[i] = row2[i];
-            next.id[i] = id2[i];
-        }
+        wait_vm<0>();  // nothing is on its way into the LDS when it is given back
     }
 }
 
@@ -1154,6 +1199,23 @@ int split_count(int32_t rows, int32_t D, int most)
 // Tiles of 16 that a rank takes, a power of two.
 int rank_tiles(int32_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
+// The kernel's dynamic-LDS limit raised to what it takes, once per device.
+int raise_lds(const void *kernel, int bytes, bool (&raised)[64])
+{
+    int dev = 0;
+    if (bytes <= 48 * 1024)
+        return MOONEP_OK;
+    if (hipGetDevice(&dev) != hipSuccess)
+        return MOONEP_ERR_HIP;
+    if (dev >= 0 && dev < 64 && raised[dev])
+        return MOONEP_OK;
+    if (hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return MOONEP_ERR_HIP;
+    if (dev >= 0 && dev < 64)
+        raised[dev] = true;
+    return MOONEP_OK;
+}
+
 template <int T, bool kNN>
 int shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
 {
@@ -1164,20 +1226,9 @@ int shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
         return MOONEP_OK;
     }
     using G = ShrinkCfg<T, kNN>;
-    static_assert(G::kLds <= 160 * 1024, "LDS");
     static bool raised[64] = {};
-    int dev = 0;
-    if (G::kLds > 64 * 1024) {
-        if (hipGetDevice(&dev) != hipSuccess)
-            return MOONEP_ERR_HIP;
-        if (dev < 0 || dev >= 64 || !raised[dev]) {
-            if (hipFuncSetAttribute((const void *)shrink_kernel<T, kNN>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds) != hipSuccess)
-                return MOONEP_ERR_HIP;
-            if (dev >= 0 && dev < 64)
-                raised[dev] = true;
-        }
-    }
+    if (raise_lds((const void *)shrink_kernel<T, kNN>, G::kLds, raised) != MOONEP_OK)
+        return MOONEP_ERR_HIP;
     hipLaunchKernelGGL((shrink_kernel<T, kNN>), dim3((unsigned)(((int64_t)rows + 63) / 64), splits),
                        dim3(kAdBlock), G::kLds, st, a);
     return MOONEP_OK;
@@ -1202,7 +1253,7 @@ void prepare(const PrepArgs &a, hipStream_t st)
 }
 
 template <int PS, bool kHalf, int CT, bool kNN>
-void expand_as(ExpandArgs a, hipStream_t st)
+int expand_as(ExpandArgs a, hipStream_t st)
 {
     const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
     if (a.r.rows <= kFewRows) {
@@ -1210,11 +1261,11 @@ void expand_as(ExpandArgs a, hipStream_t st)
         if constexpr (!kNN) {
             if (a.sums) {
                 hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4, kNN, true>), grid, dim3(kAdBlock), 0, st, a);
-                return;
+                return MOONEP_OK;
             }
         }
         hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4, kNN, false>), grid, dim3(kAdBlock), 0, st, a);
-        return;
+        return MOONEP_OK;
     }
     const int64_t blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
     int64_t per = tiles * blocks / 1024;
@@ -1222,12 +1273,18 @@ void expand_as(ExpandArgs a, hipStream_t st)
     while ((tiles + per - 1) / per > 65535)
         per *= 2;
     a.tiles = (int32_t)per;
+    using G = ExpandRing<PS, kHalf, CT>;
+    static bool raised[64] = {};
+    if (raise_lds((const void *)expand_kernel<PS, kHalf, CT, kNN>, G::kLds, raised) != MOONEP_OK)
+        return MOONEP_ERR_HIP;
     hipLaunchKernelGGL((expand_kernel<PS, kHalf, CT, kNN>),
-                       dim3((unsigned)blocks, (unsigned)((tiles + per - 1) / per)), dim3(kAdBlock), 0, st, a);
+                       dim3((unsigned)blocks, (unsigned)((tiles + per - 1) / per)), dim3(kAdBlock), G::kLds,
+                       st, a);
+    return MOONEP_OK;
 }
 
 template <bool kNN>
-void expand(const ExpandArgs &a, hipStream_t st)
+int expand(const ExpandArgs &a, hipStream_t st)
 {
     switch (rank_tiles(a.w.rank)) {
     case 1: return expand_as<1, true, 8, kNN>(a, st);
@@ -1307,8 +1364,9 @@ int launch_adapter(int32_t rows, const moonep_adapters &ad, const int32_t *ids, 
     if (!few && !ready)
         prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, sums, u, parts, 1, nullptr, nullptr,
                          nullptr}, st);
-    expand<false>(ExpandArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, parts, base, y, 0,
-                             few ? sums : nullptr, u, scale, splits}, st);
+    if (expand<false>(ExpandArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, parts, base, y, 0,
+                                 few ? sums : nullptr, u, scale, splits}, st) != MOONEP_OK)
+        return MOONEP_ERR_HIP;
     return status();
 }
 
@@ -1336,9 +1394,9 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
             return rc;
         prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, du, nullptr, dx ? parts : nullptr, 0,
                          u, d_bank ? t_du : nullptr, d_bank ? t_u : nullptr}, st);
-        if (dx)
-            expand<true>(ExpandArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts, dx_base,
-                                    dx, 0, nullptr, nullptr, nullptr, 0}, st);
+        if (dx && expand<true>(ExpandArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts,
+                                          dx_base, dx, 0, nullptr, nullptr, nullptr, 0}, st) != MOONEP_OK)
+            return MOONEP_ERR_HIP;
     }
     if (d_bank) {
         const PlanLayout pl = plan_layout(E, 1);
@@ -1360,9 +1418,9 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         const int64_t window = (int64_t)ad.rank * ((int64_t)ad.in_dim + ad.out_dim);
         a.part = carve.take<float>((size_t)(kMostChunks + ad.n) * window);
         a.d_bank = d_bank;
-        // chunks of at least 128 positions, 64 at most, for about 1024 workgroups
+        // chunks of at least 128 positions, 64 at most, for about 512 workgroups
         const int32_t width = ad.rank <= 32 ? 512 : 256, blocks = (ad.in_dim + ad.out_dim + width - 1) / width;
-        int32_t chunks = 1024 / blocks;
+        int32_t chunks = 512 / blocks;
         chunks = chunks < 1 ? 1 : (chunks > kMostChunks ? kMostChunks : chunks);
         int64_t chunk = ((int64_t)rows + chunks - 1) / chunks;
         chunk = (chunk + kStep - 1) / kStep * kStep;
