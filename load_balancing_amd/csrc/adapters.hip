@@ -44,6 +44,7 @@ namespace {
 constexpr int kAdBlock = 256;  // four waves
 constexpr int kMostSplits = 14, kMostSplitsBwd = 8;
 constexpr int kMostChunks = 64;
+constexpr unsigned kShares = 4;  // workgroups that share a tile's adapters
 constexpr int32_t kFewRows = 256;  // up to here a tile's adapters are spread over waves
 
 union Frag {
@@ -217,47 +218,68 @@ __device__ __forceinline__ void tr_frags(const uint32_t (&lo)[N], const uint32_t
         f[i].v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(r[2 * i], r[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Many rows: 64 positions a workgroup, 16 a wave, rows and matrix through a ring of
-// LDS stages of 64 values of the contraction, filled by LDS-DMA.  blockIdx.y is one
-// of gridDim.y parts of the contraction.  The matrix's stage is [16 T][64], or
-// with kNN what memory has: 64 rows of rank.
-template <int T, bool kNN>
+// Many rows: 16 positions a wave, rows and matrix through a ring of
+// LDS stages of BK values of the contraction, filled by LDS-DMA.  blockIdx.y is one
+// of gridDim.y parts of the contraction.  Of a tile's
+// adapters each of gridDim.z workgroups has every gridDim.z-th, with their rows, and
+// those without one end at once: a tile at the border of two would otherwise take
+// twice as long as all others, and the launch with it.  They come last, so that the
+// tiles with one adapter start without them, and LDS is left for them.  The matrix's stage is [16 T][BK], or
+// with kNN what memory has: BK rows of rank.
+template <int T, bool kNN, int BK, int S>
 struct ShrinkCfg {
-    static constexpr int kRows = 64, kStageX = kRows * 128, kStageW = T * 2048;
+    static constexpr int kRows = 64, kStageX = kRows * BK * 2, kStageW = 16 * T * BK * 2;
     static constexpr int kStageBytes = kStageX + kStageW;
-    static constexpr int kWInstr = T < 4 ? 1 : T / 2;  // loads of a wave for the matrix's stage
-    static constexpr int kPerStage = 2 + kWInstr;
-    static constexpr int kStages = T == 8 ? 3 : 4;
+    static constexpr int kCpr = BK / 8;                     // 16-byte chunks of a row
+    static constexpr int kXInstr = kStageX / 4096;          // loads of a wave for the stage's rows
+    static constexpr int kWInstr = kStageW < 4096 ? 1 : kStageW / 4096;  // and for its matrix
+    static constexpr int kPerStage = kXInstr + kWInstr;
+    static constexpr int kStages = S;
     static constexpr int kLds = kStages * kStageBytes;
-    // 16-byte chunk c of row r of a stage of 128-byte rows sits at c ^ swz(r)
-    __device__ static constexpr int swz(int r) { return (r / 2) % 8; }
+    // chunk c of row r of a stage sits at c ^ swz(r): rows of 256 bytes share all banks,
+    // of 128 every other one
+    __device__ static constexpr int swz(int r) { return BK == 128 ? r % 16 : r / 2 % 8; }
 };
 
-template <int T, bool kNN>
+template <int T, bool kNN, int BK, int S>
 __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 {
-    using G = ShrinkCfg<T, kNN>;
+    using G = ShrinkCfg<T, kNN, BK, S>;
     extern __shared__ __align__(16) char ring[];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int32_t D = a.w.D, rank = a.w.rank;
+    const uint32_t share = blockIdx.z, shares = gridDim.z;
     const int64_t p0 = (int64_t)blockIdx.x * G::kRows;
-    const int32_t steps = (D + 63) / 64;
+    const int32_t steps = (D + BK - 1) / BK;
     const int32_t k0 = (int32_t)((int64_t)steps * blockIdx.y / gridDim.y);
     const int32_t nk = (int32_t)((int64_t)steps * (blockIdx.y + 1) / gridDim.y) - k0;
 
-    // this lane's chunk of two rows, of its wave's two loads of a stage of rows
-    const uint16_t *xp[2];
-    int xc[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-        const int r = (v * 4 + wave) * 8 + lane / 8;
-        const int32_t row = a.r.row(p0 + r);
-        xc[v] = (lane % 8) ^ G::swz(r);
-        xp[v] = a.x + (int64_t)(row < 0 ? 0 : row) * D + xc[v] * 8;
-    }
-    uint64_t todo = ballot(a.r.id(a.r.row(p0 + lane)) >= 0);  // the same in every wave
+    // every position of the workgroup, the same in every wave
     const int32_t id_all = a.r.id(a.r.row(p0 + lane));
+    uint64_t todo = 0, left = ballot(id_all >= 0), taken = share ? 0 : ~left;
+    for (uint32_t turn = 0; left; turn = turn + 1 == shares ? 0 : turn + 1) {
+        const uint64_t same = ballot(id_all == __builtin_amdgcn_readlane(id_all, __builtin_ctzll(left)));
+        left &= ~same;
+        todo |= turn == share ? same : 0;
+    }
+    taken |= todo;
+    if (!taken)
+        return;
+    // Neighbours on an XCD begin 512 bytes apart and go round: rows of a power of two
+    // bytes, all read at one column, would keep few of the memory's channels busy
+    // (32768 x 4096, rank 16, begun alike: 61 us for 49).
+    const int32_t begin = nk ? (int32_t)(blockIdx.x / 8 * (256 / BK) % nk) : 0;
+    // this lane's chunk and row, of its wave's loads of a stage of rows
+    const uint16_t *xp[G::kXInstr];
+    int xc[G::kXInstr];
+#pragma unroll
+    for (int v = 0; v < G::kXInstr; ++v) {
+        const int r = ((v * 4 + wave) * 64 + lane) / G::kCpr;
+        const int32_t row = a.r.row(p0 + r);
+        xc[v] = ((lane % G::kCpr) ^ G::swz(r)) * 8;
+        xp[v] = a.x + (int64_t)(row < 0 ? 0 : row) * D + xc[v];
+    }
     const int64_t pos = p0 + wave * 16 + m;
     const int32_t row = a.r.row(pos), id = a.r.id(row);
     f32x4 res[T];
@@ -269,7 +291,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
         const int32_t cur = __builtin_amdgcn_readlane(id_all, __builtin_ctzll(todo));
         todo &= ~ballot(id_all == cur);
         const uint16_t *w = a.w.first + cur * a.w.stride;
-        const int32_t kn = kNN ? rank / 8 : 2 * T;  // KiB of the matrix's stage
+        const int32_t kn = kNN ? rank * BK / 512 : G::kStageW / 1024;  // KiB of the matrix's stage
         const uint16_t *wp[G::kWInstr];
         int wk[G::kWInstr];  // the value of the contraction that this lane's chunk begins at, in a stage
 #pragma unroll
@@ -279,17 +301,17 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 wk[v] = at * 8 / rank;
                 wp[v] = w + at * 8;
             } else {
-                const int r = at / 8;
-                wk[v] = ((at % 8) ^ G::swz(r)) * 8;
+                const int r = at / G::kCpr;
+                wk[v] = ((at % G::kCpr) ^ G::swz(r)) * 8;
                 wp[v] = w + (int64_t)(r < rank ? r : 0) * D + wk[v];
             }
         }
         auto issue = [&](int32_t kt, int st) {
             char *to = ring + st * G::kStageBytes;
-            const int32_t k = (k0 + kt) * 64;
+            const int32_t k = (k0 + (kt + begin < nk ? kt + begin : kt + begin - nk)) * BK;
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
-                dma16(k + xc[v] * 8 < D ? (const void *)(xp[v] + k) : kZeros, to + (v * 4 + wave) * 1024);
+            for (int v = 0; v < G::kXInstr; ++v)
+                dma16(k + xc[v] < D ? (const void *)(xp[v] + k) : kZeros, to + (v * 4 + wave) * 1024);
 #pragma unroll
             for (int v = 0; v < G::kWInstr; ++v)
                 dma16(k + wk[v] < D ? (const void *)(wp[v] + (kNN ? (int64_t)k * rank : k)) : kZeros,
@@ -319,9 +341,9 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
             if (!mine)
                 continue;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
+            for (int ks = 0; ks < BK / 32; ++ks) {
                 Frag xf, wf[T];
-                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * 128 + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * BK * 2 + (((ks * 4 + g) ^ G::swz(m)) << 4));
                 if constexpr (kNN) {
                     const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ws +
                                         (ks * 32 + g * 8 + (m >> 2)) * rank * 2 + (m & 3) * 8;
@@ -343,7 +365,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 } else {
 #pragma unroll
                     for (int t = 0; t < T; ++t)
-                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * 128 + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * BK * 2 + (((ks * 4 + g) ^ G::swz(m)) << 4));
                 }
 #pragma unroll
                 for (int t = 0; t < T; ++t)
@@ -356,7 +378,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
             for (int j = 0; j < 4; ++j)
                 res[t][j] = id == cur ? acc[t][j] : res[t][j];
     }
-    if (row < 0)
+    if (row < 0 || !(taken >> (wave * 16 + m) & 1))
         return;
     const float s = id >= 0 && a.scale ? a.scale[id] : 1.0f;
     const Parts parts(rank);
@@ -704,13 +726,17 @@ struct Expand {
     __device__ __forceinline__ void load_parts(const uint16_t *parts, int64_t tile, Frag (&f)[kSteps]) const
     {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
+        for (int s = 0; s < kSteps; ++s)
+            f[s].v = *(const bf16x8 *)(parts + ((tile * kSteps + s) * 64 + lane_id()) * 8);
+    }
+    // Zeros for chunks past the rank, where the parts hold nothing.
+    __device__ __forceinline__ void mask_parts(Frag (&f)[kSteps]) const
+    {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                f[s].w[j] = 0;
-            if (in[kHalf ? 0 : s % PS])
-                f[s].v = *(const bf16x8 *)(parts + ((tile * kSteps + s) * 64 + lane_id()) * 8);
-        }
+                f[s].w[j] = in[kHalf ? 0 : s % PS] ? f[s].w[j] : 0;
     }
     __device__ __forceinline__ void load_base(const uint16_t *base, const int32_t (&row)[4],
                                               const bool (&wanted)[4], piece (&b)[4]) const
@@ -757,9 +783,9 @@ struct Expand {
 };
 
 // Many rows: a wave keeps its columns of one adapter's matrix in registers and
-// walks row tiles.  Base rows and parts come through the wave's own ring of LDS
-// slots, kAhead tiles ahead: so many bytes in flight would not fit the registers,
-// and no wave waits for another.
+// walks row tiles.  Base rows come through the wave's own ring of LDS slots, kAhead
+// tiles ahead (so many bytes in flight would not fit the registers), parts one tile
+// ahead into registers; no wave waits for another.
 constexpr int kAhead = 2;
 constexpr int kTileRun = 32;  // row tiles whose rows and adapters are looked up at once
 
@@ -767,12 +793,10 @@ template <int PS, bool kHalf, int CT>
 struct ExpandRing {
     static constexpr int kSteps = kHalf ? 1 : 2 * PS;
     static constexpr int kLanesRow = 2 * CT;              // lanes, 16 bytes each, of a row
-    static constexpr int kBaseInstr = 16 * kLanesRow / 64;
-    static constexpr int kLoads = kBaseInstr + kSteps;    // of a tile
-    static constexpr int kBaseBytes = 16 * CT * 32;
-    static constexpr int kSlot = kBaseBytes + kSteps * 1024;
+    static constexpr int kInstr = 16 * kLanesRow / 64;    // loads of a tile
+    static constexpr int kSlot = 16 * CT * 32;
     static constexpr int kLds = 4 * (kAhead + 1) * kSlot;
-    static_assert(kAhead * (kLoads + 4) <= 63, "outstanding accesses must fit vmcnt");
+    static_assert(kAhead * (kInstr + kSteps) <= 63, "outstanding accesses must fit vmcnt");
 };
 
 template <int PS, bool kHalf, int CT, bool kNN>
@@ -807,36 +831,29 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
             char *to = ring + slot * G::kSlot;
             const int32_t c = x.c0 + lane % G::kLanesRow * 8;
 #pragma unroll
-            for (int v = 0; v < G::kBaseInstr; ++v) {
+            for (int v = 0; v < G::kInstr; ++v) {
                 const int32_t row = t < n ? rows[t * 16 + (v * 64 + lane) / G::kLanesRow] : -1;
                 dma16(row >= 0 && c < x.D ? (const void *)(a.base + (int64_t)row * x.D + c) : kZeros, to + v * 1024);
             }
-#pragma unroll
-            for (int s = 0; s < G::kSteps; ++s)
-                dma16(t < n ? (const void *)(a.parts + (((first + t) * G::kSteps + s) * 64 + lane) * 8) : kZeros,
-                      to + G::kBaseBytes + s * 1024);
         };
+        Frag u[G::kSteps], u2[G::kSteps];
+        x.load_parts(a.parts, first, u);
 #pragma unroll
         for (int t = 0; t < kAhead; ++t)
             issue(t, t);
-        int slot = 0, stored = 0;  // stored: tiles just before this one whose four stores were issued, kAhead at most
+        int slot = 0;
         for (int32_t t = 0; t < n; ++t) {
             wave_sync();
+            x.load_parts(a.parts, first + (t + 1 < n ? t + 1 : t), u2);
             issue(t + kAhead, slot ? slot - 1 : kAhead);
-            // the tile's loads have landed once only what was issued after them is
-            // outstanding: kAhead tiles' loads, and the stores in between
-            if (stored == 2)
-                wait_vm<kAhead * G::kLoads + 2 * 4>();
-            else if (stored == 1)
-                wait_vm<kAhead * G::kLoads + 4>();
-            else
-                wait_vm<kAhead * G::kLoads>();
+            // the tile's rows have landed once only the loads that were issued after them
+            // are outstanding (and stores, which are not counted: a wait for more)
+            wait_vm<kAhead * (G::kInstr + G::kSteps)>();
             asm volatile("" ::: "memory");
             const char *at = ring + slot * G::kSlot;
             slot = slot == kAhead ? 0 : slot + 1;
             int32_t row[4], id[4];
             piece b[4];
-            Frag u[G::kSteps];
             bool left[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -845,13 +862,7 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
                 left[i] = id[i] >= 0;
                 b[i] = *(const piece *)(at + (g * 4 + i) * CT * 32 + (lane & 15) * CT * 2);
             }
-#pragma unroll
-            for (int s = 0; s < G::kSteps; ++s) {
-                u[s].v = *(const bf16x8 *)(at + G::kBaseBytes + s * 1024 + lane * 16);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    u[s].w[j] = x.in[kHalf ? 0 : s % PS] ? u[s].w[j] : 0;
-            }
+            x.mask_parts(u);
             f32x4 res[CT];
 #pragma unroll
             for (int c = 0; c < CT; ++c)
@@ -879,14 +890,13 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
                 x.product(wf, u, mine, res);
             }
             bool wanted[4];
-            uint64_t all = ~(uint64_t)0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i)
                 wanted[i] = row[i] >= 0;
-                all &= ballot(wanted[i] && x.col < x.D);
-            }
             x.store(a.y, row, id, wanted, b, res);
-            stored = all == ~(uint64_t)0 ? (stored < kAhead ? stored + 1 : kAhead) : 0;
+#pragma unroll
+            for (int k = 0; k < G::kSteps; ++k)
+                u[k] = u2[k];
         }
         wait_vm<0>();  // nothing is on its way into the LDS when it is given back
     }
@@ -962,6 +972,7 @@ __global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
         }
     } else {
         x.load_parts(a.parts, blockIdx.y, u);
+        x.mask_parts(u);
     }
     f32x4 res[CT];
 #pragma unroll
@@ -1006,31 +1017,66 @@ __device__ __forceinline__ int32_t adapter_rows(const int32_t *off, const int32_
     return o >= 0 && n >= 0 && o <= rows - n ? n : 0;
 }
 
-// T tiles of 16 of the rank against 16 CT columns a wave.  blockIdx.x: columns
-// of x (dA), then of dy (dB); blockIdx.y: a chunk of positions, whole steps of 32.
-// Positions of a step that belong to another adapter are zeros in both operands.
-// The sums of an adapter whose rows lie in one chunk go to their place, those of a
-// longer one to a slot of the workspace: chunk + adapter, which no two pieces
-// share, since from one piece to the next the chunk or the adapter grows and
-// neither falls.
-template <int T, int CT>
+// One workgroup: the whole rank, T tiles of 16, against 256 columns, 64 a wave.
+// blockIdx.x: columns of x (dA), then of dy (dB); blockIdx.y: a chunk of positions,
+// whole steps of 32.  Rows and rank values come through a ring of LDS stages of one
+// step, filled by LDS-DMA; the rows' fragments, 8 positions of one column, through
+// the transposing read.  Positions of a step that belong to another adapter are
+// zeros in both operands.  The sums of an adapter whose rows lie in one chunk go to
+// their place, those of a longer one to a slot of the workspace: chunk + adapter,
+// which no two pieces share, since from one piece to the next the chunk or the
+// adapter grows and neither falls.
+constexpr int kGradCols = 256;
+constexpr int kStepRun = 32;  // steps whose rows are looked up at once
+
+template <int T, int S>
+struct WgradCfg {
+    static constexpr int kRow = kGradCols * 2, kStageQ = kStep * kRow, kStageP = 3 * T * 1024;
+    static constexpr int kStageBytes = kStageQ + kStageP;
+    static constexpr int kQInstr = kStageQ / 4096;      // loads of a wave
+    static constexpr int kPInstr = (3 * T + 3) / 4;
+    static constexpr int kPerStage = kQInstr + kPInstr;
+    static constexpr int kLds = S * kStageBytes;
+    // 16-byte chunk c of row r sits at c ^ swz(r): a transposing read takes 32 bytes of
+    // rows 4 j .. + 3 and, with the neighbouring 16 lanes, of the rows 8 further
+    __device__ static constexpr int swz(int r) { return (r & 3) << 2 | (r >> 3 & 1) << 1; }
+};
+
+template <int T, int S>
 __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
 {
-    const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
-    const int n = lane & 15, g = lane >> 4;
+    using G = WgradCfg<T, S>;
+    extern __shared__ __align__(16) char ring[];
+    __shared__ int32_t row_of[kStepRun * kStep];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int m = lane & 15, g = lane >> 4;
     const bool is_a = (int32_t)blockIdx.x < a.blocks_a;
     const int32_t D = is_a ? a.in_dim : a.out_dim, rank = a.rank, rows = a.r.rows;
-    const int32_t c0 = (((int32_t)blockIdx.x - (is_a ? 0 : a.blocks_a)) * 4 + wave) * 16 * CT;
-    if (c0 >= D)
-        return;
-    const int32_t col = c0 + n * CT;
-    const uint16_t *qp = (is_a ? a.x : a.dy) + (col < D ? col : 0);
-    const uint16_t *pp = (is_a ? a.t_du : a.t_u) + lane * 8;
+    const int32_t c0 = ((int32_t)blockIdx.x - (is_a ? 0 : a.blocks_a)) * kGradCols;
+    const uint16_t *q = is_a ? a.x : a.dy;
+    const uint16_t *t_p = is_a ? a.t_du : a.t_u;
     const int64_t window = (int64_t)rank * (a.in_dim + a.out_dim);
-    int32_t p = (int32_t)blockIdx.y * a.chunk;
-    const int32_t p_end = rows - p < a.chunk ? rows : p + a.chunk;
+    const int32_t p_begin = (int32_t)blockIdx.y * a.chunk;
+    const int32_t p_end = rows - p_begin < a.chunk ? rows : p_begin + a.chunk;
 
-    while (p < p_end) {
+    // this lane's row of a step and chunk, of its wave's loads; columns past D are
+    // not stored
+    int q_row[G::kQInstr];
+    int32_t q_col[G::kQInstr];
+#pragma unroll
+    for (int v = 0; v < G::kQInstr; ++v) {
+        const int at = (v * 4 + wave) * 64 + lane;
+        q_row[v] = at / (G::kRow / 16);
+        q_col[v] = c0 + ((at % (G::kRow / 16)) ^ G::swz(q_row[v])) * 8;
+    }
+    // LDS address of tile 0's fragment in stage 0: rows 8 g + m / 4 and four further;
+    // tile c of the wave is at ^ (c / 2 << 6) ^ (c % 2 << 5)
+    const uint32_t q_at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ring +
+                          (g * 8 + (m >> 2)) * G::kRow +
+                          (((wave * 2) ^ (m >> 2)) << 6 | (g & 1) << 5 | (m & 3) << 3);
+
+    for (int32_t p = p_begin; p < p_end;) {
+        // the adapter of position p and its last position in this chunk
         const int32_t row = a.r.order[p];
         if ((uint32_t)row >= (uint32_t)rows)
             return;
@@ -1043,108 +1089,103 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
             return;  // not this order's plan
         const int32_t end = first + cnt < p_end ? first + cnt : p_end;
 
-        f32x4 acc[T][CT];
+        f32x4 acc[T][4];
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+            for (int c = 0; c < 4; ++c)
                 acc[t][c] = f32x4{0, 0, 0, 0};
 
-        // The rows of the step at `at` (a multiple of 32); those outside [p, end)
-        // are some row inside.
-        auto rows_of = [&](int32_t at, int32_t (&r)[8]) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int32_t pos = at + g * 8 + j;
-                const int32_t i = a.r.order[pos < p || pos >= end ? p : pos];
-                r[j] = (uint32_t)i < (uint32_t)rows ? i : 0;
+        const int32_t step_end = (end + kStep - 1) / kStep;
+        for (int32_t s0 = p / kStep; s0 < step_end; s0 += kStepRun) {
+            const int32_t n = step_end - s0 < kStepRun ? step_end - s0 : kStepRun;
+            __syncthreads();  // the run before is done with the ring and the table
+            for (int32_t i = (int)threadIdx.x; i < n * kStep; i += kAdBlock) {
+                const int32_t pos = s0 * kStep + i;
+                row_of[i] = pos >= p && pos < end ? a.r.row(pos) : -1;
             }
-        };
-        auto load_q = [&](const int32_t (&r)[8], Halves<CT> (&q)[8]) {
+            __syncthreads();
+            auto issue = [&](int32_t t, int slot) {
+                char *to = ring + slot * G::kStageBytes;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                q[j] = load_halves<CT>(qp + (int64_t)r[j] * D);
-        };
-        auto step = [&](int32_t at, Halves<CT> (&q)[8]) {
-            const uint16_t *f = pp + (int64_t)(at / kStep) * 3 * T * 512;
-            const int32_t lo = p - at - g * 8, hi = end - at - g * 8;  // positions of this lane's 8
-            const bool edge = at < p || at + kStep > end;
-            if (edge) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-                        q[j].h[c] = j >= lo && j < hi ? q[j].h[c] : 0;
-            }
-            Frag qf[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    qf[c].w[j] = (uint32_t)q[2 * j].h[c] | (uint32_t)q[2 * j + 1].h[c] << 16;
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int b = 0; b < 3; ++b) {
-                    Frag pf;
-                    pf.v = *(const bf16x8 *)(f + (b * T + t) * 512);
-                    if (edge) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            pf.h[j] = j >= lo && j < hi ? pf.h[j] : 0;
-                    }
-#pragma unroll
-                    for (int c = 0; c < CT; ++c)
-                        acc[t][c] = mfma16(pf.v, qf[c].v, acc[t][c]);
+                for (int v = 0; v < G::kQInstr; ++v) {
+                    const int32_t r = row_of[t * kStep + q_row[v]];
+                    dma16(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v]) : kZeros,
+                          to + (v * 4 + wave) * 1024);
                 }
-        };
-        int32_t at = p / kStep * kStep, r[8];
-        Halves<CT> q[8], q2[8];
-        rows_of(at, r);
-        load_q(r, q);
-        if (at + kStep < end)
-            rows_of(at + kStep, r);
-        for (; at < end; at += kStep) {
-            if (at + kStep < end)
-                load_q(r, q2);
-            if (at + 2 * kStep < end)
-                rows_of(at + 2 * kStep, r);
-            step(at, q);
+                const uint16_t *src = t_p + (int64_t)(s0 + t) * 3 * T * 512 + lane * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                q[j] = q2[j];
+                for (int v = 0; v < G::kPInstr; ++v) {
+                    const int i = (v * 4 + wave) % (3 * T);  // waves without a load of their own repeat one
+                    dma16(src + i * 512, to + G::kStageQ + i * 1024);
+                }
+            };
+#pragma unroll
+            for (int t = 0; t + 1 < S; ++t)
+                if (t < n)
+                    issue(t, t);
+            int now = 0;
+            for (int32_t t = 0; t < n; ++t) {
+                if (t + S - 2 < n)
+                    wait_vm<(S - 2) * G::kPerStage>();
+                else
+                    wait_vm<0>();
+                lds_barrier();  // the stage is visible to all, the one before is free
+                if (t + S - 1 < n)
+                    issue(t + S - 1, now ? now - 1 : S - 1);
+                const char *stage = ring + now * G::kStageBytes;
+                Frag qf[4];
+                uint32_t lo[4], hi[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    lo[c] = (q_at ^ (uint32_t)(c / 2 << 6 | c % 2 << 5)) + now * G::kStageBytes;
+                    hi[c] = lo[c] + 4 * G::kRow;
+                }
+                now = now + 1 == S ? 0 : now + 1;
+                tr_frags<4>(lo, hi, qf);
+                const int32_t at = (s0 + t) * kStep;
+                const int32_t from = p - at - g * 8, to = end - at - g * 8;  // of this lane's 8 positions
+                const bool edge = at < p || at + kStep > end;
+#pragma unroll
+                for (int k = 0; k < T; ++k)
+#pragma unroll
+                    for (int b = 0; b < 3; ++b) {
+                        Frag pf;
+                        pf.v = *(const bf16x8 *)(stage + G::kStageQ + (b * T + k) * 1024 + lane * 16);
+                        if (edge) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                pf.h[j] = j >= from && j < to ? pf.h[j] : 0;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc[k][c] = mfma16(pf.v, qf[c].v, acc[k][c]);
+                    }
+            }
         }
 
-        const int32_t ch = (int32_t)blockIdx.y;
         const bool direct = first / a.chunk == (first + cnt - 1) / a.chunk;
         const bool add = direct && a.accumulate;
         float *o = direct ? a.d_bank + e * a.stride + (is_a ? a.a_off : a.b_off)
-                          : a.part + (ch + e) * window + (is_a ? 0 : (int64_t)rank * a.in_dim);
-        if (col < D) {
-            // a lane's results: indexes 16 t + 4 g .. + 3 of the rank, CT columns
+                          : a.part + ((int32_t)blockIdx.y + e) * window + (is_a ? 0 : (int64_t)rank * a.in_dim);
+        // a lane's results: indexes 16 t + 4 g .. + 3 of the rank, column m of each tile
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const int32_t at_r = t * 16 + g * 4;
-                if (at_r >= rank)
+        for (int t = 0; t < T; ++t) {
+            const int32_t at_r = t * 16 + g * 4;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int32_t col = c0 + wave * 64 + c * 16 + m;
+                if (at_r >= rank || col >= D)
                     continue;
                 if (is_a) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float *z = o + (int64_t)(at_r + i) * D + col;
-#pragma unroll
-                        for (int c = 0; c < CT; c += 4) {
-                            f32x4 val = {acc[t][c][i], acc[t][c + 1][i], acc[t][c + 2][i], acc[t][c + 3][i]};
-                            if (add)
-                                val += *(const f32x4 *)(z + c);
-                            *(f32x4 *)(z + c) = val;
-                        }
+                        *z = add ? *z + acc[t][c][i] : acc[t][c][i];
                     }
                 } else {
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        f32x4 *z = (f32x4 *)(o + (int64_t)(col + c) * rank + at_r);
-                        *z = add ? *z + acc[t][c] : acc[t][c];
-                    }
+                    f32x4 *z = (f32x4 *)(o + (int64_t)col * rank + at_r);
+                    *z = add ? *z + acc[t][c] : acc[t][c];
                 }
             }
         }
@@ -1221,15 +1262,16 @@ int shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
 {
     const int32_t rows = a.r.rows;
     if (rows <= kFewRows) {
-        hipLaunchKernelGGL((shrink_few_kernel<T, kNN>), dim3((rows + 15) / 16, splits, 4), dim3(kAdBlock), 0,
+        hipLaunchKernelGGL((shrink_few_kernel<T, kNN>), dim3((rows + 15) / 16, splits, kShares), dim3(kAdBlock), 0,
                            st, a);
         return MOONEP_OK;
     }
-    using G = ShrinkCfg<T, kNN>;
+    constexpr int kBK = 64, kS = T == 8 ? 2 : T == 4 ? 3 : 4;  // 40 to 48 KiB: three workgroups a CU
+    using G = ShrinkCfg<T, kNN, kBK, kS>;
     static bool raised[64] = {};
-    if (raise_lds((const void *)shrink_kernel<T, kNN>, G::kLds, raised) != MOONEP_OK)
+    if (raise_lds((const void *)shrink_kernel<T, kNN, kBK, kS>, G::kLds, raised) != MOONEP_OK)
         return MOONEP_ERR_HIP;
-    hipLaunchKernelGGL((shrink_kernel<T, kNN>), dim3((unsigned)(((int64_t)rows + 63) / 64), splits),
+    hipLaunchKernelGGL((shrink_kernel<T, kNN, kBK, kS>), dim3((unsigned)(((int64_t)rows + G::kRows - 1) / G::kRows), splits, kShares),
                        dim3(kAdBlock), G::kLds, st, a);
     return MOONEP_OK;
 }
@@ -1268,11 +1310,11 @@ int expand_as(ExpandArgs a, hipStream_t st)
         return MOONEP_OK;
     }
     const int64_t blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
-    int64_t per = tiles * blocks / 1024;
-    per = per < 1 ? 1 : (per > 32 ? 32 : per);
-    while ((tiles + per - 1) / per > 65535)
-        per *= 2;
-    a.tiles = (int32_t)per;
+    // two workgroups per CU, all at once
+    int64_t per = (tiles * blocks + 511) / 512;
+    per = per < (tiles + 65534) / 65535 ? (tiles + 65534) / 65535 : per;
+    a.tiles = (int32_t)(per < tiles ? per : tiles);
+    per = a.tiles;
     using G = ExpandRing<PS, kHalf, CT>;
     static bool raised[64] = {};
     if (raise_lds((const void *)expand_kernel<PS, kHalf, CT, kNN>, G::kLds, raised) != MOONEP_OK)
@@ -1294,12 +1336,17 @@ int expand(const ExpandArgs &a, hipStream_t st)
     }
 }
 
-template <int T, int CT>
-void wgrad_as(WgradArgs a, hipStream_t st)
+template <int T, int S>
+int wgrad_as(WgradArgs a, hipStream_t st)
 {
-    a.blocks_a = (a.in_dim + 64 * CT - 1) / (64 * CT);
-    const int32_t blocks = a.blocks_a + (a.out_dim + 64 * CT - 1) / (64 * CT);
-    hipLaunchKernelGGL((wgrad_kernel<T, CT>), dim3(blocks, a.nchunks), dim3(kAdBlock), 0, st, a);
+    using G = WgradCfg<T, S>;
+    static bool raised[64] = {};
+    if (raise_lds((const void *)wgrad_kernel<T, S>, G::kLds, raised) != MOONEP_OK)
+        return MOONEP_ERR_HIP;
+    a.blocks_a = (a.in_dim + kGradCols - 1) / kGradCols;
+    const int32_t blocks = a.blocks_a + (a.out_dim + kGradCols - 1) / kGradCols;
+    hipLaunchKernelGGL((wgrad_kernel<T, S>), dim3(blocks, a.nchunks), dim3(kAdBlock), G::kLds, st, a);
+    return MOONEP_OK;
 }
 
 // Consecutive arrays of the workspace, each at a multiple of 256 bytes.
@@ -1419,7 +1466,7 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         a.part = carve.take<float>((size_t)(kMostChunks + ad.n) * window);
         a.d_bank = d_bank;
         // chunks of at least 128 positions, 64 at most, for about 512 workgroups
-        const int32_t width = ad.rank <= 32 ? 512 : 256, blocks = (ad.in_dim + ad.out_dim + width - 1) / width;
+        const int32_t blocks = (ad.in_dim + ad.out_dim + kGradCols - 1) / kGradCols;
         int32_t chunks = 512 / blocks;
         chunks = chunks < 1 ? 1 : (chunks > kMostChunks ? kMostChunks : chunks);
         int64_t chunk = ((int64_t)rows + chunks - 1) / chunks;
@@ -1428,14 +1475,15 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         a.chunk = (int32_t)chunk;
         a.nchunks = (int32_t)(((int64_t)rows + chunk - 1) / chunk);
         if (rows) {
-            if (ad.rank <= 16)
-                wgrad_as<1, 8>(a, st);
-            else if (ad.rank <= 32)
-                wgrad_as<2, 8>(a, st);
-            else if (ad.rank <= 64)
-                wgrad_as<4, 4>(a, st);
-            else
-                wgrad_as<8, 4>(a, st);
+            int rc;
+            switch (rank_tiles(ad.rank)) {
+            case 1: rc = wgrad_as<1, 2>(a, st); break;
+            case 2: rc = wgrad_as<2, 2>(a, st); break;
+            case 4: rc = wgrad_as<4, 2>(a, st); break;
+            default: rc = wgrad_as<8, 2>(a, st);
+            }
+            if (rc != MOONEP_OK)
+                return rc;
         }
         const int64_t nb = (window + kAdBlock * 4 - 1) / (kAdBlock * 4);
         hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(nb < 128 ? nb : 128), ad.n), dim3(kAdBlock),
