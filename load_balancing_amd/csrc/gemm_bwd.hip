@@ -11,7 +11,7 @@
 // matrix instruction.  What differs is the memory order of the operands: the
 // forward contracts over the contiguous axis of both, d_x over the rows of W,
 // and g over the rows of both.  An operand whose contraction axis is the row
-// stays as it is in memory in its stage, [kBK rows][columns], and
+// stays as it is in memory in its stage, [BK rows][columns], and
 // ds_read_b64_tr_b16 transposes on the way to the registers: 16 lanes read a
 // block of 4 rows x 16 columns, 8 bytes each (lane s: row s / 4, columns 4 (s %
 // 4) .. + 3), and lane d gets column d, rows 0 .. 3.  Two such reads make the 8
@@ -35,8 +35,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 namespace {
-
-constexpr int kBK = 64;  // contraction per LDS stage
 
 // A lane's byte offset in a transposed stage of rows of RB bytes, for 32-column
 // tile 0 and k-step 0; tile T is at offset ^ (T << 6), k-step ks at + ks 16 RB.
@@ -140,19 +138,28 @@ __device__ __forceinline__ void lds_barrier()
 // d_x: rows of d_y against W, contracted over W's rows
 // ---------------------------------------------------------------------------
 
-template <int BM, int BN, int WM, int WN>
+// What the rows behind a segment's last are read as: zeros, so that they add
+// nothing whatever the buffer holds there.
+__device__ __align__(16) const uint32_t g_zero_row[4] = {0, 0, 0, 0};
+
+template <int BM, int BN, int WM, int WN, int BK, int S>
 struct DxCfg {
     static constexpr int kTM = WM / 32, kTN = WN / 32;
     static constexpr int kWM = BM / WM, kWN = BN / WN;
     static constexpr int kWavesG = kWM * kWN;
     static constexpr int kThreads = kWavesG * 64;
-    static constexpr int kRowA = kBK * 2, kRowB = BN * 2;  // bytes of a stage row
-    static constexpr int kStageA = BM * kRowA, kStageB = kBK * kRowB;
+    static constexpr int kRowA = BK * 2, kRowB = BN * 2;  // bytes of a stage row
+    static constexpr int kStageA = BM * kRowA, kStageB = BK * kRowB;
     static constexpr int kStageBytes = kStageA + kStageB;
     static constexpr int kAInstr = kStageA / 1024 / kWavesG, kBInstr = kStageB / 1024 / kWavesG;
+    static constexpr int kPerStage = kAInstr + kBInstr;
+    // The k-step whose reads the next stage's loads are issued behind: their address
+    // arithmetic then runs under matrix instructions, and with more than two slots there
+    // is time (256 x 256 tiles, four slots: 1515 -> 1490 us on the sweep).
+    static constexpr int kIssueAt = S > 2 ? BK / 16 - 1 : 0;
     // Epilogue: each wave's own 16 rows of WN columns, apart from the ring, which
     // is loading the next item.
-    static constexpr int kOutRow = WN * 2 + 16, kOutAt = 2 * kStageBytes;
+    static constexpr int kOutRow = WN * 2 + 16, kOutAt = S * kStageBytes;
     static constexpr int kPieces = WN / 8;  // 16-byte pieces of a row
     static constexpr int kOVec = 16 * kPieces / 64;
     static constexpr int kStores = kTM * 2 * kOVec;  // per wave and item
@@ -160,7 +167,8 @@ struct DxCfg {
     static_assert(kStageA % (1024 * kWavesG) == 0 && kStageB % (1024 * kWavesG) == 0, "DMA rounds");
     static_assert(16 * kPieces % 64 == 0, "whole stores of 16 rows");
     // 16-byte chunk c of row r of the A part sits at c ^ swz(r), as in gemm.hip
-    __device__ static constexpr int swz(int r) { return (r / 2) % 8; }
+    // (rows of 64 bytes share the banks by four, of 128 by two)
+    __device__ static constexpr int swz(int r) { return BK == 64 ? r / 2 % 8 : r / 4 % 4; }
 };
 
 struct DxArgs {
@@ -173,10 +181,10 @@ struct DxArgs {
 
 constexpr int kGroupM = 8;  // row tiles per item group, as in gemm.hip
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_kernel(DxArgs a)
+template <int BM, int BN, int WM, int WN, int BK, int S>
+__global__ __launch_bounds__((DxCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expert_dx_kernel(DxArgs a)
 {
-    using G = DxCfg<BM, BN, WM, WN>;
+    using G = DxCfg<BM, BN, WM, WN, BK, S>;
     extern __shared__ __align__(16) uint16_t lds[];
     char *ring = (char *)lds;
     int32_t *seg_start = (int32_t *)(ring + G::kSegAt);  // [E + cap + 1]
@@ -192,7 +200,7 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
     const int64_t first = xcd_slot((int)blockIdx.x, P);
     if (first >= items)
         return;
-    const int32_t nk = a.out_dim / kBK;
+    const int32_t nk = a.out_dim / BK;
     const int wm = wave / G::kWN, wn = wave % G::kWN;
 
     struct Item {
@@ -227,8 +235,8 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
         // rows and columns past the end are not stored: the first serve them
 #pragma unroll
         for (int v = 0; v < G::kAInstr; ++v) {
-            const int row = (v * G::kWavesG + wave) * 8 + lane / 8;
-            const int chunk = (lane % 8) ^ G::swz(row);
+            const int row = ((v * G::kWavesG + wave) * 64 + lane) / (BK / 8);
+            const int chunk = (lane % (BK / 8)) ^ G::swz(row);
             a_off[v] = (uint32_t)(row < i.mrows ? row : 0) * (uint32_t)a.out_dim * 2 + chunk * 16;
         }
 #pragma unroll
@@ -239,7 +247,8 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
             b_off[v] = (uint32_t)row * (uint32_t)a.in_dim * 2 + (i.n0 + chunk * 8 < a.in_dim ? chunk * 16 : 0);
         }
     };
-    // Issues the next stage into slot `to`, if one is left.
+    // Issues the next stage into slot `to`.  After the last item the loads go on
+    // with zeros, which nobody computes: so every stage is followed by as many.
     auto issue = [&](int to) {
         if (load_kt == nk) {
             load_kt = 0;
@@ -247,9 +256,13 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
             if (load_it < items)
                 begin_item();
         }
-        if (load_it >= items)
-            return;
         char *dst = ring + to * G::kStageBytes + wave * 1024;
+        if (load_it >= items) {
+#pragma unroll
+            for (int v = 0; v < G::kPerStage; ++v)
+                dma16((const char *)g_zero_row, dst + v * G::kWavesG * 1024);
+            return;
+        }
 #pragma unroll
         for (int v = 0; v < G::kAInstr; ++v)
             dma16(a_base + a_off[v], dst + v * G::kWavesG * 1024);
@@ -257,7 +270,7 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
         for (int v = 0; v < G::kBInstr; ++v)
             dma16(b_base + b_off[v], dst + G::kStageA + v * G::kWavesG * 1024);
         a_base += G::kRowA;
-        b_base += (int64_t)kBK * a.in_dim * 2;
+        b_base += (int64_t)BK * a.in_dim * 2;
         ++load_kt;
     };
 
@@ -272,9 +285,11 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
     char *mine = ring + G::kOutAt + wave * 16 * G::kOutRow;
 
     begin_item();
-    issue(0);
+#pragma unroll
+    for (int st = 0; st + 1 < S; ++st)
+        issue(st);
     int now = 0;               // slot of the stage computed next; the ring runs on across items
-    bool stores_ahead = false;  // of the loads of this item's first stage, kStores were issued
+    bool stores_ahead = false;  // behind the loads of this item's first stages, kStores were issued
     for (int64_t it = first; it < items; it += P) {
         const Item i = locate(it);
         f32x16 acc[G::kTM][G::kTN];
@@ -286,17 +301,18 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
                 for (int r = 0; r < 16; ++r)
                     acc[m][n][r] = 0.0f;
         for (int32_t kt = 0; kt < nk; ++kt) {
-            // An item's first stage was issued before the stores of the item
-            // before: where all of those were issued, they need not be waited for.
-            if (kt == 0 && stores_ahead)
-                wait_vm<G::kStores>();
+            // This stage's loads have landed once only the S - 2 stages after it are
+            // outstanding.  An item's first S - 1 were issued before the stores of the
+            // item before: where all of those were issued, they need not be waited for.
+            if (kt < S - 1 && stores_ahead)
+                wait_vm<(S - 2) * G::kPerStage + G::kStores>();
             else
-                wait_vm<0>();
+                wait_vm<(S - 2) * G::kPerStage>();
             lds_barrier();  // the stage is visible to all; the other slot is free
-            issue(now ^ 1);
+            const int free_slot = now ? now - 1 : S - 1;
             const char *sa = ring + now * G::kStageBytes;
 #pragma unroll
-            for (int ks = 0; ks < kBK / 16; ++ks) {
+            for (int ks = 0; ks < BK / 16; ++ks) {
                 bf16x8 fa[G::kTM], fb[G::kTN];
                 uint32_t at[G::kTN];
 #pragma unroll
@@ -306,6 +322,8 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
                 for (int n = 0; n < G::kTN; ++n)
                     at[n] = b_at[n] + now * G::kStageBytes + ks * 16 * G::kRowB;
                 tr_frags<G::kRowB>(at, fb);
+                if (ks == G::kIssueAt)
+                    issue(free_slot);
                 // W's columns as the instruction's rows: a lane's results are four
                 // consecutive columns of one row of d_x
 #pragma unroll
@@ -314,7 +332,7 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
                     for (int n = 0; n < G::kTN; ++n)
                         acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[n], fa[m], acc[m][n], 0, 0, 0);
             }
-            now ^= 1;
+            now = now + 1 == S ? 0 : now + 1;
         }
         // Epilogue: 16 rows at a time through the wave's own LDS, to whole lines.
         const bool full = i.mrows == BM && i.n0 + BN <= a.in_dim;
@@ -350,6 +368,7 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN>::kThreads)) void expert_dx_k
                 wave_sync();
             }
     }
+    wait_vm<0>();  // nothing is on its way into the LDS when it is given back
 }
 
 // ---------------------------------------------------------------------------
@@ -378,10 +397,6 @@ struct DwArgs {
     int64_t G, g_offset;
     float *home, *rep;
 };
-
-// What the rows behind a segment's last are read as: zeros, so that they add
-// nothing whatever the buffer holds there.
-__device__ const uint32_t g_zero_row[4] = {0, 0, 0, 0};
 
 template <int BM, int BN, int WM, int WN, int BK, int S>
 __global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expert_dw_kernel(DwArgs a)
@@ -525,8 +540,8 @@ __global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expe
             // later ones are outstanding
             wait_vm<(S - 2) * G::kPerStage>();
             lds_barrier();  // the stage is visible to all; the one before is free
-            issue(now ? now - 1 : S - 1);
             const uint32_t stage = (uint32_t)(now * G::kStageBytes);
+            const int free_slot = now ? now - 1 : S - 1;
             now = now + 1 == S ? 0 : now + 1;
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks) {
@@ -537,6 +552,10 @@ __global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expe
                 for (int i = 0; i < G::kTM + G::kTN; ++i)
                     at[i] = frag_at[i] + stage + ks * 16 * G::kRowA;
                 tr_frags<G::kRowA>(at, f);
+                // behind the stage's last reads, for their address arithmetic to run under
+                // matrix instructions (sweep: 1620 us where it came first, 1467)
+                if (ks == BK / 16 - 1)
+                    issue(free_slot);
 #pragma unroll
                 for (int i = 0; i < G::kTM; ++i)
 #pragma unroll
@@ -594,19 +613,19 @@ int prepare_launch(Kernel kernel, size_t most, bool (&raised)[64], int *cus)
     return MOONEP_OK;
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int BK, int S>
 int run_dx(const DxArgs &a, hipStream_t st)
 {
-    using G = DxCfg<BM, BN, WM, WN>;
+    using G = DxCfg<BM, BN, WM, WN, BK, S>;
     static bool raised[64] = {};
     int cus = 0;
-    const int rc = prepare_launch(expert_dx_kernel<BM, BN, WM, WN>,
+    const int rc = prepare_launch(expert_dx_kernel<BM, BN, WM, WN, BK, S>,
                                   G::kSegAt + (size_t)(2 * kMaxExperts + kMaxRanks + 1) * 4, raised, &cus);
     if (rc != MOONEP_OK)
         return rc;
     const size_t bytes = G::kSegAt + (size_t)(a.seg.E + a.seg.pl.cap + 1) * 4;
     const int per_cu = (int)((160u << 10) / bytes);
-    hipLaunchKernelGGL((expert_dx_kernel<BM, BN, WM, WN>), dim3(cus * (per_cu > 1 ? per_cu : 1)),
+    hipLaunchKernelGGL((expert_dx_kernel<BM, BN, WM, WN, BK, S>), dim3(cus * (per_cu > 1 ? per_cu : 1)),
                        dim3(G::kThreads), bytes, st, a);
     return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP;
 }
@@ -642,6 +661,7 @@ int run_dw(const DwArgs &a, hipStream_t st)
 constexpr int64_t kLargeRows = 448;    // mean rows of an expert from which d_x takes large tiles
 constexpr int64_t kLargeItemsX = 512;  // and of those tiles
 constexpr int64_t kLargeItemsW = 320;  // large tiles from which g takes them
+constexpr int64_t kFewItems = 256;     // small tiles up to which each has a CU
 
 int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *wslot, int32_t B,
                      int32_t in_dim, int32_t out_dim, const uint16_t *d_y, const uint16_t *w_home,
@@ -652,14 +672,16 @@ int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *
         return MOONEP_OK;
     const DxArgs a{seg_tables(s, plan, wslot, B), in_dim, out_dim, d_y, w_home, pool,
                    w_stride, w_offset, d_x};
-#ifdef DXV
-    return run_dx<DXV>(a, st);
-#endif
     const int64_t rows = (int64_t)s.R * s.S * s.K;
     const int64_t items = ((rows + 255) / 256 + s.E / 2) * ((in_dim + 255) / 256);
     if (rows >= kLargeRows * s.E && items >= kLargeItemsX)
-        return run_dx<256, 256, 128, 64>(a, st);
-    return run_dx<128, 128, 64, 64>(a, st);
+        return run_dx<256, 256, 128, 64, 32, 4>(a, st);
+    // where all items run at once, on a CU of their own, a third slot takes less time
+    // than a second workgroup (3387 rows, 1024 -> 192, 9 experts: 16 us for 20)
+    const int64_t small_items = ((rows + 127) / 128 + s.E / 2) * ((in_dim + 127) / 128);
+    if (small_items <= kFewItems)
+        return run_dx<128, 128, 64, 64, 64, 3>(a, st);
+    return run_dx<128, 128, 64, 64, 64, 2>(a, st);
 }
 
 int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim, int32_t out_dim,
@@ -670,13 +692,10 @@ int launch_expert_dw(const moonep_shape &s, const int32_t *plan, int32_t in_dim,
         return MOONEP_OK;
     const DwArgs a{seg_tables(s, plan, nullptr, 0), in_dim, out_dim, accumulate, x, d_y, G, g_offset,
                    home, rep};
-#ifdef DWV
-    return run_dw<DWV>(a, st);
-#endif
     const int64_t items = (int64_t)s.E * ((in_dim + 255) / 256) * ((out_dim + 255) / 256);
     if (items >= kLargeItemsW)
-        return run_dw<256, 256, 128, 64, 32, 3>(a, st);
-    return run_dw<128, 128, 64, 64, 64, 2>(a, st);
+        return run_dw<256, 256, 128, 64, 32, 4>(a, st);
+    return run_dw<128, 128, 64, 64, 64, 3>(a, st);
 }
 
 }  // namespace moonep
