@@ -45,6 +45,7 @@ constexpr int kAdBlock = 256;  // four waves
 constexpr int kMostSplits = 14, kMostSplitsBwd = 8;
 constexpr int kMostChunks = 64;
 constexpr unsigned kShares = 4;  // workgroups that share a tile's adapters
+constexpr int32_t kSomeRows = 2048;
 constexpr int32_t kFewRows = 256;  // up to here a tile's adapters are spread over waves
 
 union Frag {
@@ -394,14 +395,14 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
     }
 }
 
-// Few rows: 16 positions a workgroup, operands straight into registers.  The four
+// Few rows: 16 positions a workgroup, operands straight into registers.  The
 // waves share the rows, each with a part of the contraction, of which blockIdx.y
 // is one of gridDim.y parts; their sums are joined in LDS.  Of a tile's
 // adapters, workgroup blockIdx.z has every gridDim.z-th, and their rows.  The 16
 // rows of the instruction's tile t are indexes m T + t of the rank, so that a
 // lane's results are 4 T consecutive ones.
-template <int T, bool kNN>
-__global__ __launch_bounds__(kAdBlock) void shrink_few_kernel(ShrinkArgs a)
+template <int T, bool kNN, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void shrink_few_kernel(ShrinkArgs a)
 {
     constexpr int RT = 1;
     constexpr int U = T <= 4 ? 4 : 2;  // steps in flight
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_few_kernel(ShrinkArgs a)
     const int32_t D = a.w.D, rank = a.w.rank;
     const int64_t p0 = (int64_t)blockIdx.x * 16 * RT;
     const int32_t steps = (D + 31) / 32;
-    const int32_t cuts = (int32_t)gridDim.y * 4, cut = (int32_t)blockIdx.y * 4 + wave;
+    const int32_t cuts = (int32_t)gridDim.y * WAVES, cut = (int32_t)blockIdx.y * WAVES + wave;
     const int32_t k0 = (int32_t)((int64_t)steps * cut / cuts);
     const int32_t k1 = (int32_t)((int64_t)steps * (cut + 1) / cuts);
     const int32_t full = k1 < D / 32 ? k1 : D / 32;  // steps before this have all 32
@@ -527,7 +528,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_few_kernel(ShrinkArgs a)
     }
 
     // Row tile i is joined and written by wave i % 4.
-    __shared__ f32x4 join[RT][4][T][64];
+    __shared__ f32x4 join[RT][WAVES][T][64];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -539,22 +540,29 @@ __global__ __launch_bounds__(kAdBlock) void shrink_few_kernel(ShrinkArgs a)
         if ((i & 3) != wave || !(store[i] >> lane & 1))
             continue;
         const float s = id[i] >= 0 && a.scale ? a.scale[id[i]] : 1.0f;
+        const Parts parts(rank);
         float v[4 * T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             f32x4 sum = join[i][0][t][lane];
 #pragma unroll
-            for (int q = 1; q < 4; ++q)
+            for (int q = 1; q < WAVES; ++q)
                 sum += join[i][q][t][lane];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[j * T + t] = sum[j] * s;
+                v[j * T + t] = a.parts ? sum[j] : sum[j] * s;
         }
         float *o = a.out + ((int64_t)blockIdx.y * a.r.rows + row[i]) * rank + g * 4 * T;
 #pragma unroll
-        for (int q = 0; q < T; ++q)
-            if (g * 4 * T + q * 4 < rank)
-                *(f32x4 *)(o + q * 4) = f32x4{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+        for (int q = 0; q < T; ++q) {
+            const int32_t c = g * 4 * T + q * 4;
+            if (c >= rank)
+                continue;
+            const f32x4 w = {v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+            *(f32x4 *)(o + q * 4) = w;
+            if (a.parts)
+                parts.put(a.parts, p0 + m, c, w * s);
+        }
     }
 }
 
@@ -1225,6 +1233,12 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_join_kernel(WgradArgs a)
 
 int status() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP; }
 
+// Rows that shrink, forward and up to rank 32, takes 16 a workgroup of eight waves, each
+// with a part of the contraction: no sums over workgroups, and so one launch less
+// (1531 rows, 24 adapters, 2048 -> 1408, rank 32: 24 -> 17 us; 2000, 4096 wide, rank
+// 16: 29 -> 26; rank 64 and 300 rows: 25 -> 29, the backward's order 47 -> 66).
+bool some_rows(int32_t rows, int32_t rank) { return rows > kFewRows && rows <= kSomeRows && rank <= 32; }
+
 // Parts of a contraction over workgroups: until there are about 512.
 int split_count(int32_t rows, int32_t D, int most)
 {
@@ -1262,9 +1276,16 @@ int shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
 {
     const int32_t rows = a.r.rows;
     if (rows <= kFewRows) {
-        hipLaunchKernelGGL((shrink_few_kernel<T, kNN>), dim3((rows + 15) / 16, splits, kShares), dim3(kAdBlock), 0,
+        hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 4>), dim3((rows + 15) / 16, splits, kShares), dim3(256), 0,
                            st, a);
         return MOONEP_OK;
+    }
+    if constexpr (T <= 2 && !kNN) {
+        if (some_rows(rows, a.w.rank)) {
+            hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 8>), dim3((rows + 15) / 16, splits, kShares), dim3(512),
+                               0, st, a);
+            return MOONEP_OK;
+        }
     }
     constexpr int kBK = 64, kS = T == 8 ? 2 : T == 4 ? 3 : 4;  // 40 to 48 KiB: three workgroups a CU
     using G = ShrinkCfg<T, kNN, kBK, kS>;
@@ -1398,7 +1419,7 @@ int launch_adapter(int32_t rows, const moonep_adapters &ad, const int32_t *ids, 
         return MOONEP_OK;
     const AdRows r{ids, order, rows, ad.n};
     const bool few = rows <= kFewRows;
-    const int splits = split_count(rows, ad.in_dim, kMostSplits);
+    const int splits = some_rows(rows, ad.rank) ? 1 : split_count(rows, ad.in_dim, kMostSplits);
     Carve carve{(char *)ws};
     float *sums = splits > 1 || few ? carve.take<float>((size_t)splits * rows * ad.rank) : u;
     uint16_t *parts = few ? nullptr : carve.take<uint16_t>(parts_size(rows, ad.rank));
