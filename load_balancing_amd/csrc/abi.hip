@@ -187,7 +187,7 @@ int adapter_status(const moonep_shape *s, const moonep_adapters *ad)
     constexpr int32_t kMostDim = 1 << 22, kMostRows = 1 << 30;
     if (s->R != 1 || s->K != 1 || s->S > kMostRows || ad->n < 1 || ad->n > s->E || ad->rank < 8 ||
         ad->rank > 128 || ad->rank % 8 || ad->in_dim < 8 || ad->in_dim > kMostDim || ad->in_dim % 8 ||
-        ad->out_dim < 8 || ad->out_dim > kMostDim || ad->out_dim % 8 || ad->stride % 8 ||
+        ad->out_dim < 8 || ad->out_dim > kMostDim || ad->out_dim % 8 || ad->stride < 0 || ad->stride % 8 ||
         ad->stride > kMostElements / kMaxExperts || ad->a_offset < 0 || ad->a_offset % 8 ||
         ad->b_offset < 0 || ad->b_offset % 8)
         return MOONEP_ERR_ARG;
@@ -755,8 +755,8 @@ int moonep_expert_gemm_dx(const moonep_shape *shape, const int32_t *plan, const 
     if (rc != MOONEP_OK)
         return rc;
     if (B < 0 || (int64_t)shape->R * B >= ((int64_t)1 << 31) || !gemm_dims_ok(in_dim, out_dim) ||
-        w_stride % 8 != 0 || w_offset < 0 || w_offset % 8 != 0 ||
-        w_offset > w_stride - (int64_t)out_dim * in_dim)
+        w_stride < 0 || w_stride > ((int64_t)1 << 47) / kMaxExperts || w_stride % 8 != 0 || w_offset < 0 ||
+        w_offset % 8 != 0 || w_offset > w_stride - (int64_t)out_dim * in_dim)
         return MOONEP_ERR_ARG;
     const int64_t rows = n_entries(shape);
     const int64_t pool_rows = (int64_t)shape->R * B;
@@ -767,7 +767,9 @@ int moonep_expert_gemm_dx(const moonep_shape *shape, const int32_t *plan, const 
         !aligned(w_home, 16) || !aligned(pool, 16))
         return MOONEP_ERR_MISALIGNED;
     const Range out[] = {{d_x, (size_t)rows * in_dim * 2}};
-    const Range in[] = {{d_y, (size_t)rows * out_dim * 2},
+    const Range in[] = {{plan, (size_t)plan_layout(shape->E, shape->R).words * 4},
+                        {wslot, (size_t)(shape->E + shape->R) * 4},
+                        {d_y, (size_t)rows * out_dim * 2},
                         {w_home, (size_t)shape->E * (size_t)w_stride * 2},
                         {pool, (size_t)pool_rows * (size_t)w_stride * 2}};
     if (aliased(out, in))
@@ -784,8 +786,8 @@ int moonep_expert_gemm_dw(const moonep_shape *shape, const int32_t *plan, int32_
     int rc = shape_status(shape);
     if (rc != MOONEP_OK)
         return rc;
-    if (!gemm_dims_ok(in_dim, out_dim) || g_offset < 0 || g_offset > G - (int64_t)out_dim * in_dim ||
-        G > kMostElements / (2 * kMaxExperts))
+    if (!gemm_dims_ok(in_dim, out_dim) || G < 0 || G > kMostElements / (2 * kMaxExperts) || g_offset < 0 ||
+        g_offset > G - (int64_t)out_dim * in_dim)
         return MOONEP_ERR_ARG;
     const int64_t rows = n_entries(shape);
     if (!plan || !home_grads || !replica_grads || !present(x, rows) || !present(d_y, rows))
@@ -795,7 +797,8 @@ int moonep_expert_gemm_dw(const moonep_shape *shape, const int32_t *plan, int32_
         return MOONEP_ERR_MISALIGNED;
     const Range out[] = {{home_grads, (size_t)shape->E * (size_t)G * 4},
                          {replica_grads, (size_t)(shape->E + shape->R) * (size_t)G * 4}};
-    const Range in[] = {{x, (size_t)rows * in_dim * 2}, {d_y, (size_t)rows * out_dim * 2}};
+    const Range in[] = {{plan, (size_t)plan_layout(shape->E, shape->R).words * 4},
+                        {x, (size_t)rows * in_dim * 2}, {d_y, (size_t)rows * out_dim * 2}};
     if (aliased(out, in))
         return MOONEP_ERR_ALIAS;
     return launch_expert_dw(*shape, plan, in_dim, out_dim, x, d_y, accumulate, G, g_offset,
