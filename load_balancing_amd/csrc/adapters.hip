@@ -1027,7 +1027,7 @@ __device__ __forceinline__ int32_t adapter_rows(const int32_t *off, const int32_
 
 // One workgroup: the whole rank, T tiles of 16, against 256 columns, 64 a wave.
 // blockIdx.x: columns of x (dA), then of dy (dB); blockIdx.y: a chunk of positions,
-// whole steps of 32.  Rows and rank values come through a ring of LDS stages of one
+// whole steps of 32, of whose adapters blockIdx.z has every gridDim.z-th.  Rows and rank values come through a ring of LDS stages of one
 // step, filled by LDS-DMA; the rows' fragments, 8 positions of one column, through
 // the transposing read.  Positions of a step that belong to another adapter are
 // zeros in both operands.  The sums of an adapter whose rows lie in one chunk go to
@@ -1055,7 +1055,7 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
 {
     using G = WgradCfg<T, S>;
     extern __shared__ __align__(16) char ring[];
-    __shared__ int32_t row_of[kStepRun * kStep];
+    __shared__ int32_t row_of[kStepRun * kStep], id_of[kStepRun * kStep];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
     const bool is_a = (int32_t)blockIdx.x < a.blocks_a;
@@ -1083,63 +1083,101 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
                           (g * 8 + (m >> 2)) * G::kRow +
                           (((wave * 2) ^ (m >> 2)) << 6 | (g & 1) << 5 | (m & 3) << 3);
 
-    for (int32_t p = p_begin; p < p_end;) {
-        // the adapter of position p and its last position in this chunk
-        const int32_t row = a.r.order[p];
-        if ((uint32_t)row >= (uint32_t)rows)
+    f32x4 acc[T][4];
+    int32_t held = -1;  // the adapter whose sums these are
+    auto put = [&]() {
+        if (held < 0)
             return;
-        const int32_t e = __builtin_amdgcn_readfirstlane(a.r.ids[row]);
-        if ((uint32_t)e >= (uint32_t)a.r.n)
-            return;  // the rows without an adapter come last
         int32_t first;
-        const int32_t cnt = adapter_rows(a.off, a.keep, e, rows, &first);
-        if (p < first || p >= first + cnt)
-            return;  // not this order's plan
-        const int32_t end = first + cnt < p_end ? first + cnt : p_end;
-
-        f32x4 acc[T][4];
+        const int32_t cnt = adapter_rows(a.off, a.keep, held, rows, &first);
+        const int32_t ch = (int32_t)blockIdx.y;
+        const bool direct = cnt && first / a.chunk == ch && (first + cnt - 1) / a.chunk == ch;
+        const bool add = direct && a.accumulate;
+        float *o = direct ? a.d_bank + held * a.stride + (is_a ? a.a_off : a.b_off)
+                          : a.part + (ch + held) * window + (is_a ? 0 : (int64_t)rank * a.in_dim);
+        // a lane's results: indexes 16 t + 4 g .. + 3 of the rank, column m of each tile
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < T; ++t) {
+            const int32_t at_r = t * 16 + g * 4;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                acc[t][c] = f32x4{0, 0, 0, 0};
-
-        const int32_t step_end = (end + kStep - 1) / kStep;
-        for (int32_t s0 = p / kStep; s0 < step_end; s0 += kStepRun) {
-            const int32_t n = step_end - s0 < kStepRun ? step_end - s0 : kStepRun;
-            __syncthreads();  // the run before is done with the ring and the table
-            for (int32_t i = (int)threadIdx.x; i < n * kStep; i += kAdBlock) {
-                const int32_t pos = s0 * kStep + i;
-                row_of[i] = pos >= p && pos < end ? a.r.row(pos) : -1;
+            for (int c = 0; c < 4; ++c) {
+                const int32_t col = c0 + wave * 64 + c * 16 + m;
+                if (at_r >= rank || col >= D)
+                    continue;
+                if (is_a) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float *z = o + (int64_t)(at_r + i) * D + col;
+                        *z = add ? *z + acc[t][c][i] : acc[t][c][i];
+                    }
+                } else {
+                    f32x4 *z = (f32x4 *)(o + (int64_t)col * rank + at_r);
+                    *z = add ? *z + acc[t][c] : acc[t][c];
+                }
             }
-            __syncthreads();
+        }
+    };
+
+    for (int32_t r0 = p_begin; r0 < p_end; r0 += kStepRun * kStep) {
+        const int32_t n = p_end - r0 < kStepRun * kStep ? p_end - r0 : kStepRun * kStep;
+        __syncthreads();  // the run before is done with the ring and the tables
+        for (int32_t i = (int)threadIdx.x; i < (n + kStep - 1) / kStep * kStep; i += kAdBlock) {
+            const int32_t row = i < n ? a.r.row(r0 + i) : -1;
+            row_of[i] = row;
+            id_of[i] = a.r.id(row);
+        }
+        __syncthreads();
+        // pieces of the run: positions [p, end) of one adapter
+        uint32_t piece = 0;
+        for (int32_t p = 0, end; p < n; p = end) {
+            const int32_t id = __builtin_amdgcn_readfirstlane(id_of[p]);
+            uint64_t other = 0;
+            for (end = p; !other; end += 64) {
+                const int32_t i = end + lane;
+                other = ballot(i >= n || id_of[i < n ? i : 0] != id);
+            }
+            end += __builtin_ctzll(other) - 64;
+            if (id < 0 || piece++ % gridDim.z != blockIdx.z)
+                continue;
+            if (id != held) {
+                put();
+                held = id;
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[t][c] = f32x4{0, 0, 0, 0};
+            }
+            const int32_t s0 = p / kStep, steps = (end + kStep - 1) / kStep - s0;
             auto issue = [&](int32_t t, int slot) {
                 char *to = ring + slot * G::kStageBytes;
 #pragma unroll
                 for (int v = 0; v < G::kQInstr; ++v) {
-                    const int32_t r = row_of[t * kStep + q_row[v]];
+                    const int32_t pos = (s0 + t) * kStep + q_row[v];
+                    const int32_t r = pos >= p && pos < end ? row_of[pos] : -1;
                     dma16(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v]) : kZeros,
                           to + (v * 4 + wave) * 1024);
                 }
-                const uint16_t *src = t_p + (int64_t)(s0 + t) * 3 * T * 512 + lane * 8;
+                const uint16_t *src = t_p + (int64_t)(r0 / kStep + s0 + t) * 3 * T * 512 + lane * 8;
 #pragma unroll
                 for (int v = 0; v < G::kPInstr; ++v) {
                     const int i = (v * 4 + wave) % (3 * T);  // waves without a load of their own repeat one
                     dma16(src + i * 512, to + G::kStageQ + i * 1024);
                 }
             };
+            lds_barrier();  // the piece before is done with the ring
 #pragma unroll
             for (int t = 0; t + 1 < S; ++t)
-                if (t < n)
+                if (t < steps)
                     issue(t, t);
             int now = 0;
-            for (int32_t t = 0; t < n; ++t) {
-                if (t + S - 2 < n)
+            for (int32_t t = 0; t < steps; ++t) {
+                if (t + S - 2 < steps)
                     wait_vm<(S - 2) * G::kPerStage>();
                 else
                     wait_vm<0>();
                 lds_barrier();  // the stage is visible to all, the one before is free
-                if (t + S - 1 < n)
+                if (t + S - 1 < steps)
                     issue(t + S - 1, now ? now - 1 : S - 1);
                 const char *stage = ring + now * G::kStageBytes;
                 Frag qf[4];
@@ -1171,34 +1209,8 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
                     }
             }
         }
-
-        const bool direct = first / a.chunk == (first + cnt - 1) / a.chunk;
-        const bool add = direct && a.accumulate;
-        float *o = direct ? a.d_bank + e * a.stride + (is_a ? a.a_off : a.b_off)
-                          : a.part + ((int32_t)blockIdx.y + e) * window + (is_a ? 0 : (int64_t)rank * a.in_dim);
-        // a lane's results: indexes 16 t + 4 g .. + 3 of the rank, column m of each tile
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int32_t at_r = t * 16 + g * 4;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int32_t col = c0 + wave * 64 + c * 16 + m;
-                if (at_r >= rank || col >= D)
-                    continue;
-                if (is_a) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float *z = o + (int64_t)(at_r + i) * D + col;
-                        *z = add ? *z + acc[t][c][i] : acc[t][c][i];
-                    }
-                } else {
-                    f32x4 *z = (f32x4 *)(o + (int64_t)col * rank + at_r);
-                    *z = add ? *z + acc[t][c] : acc[t][c];
-                }
-            }
-        }
-        p = end;
     }
+    put();
 }
 
 // Adapters without rows get zeros, and the pieces of those in several chunks
@@ -1239,13 +1251,13 @@ int status() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_H
 // 16: 29 -> 26; rank 64 and 300 rows: 25 -> 29, the backward's order 47 -> 66).
 bool some_rows(int32_t rows, int32_t rank) { return rows > kFewRows && rows <= kSomeRows && rank <= 32; }
 
-// Parts of a contraction over workgroups: until there are about 512.
+// Parts of a contraction over workgroups: until there are 512 or more.
 int split_count(int32_t rows, int32_t D, int most)
 {
     const bool few = rows <= kFewRows;
     const int64_t tiles = few ? (rows + 15) / 16 : ((int64_t)rows + 63) / 64;
     const int32_t steps = (D + 127) / 128;  // two stages, or a step a wave
-    int64_t s = 512 / tiles;
+    int64_t s = few || tiles <= 256 ? 512 / tiles : (640 + tiles / 2) / tiles;
     s = s < most ? s : most;
     s = s < steps ? s : steps;
     return (int)(s < 1 ? 1 : s);
@@ -1366,7 +1378,16 @@ int wgrad_as(WgradArgs a, hipStream_t st)
         return MOONEP_ERR_HIP;
     a.blocks_a = (a.in_dim + kGradCols - 1) / kGradCols;
     const int32_t blocks = a.blocks_a + (a.out_dim + kGradCols - 1) / kGradCols;
-    hipLaunchKernelGGL((wgrad_kernel<T, S>), dim3(blocks, a.nchunks), dim3(kAdBlock), G::kLds, st, a);
+    // About as many workgroups for a chunk as it has adapters, 16 at most, while the
+    // launch is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 ->
+    // 24 us); one where a chunk is more than one run, whose pieces may go on.
+    int64_t shares = a.r.n / a.nchunks + 1;
+    shares = shares < 16 ? shares : 16;
+    shares = shares < 2048 / ((int64_t)blocks * a.nchunks) ? shares : 2048 / ((int64_t)blocks * a.nchunks);
+    if (shares < 1 || a.chunk > kStepRun * kStep)
+        shares = 1;
+    hipLaunchKernelGGL((wgrad_kernel<T, S>), dim3(blocks, a.nchunks, (unsigned)shares), dim3(kAdBlock), G::kLds,
+                       st, a);
     return MOONEP_OK;
 }
 
