@@ -525,7 +525,7 @@ int moonep_expert_glu_quant(const moonep_shape *shape, const int32_t *plan, cons
  *   d_x[r, k] = bf16( sum_n d_y[r, n] * W[n, k] )  (fp32 accumulation on the
  *               matrix cores, one rounding to nearest even).
  * d_y: bf16 [R*S*K, out_dim]; d_x: bf16 [R*S*K, in_dim], must not overlap d_y,
- * w_home or pool.  out_dim is at most 2^22 as well.
+ * w_home or pool.  out_dim is at most 2^22 as well, w_stride 2^37.
  */
 int moonep_expert_gemm_dx(const moonep_shape *shape, const int32_t *plan, const int32_t *wslot,
                           int32_t B, int32_t in_dim, int32_t out_dim, const uint16_t *d_y,
@@ -571,10 +571,11 @@ int moonep_expert_gemm_dw(const moonep_shape *shape, const int32_t *plan, int32_
  * moonep_adapter_bwd takes.  u is summed in fp32 on the matrix cores; scale * u
  * enters the second product with 16 bits (2^-17 relative), and y is rounded once.
  * A row without an adapter has u = 0 and y = base, bit for bit.
- * order: int32 [S] or NULL, the rows in the order to work in: moonep_plan's
- * src_of_slot.  Rows of one adapter that stand together share its loads, so NULL
- * (the rows as they are) is right for few rows or whole prompts one after the
- * other.  The result does not depend on it; a row that is not in it is left out.
+ * order: int32 [S] or NULL, the rows in the order to work in, each once:
+ * moonep_plan's src_of_slot.  Rows of one adapter that stand together share its
+ * loads, so NULL (the rows as they are) is right for few rows or whole prompts one
+ * after the other.  The results depend on it in the order of u's fp32 sums only; a
+ * row that is not in it is left out.
  *
  * workspace: moonep_adapter_workspace_bytes, 16-byte aligned, no initial contents
  * needed; one call at a time uses it.

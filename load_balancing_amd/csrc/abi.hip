@@ -755,7 +755,7 @@ int moonep_expert_gemm_dx(const moonep_shape *shape, const int32_t *plan, const 
     if (rc != MOONEP_OK)
         return rc;
     if (B < 0 || (int64_t)shape->R * B >= ((int64_t)1 << 31) || !gemm_dims_ok(in_dim, out_dim) ||
-        w_stride < 0 || w_stride > ((int64_t)1 << 47) / kMaxExperts || w_stride % 8 != 0 || w_offset < 0 ||
+        w_stride < 0 || w_stride > (int64_t)1 << 37 || w_stride % 8 != 0 || w_offset < 0 ||
         w_offset % 8 != 0 || w_offset > w_stride - (int64_t)out_dim * in_dim)
         return MOONEP_ERR_ARG;
     const int64_t rows = n_entries(shape);

@@ -219,40 +219,42 @@ __device__ __forceinline__ void tr_frags(const uint32_t (&lo)[N], const uint32_t
         f[i].v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(r[2 * i], r[2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Many rows: 16 positions a wave, rows and matrix through a ring of
-// LDS stages of BK values of the contraction, filled by LDS-DMA.  blockIdx.y is one
-// of gridDim.y parts of the contraction.  Of a tile's
-// adapters each of gridDim.z workgroups has every gridDim.z-th, with their rows, and
-// those without one end at once: a tile at the border of two would otherwise take
-// twice as long as all others, and the launch with it.  They come last, so that the
-// tiles with one adapter start without them, and LDS is left for them.  The matrix's stage is [16 T][BK], or
-// with kNN what memory has: BK rows of rank.
-template <int T, bool kNN, int BK, int S>
+// Many rows: 64 positions a workgroup, 16 a wave, rows and matrix through a ring of
+// LDS stages of 64 values of the contraction, filled by LDS-DMA.  The matrix's stage is
+// [16 T][64], or with kNN what memory has: 64 rows of rank.  blockIdx.y is one of
+// gridDim.y parts of the contraction.  Of a tile's adapters each of gridDim.z
+// workgroups has every gridDim.z-th, with their rows, and those without one end at
+// once: a tile at the border of two would otherwise take twice as long as all
+// others, and the launch with it.  They come last, so that the tiles with one adapter
+// start without them, and LDS is left for them.
+// Bound by memory: 32768 x 4096 rows in 49 us (5.5 TB/s) against rank 16, 65 against 64
+// with nothing written before; stages of 128 values, 128 positions and deeper rings
+// were no faster.
+template <int T, bool kNN, int S>
 struct ShrinkCfg {
-    static constexpr int kRows = 64, kStageX = kRows * BK * 2, kStageW = 16 * T * BK * 2;
+    static constexpr int kRows = 64, kK = 64, kRowBytes = 2 * kK;
+    static constexpr int kStageX = kRows * kRowBytes, kStageW = 16 * T * kRowBytes;
     static constexpr int kStageBytes = kStageX + kStageW;
-    static constexpr int kCpr = BK / 8;                     // 16-byte chunks of a row
     static constexpr int kXInstr = kStageX / 4096;          // loads of a wave for the stage's rows
     static constexpr int kWInstr = kStageW < 4096 ? 1 : kStageW / 4096;  // and for its matrix
     static constexpr int kPerStage = kXInstr + kWInstr;
-    static constexpr int kStages = S;
-    static constexpr int kLds = kStages * kStageBytes;
-    // chunk c of row r of a stage sits at c ^ swz(r): rows of 256 bytes share all banks,
-    // of 128 every other one
-    __device__ static constexpr int swz(int r) { return BK == 128 ? r % 16 : r / 2 % 8; }
+    static constexpr int kLds = S * kStageBytes;
+    // 16-byte chunk c of row r of a stage sits at c ^ swz(r): rows of 128 bytes share the
+    // banks by two
+    __device__ static constexpr int swz(int r) { return r / 2 % 8; }
 };
 
-template <int T, bool kNN, int BK, int S>
+template <int T, bool kNN, int S>
 __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 {
-    using G = ShrinkCfg<T, kNN, BK, S>;
+    using G = ShrinkCfg<T, kNN, S>;
     extern __shared__ __align__(16) char ring[];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
     const int32_t D = a.w.D, rank = a.w.rank;
     const uint32_t share = blockIdx.z, shares = gridDim.z;
     const int64_t p0 = (int64_t)blockIdx.x * G::kRows;
-    const int32_t steps = (D + BK - 1) / BK;
+    const int32_t steps = (D + G::kK - 1) / G::kK;
     const int32_t k0 = (int32_t)((int64_t)steps * blockIdx.y / gridDim.y);
     const int32_t nk = (int32_t)((int64_t)steps * (blockIdx.y + 1) / gridDim.y) - k0;
 
@@ -270,15 +272,15 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
     // Neighbours on an XCD begin 512 bytes apart and go round: rows of a power of two
     // bytes, all read at one column, would keep few of the memory's channels busy
     // (32768 x 4096, rank 16, begun alike: 61 us for 49).
-    const int32_t begin = nk ? (int32_t)(blockIdx.x / 8 * (256 / BK) % nk) : 0;
+    const int32_t begin = nk ? (int32_t)(blockIdx.x / 8 * (256 / G::kK) % nk) : 0;
     // this lane's chunk and row, of its wave's loads of a stage of rows
     const uint16_t *xp[G::kXInstr];
     int xc[G::kXInstr];
 #pragma unroll
     for (int v = 0; v < G::kXInstr; ++v) {
-        const int r = ((v * 4 + wave) * 64 + lane) / G::kCpr;
+        const int r = ((v * 4 + wave) * 64 + lane) / 8;
         const int32_t row = a.r.row(p0 + r);
-        xc[v] = ((lane % G::kCpr) ^ G::swz(r)) * 8;
+        xc[v] = ((lane % 8) ^ G::swz(r)) * 8;
         xp[v] = a.x + (int64_t)(row < 0 ? 0 : row) * D + xc[v];
     }
     const int64_t pos = p0 + wave * 16 + m;
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
         const int32_t cur = __builtin_amdgcn_readlane(id_all, __builtin_ctzll(todo));
         todo &= ~ballot(id_all == cur);
         const uint16_t *w = a.w.first + cur * a.w.stride;
-        const int32_t kn = kNN ? rank * BK / 512 : G::kStageW / 1024;  // KiB of the matrix's stage
+        const int32_t kn = kNN ? rank / 8 : G::kStageW / 1024;  // KiB of the matrix's stage
         const uint16_t *wp[G::kWInstr];
         int wk[G::kWInstr];  // the value of the contraction that this lane's chunk begins at, in a stage
 #pragma unroll
@@ -302,14 +304,14 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 wk[v] = at * 8 / rank;
                 wp[v] = w + at * 8;
             } else {
-                const int r = at / G::kCpr;
-                wk[v] = ((at % G::kCpr) ^ G::swz(r)) * 8;
+                const int r = at / 8;
+                wk[v] = ((at % 8) ^ G::swz(r)) * 8;
                 wp[v] = w + (int64_t)(r < rank ? r : 0) * D + wk[v];
             }
         }
         auto issue = [&](int32_t kt, int st) {
             char *to = ring + st * G::kStageBytes;
-            const int32_t k = (k0 + (kt + begin < nk ? kt + begin : kt + begin - nk)) * BK;
+            const int32_t k = (k0 + (kt + begin < nk ? kt + begin : kt + begin - nk)) * G::kK;
 #pragma unroll
             for (int v = 0; v < G::kXInstr; ++v)
                 dma16(k + xc[v] < D ? (const void *)(xp[v] + k) : kZeros, to + (v * 4 + wave) * 1024);
@@ -324,27 +326,27 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
             acc[t] = f32x4{0, 0, 0, 0};
         lds_barrier();  // the adapter before is done with the ring
 #pragma unroll
-        for (int st = 0; st + 1 < G::kStages; ++st)
+        for (int st = 0; st + 1 < S; ++st)
             if (st < nk)
                 issue(st, st);
         const bool mine = ballot(id == cur) != 0;
         int now = 0;
         for (int32_t kt = 0; kt < nk; ++kt) {
-            if (kt + G::kStages - 2 < nk)
-                wait_vm<(G::kStages - 2) * G::kPerStage>();
+            if (kt + S - 2 < nk)
+                wait_vm<(S - 2) * G::kPerStage>();
             else
                 wait_vm<0>();
             lds_barrier();  // the stage is visible to all, the one before is free
-            if (kt + G::kStages - 1 < nk)
-                issue(kt + G::kStages - 1, now ? now - 1 : G::kStages - 1);
+            if (kt + S - 1 < nk)
+                issue(kt + S - 1, now ? now - 1 : S - 1);
             const char *x = ring + now * G::kStageBytes, *ws = x + G::kStageX;
-            now = now + 1 == G::kStages ? 0 : now + 1;
+            now = now + 1 == S ? 0 : now + 1;
             if (!mine)
                 continue;
 #pragma unroll
-            for (int ks = 0; ks < BK / 32; ++ks) {
+            for (int ks = 0; ks < G::kK / 32; ++ks) {
                 Frag xf, wf[T];
-                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * BK * 2 + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * G::kRowBytes + (((ks * 4 + g) ^ G::swz(m)) << 4));
                 if constexpr (kNN) {
                     const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ws +
                                         (ks * 32 + g * 8 + (m >> 2)) * rank * 2 + (m & 3) * 8;
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 } else {
 #pragma unroll
                     for (int t = 0; t < T; ++t)
-                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * BK * 2 + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * G::kRowBytes + (((ks * 4 + g) ^ G::swz(m)) << 4));
                 }
 #pragma unroll
                 for (int t = 0; t < T; ++t)
@@ -400,55 +402,39 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 // is one of gridDim.y parts; their sums are joined in LDS.  Of a tile's
 // adapters, workgroup blockIdx.z has every gridDim.z-th, and their rows.  The 16
 // rows of the instruction's tile t are indexes m T + t of the rank, so that a
-// lane's results are 4 T consecutive ones.
+// lane's results are 4 T consecutive ones.  Bound by latency (16 rows of 16
+// adapters, 2048 wide, rank 16: 5.5 us of a kernel, 6.6 with the adapters one after
+// the other).
 template <int T, bool kNN, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void shrink_few_kernel(ShrinkArgs a)
 {
-    constexpr int RT = 1;
     constexpr int U = T <= 4 ? 4 : 2;  // steps in flight
     const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
     const int m = lane & 15, g = lane >> 4;
     const int32_t D = a.w.D, rank = a.w.rank;
-    const int64_t p0 = (int64_t)blockIdx.x * 16 * RT;
+    const int64_t pos = (int64_t)blockIdx.x * 16 + m;
     const int32_t steps = (D + 31) / 32;
     const int32_t cuts = (int32_t)gridDim.y * WAVES, cut = (int32_t)blockIdx.y * WAVES + wave;
     const int32_t k0 = (int32_t)((int64_t)steps * cut / cuts);
     const int32_t k1 = (int32_t)((int64_t)steps * (cut + 1) / cuts);
     const int32_t full = k1 < D / 32 ? k1 : D / 32;  // steps before this have all 32
 
-    int32_t row[RT], id[RT];
-    const uint16_t *xp[RT];
-    uint64_t todo[RT], store[RT];
-    f32x4 res[RT][T];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        row[i] = a.r.row(p0 + i * 16 + m);
-        id[i] = a.r.id(row[i]);
-        xp[i] = a.x + (int64_t)(row[i] < 0 ? 0 : row[i]) * D + g * 8;
-        todo[i] = ballot(id[i] >= 0);
-        store[i] = blockIdx.z == 0 ? ballot(row[i] >= 0 && id[i] < 0) : 0;
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-            res[i][t] = f32x4{0, 0, 0, 0};
-    }
+    const int32_t row = a.r.row(pos), id = a.r.id(row);
+    const uint16_t *xp = a.x + (int64_t)(row < 0 ? 0 : row) * D + g * 8;
     const int32_t r0 = m * T < rank ? m * T : 0;  // lanes past the rank repeat index 0: not stored
+    uint64_t todo = ballot(id >= 0), store = blockIdx.z == 0 ? ballot(row >= 0 && id < 0) : 0;
+    f32x4 res[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        res[t] = f32x4{0, 0, 0, 0};
 
-    for (uint32_t turn = 0;; turn = turn + 1 == gridDim.z ? 0 : turn + 1) {
-        int32_t cur = -1;
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            if (cur < 0 && todo[i])
-                cur = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(todo[i]));
-        if (cur < 0)
-            break;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const uint64_t mine = ballot(id[i] == cur);
-            todo[i] &= ~mine;
-            store[i] |= turn == blockIdx.z ? mine : 0;
-        }
+    for (uint32_t turn = 0; todo; turn = turn + 1 == gridDim.z ? 0 : turn + 1) {
+        const int32_t cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        const uint64_t mine = ballot(id == cur);
+        todo &= ~mine;
         if (turn != blockIdx.z)
             continue;
+        store |= mine;
         const uint16_t *w = a.w.first + cur * a.w.stride;
         w += kNN ? (int64_t)g * 8 * rank + r0 : (int64_t)r0 * D + g * 8;
         auto load_w = [&](int32_t k, Frag (&f)[T]) {
@@ -468,101 +454,73 @@ __global__ __launch_bounds__(WAVES * 64) void shrink_few_kernel(ShrinkArgs a)
                     f[t].v = *(const bf16x8 *)(w + (int64_t)t * D + k * 32);
             }
         };
-        f32x4 acc[RT][T];
+        f32x4 acc[T];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-                acc[i][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < T; ++t)
+            acc[t] = f32x4{0, 0, 0, 0};
         int32_t k = k0;
         for (; k + U <= full; k += U) {
-            Frag x[U][RT], f[U][T];
+            Frag x[U], f[U][T];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-                    x[u][i].v = *(const bf16x8 *)(xp[i] + (k + u) * 32);
+                x[u].v = *(const bf16x8 *)(xp + (k + u) * 32);
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 load_w(k + u, f[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int t = 0; t < T; ++t)
-                        acc[i][t] = mfma16(f[u][t].v, x[u][i].v, acc[i][t]);
+                for (int t = 0; t < T; ++t)
+                    acc[t] = mfma16(f[u][t].v, x[u].v, acc[t]);
         }
         for (; k < k1; ++k) {
             // the last step may end inside: chunks past D are zeros in both operands
-            Frag x[RT], f[T];
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[i].w[j] = 0;
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    f[t].w[j] = 0;
+            Frag x{}, f[T]{};
             if (k * 32 + g * 8 < D) {
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-                    x[i].v = *(const bf16x8 *)(xp[i] + k * 32);
+                x.v = *(const bf16x8 *)(xp + k * 32);
                 load_w(k, f);
             }
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int t = 0; t < T; ++t)
-                    acc[i][t] = mfma16(f[t].v, x[i].v, acc[i][t]);
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
             for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    res[i][t][j] = id[i] == cur ? acc[i][t][j] : res[i][t][j];
-    }
-
-    // Row tile i is joined and written by wave i % 4.
-    __shared__ f32x4 join[RT][WAVES][T][64];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
+                acc[t] = mfma16(f[t].v, x.v, acc[t]);
+        }
 #pragma unroll
         for (int t = 0; t < T; ++t)
-            join[i][wave][t][lane] = res[i][t];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        if ((i & 3) != wave || !(store[i] >> lane & 1))
-            continue;
-        const float s = id[i] >= 0 && a.scale ? a.scale[id[i]] : 1.0f;
-        const Parts parts(rank);
-        float v[4 * T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            f32x4 sum = join[i][0][t][lane];
-#pragma unroll
-            for (int q = 1; q < WAVES; ++q)
-                sum += join[i][q][t][lane];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[j * T + t] = a.parts ? sum[j] : sum[j] * s;
-        }
-        float *o = a.out + ((int64_t)blockIdx.y * a.r.rows + row[i]) * rank + g * 4 * T;
+                res[t][j] = id == cur ? acc[t][j] : res[t][j];
+    }
+
+    __shared__ f32x4 join[WAVES][T][64];
 #pragma unroll
-        for (int q = 0; q < T; ++q) {
-            const int32_t c = g * 4 * T + q * 4;
-            if (c >= rank)
-                continue;
-            const f32x4 w = {v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
-            *(f32x4 *)(o + q * 4) = w;
-            if (a.parts)
-                parts.put(a.parts, p0 + m, c, w * s);
-        }
+    for (int t = 0; t < T; ++t)
+        join[wave][t][lane] = res[t];
+    __syncthreads();
+    if (wave || !(store >> lane & 1))
+        return;
+    const float s = id >= 0 && a.scale ? a.scale[id] : 1.0f;
+    const Parts parts(rank);
+    float v[4 * T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        f32x4 sum = join[0][t][lane];
+#pragma unroll
+        for (int q = 1; q < WAVES; ++q)
+            sum += join[q][t][lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j * T + t] = a.parts ? sum[j] : sum[j] * s;
+    }
+    float *o = a.out + ((int64_t)blockIdx.y * a.r.rows + row) * rank;
+#pragma unroll
+    for (int q = 0; q < T; ++q) {
+        const int32_t c = g * 4 * T + q * 4;
+        if (c >= rank)
+            continue;
+        const f32x4 part = {v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+        *(f32x4 *)(o + c) = part;
+        if (a.parts)
+            parts.put(a.parts, pos, c, part * s);
     }
 }
 
@@ -1299,12 +1257,12 @@ int shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
             return MOONEP_OK;
         }
     }
-    constexpr int kBK = 64, kS = T == 8 ? 2 : T == 4 ? 3 : 4;  // 40 to 48 KiB: three workgroups a CU
-    using G = ShrinkCfg<T, kNN, kBK, kS>;
+    constexpr int kS = T == 8 ? 2 : T == 4 ? 3 : 4;  // 40 to 48 KiB: three workgroups a CU
+    using G = ShrinkCfg<T, kNN, kS>;
     static bool raised[64] = {};
-    if (raise_lds((const void *)shrink_kernel<T, kNN, kBK, kS>, G::kLds, raised) != MOONEP_OK)
+    if (raise_lds((const void *)shrink_kernel<T, kNN, kS>, G::kLds, raised) != MOONEP_OK)
         return MOONEP_ERR_HIP;
-    hipLaunchKernelGGL((shrink_kernel<T, kNN, kBK, kS>), dim3((unsigned)(((int64_t)rows + G::kRows - 1) / G::kRows), splits, kShares),
+    hipLaunchKernelGGL((shrink_kernel<T, kNN, kS>), dim3((unsigned)(((int64_t)rows + G::kRows - 1) / G::kRows), splits, kShares),
                        dim3(kAdBlock), G::kLds, st, a);
     return MOONEP_OK;
 }

@@ -186,16 +186,17 @@ def test_accumulate_and_parts_alone(gpu_ready, case):
     c.check_backward(d_x, None)  # in place, without gradients, in the rows' own order
 
 
-def test_in_place_and_order_do_not_change_the_result(gpu_ready):
-    for case in (CASES[6], CASES[11]):
+def test_in_place_gives_the_same_bits(gpu_ready):
+    for case in (CASES[6], CASES[11], (9000, 5, 16, 1024, 264)):
         c = Case(*case)
-        c.forward(True)
-        y, u = c.y.clone(), c.u.clone()
-        c.forward(False)
-        assert torch.equal(c.y, y) and torch.equal(c.u, u)
-        inplace = c.base.clone()
-        c.forward(base=inplace, y=inplace)
-        assert torch.equal(inplace, y)
+        for order in (True, False):
+            c.forward(order)
+            y, u = c.y.clone(), c.u.clone()
+            inplace = c.base.clone()
+            c.forward(order, base=inplace, y=inplace)
+            assert torch.equal(inplace, y) and torch.equal(c.u, u)
+            c.y.copy_(y)
+            c.check_forward()
 
 
 @pytest.mark.parametrize("N", [40, 2200])
