@@ -918,15 +918,13 @@ int moonep_grad_table(int64_t n, const uint64_t *src, const uint64_t *dst, const
     }
     if (need > entries)
         return MOONEP_ERR_WORKSPACE;
-    if (need && !table)
+    if (entries && !table)
         return MOONEP_ERR_NULL_PTR;
-    if (!need)
-        return MOONEP_OK;
     // every span of memory in order of its address: none may begin inside another
     struct Span {
         uint64_t at, end;
     };
-    Span *all = (Span *)malloc((size_t)spans * sizeof(Span));
+    Span *all = (Span *)malloc((size_t)(spans + 1) * sizeof(Span));
     if (!all)
         return MOONEP_ERR_WORKSPACE;
     int64_t k = 0;
@@ -955,6 +953,8 @@ int moonep_grad_table(int64_t n, const uint64_t *src, const uint64_t *dst, const
             w[3] = types[i];
         }
     }
+    for (; w < table + entries * 4; w += 4)
+        w[0] = w[1] = w[2] = w[3] = 0;
     return MOONEP_OK;
 }
 

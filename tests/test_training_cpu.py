@@ -140,10 +140,10 @@ def table(src, dst, counts, types, entries=None):
     n = len(counts)
     need = mx.moonep_grad_entries(counts)
     entries = need if entries is None else entries
-    words = (ctypes.c_int64 * (4 * max(1, need)))()
+    words = (ctypes.c_int64 * (4 * max(1, need, entries)))(*[-1] * (4 * max(1, need, entries)))
     U, I, T = ctypes.c_uint64 * n, ctypes.c_int64 * n, ctypes.c_int32 * n
     rc = mx.lib().moonep_grad_table(n, U(*src), U(*dst) if dst else None, I(*counts), T(*types), entries, words)
-    return rc, [tuple(words[4 * i:4 * i + 4]) for i in range(max(need, 0))]
+    return rc, [tuple(words[4 * i:4 * i + 4]) for i in range(max(need, entries, 0))]
 
 
 def test_grad_table(L):
@@ -157,6 +157,10 @@ def test_grad_table(L):
                     (1 << 24, 1 << 24, 5, mx.BF16)]
     rc, rows = table([1 << 20, 1 << 24], [1 << 28, 1 << 24], [2, 5], [mx.F32, mx.BF16])
     assert rc == OK and rows == [(1 << 20, 1 << 28, 2, mx.F32), (1 << 24, 1 << 24, 5, mx.BF16)]
+    # entries past the last run have no elements
+    for counts, used in (([5], 1), ([], 0)):
+        rc, rows = table([4096] * used, None, counts, [mx.F32] * used, entries=3)
+        assert rc == OK and rows[used:] == [(0, 0, 0, 0)] * (3 - used)
     # neighbours that touch are apart
     assert table([4096, 4096 + 40], None, [10, 10], [mx.F32, mx.F32])[0] == OK
 
