@@ -45,8 +45,9 @@
  * Conventions shared by every call:
  *  - All array arguments are DEVICE pointers owned by the caller; the library
  *    allocates nothing.  Between calls it keeps only the CU's LDS size (read
- *    once per process) and, per device, whether one kernel's dynamic-LDS limit
- *    has been raised for large E and R (one kernel for bf16, and the 8-bit ones).
+ *    once per process) and, per device, whether a kernel's dynamic-LDS limit has
+ *    been raised (one forward product's for large E and R, the 8-bit ones', the
+ *    experts' gradients', the adapters' gradients' above rank 32).
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).  Every
  *    call only enqueues work; none waits for the device, except
  *    moonep_read_error.  Output sizes depend on the shape alone, so no call
@@ -635,7 +636,8 @@ int moonep_adapter_bwd(const moonep_shape *shape, const moonep_adapters *ad, con
  * of the clipped one (may be the same), elements, type (MOONEP_F32 or MOONEP_BF16,
  * of both).  moonep_grad_table writes it, on the host, for the caller to copy to
  * the device: tensor i, counts[i] elements at src[i], in runs of at most
- * MOONEP_GRAD_RUN (a run is one workgroup's work; longer ones are right as well).
+ * MOONEP_GRAD_RUN (a run is one workgroup's work; longer ones are right as well);
+ * entries past the last run get no elements and add nothing.
  * dst NULL: dst[i] = src[i].  It refuses (MOONEP_ERR_ARG) a negative count or an unknown
  * type, (MOONEP_ERR_MISALIGNED) an address that is no multiple of the element,
  * (MOONEP_ERR_NULL_PTR) a NULL address of a tensor with elements,

@@ -148,6 +148,11 @@ CASES = [
     (32769, 5, 32, 136, 64),
     (33000, 2, 64, 64, 200),
     (32770, 3, 96, 72, 64),
+    (8192, 6, 16, 1024, 72),
+    (8193, 6, 16, 1016, 72),
+    (4097, 5, 32, 2048, 64),
+    (513, 6, 128, 1024, 520),
+    (4099, 32, 32, 264, 1096),
 ]
 
 
