@@ -876,16 +876,18 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
     }
 }
 
-// Few rows: the four waves of a workgroup and gridDim.z of them share a row tile
+// Few rows: the four waves of a workgroup and kFewShares of them share a row tile
 // and its 16 CT columns, each with some of the tile's adapters and their rows.
+constexpr uint32_t kFewShares = 4;  // workgroups of a row tile and its columns
+
 template <int PS, bool kHalf, int CT, bool kNN, bool kJoin>
-__global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
+__device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, uint32_t tile, uint32_t part)
 {
     using X = Expand<PS, kHalf, CT, kNN>;
     const int wave = (int)threadIdx.x >> 6, m = lane_id() & 15, g = lane_id() >> 4;
-    const X x(a.w, (int32_t)blockIdx.x * 16 * CT);
-    const uint32_t share = blockIdx.z * 4 + wave, shares = gridDim.z * 4;
-    const int64_t p0 = (int64_t)blockIdx.y * 16;
+    const X x(a.w, (int32_t)block * 16 * CT);
+    const uint32_t share = part * 4 + wave, shares = kFewShares * 4;
+    const int64_t p0 = (int64_t)tile * 16;
     // of position m, and of this lane's results
     const int32_t u_row = a.r.row(p0 + m), u_id = a.r.id(u_row);
     uint64_t left = ballot(u_id >= 0), taken = share == 0 ? ballot(u_row >= 0 && u_id < 0 && a.y != a.base) : 0;
@@ -945,7 +947,7 @@ __global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
             }
         }
     } else {
-        x.load_parts(a.parts, blockIdx.y, u);
+        x.load_parts(a.parts, tile, u);
         x.mask_parts(u);
     }
     f32x4 res[CT];
@@ -964,6 +966,12 @@ __global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
         x.product(wf, u, mine, res);
     }
     x.store(a.y, row, id, wanted, b, res);
+}
+
+template <int PS, bool kHalf, int CT>
+__global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
+{
+    expand_few<PS, kHalf, CT, false, true>(a, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // ---------------------------------------------------------------------------
@@ -1021,20 +1029,20 @@ struct WgradCfg {
 };
 
 template <int T, int S>
-__global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
+__device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t block, uint32_t chunk, uint32_t share,
+                                      uint32_t shares, char *ring)
 {
     using G = WgradCfg<T, S>;
-    extern __shared__ __align__(16) char ring[];
     __shared__ int32_t row_of[kStepRun * kStep], id_of[kStepRun * kStep];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
-    const bool is_a = (int32_t)blockIdx.x < a.blocks_a;
+    const bool is_a = (int32_t)block < a.blocks_a;
     const int32_t D = is_a ? a.in_dim : a.out_dim, rank = a.rank, rows = a.r.rows;
-    const int32_t c0 = ((int32_t)blockIdx.x - (is_a ? 0 : a.blocks_a)) * kGradCols;
+    const int32_t c0 = ((int32_t)block - (is_a ? 0 : a.blocks_a)) * kGradCols;
     const uint16_t *q = is_a ? a.x : a.dy;
     const uint16_t *t_p = is_a ? a.t_du : a.t_u;
     const int64_t window = (int64_t)rank * (a.in_dim + a.out_dim);
-    const int32_t p_begin = (int32_t)blockIdx.y * a.chunk;
+    const int32_t p_begin = (int32_t)chunk * a.chunk;
     const int32_t p_end = rows - p_begin < a.chunk ? rows : p_begin + a.chunk;
 
     // this lane's row of a step and chunk, of its wave's loads; columns past D are
@@ -1060,7 +1068,7 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
             return;
         int32_t first;
         const int32_t cnt = adapter_rows(a.off, a.keep, held, rows, &first);
-        const int32_t ch = (int32_t)blockIdx.y;
+        const int32_t ch = (int32_t)chunk;
         const bool direct = cnt && first / a.chunk == ch && (first + cnt - 1) / a.chunk == ch;
         const bool add = direct && a.accumulate;
         float *o = direct ? a.d_bank + held * a.stride + (is_a ? a.a_off : a.b_off)
@@ -1107,7 +1115,7 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
                 other = ballot(i >= n || id_of[i < n ? i : 0] != id);
             }
             end += __builtin_ctzll(other) - 64;
-            if (id < 0 || piece++ % gridDim.z != blockIdx.z)
+            if (id < 0 || piece++ % shares != share)
                 continue;
             if (id != held) {
                 put();
@@ -1181,6 +1189,51 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
         }
     }
     put();
+    if (a.nchunks > 1 || a.accumulate)
+        return;
+    // no adapter has rows in several chunks, and no join follows: those without any get
+    // their zeros here
+    const int32_t cols = D - c0 < kGradCols ? D - c0 : kGradCols;
+    for (int32_t e0 = 0; e0 < a.r.n; e0 += 64) {
+        const int32_t e = e0 + lane;
+        int32_t first;
+        uint64_t empty = ballot(e < a.r.n && (uint32_t)e % shares == share &&
+                                adapter_rows(a.off, a.keep, e < a.r.n ? e : 0, rows, &first) == 0);
+        for (; empty; empty &= empty - 1) {
+            float *o = a.d_bank + (e0 + __builtin_ctzll(empty)) * a.stride + (is_a ? a.a_off : a.b_off);
+            if (is_a) {
+                if ((int32_t)threadIdx.x < cols)
+                    for (int32_t i = 0; i < rank; ++i)
+                        o[(int64_t)i * D + c0 + threadIdx.x] = 0.0f;
+            } else {
+                for (int32_t i = (int)threadIdx.x * 4; i < cols * rank; i += kAdBlock * 4)
+                    *(f32x4 *)(o + (int64_t)c0 * rank + i) = f32x4{0, 0, 0, 0};
+            }
+        }
+    }
+}
+
+template <int T, int S>
+__global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
+{
+    extern __shared__ __align__(16) char ring[];
+    wgrad<T, S>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, ring);
+}
+
+// Few rows: the gradients and the rows of d_x in one launch, which they share by
+// workgroups (200 rows of 16 adapters, 4096 -> 4096, rank 16, 28.7 -> 24.9 us with
+// the join left out as well; 55 of 20, 840 -> 104, rank 32: 23.3 -> 19.0).
+template <int PS, bool kHalf, int CT, int T, int S>
+__global__ __launch_bounds__(kAdBlock) void few_grads_kernel(WgradArgs a, ExpandArgs e, uint32_t blocks,
+                                                             uint32_t shares, uint32_t dx_blocks)
+{
+    extern __shared__ __align__(16) char ring[];
+    if (blockIdx.x < blocks * shares) {
+        wgrad<T, S>(a, blockIdx.x % blocks, 0, blockIdx.x / blocks, shares, ring);
+        return;
+    }
+    const uint32_t i = blockIdx.x - blocks * shares, tile = i / dx_blocks;
+    expand_few<PS, kHalf, CT, true, false>(e, i % dx_blocks, tile / kFewShares, tile % kFewShares);
 }
 
 // Adapters without rows get zeros, and the pieces of those in several chunks
@@ -1300,13 +1353,13 @@ template <int PS, bool kHalf, int CT, bool kNN>
 void expand_as(ExpandArgs a, hipStream_t st)
 {
     const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
-    if (a.r.rows <= kFewRows) {
-        const dim3 grid((unsigned)((a.w.D + 63) / 64), (unsigned)tiles, 4);
-        if constexpr (!kNN)
-            hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4, kNN, true>), grid, dim3(kAdBlock), 0, st, a);
-        else
-            hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4, kNN, false>), grid, dim3(kAdBlock), 0, st, a);
-        return;
+    if constexpr (!kNN) {
+        if (a.r.rows <= kFewRows) {
+            hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4>),
+                               dim3((unsigned)((a.w.D + 63) / 64), (unsigned)tiles, kFewShares),
+                               dim3(kAdBlock), 0, st, a);
+            return;
+        }
     }
     const int64_t blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
     // two workgroups per CU, all at once (32768 rows, 4096 wide, rank 64, the whole call:
@@ -1333,36 +1386,61 @@ void expand(const ExpandArgs &a, hipStream_t st)
     }
 }
 
-template <int T, int S>
-int wgrad_as(WgradArgs a, hipStream_t st)
+// The kernel's dynamic-LDS limit raised to what it takes, once per device.
+template <class Kernel>
+int raise_lds(Kernel kernel, int bytes, bool (&raised)[64])
 {
-    using G = WgradCfg<T, S>;
-    if constexpr (G::kLds > 48 * 1024) {
-        // the kernel's dynamic-LDS limit, raised once per device
-        static bool raised[64] = {};
-        int dev = 0;
-        if (hipGetDevice(&dev) != hipSuccess)
-            return MOONEP_ERR_HIP;
-        if (dev < 0 || dev >= 64 || !raised[dev]) {
-            if (hipFuncSetAttribute((const void *)wgrad_kernel<T, S>,
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds) != hipSuccess)
-                return MOONEP_ERR_HIP;
-            if (dev >= 0 && dev < 64)
-                raised[dev] = true;
-        }
-    }
-    a.blocks_a = (a.in_dim + kGradCols - 1) / kGradCols;
-    const int32_t blocks = a.blocks_a + (a.out_dim + kGradCols - 1) / kGradCols;
-    // About as many workgroups for a chunk as it has adapters, 16 at most, while the
-    // launch is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 ->
-    // 24 us); one where a chunk is more than one run, whose pieces may go on.
+    int dev = 0;
+    if (bytes <= 48 * 1024)
+        return MOONEP_OK;
+    if (hipGetDevice(&dev) != hipSuccess)
+        return MOONEP_ERR_HIP;
+    if (dev >= 0 && dev < 64 && raised[dev])
+        return MOONEP_OK;
+    if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return MOONEP_ERR_HIP;
+    if (dev >= 0 && dev < 64)
+        raised[dev] = true;
+    return MOONEP_OK;
+}
+
+// Workgroups for a chunk: about as many as it has adapters, 16 at most, while the launch
+// is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 -> 24 us);
+// one where a chunk is more than one run, whose pieces may go on.
+uint32_t wgrad_shares(const WgradArgs &a, int32_t blocks)
+{
+    const int64_t room = 2048 / ((int64_t)blocks * a.nchunks);
     int64_t shares = a.r.n / a.nchunks + 1;
     shares = shares < 16 ? shares : 16;
-    shares = shares < 2048 / ((int64_t)blocks * a.nchunks) ? shares : 2048 / ((int64_t)blocks * a.nchunks);
-    if (shares < 1 || a.chunk > kStepRun * kStep)
-        shares = 1;
-    hipLaunchKernelGGL((wgrad_kernel<T, S>), dim3(blocks, a.nchunks, (unsigned)shares), dim3(kAdBlock), G::kLds,
-                       st, a);
+    shares = shares < room ? shares : room;
+    return shares < 1 || a.chunk > kStepRun * kStep ? 1 : (uint32_t)shares;
+}
+
+template <int T>
+int wgrad_as(const WgradArgs &a, int32_t blocks, hipStream_t st)
+{
+    using G = WgradCfg<T, 2>;
+    static bool raised[64] = {};
+    if (raise_lds(wgrad_kernel<T, 2>, G::kLds, raised) != MOONEP_OK)
+        return MOONEP_ERR_HIP;
+    hipLaunchKernelGGL((wgrad_kernel<T, 2>), dim3(blocks, a.nchunks, wgrad_shares(a, blocks)), dim3(kAdBlock),
+                       G::kLds, st, a);
+    return MOONEP_OK;
+}
+
+template <int PS, bool kHalf, int T>
+int few_grads_as(const WgradArgs &a, int32_t blocks, const ExpandArgs &e, hipStream_t st)
+{
+    using G = WgradCfg<T, 2>;
+    static bool raised[64] = {};
+    if (raise_lds(few_grads_kernel<PS, kHalf, 4, T, 2>, G::kLds, raised) != MOONEP_OK)
+        return MOONEP_ERR_HIP;
+    const uint32_t shares = a.d_bank ? wgrad_shares(a, blocks) : 0;
+    const uint32_t dx_blocks = e.y ? (uint32_t)(e.w.D + 63) / 64 : 0;
+    const uint32_t tiles = (uint32_t)(e.r.rows + 15) / 16;
+    hipLaunchKernelGGL((few_grads_kernel<PS, kHalf, 4, T, 2>),
+                       dim3(blocks * shares + dx_blocks * tiles * kFewShares), dim3(kAdBlock),
+                       shares ? G::kLds : 0, st, a, e, (uint32_t)blocks, shares, dx_blocks);
     return MOONEP_OK;
 }
 
@@ -1376,6 +1454,11 @@ struct Carve {
         X *p = (X *)at;
         at += n * sizeof(X);
         return p;
+    }
+    template <class X>
+    X *at_end() const  // the rest, for an array whose size is not counted on
+    {
+        return Carve(*this).take<X>(0);
     }
 };
 
@@ -1441,26 +1524,18 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
     if (rows == 0 && (!d_bank || accumulate))
         return MOONEP_OK;
     const AdRows r{ids, order, rows, ad.n};
-    const size_t plane = (size_t)rows * ad.rank, turned = d_bank ? turned_size(rows, ad.rank) : 0;
+    const size_t turned = d_bank ? turned_size(rows, ad.rank) : 0;
     Carve carve{(char *)ws};
     uint16_t *parts = carve.take<uint16_t>(dx ? parts_size(rows, ad.rank) : 0);
     uint16_t *t_du = carve.take<uint16_t>(turned);
     uint16_t *t_u = carve.take<uint16_t>(turned);
-    if (rows) {
-        const int splits = split_count(rows, ad.out_dim, ad.rank, kShareBwd, kMostSplitsBwd);
-        Carve sums = carve;  // done with before the gradients' pieces are made
-        float *du = sums.take<float>(splits * plane);
-        shrink<true>(ShrinkArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, dy, scale, du,
-                                nullptr}, splits, st);
-        prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, du, nullptr, dx ? parts : nullptr, 0,
-                         u, d_bank ? t_du : nullptr, d_bank ? t_u : nullptr}, st);
-        if (dx)
-            expand<true>(ExpandArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts, dx_base,
-                                    dx, 0, nullptr, nullptr, nullptr, 0}, st);
-    }
+    const bool few = rows <= kFewRows;
+    const ExpandArgs e{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts, dx_base, dx, 0,
+                       nullptr, nullptr, nullptr, 0};
+    WgradArgs a{};
+    int32_t blocks = 0;
     if (d_bank) {
         const PlanLayout pl = plan_layout(E, 1);
-        WgradArgs a{};
         a.r = r;
         a.off = plan + pl.home_row_off;
         a.keep = plan + pl.keep;
@@ -1475,34 +1550,57 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         a.t_u = t_u;
         a.x = x;
         a.dy = dy;
-        const int64_t window = (int64_t)ad.rank * ((int64_t)ad.in_dim + ad.out_dim);
-        a.part = carve.take<float>((size_t)(kMostChunks + ad.n) * window);
+        a.part = carve.at_end<float>();
         a.d_bank = d_bank;
+        a.blocks_a = (ad.in_dim + kGradCols - 1) / kGradCols;
+        blocks = a.blocks_a + (ad.out_dim + kGradCols - 1) / kGradCols;
         // 64 chunks at most, for about 512 workgroups (32768 rows, 4096 -> 4096, the whole
         // call: 297 us; 256 of them 332, 1024 315), of at least 128 positions, and of 256
         // where that leaves 256 workgroups: most adapters' rows then lie in one chunk (4099
-        // rows of 32 adapters, 2048 -> 1408: 62 -> 56; 2249 of 24, 88 -> 88: 56, 60 with 256)
-        const int32_t blocks = (ad.in_dim + ad.out_dim + kGradCols - 1) / kGradCols;
+        // rows of 32 adapters, 2048 -> 1408: 62 -> 56; 2249 of 24, 88 -> 88: 56, 60 with
+        // 256).  Few rows are one chunk: their sums need no joining.
         int32_t chunks = 512 / blocks;
         chunks = chunks < 1 ? 1 : (chunks > kMostChunks ? kMostChunks : chunks);
         int64_t chunk = ((int64_t)rows + chunks - 1) / chunks;
         chunk = (chunk + kStep - 1) / kStep * kStep;
         int64_t least = (int64_t)rows * blocks / 256 / kStep * kStep;
-        least = least < 128 ? 128 : least < 256 ? least : 256;
+        least = few || least > 256 ? 256 : least < 128 ? 128 : least;
         chunk = chunk < least ? least : chunk;
         a.chunk = (int32_t)chunk;
         a.nchunks = (int32_t)(((int64_t)rows + chunk - 1) / chunk);
-        if (rows) {
-            int rc;
+    }
+    if (rows) {
+        const int splits = split_count(rows, ad.out_dim, ad.rank, kShareBwd, kMostSplitsBwd);
+        float *du = carve.at_end<float>();  // done with before the gradients' pieces are made
+        shrink<true>(ShrinkArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, dy, scale, du,
+                                nullptr}, splits, st);
+        prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, du, nullptr, dx ? parts : nullptr, 0,
+                         u, d_bank ? t_du : nullptr, d_bank ? t_u : nullptr}, st);
+        int rc = MOONEP_OK;
+        if (few) {
             switch (rank_tiles(ad.rank)) {
-            case 1: rc = wgrad_as<1, 2>(a, st); break;
-            case 2: rc = wgrad_as<2, 2>(a, st); break;
-            case 4: rc = wgrad_as<4, 2>(a, st); break;
-            default: rc = wgrad_as<8, 2>(a, st);
+            case 1: rc = few_grads_as<1, true, 1>(a, blocks, e, st); break;
+            case 2: rc = few_grads_as<1, false, 2>(a, blocks, e, st); break;
+            case 4: rc = few_grads_as<2, false, 4>(a, blocks, e, st); break;
+            default: rc = few_grads_as<4, false, 8>(a, blocks, e, st);
             }
-            if (rc != MOONEP_OK)
-                return rc;
+            return rc != MOONEP_OK ? rc : status();
         }
+        if (dx)
+            expand<true>(e, st);
+        if (d_bank) {
+            switch (rank_tiles(ad.rank)) {
+            case 1: rc = wgrad_as<1>(a, blocks, st); break;
+            case 2: rc = wgrad_as<2>(a, blocks, st); break;
+            case 4: rc = wgrad_as<4>(a, blocks, st); break;
+            default: rc = wgrad_as<8>(a, blocks, st);
+            }
+        }
+        if (rc != MOONEP_OK)
+            return rc;
+    }
+    if (d_bank && a.nchunks != 1) {
+        const int64_t window = (int64_t)ad.rank * ((int64_t)ad.in_dim + ad.out_dim);
         const int64_t nb = (window + kAdBlock * 4 - 1) / (kAdBlock * 4);
         hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(nb < 128 ? nb : 128), ad.n), dim3(kAdBlock),
                            0, st, a);

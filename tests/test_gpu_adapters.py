@@ -153,6 +153,10 @@ CASES = [
     (4097, 5, 32, 2048, 64),
     (513, 6, 128, 1024, 520),
     (4099, 32, 32, 264, 1096),
+    # adapters without rows beside a gradient in one piece
+    (20, 500, 8, 64, 264),
+    (256, 300, 40, 520, 72),
+    (300, 120, 8, 131080, 64),
 ]
 
 
