@@ -50,11 +50,6 @@ constexpr int kMostChunks = 64;
 // 14.2, 11.6, 11.5; 1531 rows of 24: 24.0, 17.1, 17.2; 32768 rows in prompts of 800: 210,
 // 202, 202).
 constexpr unsigned kShares = 4;
-// Up to here the kernels for few rows (16 adapters, forward, us with the limit at 256 and
-// at 512: 400 rows, 4096 wide, rank 16: 17.6, 14.9; 500 rows, 4096 wide, rank 64: 30,
-// 36, rank 128: 46, 76; 1024 wide: 31, 26.  At 128, 200 rows of the backward, rank 64:
-// 50 for 44).
-constexpr int32_t kFewRows = 256;
 
 union Frag {
     uint16_t h[8];
@@ -1228,11 +1223,12 @@ __global__ __launch_bounds__(kAdBlock) void few_grads_kernel(WgradArgs a, Expand
                                                              uint32_t shares, uint32_t dx_blocks)
 {
     extern __shared__ __align__(16) char ring[];
-    if (blockIdx.x < blocks * shares) {
-        wgrad<T, S>(a, blockIdx.x % blocks, 0, blockIdx.x / blocks, shares, ring);
+    const uint32_t each = blocks * a.nchunks;
+    if (blockIdx.x < each * shares) {
+        wgrad<T, S>(a, blockIdx.x % blocks, blockIdx.x / blocks % a.nchunks, blockIdx.x / each, shares, ring);
         return;
     }
-    const uint32_t i = blockIdx.x - blocks * shares, tile = i / dx_blocks;
+    const uint32_t i = blockIdx.x - each * shares, tile = i / dx_blocks;
     expand_few<PS, kHalf, CT, true, false>(e, i % dx_blocks, tile / kFewShares, tile % kFewShares);
 }
 
@@ -1266,6 +1262,18 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_join_kernel(WgradArgs a)
 // launches
 // ---------------------------------------------------------------------------
 
+// Rows for which the kernels for few are taken: 256, up to which a narrower limit is
+// slower (200 rows, 4096 wide, rank 64, backward: 44 us for 50), or 1024 of narrow ones.
+// 16 adapters, us of the other kernels and of these, by rows x width of both sides:
+//   forward, rank 16: 300 x 4096: 17.6, 13.2   500 x 2048: 13.7, 11.4   1000 x 4096: 20, 23
+//   rank 64: 300 x 4096: 26.5, 24.6   1000 x 1024: 21, 16   500 x 4096: 27, 32
+//   backward, rank 16: 300 x 4096: 31.5, 28.7   700 x 2048: 32, 27   500 x 4096: 33, 36
+//   rank 128: 500 x 1024: 71, 58   700 x 2048: 94, 77   1000 x 4096: 136, 167.
+bool few_rows(int32_t rows, const moonep_adapters &ad)
+{
+    return rows <= 256 || (rows <= 1024 && rows * ((int64_t)ad.in_dim + ad.out_dim) <= 3 << 20);
+}
+
 int status() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP; }
 
 // Rows that shrink, forward and up to rank 32, takes 16 a workgroup of eight waves, each
@@ -1273,10 +1281,10 @@ int status() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_H
 // without it and with it, by rows x width: 1531 x 2048, rank 32: 24, 17; 8000 x 1024,
 // rank 8: 23, 20; 4000 x 2048, rank 32: 29, 27; past the limit 3000 x 4096, rank 32: 35,
 // 41; 8000 x 4096, rank 16: 60, 63; rank 64, 300 x 4096: 25, 29.  The backward's order of
-// the matrix: 47, 66.
+// the matrix: 47, 66.  (Few rows go first.)
 bool some_rows(int32_t rows, int32_t D, int32_t rank)
 {
-    return rows > kFewRows && rows <= 8192 && (int64_t)rows * D <= 1 << 23 && rank <= 32;
+    return rows <= 8192 && (int64_t)rows * D <= 1 << 23 && rank <= 32;
 }
 
 // Parts of a contraction over workgroups: about one workgroup per CU, or where there are
@@ -1286,9 +1294,8 @@ bool some_rows(int32_t rows, int32_t D, int32_t rank)
 // 36, 43), where the sums are what there is to read.  Of those each part writes 4 rank
 // bytes a row, so that there are at most D / (share rank) parts; few rows need the
 // workgroups more.
-int split_count(int32_t rows, int32_t D, int32_t rank, int32_t share, int most)
+int split_count(int32_t rows, bool few, int32_t D, int32_t rank, int32_t share, int most)
 {
-    const bool few = rows <= kFewRows;
     const int64_t tiles = few ? (rows + 15) / 16 : ((int64_t)rows + 63) / 64;
     const int32_t steps = (D + 127) / 128;  // two stages, or a step a wave
     int64_t s = tiles <= 256 ? 256 / tiles : (640 + tiles / 2) / tiles;
@@ -1307,17 +1314,19 @@ constexpr int32_t kShare = 8, kShareBwd = 4;
 // Tiles of 16 that a rank takes, a power of two.
 int rank_tiles(int32_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
+enum Form { kFew, kSome, kMany };
+
 template <int T, bool kNN>
-void shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
+void shrink_as(const ShrinkArgs &a, Form form, int splits, hipStream_t st)
 {
     const int32_t rows = a.r.rows;
-    if (rows <= kFewRows) {
+    if (form == kFew) {
         hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 4>), dim3((rows + 15) / 16, splits, kShares), dim3(256), 0,
                            st, a);
         return;
     }
     if constexpr (T <= 2 && !kNN) {
-        if (some_rows(rows, a.w.D, a.w.rank)) {
+        if (form == kSome) {
             hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 8>), dim3((rows + 15) / 16, splits, kShares), dim3(512),
                                0, st, a);
             return;
@@ -1332,13 +1341,13 @@ void shrink_as(const ShrinkArgs &a, int splits, hipStream_t st)
 }
 
 template <bool kNN>
-void shrink(const ShrinkArgs &a, int splits, hipStream_t st)
+void shrink(const ShrinkArgs &a, Form form, int splits, hipStream_t st)
 {
     switch (rank_tiles(a.w.rank)) {
-    case 1: shrink_as<1, kNN>(a, splits, st); break;
-    case 2: shrink_as<2, kNN>(a, splits, st); break;
-    case 4: shrink_as<4, kNN>(a, splits, st); break;
-    default: shrink_as<8, kNN>(a, splits, st);
+    case 1: shrink_as<1, kNN>(a, form, splits, st); break;
+    case 2: shrink_as<2, kNN>(a, form, splits, st); break;
+    case 4: shrink_as<4, kNN>(a, form, splits, st); break;
+    default: shrink_as<8, kNN>(a, form, splits, st);
     }
 }
 
@@ -1350,11 +1359,11 @@ void prepare(const PrepArgs &a, hipStream_t st)
 }
 
 template <int PS, bool kHalf, int CT, bool kNN>
-void expand_as(ExpandArgs a, hipStream_t st)
+void expand_as(ExpandArgs a, Form form, hipStream_t st)
 {
     const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
     if constexpr (!kNN) {
-        if (a.r.rows <= kFewRows) {
+        if (form == kFew) {
             hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4>),
                                dim3((unsigned)((a.w.D + 63) / 64), (unsigned)tiles, kFewShares),
                                dim3(kAdBlock), 0, st, a);
@@ -1376,13 +1385,13 @@ void expand_as(ExpandArgs a, hipStream_t st)
 }
 
 template <bool kNN>
-void expand(const ExpandArgs &a, hipStream_t st)
+void expand(const ExpandArgs &a, Form form, hipStream_t st)
 {
     switch (rank_tiles(a.w.rank)) {
-    case 1: expand_as<1, true, 8, kNN>(a, st); break;
-    case 2: expand_as<1, false, 8, kNN>(a, st); break;
-    case 4: expand_as<2, false, 8, kNN>(a, st); break;
-    default: expand_as<4, false, 4, kNN>(a, st);
+    case 1: expand_as<1, true, 8, kNN>(a, form, st); break;
+    case 2: expand_as<1, false, 8, kNN>(a, form, st); break;
+    case 4: expand_as<2, false, 8, kNN>(a, form, st); break;
+    default: expand_as<4, false, 4, kNN>(a, form, st);
     }
 }
 
@@ -1439,7 +1448,7 @@ int few_grads_as(const WgradArgs &a, int32_t blocks, const ExpandArgs &e, hipStr
     const uint32_t dx_blocks = e.y ? (uint32_t)(e.w.D + 63) / 64 : 0;
     const uint32_t tiles = (uint32_t)(e.r.rows + 15) / 16;
     hipLaunchKernelGGL((few_grads_kernel<PS, kHalf, 4, T, 2>),
-                       dim3(blocks * shares + dx_blocks * tiles * kFewShares), dim3(kAdBlock),
+                       dim3(blocks * a.nchunks * shares + dx_blocks * tiles * kFewShares), dim3(kAdBlock),
                        shares ? G::kLds : 0, st, a, e, (uint32_t)blocks, shares, dx_blocks);
     return MOONEP_OK;
 }
@@ -1497,21 +1506,21 @@ int launch_adapter(int32_t rows, const moonep_adapters &ad, const int32_t *ids, 
     if (rows == 0)
         return MOONEP_OK;
     const AdRows r{ids, order, rows, ad.n};
-    const bool few = rows <= kFewRows;
-    const int splits = some_rows(rows, ad.in_dim, ad.rank)
-                           ? 1 : split_count(rows, ad.in_dim, ad.rank, kShare, kMostSplits);
+    const bool few = few_rows(rows, ad);
+    const Form form = few ? kFew : some_rows(rows, ad.in_dim, ad.rank) ? kSome : kMany;
+    const int splits = form == kSome ? 1 : split_count(rows, few, ad.in_dim, ad.rank, kShare, kMostSplits);
     Carve carve{(char *)ws};
     float *sums = splits > 1 || few ? carve.take<float>((size_t)splits * rows * ad.rank) : u;
     uint16_t *parts = few ? nullptr : carve.take<uint16_t>(parts_size(rows, ad.rank));
     const bool ready = !few && splits == 1;  // shrink makes the parts itself
     shrink<false>(ShrinkArgs{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, x,
                              ready ? scale : nullptr, sums, ready ? parts : nullptr},
-                  splits, st);
+                  form, splits, st);
     if (!few && !ready)
         prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, sums, u, parts, 1, nullptr, nullptr,
                          nullptr}, st);
     expand<false>(ExpandArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, parts, base, y, 0,
-                             sums, u, scale, splits}, st);
+                             sums, u, scale, splits}, form, st);
     return status();
 }
 
@@ -1529,7 +1538,7 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
     uint16_t *parts = carve.take<uint16_t>(dx ? parts_size(rows, ad.rank) : 0);
     uint16_t *t_du = carve.take<uint16_t>(turned);
     uint16_t *t_u = carve.take<uint16_t>(turned);
-    const bool few = rows <= kFewRows;
+    const bool few = few_rows(rows, ad);
     const ExpandArgs e{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts, dx_base, dx, 0,
                        nullptr, nullptr, nullptr, 0};
     WgradArgs a{};
@@ -1558,22 +1567,26 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         // call: 297 us; 256 of them 332, 1024 315), of at least 128 positions, and of 256
         // where that leaves 256 workgroups: most adapters' rows then lie in one chunk (4099
         // rows of 32 adapters, 2048 -> 1408: 62 -> 56; 2249 of 24, 88 -> 88: 56, 60 with
-        // 256).  Few rows are one chunk: their sums need no joining.
+        // 256).  Few rows of many adapters are one chunk, as one run: their sums need no
+        // joining (rank 128, 1024 wide, 1000 rows of 16: 72 -> 65, 500 of 2: 65, 66, 1000 of
+        // one: 59, 93).
         int32_t chunks = 512 / blocks;
         chunks = chunks < 1 ? 1 : (chunks > kMostChunks ? kMostChunks : chunks);
         int64_t chunk = ((int64_t)rows + chunks - 1) / chunks;
         chunk = (chunk + kStep - 1) / kStep * kStep;
         int64_t least = (int64_t)rows * blocks / 256 / kStep * kStep;
-        least = few || least > 256 ? 256 : least < 128 ? 128 : least;
+        least = least < 128 ? 128 : least < 256 ? least : 256;
+        if (few && (rows <= 256 || rows <= 64 * (int64_t)ad.n))
+            least = kStepRun * kStep;
         chunk = chunk < least ? least : chunk;
         a.chunk = (int32_t)chunk;
         a.nchunks = (int32_t)(((int64_t)rows + chunk - 1) / chunk);
     }
     if (rows) {
-        const int splits = split_count(rows, ad.out_dim, ad.rank, kShareBwd, kMostSplitsBwd);
+        const int splits = split_count(rows, few, ad.out_dim, ad.rank, kShareBwd, kMostSplitsBwd);
         float *du = carve.at_end<float>();  // done with before the gradients' pieces are made
         shrink<true>(ShrinkArgs{r, {bank + ad.b_offset, ad.stride, ad.rank, ad.out_dim}, dy, scale, du,
-                                nullptr}, splits, st);
+                                nullptr}, few ? kFew : kMany, splits, st);
         prepare(PrepArgs{r, scale, ad.rank, rank_tiles(ad.rank), splits, du, nullptr, dx ? parts : nullptr, 0,
                          u, d_bank ? t_du : nullptr, d_bank ? t_u : nullptr}, st);
         int rc = MOONEP_OK;
@@ -1584,11 +1597,10 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
             case 4: rc = few_grads_as<2, false, 4>(a, blocks, e, st); break;
             default: rc = few_grads_as<4, false, 8>(a, blocks, e, st);
             }
-            return rc != MOONEP_OK ? rc : status();
+        } else if (dx) {
+            expand<true>(e, kMany, st);
         }
-        if (dx)
-            expand<true>(e, st);
-        if (d_bank) {
+        if (!few && d_bank) {
             switch (rank_tiles(ad.rank)) {
             case 1: rc = wgrad_as<1>(a, blocks, st); break;
             case 2: rc = wgrad_as<2>(a, blocks, st); break;

@@ -157,6 +157,14 @@ CASES = [
     (20, 500, 8, 64, 264),
     (256, 300, 40, 520, 72),
     (300, 120, 8, 131080, 64),
+    # few rows in one gradient's piece or several, and rows that are not few
+    (1024, 9, 40, 520, 264),
+    (1024, 2, 16, 136, 264),
+    (1025, 9, 40, 520, 264),
+    (777, 3, 96, 328, 72),
+    (900, 1, 32, 72, 72),
+    (384, 12, 16, 4096, 4096),
+    (385, 12, 16, 4096, 4096),
 ]
 
 
