@@ -765,7 +765,7 @@ struct ExpandRing {
     static constexpr int kInstr = 16 * kLanesRow / 64;    // loads of a tile
     static constexpr int kSlot = 16 * CT * 32;
     static constexpr int kLds = 4 * (kAhead + 1) * kSlot;
-    static_assert(kAhead * (kInstr + kSteps) <= 63, "outstanding accesses must fit vmcnt");
+    static_assert(kAhead * kInstr + kSteps <= 63, "outstanding accesses must fit vmcnt");
 };
 
 template <int PS, bool kHalf, int CT, bool kNN>
@@ -815,9 +815,11 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
             wave_sync();
             x.load_parts(a.parts, first + (t + 1 < n ? t + 1 : t), u2);
             issue(t + kAhead, slot ? slot - 1 : kAhead);
-            // the tile's rows have landed once only the loads that were issued after them
-            // are outstanding (and stores, which are not counted: a wait for more)
-            wait_vm<kAhead * (G::kInstr + G::kSteps)>();
+            // The tile's rows have landed once only what was issued after them is outstanding:
+            // the rows of the kAhead tiles after it and one tile's parts (the first tile's
+            // come before the ring is begun; later ones' stand between, and are needed now
+            // as well).  Matrices and stores, which are not counted, only make it wait for more.
+            wait_vm<kAhead * G::kInstr + G::kSteps>();
             asm volatile("" ::: "memory");
             const char *at = ring + slot * G::kSlot;
             slot = slot == kAhead ? 0 : slot + 1;
