@@ -245,6 +245,13 @@ struct ShrinkCfg {
     // 16-byte chunk c of row r of a stage sits at c ^ swz(r): rows of 128 bytes share the
     // banks by two
     __device__ static constexpr int swz(int r) { return r / 2 % 8; }
+    // of kNN's matrix, for the rank that fills the tiles: a transposing read takes 32 bytes
+    // of rows 4 j .. + 3 and of the rows 8 further, which would share their banks
+    // (32768 rows, 4096 wide, rank 128: 146 us without it, 87 with it)
+    __device__ static constexpr int swz_nn(int r)
+    {
+        return T == 1 ? 0 : (T == 8 ? (r & 3) << 2 : T == 4 ? (r >> 1 & 1) << 2 : 0) | (r >> 3 & 1) << 1;
+    }
 };
 
 template <int T, bool kNN, int S>
@@ -305,7 +312,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
             const int at = (v * 4 + wave) % kn * 64 + lane;  // waves without a load of their own repeat one
             if (kNN) {
                 wk[v] = at * 8 / rank;
-                wp[v] = w + at * 8;
+                wp[v] = w + (at ^ (rank == 16 * T ? G::swz_nn(wk[v]) : 0)) * 8;
             } else {
                 const int r = at / 8;
                 wk[v] = ((at % 8) ^ G::swz(r)) * 8;
@@ -353,6 +360,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 if constexpr (kNN) {
                     const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ws +
                                         (ks * 32 + g * 8 + (m >> 2)) * rank * 2 + (m & 3) * 8;
+                    const int sw = rank == 16 * T ? G::swz_nn(g * 8 + (m >> 2)) * 16 : 0;
                     constexpr int N = T < 4 ? T : 4;
 #pragma unroll
                     for (int t = 0; t < T; t += N) {
@@ -360,7 +368,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                         Frag f[N];
 #pragma unroll
                         for (int q = 0; q < N; ++q) {
-                            lo[q] = at + (t + q) * 32;
+                            lo[q] = at + ((t + q) * 32 ^ sw);
                             hi[q] = lo[q] + 8 * rank;
                         }
                         tr_frags<N>(lo, hi, f);
@@ -562,48 +570,49 @@ __device__ __forceinline__ void split3(float a, uint16_t *p0, uint16_t *p1, uint
     *p2 = (uint16_t)pack_bf16(r - bf16_lo(mid), 0.0f);
 }
 
-// One workgroup: 32 positions, 8 threads each.
+// One workgroup: 32 positions and 32 values of the rank, 4 a thread.
 __global__ __launch_bounds__(kAdBlock) void adapter_prep_kernel(PrepArgs a)
 {
-    extern __shared__ __align__(16) uint16_t turned[];  // both arrays' step, as it leaves
+    // both arrays' step and two tiles, as they leave
+    __shared__ __align__(16) uint16_t turned[2][3][2 * 512];
     const int p = (int)threadIdx.x & 31, part = (int)threadIdx.x >> 5;
-    const int32_t rank = a.rank, plane = a.tiles * 512;  // elements of one bf16 part of a step
+    const int32_t rank = a.rank, c = (int32_t)blockIdx.y * 32 + part * 4;
     const int64_t pos = (int64_t)blockIdx.x * kStep + p;
     const int32_t row = a.r.row(pos), id = a.r.id(row);
     const float s = id >= 0 ? a.scale[id] : 0.0f, by = a.scale_parts ? s : 1.0f;
-    const Parts parts(rank);
-    for (int32_t c = part * 4; c < rank; c += 32) {
+    if (c < rank) {
         f32x4 v = {0, 0, 0, 0}, w = {0, 0, 0, 0};
         if (id >= 0) {
             const float *q = a.sums + (int64_t)row * rank + c;
             v = *(const f32x4 *)q;
-            for (int32_t i = 1; i < a.splits; ++i)
-                v += *(const f32x4 *)(q + i * ((int64_t)a.r.rows * rank));
             if (a.t_u)
                 w = *(const f32x4 *)(a.u + (int64_t)row * rank + c) * s;
+#pragma unroll 4
+            for (int32_t i = 1; i < a.splits; ++i)
+                v += *(const f32x4 *)(q + i * ((int64_t)a.r.rows * rank));
         }
         if (row >= 0 && a.total)
             *(f32x4 *)(a.total + (int64_t)row * rank + c) = v;
         if (row >= 0 && a.parts)
-            parts.put(a.parts, pos, c, v * by);
+            Parts(rank).put(a.parts, pos, c, v * by);
         if (a.t_u) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int32_t r = c + j;
-                uint16_t *t = turned + (r / 16 * 64 + p / 8 * 16 + r % 16) * 8 + p % 8;
-                split3(v[j], t, t + plane, t + 2 * plane);
-                t += 3 * plane;
-                split3(w[j], t, t + plane, t + 2 * plane);
+                const int r = part * 4 + j, at = (r / 16 * 64 + p / 8 * 16 + r % 16) * 8 + p % 8;
+                split3(v[j], &turned[0][0][at], &turned[0][1][at], &turned[0][2][at]);
+                split3(w[j], &turned[1][0][at], &turned[1][1][at], &turned[1][2][at]);
             }
         }
     }
     if (!a.t_u)
         return;
     __syncthreads();
-    const int32_t words = 3 * plane / 8;
-    for (int32_t i = (int)threadIdx.x; i < 2 * words; i += kAdBlock) {
-        u32x4 *to = (u32x4 *)(i < words ? a.t_sum : a.t_u) + (int64_t)blockIdx.x * words;
-        to[i < words ? i : i - words] = ((const u32x4 *)turned)[i];
+    const int tiles = a.tiles < 2 ? 1 : 2;
+    for (int i = (int)threadIdx.x; i < 2 * 3 * tiles * 64; i += kAdBlock) {
+        const int chunk = i % (tiles * 64), b = i / (tiles * 64);  // array and part
+        u32x4 *to = (u32x4 *)(b < 3 ? a.t_sum : a.t_u) +
+                    (((int64_t)blockIdx.x * 3 + b % 3) * a.tiles + blockIdx.y * 2) * 64;
+        to[chunk] = ((const u32x4 *)turned[b / 3][b % 3])[chunk];
     }
 }
 
@@ -873,17 +882,15 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
     }
 }
 
-// Few rows: the four waves of a workgroup and kFewShares of them share a row tile
-// and its 16 CT columns, each with some of the tile's adapters and their rows.
-constexpr uint32_t kFewShares = 4;  // workgroups of a row tile and its columns
-
+// Few rows: the four waves of a workgroup, and `parts` of them, share a row tile and
+// its 16 CT columns, each with some of the tile's adapters and their rows.
 template <int PS, bool kHalf, int CT, bool kNN, bool kJoin>
-__device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, uint32_t tile, uint32_t part)
+__device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, uint32_t tile, uint32_t part, uint32_t parts)
 {
     using X = Expand<PS, kHalf, CT, kNN>;
     const int wave = (int)threadIdx.x >> 6, m = lane_id() & 15, g = lane_id() >> 4;
     const X x(a.w, (int32_t)block * 16 * CT);
-    const uint32_t share = part * 4 + wave, shares = kFewShares * 4;
+    const uint32_t share = part * 4 + wave, shares = parts * 4;
     const int64_t p0 = (int64_t)tile * 16;
     // of position m, and of this lane's results
     const int32_t u_row = a.r.row(p0 + m), u_id = a.r.id(u_row);
@@ -968,7 +975,7 @@ __device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, 
 template <int PS, bool kHalf, int CT>
 __global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
 {
-    expand_few<PS, kHalf, CT, false, true>(a, blockIdx.x, blockIdx.y, blockIdx.z);
+    expand_few<PS, kHalf, CT, false, true>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z);
 }
 
 // ---------------------------------------------------------------------------
@@ -978,7 +985,7 @@ __global__ __launch_bounds__(kAdBlock) void expand_few_kernel(ExpandArgs a)
 struct WgradArgs {
     AdRows r;  // order: the plan's
     const int32_t *off, *keep;
-    int32_t rank, in_dim, out_dim, chunk, nchunks, blocks_a, accumulate;
+    int32_t rank, tiles, in_dim, out_dim, chunk, nchunks, blocks_a, blocks, accumulate;
     int64_t stride, a_off, b_off;
     const uint16_t *t_du, *t_u;  // as adapter_prep_kernel leaves them
     const uint16_t *x, *dy;
@@ -996,9 +1003,9 @@ __device__ __forceinline__ int32_t adapter_rows(const int32_t *off, const int32_
     return o >= 0 && n >= 0 && o <= rows - n ? n : 0;
 }
 
-// One workgroup: the whole rank, T tiles of 16, against 256 columns, 64 a wave.
-// blockIdx.x: columns of x (dA), then of dy (dB); blockIdx.y: a chunk of positions,
-// whole steps of 32, of whose adapters blockIdx.z has every gridDim.z-th.  Rows and
+// One workgroup: T tiles of 16 of the rank against 256 columns, 64 a wave: of x (dA),
+// then of dy (dB); `part` counts these blocks within groups of T tiles.  Of its chunk
+// of positions, whole steps of 32, it has every shares-th adapter.  Rows and
 // rank values come through a ring of LDS stages of one step, filled by LDS-DMA; the
 // rows' fragments, 8 positions of one column, through the transposing read.
 // Positions of a step that belong to another adapter are zeros in both operands.
@@ -1026,16 +1033,17 @@ struct WgradCfg {
 };
 
 template <int T, int S>
-__device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t block, uint32_t chunk, uint32_t share,
+__device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_t chunk, uint32_t share,
                                       uint32_t shares, char *ring)
 {
     using G = WgradCfg<T, S>;
+    const int32_t block = (int32_t)part % a.blocks, tile0 = (int32_t)part / a.blocks * T;
     __shared__ int32_t row_of[kStepRun * kStep], id_of[kStepRun * kStep];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int m = lane & 15, g = lane >> 4;
-    const bool is_a = (int32_t)block < a.blocks_a;
+    const bool is_a = block < a.blocks_a;
     const int32_t D = is_a ? a.in_dim : a.out_dim, rank = a.rank, rows = a.r.rows;
-    const int32_t c0 = ((int32_t)block - (is_a ? 0 : a.blocks_a)) * kGradCols;
+    const int32_t c0 = (block - (is_a ? 0 : a.blocks_a)) * kGradCols;
     const uint16_t *q = is_a ? a.x : a.dy;
     const uint16_t *t_p = is_a ? a.t_du : a.t_u;
     const int64_t window = (int64_t)rank * (a.in_dim + a.out_dim);
@@ -1073,7 +1081,7 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t block, uint32
         // a lane's results: indexes 16 t + 4 g .. + 3 of the rank, column m of each tile
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const int32_t at_r = t * 16 + g * 4;
+            const int32_t at_r = (tile0 + t) * 16 + g * 4;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int32_t col = c0 + wave * 64 + c * 16 + m;
@@ -1133,11 +1141,11 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t block, uint32
                     dma16(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v]) : kZeros,
                           to + (v * 4 + wave) * 1024);
                 }
-                const uint16_t *src = t_p + (int64_t)(r0 / kStep + s0 + t) * 3 * T * 512 + lane * 8;
+                const uint16_t *src = t_p + ((int64_t)(r0 / kStep + s0 + t) * 3 * a.tiles + tile0) * 512 + lane * 8;
 #pragma unroll
                 for (int v = 0; v < G::kPInstr; ++v) {
                     const int i = (v * 4 + wave) % (3 * T);  // waves without a load of their own repeat one
-                    dma16(src + i * 512, to + G::kStageQ + i * 1024);
+                    dma16(src + (i / T * a.tiles + i % T) * 512, to + G::kStageQ + i * 1024);
                 }
             };
             lds_barrier();  // the piece before is done with the ring
@@ -1191,6 +1199,7 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t block, uint32
     // no adapter has rows in several chunks, and no join follows: those without any get
     // their zeros here
     const int32_t cols = D - c0 < kGradCols ? D - c0 : kGradCols;
+    const int32_t i0 = tile0 * 16, i1 = rank - i0 < T * 16 ? rank : i0 + T * 16;
     for (int32_t e0 = 0; e0 < a.r.n; e0 += 64) {
         const int32_t e = e0 + lane;
         int32_t first;
@@ -1200,11 +1209,14 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t block, uint32
             float *o = a.d_bank + (e0 + __builtin_ctzll(empty)) * a.stride + (is_a ? a.a_off : a.b_off);
             if (is_a) {
                 if ((int32_t)threadIdx.x < cols)
-                    for (int32_t i = 0; i < rank; ++i)
+                    for (int32_t i = i0; i < i1; ++i)
                         o[(int64_t)i * D + c0 + threadIdx.x] = 0.0f;
             } else {
-                for (int32_t i = (int)threadIdx.x * 4; i < cols * rank; i += kAdBlock * 4)
-                    *(f32x4 *)(o + (int64_t)c0 * rank + i) = f32x4{0, 0, 0, 0};
+                for (int32_t i = (int)threadIdx.x; i < cols * T * 4; i += kAdBlock) {
+                    const int32_t at_r = i0 + i % (T * 4) * 4;
+                    if (at_r < i1)
+                        *(f32x4 *)(o + (int64_t)(c0 + i / (T * 4)) * rank + at_r) = f32x4{0, 0, 0, 0};
+                }
             }
         }
     }
@@ -1221,17 +1233,17 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
 // workgroups (200 rows of 16 adapters, 4096 -> 4096, rank 16, 28.7 -> 24.9 us with
 // the join left out as well; 55 of 20, 840 -> 104, rank 32: 23.3 -> 19.0).
 template <int PS, bool kHalf, int CT, int T, int S>
-__global__ __launch_bounds__(kAdBlock) void few_grads_kernel(WgradArgs a, ExpandArgs e, uint32_t blocks,
-                                                             uint32_t shares, uint32_t dx_blocks)
+__global__ __launch_bounds__(kAdBlock) void few_grads_kernel(WgradArgs a, ExpandArgs e, uint32_t parts,
+                                                             uint32_t shares, uint32_t dx_blocks, uint32_t dx_parts)
 {
     extern __shared__ __align__(16) char ring[];
-    const uint32_t each = blocks * a.nchunks;
+    const uint32_t each = parts * a.nchunks;
     if (blockIdx.x < each * shares) {
-        wgrad<T, S>(a, blockIdx.x % blocks, blockIdx.x / blocks % a.nchunks, blockIdx.x / each, shares, ring);
+        wgrad<T, S>(a, blockIdx.x % parts, blockIdx.x / parts % a.nchunks, blockIdx.x / each, shares, ring);
         return;
     }
     const uint32_t i = blockIdx.x - each * shares, tile = i / dx_blocks;
-    expand_few<PS, kHalf, CT, true, false>(e, i % dx_blocks, tile / kFewShares, tile % kFewShares);
+    expand_few<PS, kHalf, CT, true, false>(e, i % dx_blocks, tile / dx_parts, tile % dx_parts, dx_parts);
 }
 
 // Adapters without rows get zeros, and the pieces of those in several chunks
@@ -1251,6 +1263,7 @@ __global__ __launch_bounds__(kAdBlock) void wgrad_join_kernel(WgradArgs a)
         f32x4 v = {0, 0, 0, 0};
         if (cnt) {
             const float *src = a.part + (ch0 + e) * window + i;
+#pragma unroll 4
             for (int32_t c = ch0; c <= ch1; ++c, src += window)
                 v += *(const f32x4 *)src;
             if (a.accumulate)
@@ -1291,16 +1304,16 @@ bool some_rows(int32_t rows, int32_t D, int32_t rank)
 
 // Parts of a contraction over workgroups: about one workgroup per CU, or where there are
 // more tiles two of them, as long as that is nearer to 640 (304 tiles, 3744 wide: 129
-// us, undivided 145).  Twice as many at fewer tiles were no faster up to rank 32 (65
-// tiles, the whole backward: 62, 64) and slower above (2000 rows, 4096 wide, rank 64:
-// 36, 43), where the sums are what there is to read.  Of those each part writes 4 rank
-// bytes a row, so that there are at most D / (share rank) parts; few rows need the
-// workgroups more.
+// us, undivided 145).  Twice as many at fewer tiles were no faster up to rank 64 (65
+// tiles, the whole backward: 62, 64; 2000 rows, 4096 wide, rank 64: 36, 43); above,
+// where a CU's one workgroup has little in flight, they are (186 tiles, 5440 wide, rank
+// 128, the whole backward: 263, 230).  Each part writes sums of 4 rank bytes a row, so
+// that there are at most D / (share rank) parts; few rows need the workgroups more.
 int split_count(int32_t rows, bool few, int32_t D, int32_t rank, int32_t share, int most)
 {
     const int64_t tiles = few ? (rows + 15) / 16 : ((int64_t)rows + 63) / 64;
     const int32_t steps = (D + 127) / 128;  // two stages, or a step a wave
-    int64_t s = tiles <= 256 ? 256 / tiles : (640 + tiles / 2) / tiles;
+    int64_t s = tiles <= 256 ? (rank > 64 ? 512 : 256) / tiles : (640 + tiles / 2) / tiles;
     if (!few && s > D / (share * rank))
         s = D / (share * rank);
     s = s < most ? s : most;
@@ -1315,6 +1328,24 @@ constexpr int32_t kShare = 8, kShareBwd = 4;
 
 // Tiles of 16 that a rank takes, a power of two.
 int rank_tiles(int32_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+// The kernel's dynamic-LDS limit raised to what it takes, once per device.
+template <class Kernel>
+int raise_lds(Kernel kernel, int bytes, bool (&raised)[64])
+{
+    int dev = 0;
+    if (bytes <= 48 * 1024)
+        return MOONEP_OK;
+    if (hipGetDevice(&dev) != hipSuccess)
+        return MOONEP_ERR_HIP;
+    if (dev >= 0 && dev < 64 && raised[dev])
+        return MOONEP_OK;
+    if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+        return MOONEP_ERR_HIP;
+    if (dev >= 0 && dev < 64)
+        raised[dev] = true;
+    return MOONEP_OK;
+}
 
 enum Form { kFew, kSome, kMany };
 
@@ -1337,9 +1368,8 @@ void shrink_as(const ShrinkArgs &a, Form form, int splits, hipStream_t st)
     constexpr int kS = T == 8 ? 2 : T == 4 ? 3 : 4;  // 40 to 48 KiB: three workgroups a CU
     using G = ShrinkCfg<T, kNN, kS>;
     static_assert(G::kLds <= 48 * 1024, "no raised limit");
-    hipLaunchKernelGGL((shrink_kernel<T, kNN, kS>),
-                       dim3((unsigned)(((int64_t)rows + G::kRows - 1) / G::kRows), splits, kShares),
-                       dim3(kAdBlock), G::kLds, st, a);
+    const dim3 grid((unsigned)(((int64_t)rows + G::kRows - 1) / G::kRows), splits, kShares);
+    hipLaunchKernelGGL((shrink_kernel<T, kNN, kS>), grid, dim3(kAdBlock), G::kLds, st, a);
 }
 
 template <bool kNN>
@@ -1355,10 +1385,14 @@ void shrink(const ShrinkArgs &a, Form form, int splits, hipStream_t st)
 
 void prepare(const PrepArgs &a, hipStream_t st)
 {
-    const size_t lds = a.t_u ? (size_t)2 * 3 * a.tiles * 512 * 2 : 0;
-    hipLaunchKernelGGL(adapter_prep_kernel, dim3((unsigned)(((int64_t)a.r.rows + kStep - 1) / kStep)),
-                       dim3(kAdBlock), lds, st, a);
+    hipLaunchKernelGGL(adapter_prep_kernel,
+                       dim3((unsigned)(((int64_t)a.r.rows + kStep - 1) / kStep), (unsigned)(a.rank + 31) / 32),
+                       dim3(kAdBlock), 0, st, a);
 }
+
+// Workgroups that share a few-rows tile and its columns, of `n` such (us with 4 and with
+// one: 16 rows, 2048 wide, n = 32: 11.5, 12.1; 830 rows, 888 -> 2648, n = 2184: 30, 24).
+uint32_t few_parts(uint32_t n) { return n <= 512 ? 4 : 1; }
 
 template <int PS, bool kHalf, int CT, bool kNN>
 void expand_as(ExpandArgs a, Form form, hipStream_t st)
@@ -1366,8 +1400,9 @@ void expand_as(ExpandArgs a, Form form, hipStream_t st)
     const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
     if constexpr (!kNN) {
         if (form == kFew) {
+            const uint32_t few_blocks = (uint32_t)(a.w.D + 63) / 64;
             hipLaunchKernelGGL((expand_few_kernel<PS, kHalf, 4>),
-                               dim3((unsigned)((a.w.D + 63) / 64), (unsigned)tiles, kFewShares),
+                               dim3(few_blocks, (unsigned)tiles, few_parts(few_blocks * (uint32_t)tiles)),
                                dim3(kAdBlock), 0, st, a);
             return;
         }
@@ -1375,7 +1410,7 @@ void expand_as(ExpandArgs a, Form form, hipStream_t st)
     const int64_t blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
     // two workgroups per CU, all at once (32768 rows, 4096 wide, rank 64, the whole call:
     // 202 us; one per CU 241, four 224)
-    int64_t per = (tiles * blocks + 511) / 512;
+    int64_t per = tiles * blocks <= 768 ? 1 : (tiles * blocks + 511) / 512;
     per = per < (tiles + 65534) / 65535 ? (tiles + 65534) / 65535 : per;
     a.tiles = (int32_t)(per < tiles ? per : tiles);
     per = a.tiles;
@@ -1393,66 +1428,83 @@ void expand(const ExpandArgs &a, Form form, hipStream_t st)
     case 1: expand_as<1, true, 8, kNN>(a, form, st); break;
     case 2: expand_as<1, false, 8, kNN>(a, form, st); break;
     case 4: expand_as<2, false, 8, kNN>(a, form, st); break;
-    default: expand_as<4, false, 4, kNN>(a, form, st);
+    default: expand_as<4, false, kNN ? 8 : 4, kNN>(a, form, st);
     }
 }
 
-// The kernel's dynamic-LDS limit raised to what it takes, once per device.
-template <class Kernel>
-int raise_lds(Kernel kernel, int bytes, bool (&raised)[64])
-{
-    int dev = 0;
-    if (bytes <= 48 * 1024)
-        return MOONEP_OK;
-    if (hipGetDevice(&dev) != hipSuccess)
-        return MOONEP_ERR_HIP;
-    if (dev >= 0 && dev < 64 && raised[dev])
-        return MOONEP_OK;
-    if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
-        return MOONEP_ERR_HIP;
-    if (dev >= 0 && dev < 64)
-        raised[dev] = true;
-    return MOONEP_OK;
-}
+// Column blocks times groups of T tiles of the rank.
+uint32_t wgrad_parts(const WgradArgs &a, int T) { return (uint32_t)(a.blocks * ((a.rank + 16 * T - 1) / (16 * T))); }
 
 // Workgroups for a chunk: about as many as it has adapters, 16 at most, while the launch
 // is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 -> 24 us);
 // one where a chunk is more than one run, whose pieces may go on.
-uint32_t wgrad_shares(const WgradArgs &a, int32_t blocks)
+uint32_t wgrad_shares(const WgradArgs &a, uint32_t parts)
 {
-    const int64_t room = 2048 / ((int64_t)blocks * a.nchunks);
+    const int64_t room = 2048 / ((int64_t)parts * a.nchunks);
     int64_t shares = a.r.n / a.nchunks + 1;
     shares = shares < 16 ? shares : 16;
     shares = shares < room ? shares : room;
     return shares < 1 || a.chunk > kStepRun * kStep ? 1 : (uint32_t)shares;
 }
 
+// Tiles of the rank that a workgroup takes: those there are, up to four (32768 rows, rank
+// 128, the whole call: 526 us, with all eight 588, with two 577; rank 64: 319, two 371),
+// and fewer where that leaves less than a workgroup per CU (us with 4, 2 and 1 tiles: 1237
+// rows, 536 -> 304, rank 128: 47, 41, 39; 97 rows of 102 adapters, 80 -> 2840, rank 32: -,
+// 32, 27; but 500 rows of 16, 1024 wide, rank 128: 46, 49, 56).
+int wgrad_tiles(const WgradArgs &a)
+{
+    int T = a.tiles < 4 ? a.tiles : 4;
+    for (; T > 1; T /= 2) {
+        const uint32_t parts = wgrad_parts(a, T);
+        if ((int64_t)parts * a.nchunks * wgrad_shares(a, parts) >= 256)
+            break;
+    }
+    return T;
+}
+
 template <int T>
-int wgrad_as(const WgradArgs &a, int32_t blocks, hipStream_t st)
+int wgrad_as(const WgradArgs &a, hipStream_t st)
 {
     using G = WgradCfg<T, 2>;
     static bool raised[64] = {};
     if (raise_lds(wgrad_kernel<T, 2>, G::kLds, raised) != MOONEP_OK)
         return MOONEP_ERR_HIP;
-    hipLaunchKernelGGL((wgrad_kernel<T, 2>), dim3(blocks, a.nchunks, wgrad_shares(a, blocks)), dim3(kAdBlock),
+    const uint32_t parts = wgrad_parts(a, T);
+    hipLaunchKernelGGL((wgrad_kernel<T, 2>), dim3(parts, a.nchunks, wgrad_shares(a, parts)), dim3(kAdBlock),
                        G::kLds, st, a);
     return MOONEP_OK;
 }
 
 template <int PS, bool kHalf, int T>
-int few_grads_as(const WgradArgs &a, int32_t blocks, const ExpandArgs &e, hipStream_t st)
+int few_grads_as(const WgradArgs &a, const ExpandArgs &e, hipStream_t st)
 {
     using G = WgradCfg<T, 2>;
     static bool raised[64] = {};
     if (raise_lds(few_grads_kernel<PS, kHalf, 4, T, 2>, G::kLds, raised) != MOONEP_OK)
         return MOONEP_ERR_HIP;
-    const uint32_t shares = a.d_bank ? wgrad_shares(a, blocks) : 0;
+    const uint32_t parts = wgrad_parts(a, T), shares = a.d_bank ? wgrad_shares(a, parts) : 0;
     const uint32_t dx_blocks = e.y ? (uint32_t)(e.w.D + 63) / 64 : 0;
-    const uint32_t tiles = (uint32_t)(e.r.rows + 15) / 16;
+    const uint32_t tiles = (uint32_t)(e.r.rows + 15) / 16, dx_parts = few_parts(dx_blocks * tiles);
     hipLaunchKernelGGL((few_grads_kernel<PS, kHalf, 4, T, 2>),
-                       dim3(blocks * a.nchunks * shares + dx_blocks * tiles * kFewShares), dim3(kAdBlock),
-                       shares ? G::kLds : 0, st, a, e, (uint32_t)blocks, shares, dx_blocks);
+                       dim3(parts * a.nchunks * shares + dx_blocks * tiles * dx_parts), dim3(kAdBlock),
+                       shares ? G::kLds : 0, st, a, e, parts, shares, dx_blocks, dx_parts);
     return MOONEP_OK;
+}
+
+template <int PS, bool kHalf, int most>
+int few_grads(const WgradArgs &a, const ExpandArgs &e, hipStream_t st)
+{
+    const int T = a.d_bank ? wgrad_tiles(a) : 1;
+    if constexpr (most >= 4) {
+        if (T == 4)
+            return few_grads_as<PS, kHalf, 4>(a, e, st);
+    }
+    if constexpr (most >= 2) {
+        if (T == 2)
+            return few_grads_as<PS, kHalf, 2>(a, e, st);
+    }
+    return few_grads_as<PS, kHalf, 1>(a, e, st);
 }
 
 // Consecutive arrays of the workspace, each at a multiple of 256 bytes.
@@ -1544,13 +1596,13 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
     const ExpandArgs e{r, {bank + ad.a_offset, ad.stride, ad.rank, ad.in_dim}, parts, dx_base, dx, 0,
                        nullptr, nullptr, nullptr, 0};
     WgradArgs a{};
-    int32_t blocks = 0;
     if (d_bank) {
         const PlanLayout pl = plan_layout(E, 1);
         a.r = r;
         a.off = plan + pl.home_row_off;
         a.keep = plan + pl.keep;
         a.rank = ad.rank;
+        a.tiles = rank_tiles(ad.rank);
         a.in_dim = ad.in_dim;
         a.out_dim = ad.out_dim;
         a.stride = ad.stride;
@@ -1564,7 +1616,7 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         a.part = carve.at_end<float>();
         a.d_bank = d_bank;
         a.blocks_a = (ad.in_dim + kGradCols - 1) / kGradCols;
-        blocks = a.blocks_a + (ad.out_dim + kGradCols - 1) / kGradCols;
+        const int32_t blocks = a.blocks = a.blocks_a + (ad.out_dim + kGradCols - 1) / kGradCols;
         // 64 chunks at most, for about 512 workgroups (32768 rows, 4096 -> 4096, the whole
         // call: 297 us; 256 of them 332, 1024 315), of at least 128 positions, and of 256
         // where that leaves 256 workgroups: most adapters' rows then lie in one chunk (4099
@@ -1594,20 +1646,19 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         int rc = MOONEP_OK;
         if (few) {
             switch (rank_tiles(ad.rank)) {
-            case 1: rc = few_grads_as<1, true, 1>(a, blocks, e, st); break;
-            case 2: rc = few_grads_as<1, false, 2>(a, blocks, e, st); break;
-            case 4: rc = few_grads_as<2, false, 4>(a, blocks, e, st); break;
-            default: rc = few_grads_as<4, false, 8>(a, blocks, e, st);
+            case 1: rc = few_grads<1, true, 1>(a, e, st); break;
+            case 2: rc = few_grads<1, false, 2>(a, e, st); break;
+            case 4: rc = few_grads<2, false, 4>(a, e, st); break;
+            default: rc = few_grads<4, false, 4>(a, e, st);
             }
         } else if (dx) {
             expand<true>(e, kMany, st);
         }
         if (!few && d_bank) {
-            switch (rank_tiles(ad.rank)) {
-            case 1: rc = wgrad_as<1>(a, blocks, st); break;
-            case 2: rc = wgrad_as<2>(a, blocks, st); break;
-            case 4: rc = wgrad_as<4>(a, blocks, st); break;
-            default: rc = wgrad_as<8>(a, blocks, st);
+            switch (wgrad_tiles(a)) {
+            case 1: rc = wgrad_as<1>(a, st); break;
+            case 2: rc = wgrad_as<2>(a, st); break;
+            default: rc = wgrad_as<4>(a, st);
             }
         }
         if (rc != MOONEP_OK)
@@ -1616,7 +1667,8 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
     if (d_bank && a.nchunks != 1) {
         const int64_t window = (int64_t)ad.rank * ((int64_t)ad.in_dim + ad.out_dim);
         const int64_t nb = (window + kAdBlock * 4 - 1) / (kAdBlock * 4);
-        hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(nb < 128 ? nb : 128), ad.n), dim3(kAdBlock),
+        const int64_t most = 2048 / ad.n > 128 ? 2048 / ad.n : 128;  // few adapters have more of them
+        hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)(nb < most ? nb : most), ad.n), dim3(kAdBlock),
                            0, st, a);
     }
     return status();
