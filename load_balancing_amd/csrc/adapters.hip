@@ -918,26 +918,31 @@ __device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, 
     Frag u[X::kSteps];
     if constexpr (kJoin) {
         const float s = u_id >= 0 ? a.scale[u_id] : 0.0f;
+        f32x4 v[PS][2];
+#pragma unroll
+        for (int k = 0; k < PS; ++k)
+            v[k][0] = v[k][1] = f32x4{0, 0, 0, 0};
+        if (u_row >= 0 && (write_total || (todo >> m & 1))) {
+            const float *p = a.sums + (int64_t)u_row * x.rank;
+            // several parts' loads in flight (100 rows of 16 adapters, 4096 wide, rank 64, both
+            // kernels: 18.6 us one after the other, 14.8)
+#pragma unroll 4
+            for (int32_t q = 0; q < a.splits; ++q, p += (int64_t)a.r.rows * x.rank)
+#pragma unroll
+                for (int k = 0; k < PS; ++k) {
+                    v[k][0] += *(const f32x4 *)(p + x.chunk[k]);
+                    v[k][1] += *(const f32x4 *)(p + x.chunk[k] + 4);
+                }
+        }
 #pragma unroll
         for (int k = 0; k < PS; ++k) {
-            f32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
-            if (u_row >= 0 && x.in[k] && (write_total || (todo >> m & 1))) {
-                const float *p = a.sums + (int64_t)u_row * x.rank + x.chunk[k];
-                v0 = *(const f32x4 *)p;
-                v1 = *(const f32x4 *)(p + 4);
-                for (int32_t q = 1; q < a.splits; ++q) {
-                    p += (int64_t)a.r.rows * x.rank;
-                    v0 += *(const f32x4 *)p;
-                    v1 += *(const f32x4 *)(p + 4);
-                }
-                if (write_total) {
-                    float *o = a.total + (int64_t)u_row * x.rank + x.chunk[k];
-                    *(f32x4 *)o = v0;
-                    *(f32x4 *)(o + 4) = v1;
-                }
+            if (u_row >= 0 && write_total && x.in[k]) {
+                float *o = a.total + (int64_t)u_row * x.rank + x.chunk[k];
+                *(f32x4 *)o = v[k][0];
+                *(f32x4 *)(o + 4) = v[k][1];
             }
-            v0 *= s;
-            v1 *= s;
+            const f32x4 v0 = x.in[k] ? v[k][0] * s : f32x4{0, 0, 0, 0};
+            const f32x4 v1 = x.in[k] ? v[k][1] * s : f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t hi, lo;
@@ -1067,12 +1072,8 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
                           (((wave * 2) ^ (m >> 2)) << 6 | (g & 1) << 5 | (m & 3) << 3);
 
     f32x4 acc[T][4];
-    int32_t held = -1;  // the adapter whose sums these are
+    int32_t held = -1, cnt = 0, first = 0;  // the adapter whose sums these are, and its rows
     auto put = [&]() {
-        if (held < 0)
-            return;
-        int32_t first;
-        const int32_t cnt = adapter_rows(a.off, a.keep, held, rows, &first);
         const int32_t ch = (int32_t)chunk;
         const bool direct = cnt && first / a.chunk == ch && (first + cnt - 1) / a.chunk == ch;
         const bool add = direct && a.accumulate;
@@ -1101,30 +1102,47 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
         }
     };
 
-    for (int32_t r0 = p_begin; r0 < p_end; r0 += kStepRun * kStep) {
-        const int32_t n = p_end - r0 < kStepRun * kStep ? p_end - r0 : kStepRun * kStep;
-        __syncthreads();  // the run before is done with the ring and the tables
-        for (int32_t i = (int)threadIdx.x; i < (n + kStep - 1) / kStep * kStep; i += kAdBlock) {
-            const int32_t row = i < n ? a.r.row(r0 + i) : -1;
-            row_of[i] = row;
-            id_of[i] = a.r.id(row);
-        }
-        __syncthreads();
-        // pieces of the run: positions [p, end) of one adapter
-        uint32_t piece = 0;
-        for (int32_t p = 0, end; p < n; p = end) {
-            const int32_t id = __builtin_amdgcn_readfirstlane(id_of[p]);
+    int32_t r0 = p_begin - kStepRun * kStep, n = 0;  // the run
+    int32_t end = 0;                                 // of the piece before
+    uint32_t piece = 0;
+    for (;;) {
+        // the next piece that is this workgroup's: positions [p, end) of the run, of one adapter
+        int32_t p, id = -1;
+        for (;;) {
+            if (end >= n) {
+                r0 += kStepRun * kStep;
+                if (r0 >= p_end)
+                    break;
+                n = p_end - r0 < kStepRun * kStep ? p_end - r0 : kStepRun * kStep;
+                end = 0;
+                __syncthreads();  // the run before is done with the ring and the tables
+                for (int32_t i = (int)threadIdx.x; i < (n + kStep - 1) / kStep * kStep; i += kAdBlock) {
+                    const int32_t row = i < n ? a.r.row(r0 + i) : -1;
+                    row_of[i] = row;
+                    id_of[i] = a.r.id(row);
+                }
+                __syncthreads();
+            }
+            p = end;
+            id = __builtin_amdgcn_readfirstlane(id_of[p]);
             uint64_t other = 0;
-            for (end = p; !other; end += 64) {
+            for (; !other; end += 64) {
                 const int32_t i = end + lane;
                 other = ballot(i >= n || id_of[i < n ? i : 0] != id);
             }
             end += __builtin_ctzll(other) - 64;
-            if (id < 0 || piece++ % shares != share)
-                continue;
+            if (id >= 0 && piece++ % shares == share)
+                break;
+            id = -1;
+        }
+        if (held >= 0 && id != held)
+            put();
+        if (id < 0)
+            break;
+        {
             if (id != held) {
-                put();
                 held = id;
+                cnt = adapter_rows(a.off, a.keep, held, rows, &first);
 #pragma unroll
                 for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -1174,18 +1192,22 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
                 tr_frags<4>(lo, hi, qf);
                 const int32_t at = (s0 + t) * kStep;
                 const int32_t from = p - at - g * 8, to = end - at - g * 8;  // of this lane's 8 positions
-                const bool edge = at < p || at + kStep > end;
+                uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+                if (at < p || at + kStep > end) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        keep[j] = (2 * j >= from && 2 * j < to ? 0xFFFFu : 0) |
+                                  (2 * j + 1 >= from && 2 * j + 1 < to ? 0xFFFF0000u : 0);
+                }
 #pragma unroll
                 for (int k = 0; k < T; ++k)
 #pragma unroll
                     for (int b = 0; b < 3; ++b) {
                         Frag pf;
                         pf.v = *(const bf16x8 *)(stage + G::kStageQ + (b * T + k) * 1024 + lane * 16);
-                        if (edge) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                pf.h[j] = j >= from && j < to ? pf.h[j] : 0;
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            pf.w[j] &= keep[j];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             acc[k][c] = mfma16(pf.v, qf[c].v, acc[k][c]);
@@ -1193,7 +1215,6 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
             }
         }
     }
-    put();
     if (a.nchunks > 1 || a.accumulate)
         return;
     // no adapter has rows in several chunks, and no join follows: those without any get
@@ -1202,7 +1223,6 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
     const int32_t i0 = tile0 * 16, i1 = rank - i0 < T * 16 ? rank : i0 + T * 16;
     for (int32_t e0 = 0; e0 < a.r.n; e0 += 64) {
         const int32_t e = e0 + lane;
-        int32_t first;
         uint64_t empty = ballot(e < a.r.n && (uint32_t)e % shares == share &&
                                 adapter_rows(a.off, a.keep, e < a.r.n ? e : 0, rows, &first) == 0);
         for (; empty; empty &= empty - 1) {
