@@ -131,7 +131,10 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t *hi, uint32_t 
 // Chunks past the rank are not written, nor used.
 struct Parts {
     int32_t per;  // chunks of a part: whole steps, or half of one
-    __host__ __device__ explicit Parts(int32_t rank) : per(rank <= 16 ? 2 : rank <= 32 ? 4 : rank <= 64 ? 8 : 16) {}
+    __host__ __device__ explicit Parts(int32_t rank)
+        : per(rank <= 16 ? 2 : rank <= 32 ? 4 : rank <= 64 ? 8 : 16)
+    {
+    }
     __host__ __device__ int32_t steps() const { return per / 2; }
     // Elements before chunk c of a position.
     __device__ int64_t at(int64_t pos, int32_t c) const
@@ -356,10 +359,12 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 #pragma unroll
             for (int ks = 0; ks < G::kK / 32; ++ks) {
                 Frag xf, wf[T];
-                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * G::kRowBytes + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                const int chunk = ((ks * 4 + g) ^ G::swz(m)) << 4;
+                xf.v = *(const bf16x8 *)(x + (wave * 16 + m) * G::kRowBytes + chunk);
                 if constexpr (kNN) {
-                    const uint32_t at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ws +
-                                        (ks * 32 + g * 8 + (m >> 2)) * rank * 2 + (m & 3) * 8;
+                    const uint32_t at =
+                        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)ws +
+                        (ks * 32 + g * 8 + (m >> 2)) * rank * 2 + (m & 3) * 8;
                     const int sw = rank == 16 * T ? G::swz_nn(g * 8 + (m >> 2)) * 16 : 0;
                     constexpr int N = T < 4 ? T : 4;
 #pragma unroll
@@ -379,7 +384,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
                 } else {
 #pragma unroll
                     for (int t = 0; t < T; ++t)
-                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * G::kRowBytes + (((ks * 4 + g) ^ G::swz(m)) << 4));
+                        wf[t].v = *(const bf16x8 *)(ws + (t * 16 + m) * G::kRowBytes + chunk);
                 }
 #pragma unroll
                 for (int t = 0; t < T; ++t)
@@ -752,7 +757,8 @@ struct Expand {
             piece o;
 #pragma unroll
             for (int t = 0; t < CT; t += 2) {
-                const uint32_t v = pack_bf16(bf16_lo(b[i][t / 2]) + res[t][i], bf16_hi(b[i][t / 2]) + res[t + 1][i]);
+                const uint32_t v = pack_bf16(bf16_lo(b[i][t / 2]) + res[t][i],
+                                             bf16_hi(b[i][t / 2]) + res[t + 1][i]);
                 o[t / 2] = id[i] >= 0 ? v : b[i][t / 2];
             }
             *(piece *)(y + (int64_t)row[i] * D + col) = o;
@@ -790,7 +796,7 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
     char *ring = ring_all + wave * (kAhead + 1) * G::kSlot;
     const bool copy = a.y != a.base;
     const int64_t tiles = ((int64_t)a.r.rows + 15) / 16;
-    const int64_t last = ((int64_t)blockIdx.y + 1) * a.tiles < tiles ? ((int64_t)blockIdx.y + 1) * a.tiles : tiles;
+    const int64_t next = ((int64_t)blockIdx.y + 1) * a.tiles, last = next < tiles ? next : tiles;
     Frag wf[PS][CT];
     int32_t have = -1;
     for (int64_t first = (int64_t)blockIdx.y * a.tiles; first < last; first += kTileRun) {
@@ -811,7 +817,8 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 #pragma unroll
             for (int v = 0; v < G::kInstr; ++v) {
                 const int32_t row = t < n ? rows[t * 16 + (v * 64 + lane) / G::kLanesRow] : -1;
-                dma16(row >= 0 && c < x.D ? (const void *)(a.base + (int64_t)row * x.D + c) : kZeros, to + v * 1024);
+                dma16(row >= 0 && c < x.D ? (const void *)(a.base + (int64_t)row * x.D + c) : kZeros,
+                      to + v * 1024);
             }
         };
         Frag u[G::kSteps], u2[G::kSteps];
@@ -885,7 +892,8 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 // Few rows: the four waves of a workgroup, and `parts` of them, share a row tile and
 // its 16 CT columns, each with some of the tile's adapters and their rows.
 template <int PS, bool kHalf, int CT, bool kNN, bool kJoin>
-__device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, uint32_t tile, uint32_t part, uint32_t parts)
+__device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, uint32_t tile, uint32_t part,
+                                           uint32_t parts)
 {
     using X = Expand<PS, kHalf, CT, kNN>;
     const int wave = (int)threadIdx.x >> 6, m = lane_id() & 15, g = lane_id() >> 4;
@@ -1139,80 +1147,78 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
             put();
         if (id < 0)
             break;
-        {
-            if (id != held) {
-                held = id;
-                cnt = adapter_rows(a.off, a.keep, held, rows, &first);
+        if (id != held) {
+            held = id;
+            cnt = adapter_rows(a.off, a.keep, held, rows, &first);
 #pragma unroll
-                for (int t = 0; t < T; ++t)
+            for (int t = 0; t < T; ++t)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[t][c] = f32x4{0, 0, 0, 0};
+                for (int c = 0; c < 4; ++c)
+                    acc[t][c] = f32x4{0, 0, 0, 0};
+        }
+        const int32_t s0 = p / kStep, steps = (end + kStep - 1) / kStep - s0;
+        auto issue = [&](int32_t t, int slot) {
+            char *to = ring + slot * G::kStageBytes;
+#pragma unroll
+            for (int v = 0; v < G::kQInstr; ++v) {
+                const int32_t pos = (s0 + t) * kStep + q_row[v];
+                const int32_t r = pos >= p && pos < end ? row_of[pos] : -1;
+                dma16(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v]) : kZeros,
+                      to + (v * 4 + wave) * 1024);
             }
-            const int32_t s0 = p / kStep, steps = (end + kStep - 1) / kStep - s0;
-            auto issue = [&](int32_t t, int slot) {
-                char *to = ring + slot * G::kStageBytes;
+            const uint16_t *src = t_p + ((int64_t)(r0 / kStep + s0 + t) * 3 * a.tiles + tile0) * 512 + lane * 8;
 #pragma unroll
-                for (int v = 0; v < G::kQInstr; ++v) {
-                    const int32_t pos = (s0 + t) * kStep + q_row[v];
-                    const int32_t r = pos >= p && pos < end ? row_of[pos] : -1;
-                    dma16(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v]) : kZeros,
-                          to + (v * 4 + wave) * 1024);
-                }
-                const uint16_t *src = t_p + ((int64_t)(r0 / kStep + s0 + t) * 3 * a.tiles + tile0) * 512 + lane * 8;
+            for (int v = 0; v < G::kPInstr; ++v) {
+                const int i = (v * 4 + wave) % (3 * T);  // waves without a load of their own repeat one
+                dma16(src + (i / T * a.tiles + i % T) * 512, to + G::kStageQ + i * 1024);
+            }
+        };
+        lds_barrier();  // the piece before is done with the ring
 #pragma unroll
-                for (int v = 0; v < G::kPInstr; ++v) {
-                    const int i = (v * 4 + wave) % (3 * T);  // waves without a load of their own repeat one
-                    dma16(src + (i / T * a.tiles + i % T) * 512, to + G::kStageQ + i * 1024);
-                }
-            };
-            lds_barrier();  // the piece before is done with the ring
+        for (int t = 0; t + 1 < S; ++t)
+            if (t < steps)
+                issue(t, t);
+        int now = 0;
+        for (int32_t t = 0; t < steps; ++t) {
+            if (t + S - 2 < steps)
+                wait_vm<(S - 2) * G::kPerStage>();
+            else
+                wait_vm<0>();
+            lds_barrier();  // the stage is visible to all, the one before is free
+            if (t + S - 1 < steps)
+                issue(t + S - 1, now ? now - 1 : S - 1);
+            const char *stage = ring + now * G::kStageBytes;
+            Frag qf[4];
+            uint32_t lo[4], hi[4];
 #pragma unroll
-            for (int t = 0; t + 1 < S; ++t)
-                if (t < steps)
-                    issue(t, t);
-            int now = 0;
-            for (int32_t t = 0; t < steps; ++t) {
-                if (t + S - 2 < steps)
-                    wait_vm<(S - 2) * G::kPerStage>();
-                else
-                    wait_vm<0>();
-                lds_barrier();  // the stage is visible to all, the one before is free
-                if (t + S - 1 < steps)
-                    issue(t + S - 1, now ? now - 1 : S - 1);
-                const char *stage = ring + now * G::kStageBytes;
-                Frag qf[4];
-                uint32_t lo[4], hi[4];
+            for (int c = 0; c < 4; ++c) {
+                lo[c] = (q_at ^ (uint32_t)(c / 2 << 6 | c % 2 << 5)) + now * G::kStageBytes;
+                hi[c] = lo[c] + 4 * G::kRow;
+            }
+            now = now + 1 == S ? 0 : now + 1;
+            tr_frags<4>(lo, hi, qf);
+            const int32_t at = (s0 + t) * kStep;
+            const int32_t from = p - at - g * 8, to = end - at - g * 8;  // of this lane's 8 positions
+            uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+            if (at < p || at + kStep > end) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    lo[c] = (q_at ^ (uint32_t)(c / 2 << 6 | c % 2 << 5)) + now * G::kStageBytes;
-                    hi[c] = lo[c] + 4 * G::kRow;
-                }
-                now = now + 1 == S ? 0 : now + 1;
-                tr_frags<4>(lo, hi, qf);
-                const int32_t at = (s0 + t) * kStep;
-                const int32_t from = p - at - g * 8, to = end - at - g * 8;  // of this lane's 8 positions
-                uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-                if (at < p || at + kStep > end) {
+                for (int j = 0; j < 4; ++j)
+                    keep[j] = (2 * j >= from && 2 * j < to ? 0xFFFFu : 0) |
+                              (2 * j + 1 >= from && 2 * j + 1 < to ? 0xFFFF0000u : 0);
+            }
+#pragma unroll
+            for (int k = 0; k < T; ++k)
+#pragma unroll
+                for (int b = 0; b < 3; ++b) {
+                    Frag pf;
+                    pf.v = *(const bf16x8 *)(stage + G::kStageQ + (b * T + k) * 1024 + lane * 16);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        keep[j] = (2 * j >= from && 2 * j < to ? 0xFFFFu : 0) |
-                                  (2 * j + 1 >= from && 2 * j + 1 < to ? 0xFFFF0000u : 0);
+                        pf.w[j] &= keep[j];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[k][c] = mfma16(pf.v, qf[c].v, acc[k][c]);
                 }
-#pragma unroll
-                for (int k = 0; k < T; ++k)
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) {
-                        Frag pf;
-                        pf.v = *(const bf16x8 *)(stage + G::kStageQ + (b * T + k) * 1024 + lane * 16);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            pf.w[j] &= keep[j];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            acc[k][c] = mfma16(pf.v, qf[c].v, acc[k][c]);
-                    }
-            }
         }
     }
     if (a.nchunks > 1 || a.accumulate)
@@ -1360,7 +1366,8 @@ int raise_lds(Kernel kernel, int bytes, bool (&raised)[64])
         return MOONEP_ERR_HIP;
     if (dev >= 0 && dev < 64 && raised[dev])
         return MOONEP_OK;
-    if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    if (hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        hipSuccess)
         return MOONEP_ERR_HIP;
     if (dev >= 0 && dev < 64)
         raised[dev] = true;
@@ -1374,14 +1381,14 @@ void shrink_as(const ShrinkArgs &a, Form form, int splits, hipStream_t st)
 {
     const int32_t rows = a.r.rows;
     if (form == kFew) {
-        hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 4>), dim3((rows + 15) / 16, splits, kShares), dim3(256), 0,
-                           st, a);
+        hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 4>), dim3((rows + 15) / 16, splits, kShares),
+                           dim3(256), 0, st, a);
         return;
     }
     if constexpr (T <= 2 && !kNN) {
         if (form == kSome) {
-            hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 8>), dim3((rows + 15) / 16, splits, kShares), dim3(512),
-                               0, st, a);
+            hipLaunchKernelGGL((shrink_few_kernel<T, kNN, 8>), dim3((rows + 15) / 16, splits, kShares),
+                               dim3(512), 0, st, a);
             return;
         }
     }
@@ -1453,7 +1460,10 @@ void expand(const ExpandArgs &a, Form form, hipStream_t st)
 }
 
 // Column blocks times groups of T tiles of the rank.
-uint32_t wgrad_parts(const WgradArgs &a, int T) { return (uint32_t)(a.blocks * ((a.rank + 16 * T - 1) / (16 * T))); }
+uint32_t wgrad_parts(const WgradArgs &a, int T)
+{
+    return (uint32_t)(a.blocks * ((a.rank + 16 * T - 1) / (16 * T)));
+}
 
 // Workgroups for a chunk: about as many as it has adapters, 16 at most, while the launch
 // is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 -> 24 us);
