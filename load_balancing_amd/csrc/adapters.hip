@@ -159,9 +159,12 @@ struct Parts {
 
 __device__ __align__(16) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
+// kStream: non-temporal, for rows that `streams` says go past the caches.
+template <bool kStream = false>
 __device__ __forceinline__ void dma16(const void *src, char *dst)
 {
-    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, 0,
+                                     kStream ? 2 : 0);
 }
 
 template <int N>
@@ -257,7 +260,7 @@ struct ShrinkCfg {
     }
 };
 
-template <int T, bool kNN, int S>
+template <int T, bool kNN, int S, bool kStream>
 __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
 {
     using G = ShrinkCfg<T, kNN, S>;
@@ -327,7 +330,8 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
             const int32_t k = (k0 + (kt + begin < nk ? kt + begin : kt + begin - nk)) * G::kK;
 #pragma unroll
             for (int v = 0; v < G::kXInstr; ++v)
-                dma16(k + xc[v] < D ? (const void *)(xp[v] + k) : kZeros, to + (v * 4 + wave) * 1024);
+                dma16<kStream>(k + xc[v] < D ? (const void *)(xp[v] + k) : kZeros,
+                               to + (v * 4 + wave) * 1024);
 #pragma unroll
             for (int v = 0; v < G::kWInstr; ++v)
                 dma16(k + wk[v] < D ? (const void *)(wp[v] + (kNN ? (int64_t)k * rank : k)) : kZeros,
@@ -746,6 +750,7 @@ struct Expand {
         }
     }
     // A row without an adapter is copied bit for bit.
+    template <bool kStream>
     __device__ __forceinline__ void store(uint16_t *y, const int32_t (&row)[4], const int32_t (&id)[4],
                                           const bool (&wanted)[4], const piece (&b)[4],
                                           const f32x4 (&res)[CT]) const
@@ -761,7 +766,11 @@ struct Expand {
                                              bf16_hi(b[i][t / 2]) + res[t + 1][i]);
                 o[t / 2] = id[i] >= 0 ? v : b[i][t / 2];
             }
-            *(piece *)(y + (int64_t)row[i] * D + col) = o;
+            piece *to = (piece *)(y + (int64_t)row[i] * D + col);
+            if constexpr (kStream)
+                __builtin_nontemporal_store(o, to);
+            else
+                *to = o;
         }
     }
 };
@@ -783,7 +792,7 @@ struct ExpandRing {
     static_assert(kAhead * kInstr + kSteps <= 63, "outstanding accesses must fit vmcnt");
 };
 
-template <int PS, bool kHalf, int CT, bool kNN>
+template <int PS, bool kHalf, int CT, bool kNN, bool kStream>
 __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 {
     using X = Expand<PS, kHalf, CT, kNN>;
@@ -817,8 +826,8 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 #pragma unroll
             for (int v = 0; v < G::kInstr; ++v) {
                 const int32_t row = t < n ? rows[t * 16 + (v * 64 + lane) / G::kLanesRow] : -1;
-                dma16(row >= 0 && c < x.D ? (const void *)(a.base + (int64_t)row * x.D + c) : kZeros,
-                      to + v * 1024);
+                dma16<kStream>(row >= 0 && c < x.D ? (const void *)(a.base + (int64_t)row * x.D + c)
+                                                   : kZeros, to + v * 1024);
             }
         };
         Frag u[G::kSteps], u2[G::kSteps];
@@ -880,7 +889,7 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 wanted[i] = row[i] >= 0;
-            x.store(a.y, row, id, wanted, b, res);
+            x.template store<kStream>(a.y, row, id, wanted, b, res);
 #pragma unroll
             for (int k = 0; k < G::kSteps; ++k)
                 u[k] = u2[k];
@@ -982,7 +991,7 @@ __device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, 
             mine[i] = id[i] == cur;
         x.product(wf, u, mine, res);
     }
-    x.store(a.y, row, id, wanted, b, res);
+    x.template store<false>(a.y, row, id, wanted, b, res);
 }
 
 template <int PS, bool kHalf, int CT>
@@ -1045,7 +1054,7 @@ struct WgradCfg {
     __device__ static constexpr int swz(int r) { return (r & 3) << 2 | (r >> 3 & 1) << 1; }
 };
 
-template <int T, int S>
+template <int T, int S, bool kStream>
 __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_t chunk, uint32_t share,
                                       uint32_t shares, char *ring)
 {
@@ -1163,8 +1172,8 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
             for (int v = 0; v < G::kQInstr; ++v) {
                 const int32_t pos = (s0 + t) * kStep + q_row[v];
                 const int32_t r = pos >= p && pos < end ? row_of[pos] : -1;
-                dma16(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v]) : kZeros,
-                      to + (v * 4 + wave) * 1024);
+                dma16<kStream>(r >= 0 && q_col[v] < D ? (const void *)(q + (int64_t)r * D + q_col[v])
+                                                      : kZeros, to + (v * 4 + wave) * 1024);
             }
             const uint16_t *src = t_p + ((int64_t)(r0 / kStep + s0 + t) * 3 * a.tiles + tile0) * 512 + lane * 8;
 #pragma unroll
@@ -1248,11 +1257,11 @@ __device__ __forceinline__ void wgrad(const WgradArgs &a, uint32_t part, uint32_
     }
 }
 
-template <int T, int S>
+template <int T, int S, bool kStream>
 __global__ __launch_bounds__(kAdBlock) void wgrad_kernel(WgradArgs a)
 {
     extern __shared__ __align__(16) char ring[];
-    wgrad<T, S>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, ring);
+    wgrad<T, S, kStream>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, ring);
 }
 
 // Few rows: the gradients and the rows of d_x in one launch, which they share by
@@ -1265,7 +1274,7 @@ __global__ __launch_bounds__(kAdBlock) void few_grads_kernel(WgradArgs a, Expand
     extern __shared__ __align__(16) char ring[];
     const uint32_t each = parts * a.nchunks;
     if (blockIdx.x < each * shares) {
-        wgrad<T, S>(a, blockIdx.x % parts, blockIdx.x / parts % a.nchunks, blockIdx.x / each, shares, ring);
+        wgrad<T, S, false>(a, blockIdx.x % parts, blockIdx.x / parts % a.nchunks, blockIdx.x / each, shares, ring);
         return;
     }
     const uint32_t i = blockIdx.x - each * shares, tile = i / dx_blocks;
@@ -1314,6 +1323,13 @@ bool few_rows(int32_t rows, const moonep_adapters &ad)
 {
     return rows <= 256 || (rows <= 1024 && rows * ((int64_t)ad.in_dim + ad.out_dim) <= 3 << 20);
 }
+
+// Whether rows are read or written past the caches (non-temporal accesses): more than
+// half of what the 256 MiB memory-side cache holds, of which the next call finds little there.
+// 32768 rows, 4096 wide: forward of rank 64 202 -> 183 us, backward of rank 16 295 -> 269.
+// With a call that reads the result the forward of 131 MB (16000 rows, rank 32) takes 151
+// us for 154, of 33 MB 48 for 47, of 10 MB 27.5 for 26.
+bool streams(int64_t rows, int64_t row_bytes) { return rows * row_bytes > (int64_t)128 << 20; }
 
 int status() { return hipGetLastError() == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP; }
 
@@ -1396,7 +1412,14 @@ void shrink_as(const ShrinkArgs &a, Form form, int splits, hipStream_t st)
     using G = ShrinkCfg<T, kNN, kS>;
     static_assert(G::kLds <= 48 * 1024, "no raised limit");
     const dim3 grid((unsigned)(((int64_t)rows + G::kRows - 1) / G::kRows), splits, kShares);
-    hipLaunchKernelGGL((shrink_kernel<T, kNN, kS>), grid, dim3(kAdBlock), G::kLds, st, a);
+    // the backward's rows are read again by the gradients
+    if constexpr (!kNN) {
+        if (streams(rows, 2 * (int64_t)a.w.D)) {
+            hipLaunchKernelGGL((shrink_kernel<T, kNN, kS, true>), grid, dim3(kAdBlock), G::kLds, st, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((shrink_kernel<T, kNN, kS, false>), grid, dim3(kAdBlock), G::kLds, st, a);
 }
 
 template <bool kNN>
@@ -1443,9 +1466,11 @@ void expand_as(ExpandArgs a, Form form, hipStream_t st)
     per = a.tiles;
     using G = ExpandRing<PS, kHalf, CT>;
     static_assert(G::kLds <= 48 * 1024, "no raised limit");
-    hipLaunchKernelGGL((expand_kernel<PS, kHalf, CT, kNN>),
-                       dim3((unsigned)blocks, (unsigned)((tiles + per - 1) / per)), dim3(kAdBlock), G::kLds,
-                       st, a);
+    const dim3 grid((unsigned)blocks, (unsigned)((tiles + per - 1) / per));
+    if (streams(a.r.rows, 2 * (int64_t)a.w.D))
+        hipLaunchKernelGGL((expand_kernel<PS, kHalf, CT, kNN, true>), grid, dim3(kAdBlock), G::kLds, st, a);
+    else
+        hipLaunchKernelGGL((expand_kernel<PS, kHalf, CT, kNN, false>), grid, dim3(kAdBlock), G::kLds, st, a);
 }
 
 template <bool kNN>
@@ -1493,17 +1518,27 @@ int wgrad_tiles(const WgradArgs &a)
     return T;
 }
 
-template <int T>
+template <int T, bool kStream>
 int wgrad_as(const WgradArgs &a, hipStream_t st)
 {
     using G = WgradCfg<T, 2>;
     static bool raised[64] = {};
-    if (raise_lds(wgrad_kernel<T, 2>, G::kLds, raised) != MOONEP_OK)
+    if (raise_lds(wgrad_kernel<T, 2, kStream>, G::kLds, raised) != MOONEP_OK)
         return MOONEP_ERR_HIP;
     const uint32_t parts = wgrad_parts(a, T);
-    hipLaunchKernelGGL((wgrad_kernel<T, 2>), dim3(parts, a.nchunks, wgrad_shares(a, parts)), dim3(kAdBlock),
+    hipLaunchKernelGGL((wgrad_kernel<T, 2, kStream>), dim3(parts, a.nchunks, wgrad_shares(a, parts)), dim3(kAdBlock),
                        G::kLds, st, a);
     return MOONEP_OK;
+}
+
+template <bool kStream>
+int wgrad_of(const WgradArgs &a, int T, hipStream_t st)
+{
+    switch (T) {
+    case 1: return wgrad_as<1, kStream>(a, st);
+    case 2: return wgrad_as<2, kStream>(a, st);
+    default: return wgrad_as<4, kStream>(a, st);
+    }
 }
 
 template <int PS, bool kHalf, int T>
@@ -1685,11 +1720,11 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
             expand<true>(e, kMany, st);
         }
         if (!few && d_bank) {
-            switch (wgrad_tiles(a)) {
-            case 1: rc = wgrad_as<1>(a, st); break;
-            case 2: rc = wgrad_as<2>(a, st); break;
-            default: rc = wgrad_as<4>(a, st);
-            }
+            const int T = wgrad_tiles(a);
+            // x and dy are read once where a workgroup has all of the rank
+            const bool once = wgrad_parts(a, T) == (uint32_t)a.blocks;
+            const int64_t D = ad.in_dim < ad.out_dim ? ad.in_dim : ad.out_dim;
+            rc = once && streams(rows, 2 * D) ? wgrad_of<true>(a, T, st) : wgrad_of<false>(a, T, st);
         }
         if (rc != MOONEP_OK)
             return rc;

@@ -116,6 +116,15 @@ __device__ __forceinline__ void dma16(const char *src, char *dst)
                                      (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
 }
 
+template <bool kStream, class T>
+__device__ __forceinline__ void put(T *p, T v)
+{
+    if constexpr (kStream)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+
 // Waits until at most N vector-memory operations of this wave are outstanding.
 template <int N>
 __device__ __forceinline__ void wait_vm()
@@ -157,6 +166,10 @@ struct DxCfg {
     // arithmetic then runs under matrix instructions, and with more than two slots there
     // is time (256 x 256 tiles, four slots: 1515 -> 1490 us on the sweep).
     static constexpr int kIssueAt = S > 2 ? BK / 16 - 1 : 0;
+    // Where large tiles are taken d_x is 64 MiB at least, of which the next call finds
+    // little in the caches: it is written past them (sweep: 1478 -> 1457 us, and with a
+    // call that reads it 277 -> 276 at 92 MB).
+    static constexpr bool kStream = BM == 256;
     // Epilogue: each wave's own 16 rows of WN columns, apart from the ring, which
     // is loading the next item.
     static constexpr int kOutRow = WN * 2 + 16, kOutAt = S * kStageBytes;
@@ -361,9 +374,9 @@ __global__ __launch_bounds__((DxCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expe
                     const int row = wm * WM + m * 32 + half * 16 + r, col = i.n0 + wn * WN + c * 8;
                     u32x4 *p = (u32x4 *)(a.d_x + (i.m0 + row) * a.in_dim + col);
                     if (full)
-                        *p = piece;
+                        put<G::kStream>(p, piece);
                     else if (row < i.mrows && col < a.in_dim)
-                        *p = piece;
+                        put<G::kStream>(p, piece);
                 }
                 wave_sync();
             }
@@ -386,6 +399,9 @@ struct DwCfg {
     static constexpr int kStageBytes = kStageA + kStageB;
     static constexpr int kAInstr = kStageA / 1024 / kWavesG, kBInstr = kStageB / 1024 / kWavesG;
     static constexpr int kPerStage = kAInstr + kBInstr;
+    // Gradients of 80 MiB or more are written past the caches (64 of 2048 x 1408, 3904
+    // rows: 179 -> 175 us)
+    static constexpr bool kStream = BM == 256;
     static_assert(kStageA % (1024 * kWavesG) == 0 && kStageB % (1024 * kWavesG) == 0, "DMA rounds");
     static_assert(S >= 2 && (S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
 };
@@ -587,7 +603,7 @@ __global__ __launch_bounds__((DwCfg<BM, BN, WM, WN, BK, S>::kThreads)) void expe
                     }
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        p[(int64_t)((r >> 2) * 8 + (r & 3)) * a.in_dim] = acc[i][j][r];
+                        put<G::kStream>(p + (int64_t)((r >> 2) * 8 + (r & 3)) * a.in_dim, acc[i][j][r]);
                 }
             }
     }
