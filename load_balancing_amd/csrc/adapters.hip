@@ -47,8 +47,8 @@ constexpr int kAdBlock = 256;  // four waves
 constexpr int kMostSplits = 14, kMostSplitsBwd = 8;
 constexpr int kMostChunks = 64;
 // Workgroups that share a tile's adapters (us with 1, 4 and 8: 16 rows of 16 adapters
-// 14.2, 11.6, 11.5; 1531 rows of 24: 24.0, 17.1, 17.2; 32768 rows in prompts of 800: 210,
-// 202, 202).
+// 12.6, 11.8, 11.8; 1531 rows of 24: 24.0, 17.1, 17.1; 32768 rows in prompts of 800: 191,
+// 183, 183).
 constexpr unsigned kShares = 4;
 
 union Frag {
@@ -236,9 +236,9 @@ __device__ __forceinline__ void tr_frags(const uint32_t (&lo)[N], const uint32_t
 // once: a tile at the border of two would otherwise take twice as long as all
 // others, and the launch with it.  They come last, so that the tiles with one adapter
 // start without them, and LDS is left for them.
-// Bound by memory: 32768 x 4096 rows in 49 us (5.5 TB/s) against rank 16, 65 against 64
-// with nothing written before; stages of 128 values, 128 positions and deeper rings
-// were no faster.
+// Bound by memory: 32768 x 4096 rows in 44 us (6.1 TB/s) against rank 16, 75 against
+// eight adapters of rank 64; stages of 128 values, 128 positions and deeper rings were
+// no faster.
 template <int T, bool kNN, int S>
 struct ShrinkCfg {
     static constexpr int kRows = 64, kK = 64, kRowBytes = 2 * kK;
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(kAdBlock) void shrink_kernel(ShrinkArgs a)
         return;
     // Neighbours on an XCD begin 512 bytes apart and go round: rows of a power of two
     // bytes, all read at one column, would keep few of the memory's channels busy
-    // (32768 x 4096, rank 16, begun alike: 61 us for 49).
+    // (32768 x 4096, rank 16, begun alike: 54 us for 44).
     const int32_t begin = nk ? (int32_t)(blockIdx.x / 8 * (256 / G::kK) % nk) : 0;
     // this lane's chunk and row, of its wave's loads of a stage of rows
     const uint16_t *xp[G::kXInstr];
@@ -776,9 +776,12 @@ struct Expand {
 };
 
 // Many rows: a wave keeps its columns of one adapter's matrix in registers and
-// walks row tiles.  Base rows come through the wave's own ring of LDS slots, kAhead
-// tiles ahead (so many bytes in flight would not fit the registers), parts one tile
-// ahead into registers; no wave waits for another.
+// walks row tiles.  Bound by memory: 32768 x 4096 base rows and results in 98 us (5.5
+// TB/s) up to rank 32, 115 at 64; at 128 in 168 forward and 178 backward, by the parts,
+// which come from the L2 once for every 64 or 128 columns (64 in the backward: 279).
+// Base rows come through the wave's own ring of LDS slots, kAhead tiles ahead (so many
+// bytes in flight would not fit the registers), parts one tile ahead into registers;
+// no wave waits for another.
 constexpr int kAhead = 2;
 constexpr int kTileRun = 32;  // row tiles whose rows and adapters are looked up at once
 
@@ -1036,8 +1039,9 @@ __device__ __forceinline__ int32_t adapter_rows(const int32_t *off, const int32_
 // share, since from one piece to the next the chunk or the adapter grows and
 // neither falls.
 // Bound by memory, the rows being read once: 32768 rows, 4096 -> 4096, rank 16, in
-// 129 us (4.2 TB/s).  Deeper rings, and one sequence of stages over the pieces, were
-// no faster.
+// 93 to 102 us (5.3 to 5.8 TB/s); rank 128, where the matrix instructions' three
+// products are 206 GFLOP, 251.  Deeper rings, and one sequence of stages over the
+// pieces, were no faster.
 constexpr int kGradCols = 256;
 constexpr int kStepRun = 32;  // steps whose rows are looked up at once
 
@@ -1459,7 +1463,8 @@ void expand_as(ExpandArgs a, Form form, hipStream_t st)
     }
     const int64_t blocks = (a.w.D + 64 * CT - 1) / (64 * CT);
     // two workgroups per CU, all at once (32768 rows, 4096 wide, rank 64, the whole call:
-    // 202 us; one per CU 241, four 224)
+    // 183 us; one per CU 222, four 208), or three with one tile each (4099 rows, 2048 wide,
+    // the whole backward: 64.0 us, 62.5)
     int64_t per = tiles * blocks <= 768 ? 1 : (tiles * blocks + 511) / 512;
     per = per < (tiles + 65534) / 65535 ? (tiles + 65534) / 65535 : per;
     a.tiles = (int32_t)(per < tiles ? per : tiles);
@@ -1503,8 +1508,8 @@ uint32_t wgrad_shares(const WgradArgs &a, uint32_t parts)
 }
 
 // Tiles of the rank that a workgroup takes: those there are, up to four (32768 rows, rank
-// 128, the whole call: 526 us, with all eight 588, with two 577; rank 64: 319, two 371),
-// and fewer where that leaves less than a workgroup per CU (us with 4, 2 and 1 tiles: 1237
+// 128, the whole call: 496 us, with two 544, with all eight 60 more than with four; rank
+// 64: 312, two 359), and fewer where that leaves less than a workgroup per CU (us with 4, 2 and 1 tiles: 1237
 // rows, 536 -> 304, rank 128: 47, 41, 39; 97 rows of 102 adapters, 80 -> 2840, rank 32: -,
 // 32, 27; but 500 rows of 16, 1024 wide, rank 128: 46, 49, 56).
 int wgrad_tiles(const WgradArgs &a)
@@ -1683,7 +1688,7 @@ int launch_adapter_bwd(int32_t rows, int32_t E, const moonep_adapters &ad, const
         a.blocks_a = (ad.in_dim + kGradCols - 1) / kGradCols;
         const int32_t blocks = a.blocks = a.blocks_a + (ad.out_dim + kGradCols - 1) / kGradCols;
         // 64 chunks at most, for about 512 workgroups (32768 rows, 4096 -> 4096, the whole
-        // call: 297 us; 256 of them 332, 1024 315), of at least 128 positions, and of 256
+        // call: 269 us; 256 of them 320, 1024 285), of at least 128 positions, and of 256
         // where that leaves 256 workgroups: most adapters' rows then lie in one chunk (4099
         // rows of 32 adapters, 2048 -> 1408: 62 -> 56; 2249 of 24, 88 -> 88: 56, 60 with
         // 256).  Few rows of many adapters are one chunk, as one run: their sums need no

@@ -22,6 +22,11 @@
 // rows are 256 or 512 bytes, a multiple of the 64 banks of 4 bytes, so the four
 // would share 16 banks; the 64-byte piece p of row r is stored at piece
 // p ^ (r % 4), which spreads them over all 64.
+//
+// Bounds, on 64 experts.  262144 rows, 2048 -> 1408: the matrix instructions, 1450 us
+// (1.04 PFLOP/s; the pipe is busy 57% of the cycles in d_x and 62% in g, at 1.75 GHz,
+// where loads and products share the power).  3904 rows, 1408 -> 2048: the weights'
+// bytes in d_x (96 us, 4.1 TB/s) and the gradients' in g (170 us, 4.5 TB/s).
 #include "segments.hpp"
 
 namespace moonep {
