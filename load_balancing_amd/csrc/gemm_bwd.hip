@@ -671,7 +671,7 @@ int run_dw(const DwArgs &a, hipStream_t st)
 
 }  // namespace
 
-// Tiles of 256 x 256, eight waves, or of 128 x 128, four waves and two
+// Tiles of 256 x 256, eight waves, or of 128 x 128 and less, four waves and two
 // workgroups per CU, measured on 64 experts, 2048 -> 1408 (d_x) and 1408 -> 2048
 // (g), us, large tile first:
 //   d_x, by mean rows of an expert:   32: 112, 92    61: 117, 95   128: 127, 123
@@ -682,7 +682,15 @@ int run_dw(const DwArgs &a, hipStream_t st)
 constexpr int64_t kLargeRows = 448;    // mean rows of an expert from which d_x takes large tiles
 constexpr int64_t kLargeItemsX = 512;  // and of those tiles
 constexpr int64_t kLargeItemsW = 320;  // large tiles from which g takes them
-constexpr int64_t kFewItems = 256;     // small tiles up to which each has a CU
+// Where all items of smaller tiles run at once, each on a CU of its own, d_x takes those of
+// 64 x 128, or of 128 x 128 with a third slot instead of a second workgroup (us with 128,
+// two or three slots, and with 64): 3387 rows, 1024 -> 192, 9 experts: 20, 16, 12; 1024
+// rows, 2048 -> 1024, 8 experts (160 items of 64): -, 25.5, 21.0; 2048 rows (288): -, 26,
+// 33.  Experts of few rows leave most of a tile empty, and what counts is how many loads
+// are in flight: 64 x 128 with four slots (mean rows 32: 93, 85; 50: 93, 84; 61: 95, 95;
+// 80: 98, 105; 32 experts, 2048 -> 1024, 64: 55, 45; 128: 53, 59).
+constexpr int64_t kFewItems = 256;
+constexpr int64_t kShortRows = 64;
 
 int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *wslot, int32_t B,
                      int32_t in_dim, int32_t out_dim, const uint16_t *d_y, const uint16_t *w_home,
@@ -697,10 +705,12 @@ int launch_expert_dx(const moonep_shape &s, const int32_t *plan, const int32_t *
     const int64_t items = ((rows + 255) / 256 + s.E / 2) * ((in_dim + 255) / 256);
     if (rows >= kLargeRows * s.E && items >= kLargeItemsX)
         return run_dx<256, 256, 128, 64, 32, 4>(a, st);
-    // where all items run at once, on a CU of their own, a third slot takes less time
-    // than a second workgroup (3387 rows, 1024 -> 192, 9 experts: 16 us for 20)
-    const int64_t small_items = ((rows + 127) / 128 + s.E / 2) * ((in_dim + 127) / 128);
-    if (small_items <= kFewItems)
+    const int64_t blocks = (in_dim + 127) / 128;
+    if (((rows + 63) / 64 + s.E / 2) * blocks <= kFewItems)
+        return run_dx<64, 128, 32, 64, 64, 3>(a, st);
+    if (rows <= kShortRows * s.E)
+        return run_dx<64, 128, 32, 64, 64, 4>(a, st);
+    if (((rows + 127) / 128 + s.E / 2) * blocks <= kFewItems)
         return run_dx<128, 128, 64, 64, 64, 3>(a, st);
     return run_dx<128, 128, 64, 64, 64, 2>(a, st);
 }

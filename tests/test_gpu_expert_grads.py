@@ -47,6 +47,11 @@ CASES = [
     (8, 16, 4099, 2, 576, 128, 1),
     (4, 64, 40, 2, 832, 384, 0),
     (2, 32, 300, 4, 1088, 640, 1),
+    # d_x: small tiles of 128 rows, each on a CU and not, and of 64 rows in several rounds
+    (2, 4, 1000, 2, 640, 256, 1),
+    (8, 16, 1500, 2, 576, 128, 1),
+    (8, 64, 500, 4, 704, 128, 2),
+    (4, 64, 200, 4, 1344, 128, 2),
 ]
 
 
