@@ -1495,14 +1495,15 @@ uint32_t wgrad_parts(const WgradArgs &a, int T)
     return (uint32_t)(a.blocks * ((a.rank + 16 * T - 1) / (16 * T)));
 }
 
-// Workgroups for a chunk: about as many as it has adapters, 16 at most, while the launch
-// is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 -> 24 us);
-// one where a chunk is more than one run, whose pieces may go on.
+// Workgroups for a chunk: about as many as it has adapters, 32 at most, while the launch
+// is small (55 rows, 20 adapters, 840 -> 104, rank 32: the whole backward 61 -> 24 us; us
+// with at most 16, 32 and 64: 361 rows of 129 adapters: 46, 39, 38; 200 of 200, 2048
+// wide: 53, 49, 68); one where a chunk is more than one run, whose pieces may go on.
 uint32_t wgrad_shares(const WgradArgs &a, uint32_t parts)
 {
     const int64_t room = 2048 / ((int64_t)parts * a.nchunks);
     int64_t shares = a.r.n / a.nchunks + 1;
-    shares = shares < 16 ? shares : 16;
+    shares = shares < 32 ? shares : 32;
     shares = shares < room ? shares : room;
     return shares < 1 || a.chunk > kStepRun * kStep ? 1 : (uint32_t)shares;
 }
