@@ -668,9 +668,9 @@ int moonep_grad_norm(int64_t entries, const int64_t *table, double *sumsq, float
  *   dst = g * fp32(max_norm / norm)   if norm > max_norm and norm is finite,
  *   dst = g                           otherwise (nothing is written where dst is
  *                                     the gradient itself),
- * rounded once to the gradient's type.  An infinity or a NaN among the gradients
- * leaves them all as they are, and norm says so.  max_norm is finite and >= 0
- * (MOONEP_ERR_ARG).  workspace may be NULL where sumsq is given.
+ * the exact product rounded once to the gradient's type.  An infinity or a NaN among
+ * the gradients leaves them all as they are, and norm says so.  max_norm is finite
+ * and >= 0 (MOONEP_ERR_ARG).  workspace may be NULL where sumsq is given.
  */
 int moonep_grad_clip(int64_t entries, const int64_t *table, double max_norm, const double *sumsq,
                      float *norm, void *workspace, size_t workspace_bytes, void *stream);

@@ -152,14 +152,36 @@ __global__ __launch_bounds__(kGradBlock) void grad_norm_kernel(const double *sum
     }
 }
 
+// A product of bf16 by f has up to 32 bits.  Rounded to fp32 and then to bf16 it is
+// off where the first rounding makes a tie for the second (one value in 1.5e5): those, and what
+// is a tie by itself, are rounded again from the exact product, which fp64 holds.
+__device__ __forceinline__ bool bf16_tie(float p) { return (uint16_t)__float_as_uint(p) == 0x8000; }
+__device__ __forceinline__ uint32_t scaled_exactly(float g, float f)
+{
+    return bf16_of_double((double)g * (double)f);
+}
+
 template <bool kBf16>
 __device__ __forceinline__ u32x4 scaled(u32x4 v, float f)
 {
     u32x4 o;
+    bool tie = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = kBf16 ? pack_bf16(bf16_lo(v[i]) * f, bf16_hi(v[i]) * f)
-                     : __float_as_uint(__uint_as_float(v[i]) * f);
+    for (int i = 0; i < 4; ++i) {
+        if (kBf16) {
+            const float a = bf16_lo(v[i]) * f, b = bf16_hi(v[i]) * f;
+            o[i] = pack_bf16(a, b);
+            tie |= bf16_tie(a);
+            tie |= bf16_tie(b);
+        } else {
+            o[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+        }
+    }
+    if (kBf16 && tie) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = scaled_exactly(bf16_lo(v[i]), f) | scaled_exactly(bf16_hi(v[i]), f) << 16;
+    }
     return o;
 }
 
@@ -183,11 +205,11 @@ __device__ __forceinline__ void run_scale(const GradRun &r, float f)
     for (; i < vecs; i += kGradBlock)
         store16_nt(dst + i * 16, scaled<kBf16>(load16_nt(src + i * 16), f));
     for (int64_t e = vecs * kPer + threadIdx.x; e < r.count; e += kGradBlock) {
-        const float o = load1(src + e * kSize, kBf16) * f;
+        const float g = load1(src + e * kSize, kBf16);
         if (kBf16)
-            *(MOONEP_GLOBAL uint16_t *)(dst + e * kSize) = (uint16_t)pack_bf16(o, 0.0f);
+            *(MOONEP_GLOBAL uint16_t *)(dst + e * kSize) = (uint16_t)scaled_exactly(g, f);
         else
-            *(MOONEP_GLOBAL float *)(dst + e * kSize) = o;
+            *(MOONEP_GLOBAL float *)(dst + e * kSize) = g * f;
     }
 }
 
