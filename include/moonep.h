@@ -664,13 +664,15 @@ int moonep_grad_norm(int64_t entries, const int64_t *table, double *sumsq, float
                      void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * The same norm (of sumsq[0] if it is given: the sum over all ranks), and
+ * The same norm (of sumsq[0] if it is given: the sum over all ranks), and, with
+ * the fp64 root in the place of norm,
  *   dst = g * fp32(max_norm / norm)   if norm > max_norm and norm is finite,
  *   dst = g                           otherwise (nothing is written where dst is
  *                                     the gradient itself),
  * the exact product rounded once to the gradient's type.  An infinity or a NaN among
- * the gradients leaves them all as they are, and norm says so.  max_norm is finite
- * and >= 0 (MOONEP_ERR_ARG).  workspace may be NULL where sumsq is given.
+ * the gradients leaves them all as they are, and norm says so; finite ones whose
+ * norm is beyond fp32 are scaled as above, norm[0] being an infinity.  max_norm is
+ * finite and >= 0 (MOONEP_ERR_ARG).  workspace may be NULL where sumsq is given.
  */
 int moonep_grad_clip(int64_t entries, const int64_t *table, double max_norm, const double *sumsq,
                      float *norm, void *workspace, size_t workspace_bytes, void *stream);

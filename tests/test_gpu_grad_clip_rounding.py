@@ -50,3 +50,18 @@ def test_one_rounding(gpu_ready, scale, in_place):
     for f in FACTORS:
         want = once(g.double() * f)  # 8 bits by 24: exact in fp64
         assert torch.equal(clipped(g, f, in_place), want), f
+
+
+def test_a_norm_beyond_fp32(gpu_ready):
+    """Finite gradients whose norm is not finite in fp32 are clipped; the norm says infinity."""
+    g = torch.full((1000,), 3.0e38, device="cuda")
+    h = g[:10].bfloat16()
+    total = ((g.double() ** 2).sum() + (h.double() ** 2).sum()).sqrt().item()
+    f = torch.tensor(1.0e30 / total).float().item()
+    out = [torch.zeros_like(g), torch.zeros_like(h)]
+    norm, work = torch.empty(1, device="cuda"), torch.empty(mx.GRAD_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    mx.moonep_grad_clip(mx.moonep_grad_table([g, h], out), 1.0e30, norm, work)
+    assert norm.item() == float("inf")
+    # the sum of squares in another order may give the factor's neighbour
+    assert ((out[0].double() - g.double() * f).abs() <= 2.0 ** -22 * g.double() * f).all()
+    assert ((out[1].double() - h.double() * f).abs() <= (2.0 ** -8 + 2.0 ** -22) * h.double() * f).all()
