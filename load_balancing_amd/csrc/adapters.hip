@@ -115,11 +115,19 @@ struct ShrinkArgs {
     uint16_t *parts;        // or NULL: scale * result, see Parts
 };
 
+// Bits of the first bf16 part of a, whose nearest bf16 has bits `near`: that, but a's upper
+// half where a is finite and the nearest is not (from 255.5 2^120 on).
+__device__ __forceinline__ uint32_t first_part(float a, uint32_t near)
+{
+    return (near & 0x7FFF) == 0x7F80 ? __float_as_uint(a) >> 16 : near;
+}
+
 // Two bf16 parts of a pair of values, packed: 16 bits of each.  The second part
 // of an infinity is 0.
 __device__ __forceinline__ void split2(float a, float b, uint32_t *hi, uint32_t *lo)
 {
-    const uint32_t h = pack_bf16(a, b);
+    const uint32_t near = pack_bf16(a, b);
+    const uint32_t h = first_part(a, near & 0xFFFF) | first_part(b, near >> 16) << 16;
     const float h0 = bf16_lo(h), h1 = bf16_hi(h);
     *hi = h;
     *lo = pack_bf16(__builtin_isfinite(h0) ? a - h0 : 0.0f, __builtin_isfinite(h1) ? b - h1 : 0.0f);
@@ -570,7 +578,7 @@ struct PrepArgs {
 // The three bf16 parts of a value, all 24 bits; the later ones of an infinity are 0.
 __device__ __forceinline__ void split3(float a, uint16_t *p0, uint16_t *p1, uint16_t *p2)
 {
-    const uint32_t hi = pack_bf16(a, 0.0f);
+    const uint32_t hi = first_part(a, pack_bf16(a, 0.0f) & 0xFFFF);
     const float h = bf16_lo(hi);
     const float r = __builtin_isfinite(h) ? a - h : 0.0f;
     const uint32_t mid = pack_bf16(r, 0.0f);

@@ -1,0 +1,53 @@
+"""Adapters on an MI355X with the values at which split products can go wrong: infinities
+and NaN in matrices and rows, sums at the end of fp32's range, and gradients that need all
+24 bits of u and du."""
+import pytest
+import torch
+
+from test_gpu_adapters import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def all_gradients(c):
+    d_x = torch.full_like(c.dx_base, 7.0)
+    d_bank = torch.full((c.M, c.ad.stride), 7.0, device="cuda")
+    c.backward(d_bank=d_bank, d_x=d_x, dx_base=c.dx_base)
+    return d_x, d_bank
+
+
+NEAR_THE_END = 255 * 2.0 ** 120 + 0.75 * 2.0 ** 120  # of fp32; its nearest bf16 is an infinity
+
+
+@pytest.mark.parametrize("rank", [8, 24, 64, 128])
+@pytest.mark.parametrize("N", [40, 2200])
+def test_sums_at_the_end_of_fp32(gpu_ready, N, rank):
+    """u and du that fp32 holds and bf16 does not: finite results where the formula's are."""
+    c = Case(N, 3, rank, 64, 72, seed=13)
+    A, B = c.mats(c.bank)
+    c.scale.fill_(1.0)
+    sign = torch.where(torch.rand(N, generator=c.g, device="cuda") < 0.5, -1.0, 1.0)
+    tiny = 2.0 ** -100
+    c.x.zero_()
+    c.x[:, 0], c.x[:, 1] = 255 * 2.0 ** 120 * sign, 0.75 * 2.0 ** 120 * sign
+    A.fill_(1.0)
+    B *= tiny
+    c.base *= tiny
+    c.forward()
+    assert (c.u[c.ids < 3].abs() == NEAR_THE_END).all()
+    c.check_forward()
+    # d_y tiny: dB takes u
+    c.d_y *= tiny
+    c.dx_base *= tiny
+    B /= tiny
+    A.copy_(torch.randn(A.shape, generator=c.g, device="cuda"))
+    c.x.copy_(torch.randn(c.x.shape, generator=c.g, device="cuda"))
+    c.check_backward(*all_gradients(c))
+    # du as large: d_x and dA take it
+    c.u *= tiny * tiny
+    c.d_y.zero_()
+    c.d_y[:, 0], c.d_y[:, 1] = 255 * 2.0 ** 120 * sign, 0.75 * 2.0 ** 120 * sign
+    B.fill_(1.0)
+    A *= tiny
+    c.x *= tiny
+    c.check_backward(*all_gradients(c))
