@@ -757,6 +757,50 @@ struct Expand {
                 res[t][i] = mine[i] ? acc[i] : res[t][i];
         }
     }
+    // Whether the wave holds a NaN: a maximum that is one if any value is (32768 x 4096 rows,
+    // rank 8 to 64, the whole call: 175 to 199 us without the question, 176 to 200.5 with it).
+    __device__ __forceinline__ bool any_nan(const f32x4 (&res)[CT]) const
+    {
+        float m = 0.0f;
+#pragma unroll
+        for (int t = 0; t < CT; t += 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, res[t][i]), res[t + 1][i]);
+        return ballot(__builtin_isnan(m)) != 0;
+    }
+    // For rows that any_nan holds of, once they are stored.  A value's second part may be 0
+    // or of the first's other sign, so that an infinite weight makes a NaN of the two: there
+    // the first part alone gives what the value itself does.
+    __device__ __forceinline__ void store_nans_again(const Frag (&w)[PS][CT], const Frag (&u)[kSteps],
+                                                     const bool (&mine)[4], const int32_t (&row)[4],
+                                                     const piece (&b)[4], uint16_t *y) const
+    {
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            f32x4 both = {0, 0, 0, 0}, first = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                both = mfma16(u[s].v, w[kHalf ? 0 : s % PS][t].v, both);
+#pragma unroll
+            for (int s = 0; s < PS; ++s) {
+                Frag uf = u[s], wf = w[s][t];
+#pragma unroll
+                for (int j = 0; kHalf && j < 4; ++j) {  // zeros in both for lanes of the second
+                    uf.w[j] = lane_id() < 32 ? uf.w[j] : 0;
+                    wf.w[j] = lane_id() < 32 ? wf.w[j] : 0;
+                }
+                first = mfma16(uf.v, wf.v, first);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (mine[i] && col < D && __builtin_isnan(both[i])) {
+                    const float base = t % 2 ? bf16_hi(b[i][t / 2]) : bf16_lo(b[i][t / 2]);
+                    y[(int64_t)row[i] * D + col + t] = (uint16_t)pack_bf16(base + first[i], 0.0f);
+                }
+            __builtin_amdgcn_sched_barrier(0);  // one tile after the other, for registers
+        }
+    }
     // A row without an adapter is copied bit for bit.
     template <bool kStream>
     __device__ __forceinline__ void store(uint16_t *y, const int32_t (&row)[4], const int32_t (&id)[4],
@@ -874,7 +918,9 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
 #pragma unroll
             for (int c = 0; c < CT; ++c)
                 res[c] = f32x4{0, 0, 0, 0};
-            for (;;) {
+            // the next adapter of the rows left, its matrix and its rows; false if there is none
+            bool mine[4];
+            auto next_adapter = [&]() -> bool {
                 int32_t cur = -1;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -883,24 +929,34 @@ __global__ __launch_bounds__(kAdBlock) void expand_kernel(ExpandArgs a)
                         cur = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(some));
                 }
                 if (cur < 0)
-                    break;
+                    return false;
                 if (cur != have) {
                     have = cur;
                     x.load_w(a.w.first + cur * a.w.stride, wf);
                 }
-                bool mine[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     mine[i] = id[i] == cur;
                     left[i] = left[i] && !mine[i];
                 }
+                return true;
+            };
+            while (next_adapter())
                 x.product(wf, u, mine, res);
-            }
             bool wanted[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 wanted[i] = row[i] >= 0;
+            const bool nan = x.any_nan(res);
             x.template store<kStream>(a.y, row, id, wanted, b, res);
+            if (nan) {
+                wait_vm<0>();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    left[i] = id[i] >= 0;
+                while (next_adapter())
+                    x.store_nans_again(wf, u, mine, row, b, a.y);
+            }
 #pragma unroll
             for (int k = 0; k < G::kSteps; ++k)
                 u[k] = u2[k];
@@ -991,18 +1047,28 @@ __device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, 
 #pragma unroll
     for (int t = 0; t < CT; ++t)
         res[t] = f32x4{0, 0, 0, 0};
-    while (todo) {
-        const int32_t cur = __builtin_amdgcn_readlane(u_id, __builtin_ctzll(todo));
-        Frag wf[PS][CT];
+    Frag wf[PS][CT];
+    bool mine[4];
+    auto next_adapter = [&](uint64_t &left) -> bool {  // as in expand_kernel
+        if (!left)
+            return false;
+        const int32_t cur = __builtin_amdgcn_readlane(u_id, __builtin_ctzll(left));
         x.load_w(a.w.first + cur * a.w.stride, wf);
-        todo &= ~ballot(u_id == cur);
-        bool mine[4];
+        left &= ~ballot(u_id == cur);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             mine[i] = id[i] == cur;
+        return true;
+    };
+    for (uint64_t rest = todo; next_adapter(rest);)
         x.product(wf, u, mine, res);
-    }
+    const bool nan = x.any_nan(res);
     x.template store<false>(a.y, row, id, wanted, b, res);
+    if (nan) {
+        wait_vm<0>();
+        for (uint64_t rest = todo; next_adapter(rest);)
+            x.store_nans_again(wf, u, mine, row, b, a.y);
+    }
 }
 
 template <int PS, bool kHalf, int CT>

@@ -8,6 +8,42 @@ from test_gpu_adapters import Case
 
 pytestmark = pytest.mark.gpu
 
+INF = float("inf")
+
+
+def same_kind_and_near(got, want, tol):
+    """NaN and the infinities where the fp64 formula has them, and within tol elsewhere."""
+    got = got.double()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf())
+    fin = want.isfinite()
+    assert ((got - want).abs()[fin] <= tol[fin]).all()
+
+
+@pytest.mark.parametrize("order", [True, False])
+@pytest.mark.parametrize("rank", [8, 16, 24, 40, 64, 128])
+@pytest.mark.parametrize("N", [40, 2200])
+def test_infinities_in_the_forward(gpu_ready, N, rank, order):
+    """An infinite weight gives its column infinities of u's signs, an infinite row its results."""
+    c = Case(N, 4, rank, 64, 72, seed=11)
+    A, B = c.mats(c.bank)
+    B[1, 5, 3] = INF
+    B[2, 70, rank - 1] = -INF
+    B[3, 8, 1], B[3, 8, 2] = INF, -INF
+    for m in (0, 1):
+        c.x[torch.nonzero(c.ids == m)[0, 0], 9] = INF
+    c.forward(order)
+    for m in range(4):
+        at, s = c.ids == m, c.scale[m].double()
+        x, a, b, base = c.x[at].double(), A[m].double(), B[m].double(), c.base[at].double()
+        u = x @ a.T
+        same_kind_and_near(c.u[at], u, 64 * 2.0 ** -23 * (x.abs() @ a.abs().T))
+        su = s * c.u[at].double()
+        want, mag = base + su @ b.T, su.abs() @ b.abs().T
+        # the split to 16 bits, the scale's rounding, 2 rank additions and that of base; bf16's rounding
+        tol = 1.01 * (2.0 ** -16 + (2 * rank + 2) * 2.0 ** -23) * mag + 2.0 ** -23 * (base.abs() + mag)
+        same_kind_and_near(c.y[at], want, tol + 2.0 ** -8 * want.abs())
+
 
 def all_gradients(c):
     d_x = torch.full_like(c.dx_base, 7.0)
