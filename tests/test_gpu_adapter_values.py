@@ -52,6 +52,28 @@ def all_gradients(c):
     return d_x, d_bank
 
 
+@pytest.mark.parametrize("rank", [8, 16, 24, 40, 64, 128])
+@pytest.mark.parametrize("N", [60, 1000, 2200, 9000])
+def test_infinities_in_the_backward(gpu_ready, N, rank):
+    """Infinite weights, rows and gradients, and a NaN, each of another adapter or place."""
+    c = Case(N, 5, rank, 64, 72, seed=12)
+    c.u = torch.randn((N, rank), generator=c.g, device="cuda")
+    A, B = c.mats(c.bank)
+    A[1, 2, 6], A[1, 4, 60] = INF, -INF
+    B[2, 9, 3] = INF
+    first = lambda m, k=0: torch.nonzero(c.ids == m)[k, 0]  # noqa: E731
+    c.x[first(3), 4], c.x[first(3, 1), 50] = INF, -INF
+    c.x[first(3, 1), 4] = INF
+    c.d_y[first(0), 8] = -INF
+    c.x[first(4), 33] = float("nan")
+    c.u[first(4), 5] = INF
+    d_x, d_bank = all_gradients(c)
+    dx, t_x, grads, tols = c.reference_backward()
+    same_kind_and_near(d_x, dx, t_x)
+    for got, want, tol in zip(c.mats(d_bank), grads, tols):
+        same_kind_and_near(got, want, tol)
+
+
 NEAR_THE_END = 255 * 2.0 ** 120 + 0.75 * 2.0 ** 120  # of fp32; its nearest bf16 is an infinity
 
 
