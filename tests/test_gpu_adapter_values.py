@@ -109,3 +109,60 @@ def test_sums_at_the_end_of_fp32(gpu_ready, N, rank):
     A *= tiny
     c.x *= tiny
     c.check_backward(*all_gradients(c))
+
+
+EXACT = [
+    # N, M, rank: few rows in one piece and several, many rows, adapters over several chunks
+    (40, 5, 8), (40, 40, 24), (700, 9, 72), (200, 3, 128), (2200, 6, 8), (2200, 90, 40),
+    (9000, 1, 24), (9000, 2, 72), (9000, 3, 128), (5000, 3, 64), (5000, 2, 16), (33000, 2, 32),
+]
+
+
+def one_row_each(c, n):
+    """For every adapter with rows, one of them for each of n columns."""
+    rows = [torch.nonzero(c.ids == m)[:, 0] for m in range(c.M)]
+    return [r[torch.randint(0, r.numel(), (n,), generator=c.g, device="cuda")] if r.numel() else None for r in rows]
+
+
+@pytest.mark.parametrize("N,M,rank", EXACT)
+def test_all_bits_of_u_reach_the_gradient(gpu_ready, N, M, rank):
+    """d_y is 1 in one row of each column and 0 elsewhere: dB holds rows of u, to the bit."""
+    c = Case(N, M, rank, 64, 72, seed=14)
+    c.scale.fill_(1.0)
+    c.u = torch.randn((N, rank), generator=c.g, device="cuda")
+    c.d_y.zero_()
+    hot, cols = one_row_each(c, c.out), torch.arange(c.out, device="cuda")
+    for r in hot:
+        if r is not None:
+            c.d_y[r, cols] = 1.0
+    d_bank = torch.full((M, c.ad.stride), 7.0, device="cuda")
+    c.backward(d_bank=d_bank)
+    dB = c.mats(d_bank)[1]
+    for m, r in enumerate(hot):
+        assert torch.equal(dB[m], c.u[r] if r is not None else torch.zeros_like(dB[m])), m
+
+
+@pytest.mark.parametrize("N,M,rank", EXACT)
+def test_all_bits_of_du_reach_the_gradient(gpu_ready, N, M, rank):
+    """du is an integer of 24 bits, in exact sums of three products; x is 1 in one row of
+    each column and 0 elsewhere: dA holds rows of du, to the bit."""
+    c = Case(N, M, rank, 64, 72, seed=15)
+    c.scale.fill_(1.0)
+    c.d_y.zero_()
+    c.d_y[:, :3] = torch.where(torch.rand((N, 3), generator=c.g, device="cuda") < 0.5, -1.0, 1.0).bfloat16()
+    _, B = c.mats(c.bank)
+    digits = torch.randint(128, 256, (M, 3, rank), generator=c.g, device="cuda").float()
+    B[:, :3] = (digits * torch.tensor([65536.0, 256.0, 1.0], device="cuda")[None, :, None]).bfloat16()
+    c.x.zero_()
+    hot, cols = one_row_each(c, c.inp), torch.arange(c.inp, device="cuda")
+    for r in hot:
+        if r is not None:
+            c.x[r, cols] = 1.0
+    c.u.zero_()
+    d_bank = torch.full((M, c.ad.stride), 7.0, device="cuda")
+    c.backward(d_bank=d_bank)
+    dA, dB = c.mats(d_bank)
+    assert (dB == 0).all()
+    for m, r in enumerate(hot):
+        du = c.d_y[r, :3].double() @ B[m, :3].double() if r is not None else torch.zeros((c.inp, rank), device="cuda")
+        assert torch.equal(dA[m], du.T.float()), m
