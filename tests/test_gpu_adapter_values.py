@@ -166,3 +166,23 @@ def test_all_bits_of_du_reach_the_gradient(gpu_ready, N, M, rank):
     for m, r in enumerate(hot):
         du = c.d_y[r, :3].double() @ B[m, :3].double() if r is not None else torch.zeros((c.inp, rank), device="cuda")
         assert torch.equal(dA[m], du.T.float()), m
+
+
+WIDE = [
+    # more rows than few, of contractions in several parts, at the ranks above 32
+    (1100, 5, 64, 2048, 2056), (1100, 4, 40, 2056, 4096), (1100, 3, 128, 4096, 2048), (1100, 3, 96, 2048, 4104),
+    # rows and results past the caches (over 128 MiB) at every form of the rank
+    (9000, 5, 24, 8192, 8192), (9000, 4, 64, 8200, 8192), (9000, 3, 128, 8192, 8200),
+]
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_wide_rows(gpu_ready, case):
+    c = Case(*case, gap=8, seed=16)
+    c.forward()
+    c.check_forward()
+    d_x, d_bank = all_gradients(c)
+    c.check_backward(d_x, d_bank)
+    for m in c.mats(d_bank):
+        m.fill_(7.0)
+    assert (d_bank == 7.0).all()
