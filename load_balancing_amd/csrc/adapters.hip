@@ -1047,27 +1047,33 @@ __device__ __forceinline__ void expand_few(const ExpandArgs &a, uint32_t block, 
 #pragma unroll
     for (int t = 0; t < CT; ++t)
         res[t] = f32x4{0, 0, 0, 0};
-    Frag wf[PS][CT];
-    bool mine[4];
-    auto next_adapter = [&](uint64_t &left) -> bool {  // as in expand_kernel
-        if (!left)
-            return false;
-        const int32_t cur = __builtin_amdgcn_readlane(u_id, __builtin_ctzll(left));
+    uint64_t again = todo;  // loops of their own: one for both took 0.3 of 6 us more
+    while (todo) {
+        const int32_t cur = __builtin_amdgcn_readlane(u_id, __builtin_ctzll(todo));
+        Frag wf[PS][CT];
         x.load_w(a.w.first + cur * a.w.stride, wf);
-        left &= ~ballot(u_id == cur);
+        todo &= ~ballot(u_id == cur);
+        bool mine[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             mine[i] = id[i] == cur;
-        return true;
-    };
-    for (uint64_t rest = todo; next_adapter(rest);)
         x.product(wf, u, mine, res);
+    }
     const bool nan = x.any_nan(res);
     x.template store<false>(a.y, row, id, wanted, b, res);
-    if (nan) {
-        wait_vm<0>();
-        for (uint64_t rest = todo; next_adapter(rest);)
-            x.store_nans_again(wf, u, mine, row, b, a.y);
+    if (!nan)
+        return;
+    wait_vm<0>();
+    while (again) {
+        const int32_t cur = __builtin_amdgcn_readlane(u_id, __builtin_ctzll(again));
+        Frag wf[PS][CT];
+        x.load_w(a.w.first + cur * a.w.stride, wf);
+        again &= ~ballot(u_id == cur);
+        bool mine[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine[i] = id[i] == cur;
+        x.store_nans_again(wf, u, mine, row, b, a.y);
     }
 }
 
