@@ -578,8 +578,9 @@ int moonep_expert_gemm_dw(const moonep_shape *shape, const int32_t *plan, int32_
  * after the other.  The results depend on it in the order of u's fp32 sums only; a
  * row that is not in it is left out.
  *
- * workspace: moonep_adapter_workspace_bytes, 16-byte aligned, no initial contents
- * needed; one call at a time uses it.
+ * workspace: moonep_adapter_workspace_bytes (64 rank bytes a row, what the call in most
+ * parts takes), 16-byte aligned, no initial contents needed; one call at a time uses it.
+ * Infinities and NaN come out where the formulas have them, and reach no other row.
  * Limits (MOONEP_ERR_ARG): 1 <= n <= E, rank, in_dim and out_dim multiples of 8,
  * rank at most 128, in_dim and out_dim at most 2^22, stride and offsets multiples
  * of 8, windows inside the row and apart.  bf16 arrays, u and workspace 16-byte
@@ -621,8 +622,8 @@ int moonep_adapter(const moonep_shape *shape, const moonep_adapters *ad, const i
  * order and plan: moonep_plan's src_of_slot and plan for `shape` and ids (order
  * may be NULL where d_bank is).  With another plan's tables d_bank is unspecified,
  * but every access stays in bounds.  The other arguments and the limits are
- * moonep_adapter's; workspace: moonep_adapter_bwd_workspace_bytes; d_bank 16-byte
- * aligned.
+ * moonep_adapter's; workspace: moonep_adapter_bwd_workspace_bytes (68 rank bytes a row
+ * and n + 64 fp32 windows, whatever is computed); d_bank 16-byte aligned.
  */
 int moonep_adapter_bwd(const moonep_shape *shape, const moonep_adapters *ad, const int32_t *ids,
                        const int32_t *order, const int32_t *plan, const uint16_t *x, const float *u,

@@ -829,11 +829,13 @@ struct Expand {
 
 // Many rows: a wave keeps its columns of one adapter's matrix in registers and
 // walks row tiles.  Bound by memory: 32768 x 4096 base rows and results in 98 us (5.5
-// TB/s) up to rank 32, 115 at 64; at 128 in 168 forward and 178 backward, by the parts,
+// TB/s) up to rank 32, 112 at 64; at 128 in 168 forward and 178 backward, by the parts,
 // which come from the L2 once for every 64 or 128 columns (64 in the backward: 279).
-// Base rows come through the wave's own ring of LDS slots, kAhead tiles ahead (so many
-// bytes in flight would not fit the registers), parts one tile ahead into registers;
-// no wave waits for another.
+// Base rows come through the wave's own ring of LDS slots (so many bytes in flight would
+// not fit the registers), requested kAhead tiles ahead, and parts one tile ahead into
+// registers; no wave waits for another.  The parts enter the registers of the next tile
+// behind a wait for everything requested, so a tile costs a round trip, which only the
+// SIMD's other waves hide.
 constexpr int kAhead = 2;
 constexpr int kTileRun = 32;  // row tiles whose rows and adapters are looked up at once
 

@@ -171,9 +171,10 @@ struct DxCfg {
     // arithmetic then runs under matrix instructions, and with more than two slots there
     // is time (256 x 256 tiles, four slots: 1515 -> 1490 us on the sweep).
     static constexpr int kIssueAt = S > 2 ? BK / 16 - 1 : 0;
-    // Where large tiles are taken d_x is 64 MiB at least, of which the next call finds
-    // little in the caches: it is written past them (sweep: 1478 -> 1457 us, and with a
-    // call that reads it 277 -> 276 at 92 MB).
+    // Large tiles write d_x past the caches: it is 64 MiB at least where they are full, of
+    // which the next call finds little there (sweep: 1478 -> 1457 us, and with a call that reads
+    // it 277 -> 276 at 92 MB).  Narrow rows take them with less (14 MiB: 256 experts, 64
+    // wide); that was not timed.
     static constexpr bool kStream = BM == 256;
     // Epilogue: each wave's own 16 rows of WN columns, apart from the ring, which
     // is loading the next item.
@@ -404,8 +405,9 @@ struct DwCfg {
     static constexpr int kStageBytes = kStageA + kStageB;
     static constexpr int kAInstr = kStageA / 1024 / kWavesG, kBInstr = kStageB / 1024 / kWavesG;
     static constexpr int kPerStage = kAInstr + kBInstr;
-    // Gradients of 80 MiB or more are written past the caches (64 of 2048 x 1408, 3904
-    // rows: 179 -> 175 us)
+    // Large tiles write the gradients past the caches: 80 MiB or more where they are full (64 of
+    // 2048 x 1408, 3904 rows: 179 -> 175 us, without a call that reads them).  Narrow layers
+    // take them with less (16 MiB: 512 experts, 64 -> 128); that was not timed.
     static constexpr bool kStream = BM == 256;
     static_assert(kStageA % (1024 * kWavesG) == 0 && kStageB % (1024 * kWavesG) == 0, "DMA rounds");
     static_assert(S >= 2 && (S - 2) * kPerStage <= 63, "outstanding loads must fit vmcnt");
@@ -682,6 +684,9 @@ int run_dw(const DwArgs &a, hipStream_t st)
 constexpr int64_t kLargeRows = 448;    // mean rows of an expert from which d_x takes large tiles
 constexpr int64_t kLargeItemsX = 512;  // and of those tiles
 constexpr int64_t kLargeItemsW = 320;  // large tiles from which g takes them
+// Tiles that the dims leave part-empty count as full ones here; layers narrower than 256 with
+// many experts, where that matters, were not measured.
+
 // Where all items of smaller tiles run at once, each on a CU of its own, d_x takes those of
 // 64 x 128, or of 128 x 128 with a third slot instead of a second workgroup (us with 128,
 // two or three slots, and with 64): 3387 rows, 1024 -> 192, 9 experts: 20, 16, 12; 1024
